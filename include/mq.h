@@ -70,11 +70,14 @@ typedef int mq_status;
 #define MQ_DEV_TIMEOUT 4u        /* a kernel's bounded wait on its copy pipeline gave up; outputs not written */
 #define MQ_DEV_ALIAS 8u          /* a persistent step's input overlaps an output of the same launch outside
                                     the MQ_STEP_CHAINED pattern; nothing was written */
+#define MQ_DEV_KV_RANGE 16u      /* a sequence, slot, page, length or tree node outside the key/value cache or
+                                    the call's host bounds; what it concerns was skipped */
 
 /* quantization types (mq_concat_rows*) */
 #define MQ_TYPE_Q4_K 1
 #define MQ_TYPE_Q8_0 2
 #define MQ_TYPE_Q4_0 3  /* 32 weights in 18 bytes: f16 d, 16 bytes of nibbles (see mq_matvec_q4_0_q8_0) */
+#define MQ_TYPE_F16 4   /* plain binary16: key/value cache and attention output only */
 
 /* limits: K * ncols <= MQ_MAX_K_TIMES_NCOLS (the q8_0 activation is staged in
  * shared memory), K <= MQ_MAX_K, ncols <= MQ_MAX_NCOLS */
@@ -338,6 +341,140 @@ mq_status mq_mmq_q4K_q8_0(const mq_mv_desc* d_desc, int32_t rows, int32_t K, int
 mq_status mq_dequant_q4K_f16(const void* W, void* W16, int64_t rows, int64_t K, void* stream);
 mq_status mq_convert_f32_f16(const float* x, void* y, int64_t n, void* stream);
 mq_status mq_gemm_f16(const void* W16, const void* X16, float* Y, int32_t R, int32_t K, int32_t T, void* stream);
+
+/* ---- the key/value cache and the attention of a decode step ---------------------------
+ * What stands between the q|k|v projection and the o projection:
+ *   mq_kv_append   y_qkv -> per-head norms, rotation -> q (f16), K and V into the cache
+ *   mq_attn_tree   q against the cache -> f16, or q8_0 columns that the o
+ *                  projection reads as xq (mq_mv_desc)
+ *   mq_kv_accept   after a tree was verified: its accepted path becomes context
+ *   mq_kv_read     cached K and V back as f16
+ * A sequence's cache is ctx tokens of context in slots 0..ctx-1 and then the
+ * nodes of a tree of drafted tokens, node j in slot ctx + j; plain decoding is
+ * a tree of one node.  Lengths, page numbers, positions and masks live in
+ * device memory, so a captured graph follows them; the structs below are host
+ * structs that the call copies, and with the host bounds in them they are the
+ * capture key.  Device data is checked in the kernels: what lies outside the
+ * cache or the bounds is skipped and sets MQ_DEV_KV_RANGE.
+ *
+ * Layout of the cache: a pool of n_pages pages of MQ_KV_PAGE_TOKENS tokens;
+ * table[s][i] is the page of sequence s's slots 64i..64i+63.  A page is one
+ * block per key/value head, and a block
+ *   MQ_TYPE_F16   K as head_dim/64 planes of [64 tokens][64 f16], then V alike;
+ *                 the 16-byte chunk c (0..7) of token r's 128-byte row lies at
+ *                 chunk c ^ (r % 8)
+ *   MQ_TYPE_Q8_0  K codes [64 tokens][head_dim] bytes, V codes, the f16 scales
+ *                 of K [64][head_dim/32], those of V; a byte is code + 128; the
+ *                 16-byte chunk c of token r's row lies at c ^ (r % 8) for
+ *                 head_dim 128 and at c ^ (r/2 % 4) for head_dim 64
+ * A q8_0 element stands for f16(scale * code), rounded once: every call sees
+ * that value.  Codes and scales are those of mq_quantize_q8_0.  A page that two
+ * sequences share may be read by both; writes to it are the caller's to order.
+ * Only slots that were written are ever read.
+ *
+ * head_dim is 64 or 128; the pool is 128-byte aligned. */
+#define MQ_KV_PAGE_TOKENS 64
+#define MQ_TREE_MAX_TOKENS 64
+#define MQ_MAX_SEQS 4096
+#define MQ_MAX_KV_HEADS 256
+#define MQ_MAX_HEADS 1024 /* query heads */
+typedef struct mq_kv_cache {
+    void* pages;          /* device, n_pages * mq_kv_page_bytes(...) bytes, 128-byte aligned */
+    const int32_t* table; /* device [n_seqs][table_ld] page numbers */
+    int64_t n_pages;
+    int32_t n_seqs;
+    int32_t table_ld;     /* pages a sequence can have */
+    int32_t type;         /* MQ_TYPE_F16 or MQ_TYPE_Q8_0 */
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t reserved;     /* 0 */
+} mq_kv_cache;
+
+/* bytes of a page; 0 for a type or size the cache does not have */
+size_t mq_kv_page_bytes(int32_t type, int32_t n_kv_heads, int32_t head_dim);
+/* host-side validation of a cache struct (shapes, alignment, nulls) */
+mq_status mq_check_kv_cache(const mq_kv_cache* h_cache);
+
+/* Token n's row of qkv holds n_heads query heads, then n_kv_heads key heads,
+ * then n_kv_heads value heads of head_dim fp32.  For each query and key head:
+ * x = x * rsqrt(mean(x^2) + eps) * w where a norm weight is given, then the
+ * rotation of its first rot_dims values by the angles pos[n] * inv_freq[i]:
+ * pairs (i, i + rot_dims/2), or (2i, 2i+1) with MQ_ROPE_INTERLEAVED.  The
+ * angle is the exact product of the integer position and the fp32 frequency
+ * (reduced to a turn in 64-bit fixed point), so long positions lose nothing.
+ * q goes to q_out, K and V into slot[n] of sequence seq[n].  A negative slot
+ * writes q only (padding).  Two tokens of one call must not name the same slot.
+ * n_tokens == 0 launches nothing. */
+#define MQ_ROPE_INTERLEAVED 1u
+typedef struct mq_kv_append_args {
+    const float* qkv;      /* [n_tokens][qkv_ld], 8-byte aligned, qkv_ld even */
+    const float* q_norm;   /* [head_dim], 8-byte aligned, or NULL */
+    const float* k_norm;   /* [head_dim], 8-byte aligned, or NULL */
+    const float* inv_freq; /* [rot_dims/2]; not read when rot_dims == 0 */
+    const int32_t* pos;    /* [n_tokens]; not read when rot_dims == 0 */
+    const int32_t* seq;    /* [n_tokens] */
+    const int32_t* slot;   /* [n_tokens] */
+    void* q_out;           /* f16 [n_tokens][q_ld], 4-byte aligned, q_ld even */
+    int64_t qkv_ld;
+    int64_t q_ld;
+    int32_t n_tokens;
+    int32_t n_heads;
+    int32_t rot_dims;      /* even, 0..head_dim */
+    uint32_t flags;        /* MQ_ROPE_* */
+    float eps;
+    int32_t reserved;      /* 0 */
+} mq_kv_append_args;
+mq_status mq_kv_append(const mq_kv_cache* h_cache, const mq_kv_append_args* h_args, void* stream);
+
+/* k_out, v_out f16 [n][n_kv_heads][head_dim] (16-byte aligned): the cached
+ * values of slot[i] of sequence seq[i].  A pair outside the cache leaves its
+ * rows unwritten.  n == 0 launches nothing. */
+mq_status mq_kv_read(const mq_kv_cache* h_cache, const int32_t* seq, const int32_t* slot, int32_t n, void* k_out,
+                     void* v_out, void* stream);
+
+/* For every sequence s: slot ctx_len[s] + i takes what slot ctx_len[s] +
+ * path[s][i] held before the call, for i < n_path[s] (K, V and scales, moved
+ * as they are).  path: device [n_seqs][path_ld], node numbers 0..63 in any
+ * order; n_path 0..path_ld; path_ld <= MQ_TREE_MAX_TOKENS.  ctx_len is not
+ * changed.  A sequence with an entry outside the bounds keeps its slots. */
+mq_status mq_kv_accept(const mq_kv_cache* h_cache, const int32_t* ctx_len, const int32_t* path,
+                       const int32_t* n_path, int32_t path_ld, void* stream);
+
+/* Attention of every tree's nodes.  Sequence s owns the tokens
+ * tok_start[s]..tok_start[s+1]-1 (T of them, 0..max_tokens); its node i sees
+ * the context slots 0..ctx_len[s]-1 and the nodes j (slot ctx_len[s] + j) whose
+ * bit j of mask[token] is set; without a mask, the nodes j <= i.  Per query
+ * head h, with key/value head h / (n_heads/n_kv_heads):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j     over the keys it sees
+ * in fp32 sums and statistics; a node that sees no key gives zeros, and what
+ * it does not see never reaches it, NaN and infinities included.
+ * out_type MQ_TYPE_F16: out f16 [n_tokens][out_ld]; MQ_TYPE_Q8_0: dense q8_0
+ * columns [n_tokens][n_heads*head_dim/32 blocks] (out_ld not read), the xq of
+ * an o projection.  Tokens outside every sequence are not written.
+ * max_len bounds ctx_len[s] + T, max_tokens bounds T (host values; they size
+ * the launch and pick its kernel).
+ * workspace: mq_attn_workspace_bytes bytes, 128-byte aligned, zeroed once by
+ * the caller; every call leaves it ready for the next.  Two calls that overlap
+ * on the GPU must not share one. */
+typedef struct mq_attn_args {
+    const void* q;            /* f16 [n_tokens][q_ld], 16-byte aligned, q_ld % 8 == 0 */
+    void* out;                /* 16-byte aligned (q8_0: 2-byte) */
+    const int32_t* tok_start; /* [n_seqs + 1] */
+    const int32_t* ctx_len;   /* [n_seqs] */
+    const uint64_t* mask;     /* [n_tokens], 8-byte aligned, or NULL */
+    int64_t q_ld;
+    int64_t out_ld;           /* f16 values per token, % 8 == 0 */
+    int32_t n_tokens;
+    int32_t n_heads;          /* a multiple of n_kv_heads */
+    int32_t max_len;
+    int32_t max_tokens;       /* 1..MQ_TREE_MAX_TOKENS */
+    int32_t out_type;
+    float scale;
+} mq_attn_args;
+/* needs mq_init for the current device (the size goes by its SMs) */
+mq_status mq_attn_workspace_bytes(const mq_kv_cache* h_cache, int32_t n_heads, int32_t max_tokens, size_t* bytes);
+mq_status mq_attn_tree(const mq_kv_cache* h_cache, const mq_attn_args* h_args, void* workspace, size_t ws_bytes,
+                       void* stream);
 
 /* ---- the FFN without caller scratch --------------------------------------------------
  * No counterpart in the pages: they describe the FFN kernels, not how a

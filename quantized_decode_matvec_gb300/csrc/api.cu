@@ -836,6 +836,126 @@ mq_status mq_mmq_q4K_q8_0(const mq_mv_desc* d_desc, int32_t rows, int32_t K, int
     return e == cudaSuccess ? MQ_OK : cuda_fail(e);
 }
 
+// ---- key/value cache and attention ----------------------------------------------------------
+
+size_t mq_kv_page_bytes(int32_t type, int32_t n_kv_heads, int32_t head_dim)
+{
+    if ((head_dim != 64 && head_dim != 128) || n_kv_heads < 1 || n_kv_heads > MQ_MAX_KV_HEADS) return 0;
+    if (type != MQ_TYPE_F16 && type != MQ_TYPE_Q8_0) return 0;
+    const size_t values = size_t(2) * MQ_KV_PAGE_TOKENS * head_dim;  // of one head's block
+    return n_kv_heads * (type == MQ_TYPE_F16 ? 2 * values : values + values / 16);
+}
+
+mq_status mq_check_kv_cache(const mq_kv_cache* c)
+{
+    if (!c || c->reserved != 0) return MQ_ERR_INVALID_ARG;
+    if (c->type != MQ_TYPE_F16 && c->type != MQ_TYPE_Q8_0) return MQ_ERR_INVALID_ARG;
+    if (c->n_pages < 0 || c->n_pages > INT32_MAX || c->n_seqs < 0 || c->table_ld < 0 || c->n_kv_heads < 1)
+        return MQ_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128) return MQ_ERR_SHAPE;
+    if (c->n_seqs > MQ_MAX_SEQS || c->n_kv_heads > MQ_MAX_KV_HEADS || c->table_ld > INT32_MAX / MQ_KV_PAGE_TOKENS)
+        return MQ_ERR_UNSUPPORTED;
+    if (!c->pages || !c->table) return MQ_ERR_INVALID_ARG;
+    if (!aligned(c->pages, 128) || !aligned(c->table, 4)) return MQ_ERR_ALIGN;
+    return MQ_OK;
+}
+
+mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_append_args* a, void* stream)
+{
+    mq_status st = mq_check_kv_cache(cache);
+    if (st != MQ_OK) return st;
+    if (!a || a->reserved != 0 || (a->flags & ~MQ_ROPE_INTERLEAVED)) return MQ_ERR_INVALID_ARG;
+    const int D = cache->head_dim;
+    if (a->n_tokens < 0 || a->n_heads < 0 || a->rot_dims < 0 || a->rot_dims > D || a->rot_dims % 2) return MQ_ERR_SHAPE;
+    if (a->n_heads > MQ_MAX_HEADS) return MQ_ERR_UNSUPPORTED;
+    if (a->qkv_ld < int64_t(a->n_heads + 2 * cache->n_kv_heads) * D || a->qkv_ld % 2) return MQ_ERR_SHAPE;
+    if (a->n_heads > 0 && (a->q_ld < int64_t(a->n_heads) * D || a->q_ld % 2)) return MQ_ERR_SHAPE;
+    if (!(a->eps >= 0.0f)) return MQ_ERR_INVALID_ARG;
+    if (a->n_tokens == 0) return MQ_OK;
+    if (!a->qkv || !a->seq || !a->slot || (a->n_heads > 0 && !a->q_out)) return MQ_ERR_INVALID_ARG;
+    if (a->rot_dims > 0 && (!a->inv_freq || !a->pos)) return MQ_ERR_INVALID_ARG;
+    if (!aligned(a->qkv, 8) || !aligned(a->q_norm, 8) || !aligned(a->k_norm, 8) || !aligned(a->inv_freq, 4) ||
+        !aligned(a->pos, 4) || !aligned(a->seq, 4) || !aligned(a->slot, 4) || !aligned(a->q_out, 4))
+        return MQ_ERR_ALIGN;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    cudaError_t e = mq::launch_kv_append(*cache, *a, dev->num_sms, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+mq_status mq_kv_read(const mq_kv_cache* cache, const int32_t* seq, const int32_t* slot, int32_t n, void* k_out,
+                     void* v_out, void* stream)
+{
+    mq_status st = mq_check_kv_cache(cache);
+    if (st != MQ_OK) return st;
+    if (n < 0) return MQ_ERR_SHAPE;
+    if (n == 0) return MQ_OK;
+    if (!seq || !slot || !k_out || !v_out) return MQ_ERR_INVALID_ARG;
+    if (!aligned(seq, 4) || !aligned(slot, 4) || !aligned(k_out, 16) || !aligned(v_out, 16)) return MQ_ERR_ALIGN;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    cudaError_t e = mq::launch_kv_read(*cache, seq, slot, n, k_out, v_out, dev->num_sms, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+mq_status mq_kv_accept(const mq_kv_cache* cache, const int32_t* ctx_len, const int32_t* path, const int32_t* n_path,
+                       int32_t path_ld, void* stream)
+{
+    mq_status st = mq_check_kv_cache(cache);
+    if (st != MQ_OK) return st;
+    if (path_ld < 0 || path_ld > MQ_TREE_MAX_TOKENS) return MQ_ERR_SHAPE;
+    if (path_ld == 0 || cache->n_seqs == 0) return MQ_OK;
+    if (!ctx_len || !path || !n_path) return MQ_ERR_INVALID_ARG;
+    if (!aligned(ctx_len, 4) || !aligned(path, 4) || !aligned(n_path, 4)) return MQ_ERR_ALIGN;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    cudaError_t e = mq::launch_kv_accept(*cache, ctx_len, path, n_path, path_ld, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+static mq_status check_attn_shape(const mq_kv_cache* cache, int32_t n_heads, int32_t max_tokens)
+{
+    if (n_heads < 1 || n_heads % cache->n_kv_heads || max_tokens < 1 || max_tokens > MQ_TREE_MAX_TOKENS)
+        return MQ_ERR_SHAPE;
+    return n_heads > MQ_MAX_HEADS ? MQ_ERR_UNSUPPORTED : MQ_OK;
+}
+
+mq_status mq_attn_workspace_bytes(const mq_kv_cache* cache, int32_t n_heads, int32_t max_tokens, size_t* bytes)
+{
+    mq_status st = mq_check_kv_cache(cache);
+    if (st != MQ_OK) return st;
+    if (!bytes) return MQ_ERR_INVALID_ARG;
+    if ((st = check_attn_shape(cache, n_heads, max_tokens)) != MQ_OK) return st;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    *bytes = mq::attn_workspace_bytes(*cache, n_heads, max_tokens, dev->num_sms);
+    return MQ_OK;
+}
+
+mq_status mq_attn_tree(const mq_kv_cache* cache, const mq_attn_args* a, void* workspace, size_t ws_bytes, void* stream)
+{
+    mq_status st = mq_check_kv_cache(cache);
+    if (st != MQ_OK) return st;
+    if (!a) return MQ_ERR_INVALID_ARG;
+    if ((st = check_attn_shape(cache, a->n_heads, a->max_tokens)) != MQ_OK) return st;
+    if (a->n_tokens < 0 || a->max_len < 0) return MQ_ERR_SHAPE;
+    if (a->out_type != MQ_TYPE_F16 && a->out_type != MQ_TYPE_Q8_0) return MQ_ERR_INVALID_ARG;
+    const int64_t width = int64_t(a->n_heads) * cache->head_dim;
+    if (a->q_ld < width || a->q_ld % 8) return MQ_ERR_SHAPE;
+    if (a->out_type == MQ_TYPE_F16 && (a->out_ld < width || a->out_ld % 8)) return MQ_ERR_SHAPE;
+    if (!(a->scale - a->scale == 0.0f)) return MQ_ERR_INVALID_ARG;  // not finite
+    if (a->n_tokens == 0 || cache->n_seqs == 0) return MQ_OK;
+    if (!a->q || !a->out || !a->tok_start || !a->ctx_len || !workspace) return MQ_ERR_INVALID_ARG;
+    if (!aligned(a->q, 16) || !aligned(a->out, a->out_type == MQ_TYPE_F16 ? 16 : 2) || !aligned(a->tok_start, 4) ||
+        !aligned(a->ctx_len, 4) || !aligned(a->mask, 8) || !aligned(workspace, 128))
+        return MQ_ERR_ALIGN;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    if (ws_bytes < mq::attn_workspace_bytes(*cache, a->n_heads, a->max_tokens, dev->num_sms)) return MQ_ERR_INVALID_ARG;
+    cudaError_t e = mq::launch_attn(*cache, *a, workspace, dev->num_sms, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
 mq_status mq_dequant_q4K_f16(const void* W, void* W16, int64_t rows, int64_t K, void* stream)
 {
     if (rows < 0 || K <= 0 || K % 256) return MQ_ERR_SHAPE;

@@ -164,6 +164,16 @@ cudaError_t launch_dequant_q4K_f16(const void* W, void* W16, int64_t nblocks, in
 cudaError_t launch_f32_to_f16(const float* x, void* y, int64_t n, int num_sms, cudaStream_t s);
 cudaError_t launch_gemm_f16(const void* W16, const void* X16, float* Y, int R, int K, int T, int num_sms,
                             unsigned* status, cudaStream_t s);
+// key/value cache (kv.cu) and the attention over it (attn.cu)
+cudaError_t launch_kv_append(const mq_kv_cache& cache, const mq_kv_append_args& a, int num_sms, unsigned* status,
+                             cudaStream_t s);
+cudaError_t launch_kv_read(const mq_kv_cache& cache, const int32_t* seq, const int32_t* slot, int n, void* k_out,
+                           void* v_out, int num_sms, unsigned* status, cudaStream_t s);
+cudaError_t launch_kv_accept(const mq_kv_cache& cache, const int32_t* ctx_len, const int32_t* path,
+                             const int32_t* n_path, int path_ld, unsigned* status, cudaStream_t s);
+size_t attn_workspace_bytes(const mq_kv_cache& cache, int n_heads, int max_tokens, int num_sms);
+cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* ws, int num_sms, unsigned* status,
+                        cudaStream_t s);
 // looks up the device address of the no-alloc FFN's fixed scratch on device
 // `dev` (current) and caches it
 cudaError_t noalloc_setup(int dev);

@@ -41,6 +41,7 @@ MQ_DEV_DESC_MISMATCH = 1
 MQ_DEV_DESC_ALIGN = 2
 MQ_DEV_TIMEOUT = 4
 MQ_DEV_ALIAS = 8
+MQ_DEV_KV_RANGE = 16
 MQ_VARIANT_AUTO = 0
 MQ_VARIANT_FORCE_REGISTER = 1
 MQ_FAULT_NONE = 0
@@ -50,6 +51,7 @@ MQ_FAULT_WITHHOLD_COUNT = 3
 MQ_TYPE_Q4_K = 1
 MQ_TYPE_Q8_0 = 2
 MQ_TYPE_Q4_0 = 3
+MQ_TYPE_F16 = 4
 MQ_MAX_NCOLS = 8
 MQ_MAX_K = 131072
 MQ_MAX_K_TIMES_NCOLS = 163840
@@ -59,6 +61,9 @@ MQ_STEP_CHAINED = 4
 MQ_STEP_WORKSPACE_BYTES = 4352
 MQ_NOALLOC_HQ8_MAX_BYTES = 131072
 MQ_MMQ_MAX_NCOLS = 64
+MQ_KV_PAGE_TOKENS = 64
+MQ_TREE_MAX_TOKENS = 64
+MQ_ROPE_INTERLEAVED = 1
 MQ_PLAN_MATVEC = 0
 MQ_PLAN_DOWN = 1
 MQ_PLAN_GATE_UP = 2
@@ -84,6 +89,24 @@ class LayerDesc(ctypes.Structure):
 class StepShape(ctypes.Structure):
     _fields_ = [("n_layers", c_i32), ("H", c_i32), ("I", c_i32), ("qkv_rows", c_i32), ("o_rows", c_i32),
                 ("o_K", c_i32), ("ncols", c_i32), ("flags", c_u32), ("workspace", c_vp)]
+
+
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = [("pages", c_vp), ("table", c_vp), ("n_pages", c_i64), ("n_seqs", c_i32), ("table_ld", c_i32),
+                ("type", c_i32), ("n_kv_heads", c_i32), ("head_dim", c_i32), ("reserved", c_i32)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [("qkv", c_vp), ("q_norm", c_vp), ("k_norm", c_vp), ("inv_freq", c_vp), ("pos", c_vp), ("seq", c_vp),
+                ("slot", c_vp), ("q_out", c_vp), ("qkv_ld", c_i64), ("q_ld", c_i64), ("n_tokens", c_i32),
+                ("n_heads", c_i32), ("rot_dims", c_i32), ("flags", c_u32), ("eps", ctypes.c_float),
+                ("reserved", c_i32)]
+
+
+class AttnArgs(ctypes.Structure):
+    _fields_ = [("q", c_vp), ("out", c_vp), ("tok_start", c_vp), ("ctx_len", c_vp), ("mask", c_vp), ("q_ld", c_i64),
+                ("out_ld", c_i64), ("n_tokens", c_i32), ("n_heads", c_i32), ("max_len", c_i32),
+                ("max_tokens", c_i32), ("out_type", c_i32), ("scale", ctypes.c_float)]
 
 
 def _sig(name, res, *args):
@@ -121,6 +144,13 @@ _sig("mq_mmq_q4K_q8_0", c_i32, c_vp, c_i32, c_i32, c_i32, c_vp, ctypes.c_size_t,
 _sig("mq_dequant_q4K_f16", c_i32, c_vp, c_vp, c_i64, c_i64, c_vp)
 _sig("mq_convert_f32_f16", c_i32, c_vp, c_vp, c_i64, c_vp)
 _sig("mq_gemm_f16", c_i32, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp)
+_sig("mq_kv_page_bytes", ctypes.c_size_t, c_i32, c_i32, c_i32)
+_sig("mq_check_kv_cache", c_i32, ctypes.POINTER(KvCacheStruct))
+_sig("mq_kv_append", c_i32, ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvAppendArgs), c_vp)
+_sig("mq_kv_read", c_i32, ctypes.POINTER(KvCacheStruct), c_vp, c_vp, c_i32, c_vp, c_vp, c_vp)
+_sig("mq_kv_accept", c_i32, ctypes.POINTER(KvCacheStruct), c_vp, c_vp, c_vp, c_i32, c_vp)
+_sig("mq_attn_workspace_bytes", c_i32, ctypes.POINTER(KvCacheStruct), c_i32, c_i32, ctypes.POINTER(ctypes.c_size_t))
+_sig("mq_attn_tree", c_i32, ctypes.POINTER(KvCacheStruct), ctypes.POINTER(AttnArgs), c_vp, ctypes.c_size_t, c_vp)
 _sig("mq_debug_block_sums_q4K_q8_0", c_i32, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp)
 _sig("mq_debug_set_variant", c_i32, c_i32)
 _sig("mq_debug_set_fault", c_i32, c_i32)
@@ -134,6 +164,8 @@ EXPORTS = ["mq_status_string", "mq_abi_version", "mq_last_cuda_error", "mq_init"
            "mq_matvec_q4K_q8_0", "mq_matvec_q4_0_q8_0", "mq_matvec_q8_0_q8_0", "mq_check_ffn_desc", "mq_ffn_gu_silu_down", "mq_ffn_gate_up", "mq_step", "mq_step_workspace_bytes",
            "mq_ffn_gu_silu_down_noalloc", "mq_dequant_q4K_f16", "mq_convert_f32_f16", "mq_gemm_f16",
            "mq_mmq_workspace_bytes", "mq_mmq_q4K_q8_0",
+           "mq_kv_page_bytes", "mq_check_kv_cache", "mq_kv_append", "mq_kv_read", "mq_kv_accept",
+           "mq_attn_workspace_bytes", "mq_attn_tree",
            "mq_debug_block_sums_q4K_q8_0", "mq_debug_set_variant", "mq_debug_set_fault", "mq_debug_plan_mv",
            "mq_debug_plan_step"]
 
@@ -276,6 +308,36 @@ def mq_convert_f32_f16(x: int, y: int, n: int, stream: int = 0) -> int:
 
 def mq_gemm_f16(W16: int, X16: int, Y: int, R: int, K: int, T: int, stream: int = 0) -> int:
     return _lib.mq_gemm_f16(c_vp(W16), c_vp(X16), c_vp(Y), R, K, T, c_vp(stream))
+
+
+def mq_kv_page_bytes(ttype: int, n_kv_heads: int, head_dim: int) -> int:
+    return _lib.mq_kv_page_bytes(ttype, n_kv_heads, head_dim)
+
+
+def mq_check_kv_cache(cache: KvCacheStruct) -> int:
+    return _lib.mq_check_kv_cache(cache)
+
+
+def mq_kv_append(cache: KvCacheStruct, args: KvAppendArgs, stream: int = 0) -> int:
+    return _lib.mq_kv_append(cache, args, stream)
+
+
+def mq_kv_read(cache: KvCacheStruct, seq: int, slot: int, n: int, k_out: int, v_out: int, stream: int = 0) -> int:
+    return _lib.mq_kv_read(cache, seq, slot, n, k_out, v_out, stream)
+
+
+def mq_kv_accept(cache: KvCacheStruct, ctx_len: int, path: int, n_path: int, path_ld: int, stream: int = 0) -> int:
+    return _lib.mq_kv_accept(cache, ctx_len, path, n_path, path_ld, stream)
+
+
+def mq_attn_workspace_bytes(cache: KvCacheStruct, n_heads: int, max_tokens: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.mq_attn_workspace_bytes(cache, n_heads, max_tokens, ctypes.byref(n)), "mq_attn_workspace_bytes")
+    return int(n.value)
+
+
+def mq_attn_tree(cache: KvCacheStruct, args: AttnArgs, workspace: int, ws_bytes: int, stream: int = 0) -> int:
+    return _lib.mq_attn_tree(cache, args, workspace, ws_bytes, stream)
 
 
 def mq_debug_block_sums_q4K_q8_0(d_desc: int, rows: int, K: int, ncols: int, sumi: int, sumq: int,
@@ -531,6 +593,169 @@ def gemm_f16(W16, X16, out=None, stream=None):
     if out is None:
         out = torch.empty((T, R), dtype=torch.float32, device=W16.device)
     _check(mq_gemm_f16(_ptr(W16), _ptr(X16), _ptr(out), R, K, T, _stream(stream)), "mq_gemm_f16")
+    return out
+
+
+KV_TYPES = {"f16": MQ_TYPE_F16, "q8_0": MQ_TYPE_Q8_0}
+
+
+def _want(t, name: str, dtype, shape=None, device=None):
+    """Refuse a tensor that the raw call would misread (the C ABI sees addresses only)."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor is wanted, got {t.dtype} with strides {t.stride()}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {shape} is wanted, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, dtype, device, width: Optional[int] = None):
+    """Address and row stride of a 2-D tensor whose rows are dense (the row stride is free)."""
+    if t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or t.device != device:
+        raise ValueError(f"{name}: a 2-D {dtype} tensor with dense rows on {device} is wanted, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    if width is not None and t.shape[1] != width:
+        raise ValueError(f"{name}: rows of {width} are wanted, got {t.shape[1]}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor for the call's result, allocated on the stream that will write it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    on = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(on):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+class KVCache:
+    """A paged key/value cache (mq_kv_cache): the page pool and the page table.
+
+    ``pages``: uint8 cuda tensor of n_pages * mq_kv_page_bytes bytes; ``table``: int32
+    [n_seqs, pages per sequence].  ``type`` is "f16" or "q8_0".  The tensors are the
+    caller's; the handle keeps references to them.
+    """
+
+    def __init__(self, pages, table, type: str, n_kv_heads: int, head_dim: int):
+        torch = _torch()
+        self.type_name, self.n_kv_heads, self.head_dim = type, n_kv_heads, head_dim
+        self.pages, self.table, self.device = pages, table, pages.device
+        if type not in KV_TYPES:
+            raise ValueError(f"cache type {type!r}: one of {sorted(KV_TYPES)}")
+        page = mq_kv_page_bytes(KV_TYPES[type], n_kv_heads, head_dim)
+        if not page:
+            raise MQError(MQ_ERR_SHAPE, "mq_kv_page_bytes")
+        if table.dim() != 2:
+            raise ValueError("table: a 2-D tensor is wanted")
+        if pages.numel() % page:
+            raise ValueError(f"pages: {pages.numel()} bytes are no whole number of {page}-byte pages")
+        self.n_seqs = table.shape[0]
+        self.struct = KvCacheStruct(_want(pages, "pages", torch.uint8), _want(table, "table", torch.int32, device=pages.device),
+                                    pages.numel() // page, table.shape[0], table.shape[1], KV_TYPES[type], n_kv_heads,
+                                    head_dim, 0)
+        _check(mq_check_kv_cache(self.struct), "mq_check_kv_cache")
+
+    @classmethod
+    def alloc(cls, n_pages: int, table, type: str, n_kv_heads: int, head_dim: int) -> "KVCache":
+        """A cache with a new (unwritten) pool of n_pages pages."""
+        torch = _torch()
+        page = mq_kv_page_bytes(KV_TYPES.get(type, 0), n_kv_heads, head_dim)
+        if not page:
+            raise MQError(MQ_ERR_SHAPE, "mq_kv_page_bytes")
+        return cls(torch.empty(n_pages * page, dtype=torch.uint8, device=table.device), table, type, n_kv_heads, head_dim)
+
+
+def kv_append(cache: KVCache, qkv, pos, seq, slot, n_heads: int, inv_freq=None, interleaved: bool = False,
+              q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None, stream=None):
+    """Norms and rotation of y_qkv [n, (n_heads + 2 n_kv_heads) * head_dim] (fp32, rows may be strided), K and V into
+    the cache.  Returns q, f16 [n, n_heads * head_dim].  rot_dims is twice inv_freq's length (None: no rotation)."""
+    torch = _torch()
+    dev, D = cache.device, cache.head_dim
+    x, ld = _rows(qkv, "qkv", torch.float32, dev, (n_heads + 2 * cache.n_kv_heads) * D)
+    n = qkv.shape[0]
+    if q_out is None:
+        q_out = _new((n, n_heads * D), torch.float16, dev, stream)
+    q, q_ld = _rows(q_out, "q_out", torch.float16, dev, n_heads * D)
+    if q_out.shape[0] != n:
+        raise ValueError(f"q_out: {n} rows are wanted, got {q_out.shape[0]}")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    a = KvAppendArgs(x, None if q_norm is None else _want(q_norm, "q_norm", torch.float32, (D,), dev),
+                     None if k_norm is None else _want(k_norm, "k_norm", torch.float32, (D,), dev),
+                     None if not rot else _want(inv_freq, "inv_freq", torch.float32, None, dev),
+                     None if not rot else _want(pos, "pos", torch.int32, (n,), dev),
+                     _want(seq, "seq", torch.int32, (n,), dev), _want(slot, "slot", torch.int32, (n,), dev), q, ld, q_ld,
+                     n, n_heads, rot, MQ_ROPE_INTERLEAVED if interleaved else 0, eps, 0)
+    _check(mq_kv_append(cache.struct, a, _stream(stream)), "mq_kv_append")
+    return q_out
+
+
+def kv_read(cache: KVCache, seq, slot, k_out=None, v_out=None, stream=None):
+    """Cached keys and values of (sequence, slot) pairs: two f16 tensors [n, n_kv_heads, head_dim]."""
+    torch = _torch()
+    n, dev = seq.numel(), cache.device
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    k_out = _new(shape, torch.float16, dev, stream) if k_out is None else k_out
+    v_out = _new(shape, torch.float16, dev, stream) if v_out is None else v_out
+    _check(mq_kv_read(cache.struct, _want(seq, "seq", torch.int32, (n,), dev), _want(slot, "slot", torch.int32, (n,), dev),
+                      n, _want(k_out, "k_out", torch.float16, shape, dev), _want(v_out, "v_out", torch.float16, shape, dev),
+                      _stream(stream)), "mq_kv_read")
+    return k_out, v_out
+
+
+def kv_accept(cache: KVCache, ctx_len, path, n_path, stream=None) -> None:
+    """Move each sequence's accepted nodes path[s, :n_path[s]] to the slots from ctx_len[s] on."""
+    torch = _torch()
+    dev, S = cache.device, cache.n_seqs
+    if path.dim() != 2 or path.shape[0] != S:
+        raise ValueError(f"path: [{S}, path_ld] is wanted, got {tuple(path.shape)}")
+    _check(mq_kv_accept(cache.struct, _want(ctx_len, "ctx_len", torch.int32, (S,), dev),
+                        _want(path, "path", torch.int32, None, dev), _want(n_path, "n_path", torch.int32, (S,), dev),
+                        path.shape[1], _stream(stream)), "mq_kv_accept")
+
+
+def attn_workspace(cache: KVCache, n_heads: int, max_tokens: int = MQ_TREE_MAX_TOKENS):
+    """A zeroed workspace for attn_tree (one per stream that runs it)."""
+    torch = _torch()
+    return torch.zeros(mq_attn_workspace_bytes(cache.struct, n_heads, max_tokens), dtype=torch.uint8, device=cache.device)
+
+
+def attn_tree(cache: KVCache, q, tok_start, ctx_len, mask=None, scale: Optional[float] = None,
+              max_len: Optional[int] = None, max_tokens: int = MQ_TREE_MAX_TOKENS, out_type: str = "f16", out=None,
+              workspace=None, stream=None):
+    """Attention of every tree's nodes (q: f16 [n, n_heads * head_dim], rows may be strided) over the cache.
+
+    ``mask``: int64 [n], bit j = node j of the token's tree is seen (None: a chain).  ``max_len`` bounds context plus
+    tree of any sequence (default: what the table can hold).  Returns f16 [n, n_heads * head_dim], or with
+    ``out_type="q8_0"`` uint8 [n, n_heads * head_dim / 32 * 34], the ``xq`` of a projection."""
+    torch = _torch()
+    dev, D, S = cache.device, cache.head_dim, cache.n_seqs
+    n, width = q.shape
+    qp, q_ld = _rows(q, "q", torch.float16, dev)
+    if width % D:
+        raise ValueError(f"q: rows of whole heads of {D} are wanted, got {width}")
+    if out_type == "f16":
+        out = _new((n, width), torch.float16, dev, stream) if out is None else out
+        op, out_ld = _rows(out, "out", torch.float16, dev, width)
+    elif out_type == "q8_0":
+        out = _new((n, width // 32 * 34), torch.uint8, dev, stream) if out is None else out
+        op, out_ld = _want(out, "out", torch.uint8, (n, width // 32 * 34), dev), 0
+    else:
+        raise ValueError(f"out_type {out_type!r}: \"f16\" or \"q8_0\"")
+    if out.shape[0] != n:
+        raise ValueError(f"out: {n} rows are wanted, got {out.shape[0]}")
+    if workspace is None:
+        on = None if stream is None else torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+        with torch.cuda.stream(on):
+            workspace = attn_workspace(cache, width // D, max_tokens)
+    if max_len is None:
+        max_len = cache.table.shape[1] * MQ_KV_PAGE_TOKENS
+    a = AttnArgs(qp, op, _want(tok_start, "tok_start", torch.int32, (S + 1,), dev),
+                 _want(ctx_len, "ctx_len", torch.int32, (S,), dev),
+                 None if mask is None else _want(mask, "mask", torch.int64, (n,), dev), q_ld, out_ld, n, width // D,
+                 max_len, max_tokens, KV_TYPES[out_type], D ** -0.5 if scale is None else scale)
+    _check(mq_attn_tree(cache.struct, a, workspace.data_ptr(), workspace.numel(), _stream(stream)), "mq_attn_tree")
     return out
 
 
