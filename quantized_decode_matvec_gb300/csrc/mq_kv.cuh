@@ -64,6 +64,18 @@ __device__ __forceinline__ uint32_t kv_pair(uint32_t u, __half2 scale)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// one element of a block as fp32 (rare paths)
+template <int D, bool Q8>
+__device__ __forceinline__ float kv_value(const uint8_t* blk, int r, int d, int is_v)
+{
+    using B = KvBlock<D, Q8>;
+    const uint8_t* const rows = blk + (is_v ? B::kVOff : 0);
+    if (!Q8) return __half2float(*reinterpret_cast<const __half*>(rows + B::chunk(r, d >> 3) + (d & 7) * 2));
+    const __half sc =
+        *reinterpret_cast<const __half*>(blk + B::kScK + is_v * B::kScBytes + (r * (D / 32) + (d >> 5)) * 2);
+    return __half2float(__hmul(__int2half_rn(int(rows[B::chunk(r, d >> 4) + (d & 15)]) - 128), sc));
+}
+
 // first byte of the page that holds slot `slot` of sequence `seq`, as an
 // offset into pages; -1 where the sequence, the slot or its page lies outside
 // the cache (table entries are device data and are not trusted).

@@ -399,9 +399,15 @@ def _check(st: int, where: str):
 
 # ---- tensor-level marshalling (torch owns memory and streams) ------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> int:
@@ -600,24 +606,28 @@ KV_TYPES = {"f16": MQ_TYPE_F16, "q8_0": MQ_TYPE_Q8_0}
 
 
 def _want(t, name: str, dtype, shape=None, device=None):
-    """Refuse a tensor that the raw call would misread (the C ABI sees addresses only)."""
-    if t.dtype != dtype or not t.is_contiguous():
+    """Address of a tensor; refuses one that the raw call would misread (the C ABI sees addresses only)."""
+    if t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor is wanted, got {t.dtype} with strides {t.stride()}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {shape} is wanted, got {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
     return t.data_ptr()
 
 
-def _rows(t, name: str, dtype, device, width: Optional[int] = None):
-    """Address and row stride of a 2-D tensor whose rows are dense (the row stride is free)."""
-    if t.dtype != dtype or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or t.device != device:
-        raise ValueError(f"{name}: a 2-D {dtype} tensor with dense rows on {device} is wanted, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    if width is not None and t.shape[1] != width:
-        raise ValueError(f"{name}: rows of {width} are wanted, got {t.shape[1]}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t, name: str, dtype, device, width: int, n: Optional[int] = None):
+    """Address and row stride of a 2-D tensor with dense rows of ``width`` (the row stride is free)."""
+    if t.dtype is not dtype or t.dim() != 2 or t.device != device:
+        raise ValueError(f"{name}: a 2-D {dtype} tensor on {device} is wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    rows, cols = t.shape
+    if cols != width or (n is not None and rows != n):
+        raise ValueError(f"{name}: rows of {width}{'' if n is None else f', {n} of them,'} are wanted, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name}: dense rows are wanted, got strides {t.stride()}")
+    return t.data_ptr(), t.stride(0)
 
 
 def _new(shape, dtype, device, stream):
@@ -628,6 +638,13 @@ def _new(shape, dtype, device, stream):
     on = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.stream(on):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _stream_on(stream, device) -> int:
+    """The stream handle of a call on ``device`` (None: torch's current stream there)."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 class KVCache:
@@ -670,55 +687,65 @@ class KVCache:
 def kv_append(cache: KVCache, qkv, pos, seq, slot, n_heads: int, inv_freq=None, interleaved: bool = False,
               q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None, stream=None):
     """Norms and rotation of y_qkv [n, (n_heads + 2 n_kv_heads) * head_dim] (fp32, rows may be strided), K and V into
-    the cache.  Returns q, f16 [n, n_heads * head_dim].  rot_dims is twice inv_freq's length (None: no rotation)."""
+    the cache.  Returns q, f16 [n, n_heads * head_dim].  rot_dims is twice inv_freq's length (None: no rotation, and
+    pos is not read)."""
     torch = _torch()
-    dev, D = cache.device, cache.head_dim
-    x, ld = _rows(qkv, "qkv", torch.float32, dev, (n_heads + 2 * cache.n_kv_heads) * D)
+    dev, D, i32, f32 = cache.device, cache.head_dim, torch.int32, torch.float32
+    width = n_heads * D
+    x, ld = _rows(qkv, "qkv", f32, dev, width + 2 * cache.n_kv_heads * D)
     n = qkv.shape[0]
     if q_out is None:
-        q_out = _new((n, n_heads * D), torch.float16, dev, stream)
-    q, q_ld = _rows(q_out, "q_out", torch.float16, dev, n_heads * D)
-    if q_out.shape[0] != n:
-        raise ValueError(f"q_out: {n} rows are wanted, got {q_out.shape[0]}")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    a = KvAppendArgs(x, None if q_norm is None else _want(q_norm, "q_norm", torch.float32, (D,), dev),
-                     None if k_norm is None else _want(k_norm, "k_norm", torch.float32, (D,), dev),
-                     None if not rot else _want(inv_freq, "inv_freq", torch.float32, None, dev),
-                     None if not rot else _want(pos, "pos", torch.int32, (n,), dev),
-                     _want(seq, "seq", torch.int32, (n,), dev), _want(slot, "slot", torch.int32, (n,), dev), q, ld, q_ld,
+        q_out = _new((n, width), torch.float16, dev, stream)
+        q, q_ld = q_out.data_ptr(), width
+    else:
+        q, q_ld = _rows(q_out, "q_out", torch.float16, dev, width, n)
+    rot, f, at = 0, None, None
+    if inv_freq is not None and inv_freq.numel():
+        rot, f = 2 * inv_freq.numel(), _want(inv_freq, "inv_freq", f32, None, dev)
+        at = _want(pos, "pos", i32, (n,), dev)
+    a = KvAppendArgs(x, None if q_norm is None else _want(q_norm, "q_norm", f32, (D,), dev),
+                     None if k_norm is None else _want(k_norm, "k_norm", f32, (D,), dev), f, at,
+                     _want(seq, "seq", i32, (n,), dev), _want(slot, "slot", i32, (n,), dev), q, ld, q_ld,
                      n, n_heads, rot, MQ_ROPE_INTERLEAVED if interleaved else 0, eps, 0)
-    _check(mq_kv_append(cache.struct, a, _stream(stream)), "mq_kv_append")
+    st = _lib.mq_kv_append(cache.struct, a, _stream_on(stream, dev))
+    if st:
+        raise MQError(st, "mq_kv_append")
     return q_out
 
 
 def kv_read(cache: KVCache, seq, slot, k_out=None, v_out=None, stream=None):
     """Cached keys and values of (sequence, slot) pairs: two f16 tensors [n, n_kv_heads, head_dim]."""
     torch = _torch()
-    n, dev = seq.numel(), cache.device
+    n, dev, i32 = seq.numel(), cache.device, torch.int32
     shape = (n, cache.n_kv_heads, cache.head_dim)
     k_out = _new(shape, torch.float16, dev, stream) if k_out is None else k_out
     v_out = _new(shape, torch.float16, dev, stream) if v_out is None else v_out
-    _check(mq_kv_read(cache.struct, _want(seq, "seq", torch.int32, (n,), dev), _want(slot, "slot", torch.int32, (n,), dev),
-                      n, _want(k_out, "k_out", torch.float16, shape, dev), _want(v_out, "v_out", torch.float16, shape, dev),
-                      _stream(stream)), "mq_kv_read")
+    st = _lib.mq_kv_read(cache.struct, _want(seq, "seq", i32, (n,), dev), _want(slot, "slot", i32, (n,), dev), n,
+                         _want(k_out, "k_out", torch.float16, shape, dev),
+                         _want(v_out, "v_out", torch.float16, shape, dev), _stream_on(stream, dev))
+    if st:
+        raise MQError(st, "mq_kv_read")
     return k_out, v_out
 
 
 def kv_accept(cache: KVCache, ctx_len, path, n_path, stream=None) -> None:
     """Move each sequence's accepted nodes path[s, :n_path[s]] to the slots from ctx_len[s] on."""
-    torch = _torch()
-    dev, S = cache.device, cache.n_seqs
+    i32, dev, S = _torch().int32, cache.device, cache.n_seqs
     if path.dim() != 2 or path.shape[0] != S:
         raise ValueError(f"path: [{S}, path_ld] is wanted, got {tuple(path.shape)}")
-    _check(mq_kv_accept(cache.struct, _want(ctx_len, "ctx_len", torch.int32, (S,), dev),
-                        _want(path, "path", torch.int32, None, dev), _want(n_path, "n_path", torch.int32, (S,), dev),
-                        path.shape[1], _stream(stream)), "mq_kv_accept")
+    st = _lib.mq_kv_accept(cache.struct, _want(ctx_len, "ctx_len", i32, (S,), dev), _want(path, "path", i32, None, dev),
+                           _want(n_path, "n_path", i32, (S,), dev), path.shape[1], _stream_on(stream, dev))
+    if st:
+        raise MQError(st, "mq_kv_accept")
 
 
-def attn_workspace(cache: KVCache, n_heads: int, max_tokens: int = MQ_TREE_MAX_TOKENS):
+def attn_workspace(cache: KVCache, n_heads: int, max_tokens: int = MQ_TREE_MAX_TOKENS, stream=None):
     """A zeroed workspace for attn_tree (one per stream that runs it)."""
+    out = _new(mq_attn_workspace_bytes(cache.struct, n_heads, max_tokens), _torch().uint8, cache.device, stream)
     torch = _torch()
-    return torch.zeros(mq_attn_workspace_bytes(cache.struct, n_heads, max_tokens), dtype=torch.uint8, device=cache.device)
+    with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(_stream_on(stream, cache.device),
+                                                                                 device=cache.device)):
+        return out.zero_()
 
 
 def attn_tree(cache: KVCache, q, tok_start, ctx_len, mask=None, scale: Optional[float] = None,
@@ -728,34 +755,38 @@ def attn_tree(cache: KVCache, q, tok_start, ctx_len, mask=None, scale: Optional[
 
     ``mask``: int64 [n], bit j = node j of the token's tree is seen (None: a chain).  ``max_len`` bounds context plus
     tree of any sequence (default: what the table can hold).  Returns f16 [n, n_heads * head_dim], or with
-    ``out_type="q8_0"`` uint8 [n, n_heads * head_dim / 32 * 34], the ``xq`` of a projection."""
+    ``out_type="q8_0"`` uint8 [n, n_heads * head_dim / 32 * 34], the ``xq`` of a projection.  A program that calls
+    this every step keeps the workspace (attn_workspace)."""
     torch = _torch()
-    dev, D, S = cache.device, cache.head_dim, cache.n_seqs
+    dev, D, S, i32 = cache.device, cache.head_dim, cache.n_seqs, torch.int32
+    if q.dim() != 2 or q.shape[1] % D:
+        raise ValueError(f"q: rows of whole heads of {D} are wanted, got {tuple(q.shape)}")
     n, width = q.shape
-    qp, q_ld = _rows(q, "q", torch.float16, dev)
-    if width % D:
-        raise ValueError(f"q: rows of whole heads of {D} are wanted, got {width}")
+    qp, q_ld = _rows(q, "q", torch.float16, dev, width)
     if out_type == "f16":
-        out = _new((n, width), torch.float16, dev, stream) if out is None else out
-        op, out_ld = _rows(out, "out", torch.float16, dev, width)
+        if out is None:
+            out = _new((n, width), torch.float16, dev, stream)
+            op, out_ld = out.data_ptr(), width
+        else:
+            op, out_ld = _rows(out, "out", torch.float16, dev, width, n)
+        kind = MQ_TYPE_F16
     elif out_type == "q8_0":
-        out = _new((n, width // 32 * 34), torch.uint8, dev, stream) if out is None else out
-        op, out_ld = _want(out, "out", torch.uint8, (n, width // 32 * 34), dev), 0
+        shape = (n, width // 32 * 34)
+        out = _new(shape, torch.uint8, dev, stream) if out is None else out
+        op, out_ld, kind = _want(out, "out", torch.uint8, shape, dev), 0, MQ_TYPE_Q8_0
     else:
         raise ValueError(f"out_type {out_type!r}: \"f16\" or \"q8_0\"")
-    if out.shape[0] != n:
-        raise ValueError(f"out: {n} rows are wanted, got {out.shape[0]}")
-    if workspace is None:
-        on = None if stream is None else torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
-        with torch.cuda.stream(on):
-            workspace = attn_workspace(cache, width // D, max_tokens)
     if max_len is None:
         max_len = cache.table.shape[1] * MQ_KV_PAGE_TOKENS
-    a = AttnArgs(qp, op, _want(tok_start, "tok_start", torch.int32, (S + 1,), dev),
-                 _want(ctx_len, "ctx_len", torch.int32, (S,), dev),
+    a = AttnArgs(qp, op, _want(tok_start, "tok_start", i32, (S + 1,), dev), _want(ctx_len, "ctx_len", i32, (S,), dev),
                  None if mask is None else _want(mask, "mask", torch.int64, (n,), dev), q_ld, out_ld, n, width // D,
-                 max_len, max_tokens, KV_TYPES[out_type], D ** -0.5 if scale is None else scale)
-    _check(mq_attn_tree(cache.struct, a, workspace.data_ptr(), workspace.numel(), _stream(stream)), "mq_attn_tree")
+                 max_len, max_tokens, kind, D ** -0.5 if scale is None else scale)
+    if workspace is None:
+        workspace = attn_workspace(cache, width // D, max_tokens, stream)
+    st = _lib.mq_attn_tree(cache.struct, a, _want(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
+                           _stream_on(stream, dev))
+    if st:
+        raise MQError(st, "mq_attn_tree")
     return out
 
 
