@@ -58,6 +58,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ int load_acquire(const int* p)
+{
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_release(int* p, int v)
+{
+    asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+
 // transpose of an 8x8 matrix of 16-bit values, lane l holding row l/4, columns 2(l%4), +1
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
 {
@@ -103,24 +114,74 @@ struct RowState {
     float m[NT][2];      // running maxima of rows 2t, 2t + 1
 };
 
-__device__ __forceinline__ bool f16_not_finite(uint32_t h) { return (h & 0x7c00u) == 0x7c00u; }
-
-// zeroes the halves of v that are not finite; true where there were some
-__device__ __forceinline__ bool drop_not_finite(uint32_t* v)
+// A tile that reaches past the context, before its values are used: rows past
+// the sequence's end become zeros, and so do values that are not finite, since
+// 0 * NaN would reach rows that do not see the key; those values are added to
+// the outputs of the rows that do (whatever a key's weight is, they make the
+// output what they are).  The warp owns the tile's rows of the stage.
+template <int D, bool Q8>
+__device__ __noinline__ bool clean_values(uint8_t* blk, int r0, int key0, int len)  // true: not finite ones remain
 {
-    const bool lo = f16_not_finite(*v), hi = f16_not_finite(*v >> 16);
-    if (lo) *v &= 0xffff0000u;
-    if (hi) *v &= 0x0000ffffu;
-    return lo || hi;
+    using B = KvBlock<D, Q8>;
+    const int lane = threadIdx.x & 31;
+    bool suspect = false;
+    if (Q8) {
+        // codes are finite; a product with the scale overflows only above 65504 / 127
+        __half* const sc = reinterpret_cast<__half*>(blk + B::kScK + B::kScBytes) + r0 * (D / 32);
+        for (int i = lane; i < 16 * (D / 32); i += 32) {
+            if (key0 + i / (D / 32) >= len)
+                sc[i] = __ushort_as_half(0);
+            else
+                suspect |= !(fabsf(__half2float(sc[i])) < 512.0f);
+        }
+    } else {
+        for (int i = lane; i < 16 * (D / 8); i += 32) {
+            const int r = i / (D / 8);
+            uint4* const x = reinterpret_cast<uint4*>(blk + B::kVOff + B::chunk(r0 + r, i % (D / 8)));
+            if (key0 + r >= len) {
+                *x = make_uint4(0, 0, 0, 0);
+            } else {
+                const uint4 v = *x;  // exponent bits all ones carry into the sign's place
+                const uint32_t m = 0x7c007c00u, a = 0x04000400u;
+                suspect |= ((((v.x & m) + a) | ((v.y & m) + a) | ((v.z & m) + a) | ((v.w & m) + a)) & 0x80008000u) != 0;
+            }
+        }
+    }
+    return __any_sync(0xffffffffu, suspect);
 }
 
-// TAIL: the tile reaches past the context, so visibility is tested per key and
-// row, and values that are not finite are kept out of the products (0 * NaN
-// would reach rows that do not see the key) and added to the rows that do.
-template <int D, bool Q8, int NT, bool TAIL>
-__device__ __forceinline__ void rows_tile(const uint8_t* blk, int r0, int key0, const uint32_t (&q)[NT][D / 16][2],
+// zeroes the tile's values that are not finite
+template <int D, bool Q8>
+__device__ __noinline__ void drop_values(uint8_t* blk, int r0)
+{
+    using B = KvBlock<D, Q8>;
+    const int lane = threadIdx.x & 31;
+    for (int r = r0; r < r0 + 16; ++r) {
+        uint32_t drop = 0;
+        for (int e = 0; e < D / 32; ++e) {
+            const float v = kv_value<D, Q8>(blk, r, lane + 32 * e, 1);
+            drop |= !(v - v == 0.0f) ? 1u << e : 0u;
+        }
+        __syncwarp();
+        for (int e = 0; e < D / 32; ++e) {
+            const int d = lane + 32 * e;
+            if (Q8) {  // the code of zero, and a finite scale
+                if (drop >> e & 1) blk[B::kVOff + B::chunk(r, d >> 4) + (d & 15)] = 128;
+                __half* const sc = reinterpret_cast<__half*>(blk + B::kScK + B::kScBytes) + r * (D / 32) + e;
+                if (lane == 0 && !(fabsf(__half2float(*sc)) <= 65504.0f)) *sc = __ushort_as_half(0);
+            } else if (drop >> e & 1) {
+                *reinterpret_cast<uint16_t*>(blk + B::kVOff + B::chunk(r, d >> 3) + (d & 7) * 2) = 0;
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// tail: the tile reaches past the context, so what a row sees is tested key by key
+template <int D, bool Q8, int NT>
+__device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const uint32_t (&q)[NT][D / 16][2],
                                           float scale_log2, RowState<D, Q8, NT>& st, int ctx, int len,
-                                          const uint64_t* row_mask)
+                                          const uint64_t* row_mask, bool tail)
 {
     using B = KvBlock<D, Q8>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -167,13 +228,13 @@ __device__ __forceinline__ void rows_tile(const uint8_t* blk, int r0, int key0, 
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s[n][e] *= scale_log2;
-            if (TAIL) {
+        for (int e = 0; e < 4; ++e) s[n][e] *= scale_log2;
+        if (tail) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
                 const int j = key0 + g + (e >> 1) * 8;
                 const uint64_t bits = row_mask[8 * n + 2 * t + (e & 1)];
-                const bool sees = j < ctx || (j < len && ((bits >> (j - ctx)) & 1));
-                if (!sees) s[n][e] = -INFINITY;
+                if (!(j < ctx || (j < len && ((bits >> (j - ctx)) & 1)))) s[n][e] = -INFINITY;
             }
         }
         raise |= fmaxf(s[n][0], s[n][2]) > st.m[n][0] + kRaise || fmaxf(s[n][1], s[n][3]) > st.m[n][1] + kRaise;
@@ -209,22 +270,34 @@ __device__ __forceinline__ void rows_tile(const uint8_t* blk, int r0, int key0, 
     // ---- O^T: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the tile
     const int k0 = r0 + 2 * t;
     const uint8_t* const vb = blk + B::kVOff;
-    bool dropped = false;
-    bool in0 = true, in1 = true, in2 = true, in3 = true;  // TAIL: the key is within the sequence
-    if (TAIL) {
-        const int j = key0 + 2 * t;
-        in0 = j < len, in1 = j + 1 < len, in2 = j + 8 < len, in3 = j + 9 < len;
+    if (tail) {
+        if (clean_values<D, Q8>(blk, r0, key0, len)) {
+#pragma unroll 1
+            for (int k = 0; k < min(16, len - key0); ++k) {
+                const int j = key0 + k, r = r0 + k;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint64_t bits = row_mask[8 * n + 2 * t + e];
+                        if (!(j < ctx || ((bits >> (j - ctx)) & 1))) continue;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float v = kv_value<D, Q8>(blk, r, vdim<D, Q8>(g, i) + x, 1);
+                                if (!(v - v == 0.0f)) st.o[n][i][e + 2 * x] += v;
+                            }
+                    }
+            }
+            __syncwarp();
+            drop_values<D, Q8>(blk, r0);
+        }
+        // the next bulk copy into this stage comes after these writes
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
     }
     auto product = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-        if (TAIL) {
-            const uint32_t m01 = (in0 ? 0xffffu : 0u) | (in1 ? 0xffff0000u : 0u);
-            const uint32_t m23 = (in2 ? 0xffffu : 0u) | (in3 ? 0xffff0000u : 0u);
-            a0 &= m01, a1 &= m01, a2 &= m23, a3 &= m23;
-            dropped |= drop_not_finite(&a0);
-            dropped |= drop_not_finite(&a1);
-            dropped |= drop_not_finite(&a2);
-            dropped |= drop_not_finite(&a3);
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) mma16816(st.o[n][i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
     };
@@ -268,102 +341,145 @@ __device__ __forceinline__ void rows_tile(const uint8_t* blk, int r0, int key0, 
                         __byte_perm(v2[w], v3[w], 0x5410), __byte_perm(v2[w], v3[w], 0x7632));
         }
     }
-    if (TAIL && __any_sync(0xffffffffu, dropped)) {
-        // rare: whatever its weight, such a value makes the outputs of the rows that see it what it is
-        for (int k = 0; k < 16; ++k) {
-            const int j = key0 + k;
-            if (j >= len) break;
-            const int r = r0 + k;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint64_t bits = row_mask[8 * n + 2 * t + e];
-                    if (!(j < ctx || ((bits >> (j - ctx)) & 1))) continue;
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float v = kv_value<D, Q8>(blk, r, vdim<D, Q8>(g, i) + x, 1);
-                            if (!(v - v == 0.0f)) st.o[n][i][e + 2 * x] += v;
-                        }
-                }
-        }
-    }
 }
 
 // ---- the kernel ----------------------------------------------------------------------------
+// what the producer hands over with a segment, besides its query rows
+struct RowsSegment {
+    AttnSegment g;
+    int split;  // index among the CTA's groups that it shares with others (at most two), or -1
+};
+
+template <int D, bool Q8, int NT>
+struct RowsSmem {
+    using B = KvBlock<D, Q8>;
+    using C = RowsCfg<NT>;
+    static constexpr int kQ = C::kRows * D * 2;            // a segment's query rows
+    static constexpr int kTile = 32 * 4 + 4;               // floats of one output tile of a warp, padded
+    static constexpr int kWarpOut = NT * (D / 16) * kTile; // floats of a warp's outputs
+    static constexpr int kFixed = kSegs * kQ + C::kWarps * kWarpOut * 4;
+};
+
 template <int D, bool Q8, int NT>
 __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
     attn_rows_kernel(const AttnParams p, const int stages, unsigned* status)
 {
     using B = KvBlock<D, Q8>;
     using C = RowsCfg<NT>;
+    using S = RowsSmem<D, Q8, NT>;
     constexpr int RT = C::kRows, kWarps = C::kWarps, kCons = 32 * kWarps;
     extern __shared__ __align__(128) uint8_t sm[];
     uint8_t* const ring = sm;
-    float* const merge = reinterpret_cast<float*>(sm + stages * B::kBytes);  // [kTeam][RT][D]
+    __half* const q_s = reinterpret_cast<__half*>(sm + stages * B::kBytes);
+    float* const out_s = reinterpret_cast<float*>(sm + stages * B::kBytes + kSegs * S::kQ);
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], seg_full[kSegs], seg_empty[kSegs];
-    __shared__ AttnSegment seg_s[kSegs];
-    __shared__ uint64_t mask_s[RT];
-    __shared__ float m_s[kWarps][RT], l_s[kWarps][RT];
-    __shared__ int64_t scratch[kWarps + 1], at_s;
-    __shared__ float sum_s[RT];
-    __shared__ int seq_s, bad_s[kMaxStages], ok_s[kWarps], seg_bad_s, is_last_s, gone_s;
+    __shared__ __align__(8) uint64_t part_full[2], part_done[2];
+    __shared__ RowsSegment seg_s[kSegs];
+    __shared__ AttnSegment split_s[2];
+    __shared__ uint64_t mask_s[kSegs][RT];
+    __shared__ float m_s[kWarps][RT], l_s[kWarps][RT], sum_s[RT];
+    __shared__ int2 at_s;
+    __shared__ int scratch[kWarps + 1], bad_s[kMaxStages], seen_s[kMaxStages], ok_s[kWarps], pages_bad_s[kWarps], last_s[2], gone_s;
     __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
+        gone_s = 0;
         for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kTeam);
+            seen_s[s] = 0;
         }
         for (int s = 0; s < kSegs; ++s) {
             mbar_init(&seg_full[s], 1);
             mbar_init(&seg_empty[s], kWarps);
         }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&part_full[s], kWarps);
+            mbar_init(&part_done[s], 1);
+        }
         fence_barrier_init();
     }
-    const AttnRange rg = attn_range(p, RT, status, scratch, &seq_s, &at_s);  // synchronises the CTA
+    const AttnRange rg = attn_range(p, RT, status, scratch, &at_s);  // synchronises the CTA
     if (rg.first >= rg.last) return;
 
+    // one outcome for the whole warp
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.limit_ns));
+        if (!ok) abort_flag = 1;
+        return ok;
+    };
+
     if (warp == kWarps) {
-        // ---- producer
-        if (lane == 0) {
-            AttnRange w = rg;
-            AttnSegment g;
-            int64_t at = rg.first;
-            const int64_t page_bytes = int64_t(p.c.n_kv_heads) * B::kBytes;
-            int it = 0, sg = 0;
-            for (; !abort_flag && attn_next(p, RT, &w, &at, &g); ++sg) {
-                const int ss = sg % kSegs;
-                if (sg >= kSegs && !mbar_wait_bounded(&seg_empty[ss], uint32_t(sg / kSegs - 1) & 1u, p.limit_ns)) {
-                    abort_flag = 1;
-                    break;
-                }
-                seg_s[ss] = g;
-                mbar_arrive(&seg_full[ss]);
-                for (int i = 0; i < g.n; ++i, ++it) {
+        // ---- producer: lane 0 waits and copies, the warp reads page numbers 32 at a time
+        AttnRange w = rg;
+        AttnSegment g;
+        int at = rg.first, it = 0, sg = 0, splits = 0;
+        bool ok = true;
+        for (; ok && attn_next(p, RT, &w, &at, &g); ++sg) {
+            const int ss = sg % kSegs, rows = min(RT, g.T * p.group - g.row0);
+            const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0;
+            int32_t page_l = lane < g.n ? __ldg(table + lane) : 0;
+            uint64_t bits = 0;
+            const int node = (g.row0 + lane) / p.group;
+            if (lane < rows) bits = p.a.mask ? __ldg(p.a.mask + g.t0 + node) : ~0ull >> (63 - node);
+            if (sg >= kSegs) ok = wait_all(&seg_empty[ss], uint32_t(sg / kSegs - 1) & 1u);
+            if (!ok) break;
+            const int split = g.n_ctas > 1 ? splits++ : -1;
+            if (lane < RT) mask_s[ss][lane] = bits;
+            if (lane == 0) {
+                seg_s[ss].g = g;
+                seg_s[ss].split = split;
+                if (split >= 0) split_s[split] = g;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&seg_full[ss], uint32_t(rows) * D * 2);
+            __syncwarp();
+            if (lane < rows) {
+                const int row = g.row0 + lane;
+                bulk_copy_g2s(q_s + (ss * RT + lane) * D,
+                              static_cast<const __half*>(p.a.q) + int64_t(g.t0 + node) * p.a.q_ld +
+                                  (g.head * p.group + row - node * p.group) * D,
+                              D * 2, &seg_full[ss]);
+            }
+            for (int i0 = 0; ok && i0 < g.n; i0 += 32) {
+                const int32_t page_now = page_l;
+                if (i0 + 32 + lane < g.n) page_l = __ldg(table + i0 + 32 + lane);
+                const int m = min(32, g.n - i0);
+                for (int i = 0; i < m; ++i, ++it) {
                     const int s = it % stages;
-                    if (it >= stages && !mbar_wait_bounded(&empty[s], uint32_t(it / stages - 1) & 1u, p.limit_ns)) {
-                        abort_flag = 1;
-                        break;
+                    const int32_t page = __shfl_sync(0xffffffffu, page_now, i);
+                    if (it >= stages) ok = wait_all(&empty[s], uint32_t(it / stages - 1) & 1u);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const bool bad = page < 0 || page >= p.c.n_pages;  // table entries are not trusted
+                        bad_s[s] = bad;
+                        if (bad) {
+                            mbar_arrive(&full[s]);
+                        } else {
+                            mbar_arrive_expect_tx(&full[s], B::kBytes);
+                            bulk_copy_g2s(ring + s * B::kBytes,
+                                          p.c.pages + (int64_t(page) * p.c.n_kv_heads + g.head) * B::kBytes, B::kBytes,
+                                          &full[s]);
+                        }
                     }
-                    const int64_t page = kv_page_of(p.c, g.seq, (g.page0 + i) * kKvPage, page_bytes);
-                    bad_s[s] = page < 0;
-                    if (page < 0) {
-                        mbar_arrive(&full[s]);
-                        continue;
-                    }
-                    mbar_arrive_expect_tx(&full[s], B::kBytes);
-                    bulk_copy_g2s(ring + s * B::kBytes, p.c.pages + page + int64_t(g.head) * B::kBytes, B::kBytes, &full[s]);
                 }
             }
-            // copies still in flight land before the CTA can exit
-            for (int j = it > stages ? it - stages : 0; j < it; ++j)
-                (void)mbar_wait_bounded(&full[j % stages], uint32_t(j / stages) & 1u, p.limit_ns);
         }
+        // the shared groups' arrivals, once the consumers have written their parts
+        for (int k = 0; k < splits; ++k) {
+            const bool there = mbar_wait_bounded(&part_full[k], 0, p.limit_ns) && !abort_flag;
+            if (lane == 0) {
+                last_s[k] = there && attn_arrive(p, split_s[k]);
+                mbar_arrive(&part_done[k]);
+            }
+        }
+        // copies still in flight land before the CTA can exit
+        for (int j = it > stages ? it - stages : 0; j < it; ++j)
+            (void)mbar_wait_bounded(&full[j % stages], uint32_t(j / stages) & 1u, p.limit_ns);
+        for (int j = sg > kSegs ? sg - kSegs : 0; j < sg; ++j)
+            (void)mbar_wait_bounded(&seg_full[j % kSegs], uint32_t(j / kSegs) & 1u, p.limit_ns);
         __syncwarp();
         if (abort_flag && lane == 0) atomicOr(status, MQ_DEV_TIMEOUT);
         return;
@@ -371,72 +487,75 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
 
     // ---- consumers
     const int team = warp / kTeam, wi = warp % kTeam, g8 = lane >> 2, t4 = lane & 3;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = __all_sync(0xffffffffu, !abort_flag && mbar_wait_bounded(bar, parity, p.limit_ns));
+    auto wait_seen = [&](int* word, int value) {
+        bool ok = load_acquire(word) >= value;
+        if (!ok) {
+            const uint64_t t0 = global_timer_ns();
+            while (!(ok = load_acquire(word) >= value) && global_timer_ns() - t0 < p.limit_ns) {}
+        }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) abort_flag = 1;
         return ok;
     };
-    int it = 0;
-    int64_t done = rg.first;
+    int it = 0, done = rg.first, splits = 0;
+    bool all_ok = true;
     for (int sg = 0; done < rg.last; ++sg) {
         const int ss = sg % kSegs;
         bool ok = wait_all(&seg_full[ss], uint32_t(sg / kSegs) & 1u);
-        const AttnSegment g = seg_s[ss];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_empty[ss]);
-        const int rows = ok ? min(RT, g.T * p.group - g.row0) : 0, len = g.ctx + g.T;
+        const AttnSegment& g = seg_s[ss].g;  // stays until this warp's arrival at seg_empty
+        const int ctx = g.ctx, len = ctx + g.T, seg_n = g.n, first_key = g.page0 * kKvPage + 16 * wi;
         RowState<D, Q8, NT> st;
         uint32_t q[NT][D / 16][2];
-        if (ok) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int r = 8 * n + g8, row = g.row0 + r;
-                const __half* const src = static_cast<const __half*>(p.a.q) +
-                                          int64_t(g.t0 + row / p.group) * p.a.q_ld +
-                                          (g.head * p.group + row % p.group) * D;
+        for (int n = 0; n < NT; ++n) {
+            // rows past the block's hold what was there: they stay in their own columns
+            const __half* const src = q_s + (ss * RT + 8 * n + g8) * D;
 #pragma unroll
-                for (int j = 0; j < D / 16; j += 2) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (r < rows) v = __ldg(reinterpret_cast<const uint4*>(src + kdim<D, Q8>(t4, j)));
-                    q[n][j][0] = v.x, q[n][j][1] = v.y, q[n][j + 1][0] = v.z, q[n][j + 1][1] = v.w;
-                }
-                st.m[n][0] = st.m[n][1] = -3.402823466e38f;  // finite: a row without keys stays at 0 / 0 sums
+            for (int j = 0; j < D / 16; j += 2) {
+                const uint4 v = *reinterpret_cast<const uint4*>(src + kdim<D, Q8>(t4, j));
+                q[n][j][0] = v.x, q[n][j][1] = v.y, q[n][j + 1][0] = v.z, q[n][j + 1][1] = v.w;
+            }
+            st.m[n][0] = st.m[n][1] = -3.402823466e38f;  // finite: a row without keys keeps zero sums
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    st.l[n][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) {
+                st.l[n][e] = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) st.o[n][i][e] = 0.0f;
-                }
+                for (int i = 0; i < D / 16; ++i) st.o[n][i][e] = 0.0f;
             }
         }
-        // the rows' masks (the previous segment's readers are past the merge's barriers)
-        if (threadIdx.x < RT) {
-            uint64_t bits = 0;
-            const int node = (g.row0 + int(threadIdx.x)) / p.group;
-            if (ok && int(threadIdx.x) < rows) bits = p.a.mask ? __ldg(p.a.mask + g.t0 + node) : ~0ull >> (63 - node);
-            mask_s[threadIdx.x] = bits;
-        }
-        named_barrier_sync(1, kCons);
         bool bad = false;
-        for (int i = team; ok && i < g.n; i += C::kTeams) {
+#pragma unroll 1
+        for (int i = team; ok && i < seg_n; i += C::kTeams) {
             const int n = it + i, s = n % stages;
-            ok = wait_all(&full[s], uint32_t(n / stages) & 1u);
+            // The stage's previous use was another team's page, which may not even have
+            // landed; a wait by parity tells two successive uses apart only, so that team's
+            // word that it has comes first.
+            ok = n < stages || wait_seen(&seen_s[s], n - stages + 1);
+            ok = ok && wait_all(&full[s], uint32_t(n / stages) & 1u);
+            if (ok && wi == 0 && lane == 0) store_release(&seen_s[s], n + 1);
             if (!ok) break;
             bad |= bad_s[s] != 0;
-            const uint8_t* const blk = ring + s * B::kBytes;
-            const int key0 = (g.page0 + i) * kKvPage + 16 * wi;
-            if (key0 + 16 <= g.ctx)
-                rows_tile<D, Q8, NT, false>(blk, 16 * wi, key0, q, p.scale_log2, st, g.ctx, len, mask_s);
-            else if (key0 < len)
-                rows_tile<D, Q8, NT, true>(blk, 16 * wi, key0, q, p.scale_log2, st, g.ctx, len, mask_s);
+            uint8_t* const blk = ring + s * B::kBytes;
+            const int key0 = first_key + i * kKvPage;
+            if (key0 < len)
+                rows_tile<D, Q8, NT>(blk, 16 * wi, key0, q, p.scale_log2, st, ctx, len, mask_s[ss], key0 + 16 > ctx);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
         }
-        it += g.n;
-        done += g.n;
+        it += seg_n;
+        done += seg_n;
 
-        // ---- join the warps: common maxima, then the teams add up in order
-        if (g8 == 0)
+        // ---- join the warps that had pages: each leaves its tiles as it holds them
+        float* const mine = out_s + warp * S::kWarpOut;
+        if (team < seg_n) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    *reinterpret_cast<float4*>(mine + (n * (D / 16) + i) * S::kTile + 4 * lane) =
+                        make_float4(st.o[n][i][0], st.o[n][i][1], st.o[n][i][2], st.o[n][i][3]);
+        }
+        if (g8 == 0) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -444,56 +563,40 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
                     m_s[warp][8 * n + 2 * t4 + e] = st.m[n][e];
                     l_s[warp][8 * n + 2 * t4 + e] = st.l[n][e];
                 }
-        if (lane == 0) ok_s[warp] = ok;
-        if (threadIdx.x == 0) seg_bad_s = 0, gone_s = 0;
+        }
+        if (lane == 0) ok_s[warp] = ok, pages_bad_s[warp] = bad;
         named_barrier_sync(1, kCons);
         // a wait that ran out in any warp ends all of them here, together
-        bool all_ok = true;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) all_ok &= ok_s[w] != 0;
+        const int flags = lane < kWarps ? (ok_s[lane] ? 0 : 1) | (pages_bad_s[lane] ? 2 : 0) : 0;
+        all_ok = !__any_sync(0xffffffffu, flags & 1);
+        const bool seg_bad = __any_sync(0xffffffffu, flags & 2);
         if (!all_ok) break;
-        if (bad && lane == 0) seg_bad_s = 1;  // read after the next barrier
-        float f[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mm = m_s[0][8 * n + 2 * t4 + e];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, m_s[w][8 * n + 2 * t4 + e]);
-                f[n][e] = ex2(st.m[n][e] - mm);
-            }
-        for (int tm = 0; tm < C::kTeams; ++tm) {
-            if (team == tm) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float* const row = merge + (wi * RT + 8 * n + 2 * t4 + e) * D;
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            float2* const x = reinterpret_cast<float2*>(row + vdim<D, Q8>(g8, i));
-                            float2 v = make_float2(st.o[n][i][e] * f[n][e], st.o[n][i][e + 2] * f[n][e]);
-                            if (tm) {
-                                const float2 y = *x;
-                                v.x += y.x, v.y += y.y;
-                            }
-                            *x = v;
-                        }
-                    }
-            }
-            named_barrier_sync(1, kCons);
-        }
-        const bool seg_bad = seg_bad_s != 0;
-        const bool whole = g.n_ctas == 1;
+        const int split = seg_s[ss].split, rows = min(RT, g.T * p.group - g.row0);
+        const int nw = min(C::kTeams, seg_n) * kTeam;  // warps that had pages
         float* const slot = p.parts + (int64_t(blockIdx.x) * 2 + g.slot) * attn_slot_floats(RT, D);
+#pragma unroll 1
         for (int x = warp; x < rows * (D / 32); x += kWarps) {
             const int r = x / (D / 32), d = (x % (D / 32)) * 32 + lane;
-            float mm = m_s[0][r], sum = 0.0f, v = 0.0f;
-            for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, m_s[w][r]);
-            for (int w = 0; w < kWarps; ++w) sum += l_s[w][r] * ex2(m_s[w][r] - mm);
-            for (int w = 0; w < kTeam; ++w) v += merge[(w * RT + r) * D + d];
-            if (whole) {
+            // lane w: warp w's maximum and weight
+            const float mw = lane < nw ? m_s[lane][r] : -3.402823466e38f;
+            float mm = mw;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+            const float fw = ex2(mw - mm);
+            float sum = lane < nw ? l_s[lane][r] * fw : 0.0f;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            mm = __shfl_sync(0xffffffffu, mm, 0);
+            sum = __shfl_sync(0xffffffffu, sum, 0);
+            // value d of row r in a warp's tiles
+            const int g_of = Q8 && D == 128 ? d / 16 : (d % 64) / 8;
+            const int i_of = Q8 && D == 128 ? (d % 16) / 2 : 4 * (d / 64) + (d % 8) / 2;
+            const float* const src = out_s + ((r / 8) * (D / 16) + i_of) * S::kTile +
+                                     4 * (4 * g_of + (r % 8) / 2) + (r & 1) + 2 * (d & 1);
+            float v = 0.0f;
+#pragma unroll 4
+            for (int w = 0; w < nw; ++w) v = fmaf(src[w * S::kWarpOut], __shfl_sync(0xffffffffu, fw, w), v);
+            if (split < 0) {
                 if (!seg_bad) attn_emit(p, g, g.row0 + r, D, d - lane, sum == 0.0f ? 0.0f : v / sum);
             } else {
                 if (d == 0) {
@@ -503,61 +606,111 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
                 slot[2 * RT + r * D + d] = v;
             }
         }
-        if (whole) {
-            if (seg_bad && threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-            named_barrier_sync(1, kCons);
+        __syncwarp();
+        if (lane == 0) {
+            if (split >= 0) mbar_arrive(&part_full[split]);
+            mbar_arrive(&seg_empty[ss]);
+        }
+        if (split < 0 && seg_bad && threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+        splits += split >= 0;
+        named_barrier_sync(1, kCons);  // out_s, m_s, l_s are free again
+    }
+    if (!all_ok) {
+        if (lane == 0)
+            for (int k = splits; k < 2; ++k) mbar_arrive(&part_full[k]);  // the producer finds abort_flag set
+        return;
+    }
+
+    // ---- the shared groups whose last CTA this is: their segments joined in CTA order
+    if (splits > 0) {
+        bool ok = true;
+        for (int k = 0; k < splits; ++k) ok = wait_all(&part_done[k], 0) && ok;
+        if (lane == 0) ok_s[warp] = ok;
+        named_barrier_sync(1, kCons);
+        if (__any_sync(0xffffffffu, lane < kWarps && !ok_s[lane])) return;
+    }
+    for (int k = 0; k < splits; ++k) {
+        if (!last_s[k]) continue;
+        const AttnSegment& g = split_s[k];
+        const int rows = min(RT, g.T * p.group - g.row0);
+        float* const wgt = reinterpret_cast<float*>(ring);  // [n_ctas][RT]; every copy has landed and been read
+        auto slot_of = [&](int c) {
+            return p.parts + (int64_t(g.cta0 + c) * 2 + (c == 0 ? g.slot0 : 0)) * attn_slot_floats(RT, D);
+        };
+        bool gone = false;
+        for (int r = warp; r < RT; r += kWarps) {
+            float mm = -3.402823466e38f, sum = 0.0f;
+            if (r < rows) {
+                for (int c = lane; c < g.n_ctas; c += 32) mm = fmaxf(mm, __ldcg(slot_of(c) + r));
+#pragma unroll
+                for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+            }
+            for (int c = lane; c < g.n_ctas; c += 32) {
+                float f1 = 0.0f;
+                if (r < rows) {
+                    const float l = __ldcg(slot_of(c) + RT + r);
+                    f1 = ex2(__ldcg(slot_of(c) + r) - mm);
+                    gone |= l < 0.0f;
+                    sum = fmaf(l, f1, sum);
+                }
+                wgt[c * RT + r] = f1;
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) sum_s[r] = sum;
+        }
+        if (gone) gone_s = 1 + k;
+        named_barrier_sync(1, kCons);
+        if (gone_s == 1 + k) {
+            if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
             continue;
         }
-        named_barrier_sync(1, kCons);
-        if (threadIdx.x == 0) is_last_s = attn_arrive(p, g);
-        named_barrier_sync(1, kCons);
-        if (is_last_s) {
-            // ---- the group's last CTA joins its segments, in CTA order
-            float* const wgt = merge;  // [n_ctas][RT], free here
-            auto slot_of = [&](int c) {
-                return p.parts + (int64_t(g.cta0 + c) * 2 + (c == 0 ? g.slot0 : 0)) * attn_slot_floats(RT, D);
-            };
-            bool gone = false;
-            for (int r = warp; r < rows; r += kWarps) {
-                float mm = -3.402823466e38f, sum = 0.0f;
-                for (int c = lane; c < g.n_ctas; c += 32) mm = fmaxf(mm, __ldcg(slot_of(c) + r));
-                for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-                for (int c = lane; c < g.n_ctas; c += 32) {
-                    const float f1 = ex2(__ldcg(slot_of(c) + r) - mm), l = __ldcg(slot_of(c) + RT + r);
-                    gone |= l < 0.0f;
-                    wgt[c * RT + r] = f1;
-                    sum += l * f1;
-                }
-                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (lane == 0) sum_s[r] = sum;
+        // warp w adds up CTAs w, w + kWarps, ...; a lane holds four values of each 128 of the rows
+        constexpr int NV = RT * D / 128;
+        float4 acc[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c = warp; c < g.n_ctas; c += kWarps) {
+            const float4* const src = reinterpret_cast<const float4*>(slot_of(c) + 2 * RT) + lane;
+            float4 x[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                x[v] = (v * 128 + lane * 4) / D < rows ? __ldcg(src + v * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const float f1 = wgt[c * RT + (v * 128 + lane * 4) / D];
+                acc[v].x = fmaf(x[v].x, f1, acc[v].x);
+                acc[v].y = fmaf(x[v].y, f1, acc[v].y);
+                acc[v].z = fmaf(x[v].z, f1, acc[v].z);
+                acc[v].w = fmaf(x[v].w, f1, acc[v].w);
             }
-            if (gone) gone_s = 1;
-            named_barrier_sync(1, kCons);
-            if (gone_s) {
-                if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-            } else {
-                for (int x = warp; x < rows * (D / 32); x += kWarps) {
-                    const int r = x / (D / 32), d = (x % (D / 32)) * 32 + lane;
-                    float v = 0.0f;
-#pragma unroll 8
-                    for (int c = 0; c < g.n_ctas; ++c)
-                        v = fmaf(__ldcg(slot_of(c) + 2 * RT + r * D + d), wgt[c * RT + r], v);
-                    attn_emit(p, g, g.row0 + r, D, d - lane, sum_s[r] == 0.0f ? 0.0f : v / sum_s[r]);
-                }
-            }
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            *reinterpret_cast<float4*>(out_s + warp * RT * D + v * 128 + lane * 4) = acc[v];
+        named_barrier_sync(1, kCons);
+        for (int x = warp; x < rows * (D / 32); x += kWarps) {
+            const int r = x / (D / 32), d = (x % (D / 32)) * 32 + lane;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += out_s[(w * RT + r) * D + d];
+            attn_emit(p, g, g.row0 + r, D, d - lane, sum_s[r] == 0.0f ? 0.0f : v / sum_s[r]);
         }
         named_barrier_sync(1, kCons);
     }
 }
 
+constexpr int kRowsSmem = 222 * 1024;  // ring and merge buffers; the kernel's static arrays come on top
+
 template <int D, bool Q8, int NT>
 cudaError_t launch_rows(const AttnParams& p, int grid, int max_smem, unsigned* status, cudaStream_t s)
 {
     using B = KvBlock<D, Q8>;
-    constexpr int kMerge = kTeam * RowsCfg<NT>::kRows * D * 4;
-    int stages = (max_smem - kMerge) / B::kBytes;
+    using S = RowsSmem<D, Q8, NT>;
+    int stages = (max_smem - S::kFixed) / B::kBytes;
     if (stages > kMaxStages) stages = kMaxStages;
-    const int smem = stages * B::kBytes + kMerge;
+    static_assert((kRowsSmem - S::kFixed) / B::kBytes >= RowsCfg<NT>::kTeams, "each team needs a page to work on");
+    const int smem = stages * B::kBytes + S::kFixed;
     attn_rows_kernel<D, Q8, NT><<<grid, RowsCfg<NT>::kThreads, smem, s>>>(p, stages, status);
     return cudaGetLastError();
 }
@@ -573,7 +726,6 @@ cudaError_t launch_rows_nt(const mq_kv_cache& c, const AttnParams& p, int grid, 
                              : launch_rows<64, false, NT>(p, grid, max_smem, status, s);
 }
 
-constexpr int kRowsSmem = 220 * 1024;  // ring and merge buffers; the kernel's static arrays come on top
 
 }  // namespace
 

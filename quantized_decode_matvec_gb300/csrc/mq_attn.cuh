@@ -3,8 +3,7 @@
 //
 // The work of a call is a line of units.  Sequence s, key/value head h and
 // block b of its query rows (token * group + head of the group) form a group;
-// a group's units are its pages of kKvPage keys, and the groups follow one
-// another in the order (s, h, b).  CTA c of N takes the units
+// a group's units are its pages of kKvPage keys, and the groups follow one another in the order (s, h, b).  CTA c of N takes the units
 // [c*W/N, (c+1)*W/N) of all W, so every CTA has the same number of pages
 // whatever the lengths are, and lengths are read on the device only.  A CTA's
 // stretch of a group is a segment.  A group that lies in one CTA is finished
@@ -52,25 +51,32 @@ __device__ __forceinline__ bool attn_seq(const AttnParams& p, int s, AttnSeq* q,
 }
 
 // units of sequence s with row blocks of RT rows
-__device__ __forceinline__ int64_t attn_units(const AttnParams& p, const AttnSeq& q, int RT)
+__device__ __forceinline__ int attn_units(const AttnParams& p, const AttnSeq& q, int RT)
 {
-    return int64_t(q.pages) * p.c.n_kv_heads * ((q.T * p.group + RT - 1) / RT);
+    return q.pages * p.c.n_kv_heads * ((q.T * p.group + RT - 1) / RT);
 }
 
-// Where a CTA's range starts: sequence and unit within it.  Called by all
-// threads of the CTA; scratch: 33 int64 of shared memory.
+// The cut of the line, and where this CTA's stretch starts.
 struct AttnRange {
-    int64_t total, first, last;  // all units; this CTA's [first, last)
-    int64_t ctas;                // those that take part: each has a unit at least
-    int64_t seq_first;           // first unit of the sequence that the walk is at
-    int seq;
+    int total, ctas;  // all units; the CTAs that take part (each has a unit at least)
+    int quot, rem;    // total / ctas, total % ctas
+    int first, last;  // this CTA's units
+    int seq;          // sequence that the walk is at, and its first unit
+    int seq_first;
+    __device__ __forceinline__ int begin(int c) const { return c * quot + min(c, rem); }
+    __device__ __forceinline__ int owner(int u) const
+    {
+        const int longer = rem * (quot + 1);
+        return u < longer ? u / (quot + 1) : rem + (u - longer) / quot;
+    }
 };
-__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status, int64_t* scratch,
-                                                int* seq_s, int64_t* at_s)
+
+// Called by all threads of the CTA; scratch: an int per warp.
+__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status, int* scratch, int2* at_s)
 {
     const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.c.n_seqs + nthr - 1) / nthr, s0 = min(tid * per, p.c.n_seqs), s1 = min(s0 + per, p.c.n_seqs);
-    int64_t mine = 0;
+    int mine = 0;
     bool any_bad = false;
     for (int s = s0; s < s1; ++s) {
         AttnSeq q;
@@ -79,91 +85,87 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, uns
         any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-    int64_t incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
     AttnRange r;
-    int64_t before = 0, total = 0;
-    for (int w = 0; w < (nthr + 31) / 32; ++w) {
-        if (w == warp) before = total;
-        total += scratch[w];
+    int before = 0;
+    r.total = 0;
+    for (int w = 0; w < nthr / 32; ++w) {
+        if (w == warp) before = r.total;
+        r.total += scratch[w];
     }
-    r.total = total;
-    r.ctas = total < gridDim.x ? total : gridDim.x;
-    const int64_t c = blockIdx.x;
-    r.first = c < r.ctas ? total * c / r.ctas : total;
-    r.last = c < r.ctas ? total * (c + 1) / r.ctas : total;
-    int64_t at = before + incl - mine;
+    r.ctas = min(r.total, int(gridDim.x));
+    const int c = blockIdx.x;
+    r.quot = r.ctas ? r.total / r.ctas : 0;
+    r.rem = r.total - r.quot * r.ctas;
+    r.first = c < r.ctas ? r.begin(c) : r.total;
+    r.last = c < r.ctas ? r.begin(c + 1) : r.total;
+    int at = before + incl - mine;
     if (r.first >= at && r.first < at + mine) {
         for (int s = s0; s < s1; ++s) {
             AttnSeq q;
             bool bad;
             if (!attn_seq(p, s, &q, &bad)) continue;
-            const int64_t u = attn_units(p, q, RT);
+            const int u = attn_units(p, q, RT);
             if (r.first < at + u) {
-                *seq_s = s;
-                *at_s = at;
+                *at_s = make_int2(s, at);
                 break;
             }
             at += u;
         }
     }
     __syncthreads();
-    r.seq = *seq_s;
-    r.seq_first = *at_s;
+    r.seq = at_s->x;
+    r.seq_first = at_s->y;
     return r;
 }
 
 // one segment, as the producer describes it to the other roles
 struct AttnSegment {
     int seq, t0, T, ctx;
-    int head, row0;     // key/value head; first query row of the block
-    int page0, n;       // its pages page0 .. page0 + n - 1
-    int group_index;    // of the counters
-    int cta0, n_ctas;   // the CTAs that share the group
-    int slot0;          // workspace slot of the first of them (the others use 0)
-    int slot;           // this CTA's slot
+    int head, row0;   // key/value head; first query row of the block
+    int page0, n;     // its pages page0 .. page0 + n - 1
+    int group_index;  // of the counters
+    int cta0, n_ctas; // the CTAs that share the group
+    int slot0;        // workspace slot of the first of them (the others use 0)
+    int slot;         // this CTA's slot
 };
 
-// the CTA that owns unit u
-__device__ __forceinline__ int attn_owner(int64_t u, const AttnRange& r)
-{
-    return int(((u + 1) * r.ctas - 1) / r.total);
-}
-
-// The next segment of a CTA's range, which starts at unit *at of sequence
+// The next segment of a CTA's stretch, which starts at unit *at of sequence
 // w->seq or a later one; *at moves past it.
-__device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange* w, int64_t* at, AttnSegment* g)
+__device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange* w, int* at, AttnSegment* g)
 {
-    const int64_t u = *at;
+    const int u = *at;
     if (u >= w->last) return false;
     AttnSeq q;
     bool bad;
-    int64_t units = 0;
+    int units = 0;
     for (;; ++w->seq, w->seq_first += units) {
         if (w->seq >= p.c.n_seqs) return false;  // not reached unless the lengths change under the call
         units = attn_seq(p, w->seq, &q, &bad) ? attn_units(p, q, RT) : 0;
         if (u < w->seq_first + units) break;
     }
     const int blocks = (q.T * p.group + RT - 1) / RT;
-    const int64_t k = (u - w->seq_first) / q.pages;  // group within the sequence
-    const int64_t g0 = w->seq_first + k * q.pages, g1 = g0 + q.pages;
+    const int k = (u - w->seq_first) / q.pages;  // group within the sequence
+    const int g0 = w->seq_first + k * q.pages, g1 = g0 + q.pages;
     g->seq = w->seq;
     g->t0 = q.t0, g->T = q.T, g->ctx = q.ctx;
-    g->head = int(k / blocks);
-    g->row0 = int(k % blocks) * RT;
-    g->page0 = int(u - g0);
-    g->n = int((g1 < w->last ? g1 : w->last) - u);
+    g->head = k / blocks;
+    g->row0 = (k - g->head * blocks) * RT;
+    g->page0 = u - g0;
+    g->n = min(g1, w->last) - u;
     const int most = (p.a.max_tokens * p.group + RT - 1) / RT;
-    g->group_index = (w->seq * p.c.n_kv_heads + g->head) * most + int(k % blocks);
-    g->cta0 = attn_owner(g0, *w);
-    g->n_ctas = attn_owner(g1 - 1, *w) - g->cta0 + 1;
-    g->slot0 = g0 > w->total * g->cta0 / w->ctas ? 1 : 0;
+    g->group_index = (w->seq * p.c.n_kv_heads + g->head) * most + k - g->head * blocks;
+    const bool whole = g0 >= w->first && g1 <= w->last;
+    g->cta0 = whole ? int(blockIdx.x) : w->owner(g0);
+    g->n_ctas = whole ? 1 : w->owner(g1 - 1) - g->cta0 + 1;
+    g->slot0 = g0 > w->begin(g->cta0) ? 1 : 0;
     g->slot = u > w->first ? 1 : 0;
     *at = u + g->n;
     return true;

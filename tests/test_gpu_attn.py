@@ -121,6 +121,13 @@ def test_long_contexts(cuda_ready, ctype, T):
 
 
 @pytest.mark.parametrize("ctype", ["q8_0", "f16"])
+@pytest.mark.parametrize("Hq,Hkv,D,T", [(14, 2, 128, 1), (16, 2, 64, 1), (14, 2, 128, 2), (14, 2, 64, 2)])
+def test_many_pages_per_sm(cuda_ready, ctype, Hq, Hkv, D, T):
+    # every SM's ring of pages goes round several times
+    run_case(cuda_ready, np.random.default_rng(T), [150000, 3], [T, T], Hq, Hkv, D, ctype)
+
+
+@pytest.mark.parametrize("ctype", ["q8_0", "f16"])
 def test_large_scores_and_scales(cuda_ready, ctype):
     rng = np.random.default_rng(77)
     for scale in (0.0, -0.3, 4.0, 1e-6):

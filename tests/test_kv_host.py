@@ -108,7 +108,7 @@ def test_attn_checks(mq_lib):
                    (dict(q=0), m.MQ_ERR_INVALID_ARG), (dict(tok_start=0), m.MQ_ERR_INVALID_ARG),
                    (dict(q=0x1008), m.MQ_ERR_ALIGN), (dict(out=0x2008), m.MQ_ERR_ALIGN),
                    (dict(mask=0x5004), m.MQ_ERR_ALIGN), (dict(n_heads=1028, q_ld=2**20, out_ld=2**20), m.MQ_ERR_UNSUPPORTED),
-                   (dict(n_tokens=0, q=0), m.MQ_OK)):
+                   (dict(max_len=2**31 - 1, max_tokens=64), m.MQ_ERR_UNSUPPORTED), (dict(n_tokens=0, q=0), m.MQ_OK)):
         assert m.mq_attn_tree(c, attn(m, **kw), 0x9000, 2**40) == st, kw
     assert m.mq_attn_tree(c, attn(m), 0, 2**40) == m.MQ_ERR_INVALID_ARG
     assert m.mq_attn_tree(c, attn(m), 0x9010, 2**40) == m.MQ_ERR_ALIGN
