@@ -58,6 +58,25 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16u(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+
 __device__ __forceinline__ int load_acquire(const int* p)
 {
     int v;
@@ -177,29 +196,58 @@ __device__ __noinline__ void drop_values(uint8_t* blk, int r0)
     __syncwarp();
 }
 
+// A lane's places in a tile of the warp's rows r0.. of a block, in bytes from
+// the block's start (the rows 8 further have the same permutation, so their
+// places are constants away).
+template <int D, bool Q8>
+struct TilePlaces {
+    using B = KvBlock<D, Q8>;
+    uint32_t k;       // first 16-byte run of K row r0 + g; the next is at ^ 16 (where there is one)
+    uint32_t v0, v1;  // run of V rows r0 + 2t and r0 + 2t + 1
+    uint32_t sk, sv;  // q8_0: scales of those K and V rows
+    __device__ __forceinline__ TilePlaces(int r0, int g, int t)
+    {
+        const int ra = r0 + g, rv = r0 + 2 * t;
+        if (Q8) {
+            k = B::chunk(ra, (D / 64) * t);
+            v0 = B::kVOff + B::chunk(rv, D == 128 ? g : g >> 1) + (D == 128 ? 0 : (g & 1) * 8);
+            v1 = B::kVOff + B::chunk(rv + 1, D == 128 ? g : g >> 1) + (D == 128 ? 0 : (g & 1) * 8);
+            sk = B::kScK + (ra * (D / 32) + (D == 128 ? t : t >> 1)) * 2;
+            sv = B::kScK + B::kScBytes + (rv * (D / 32) + (D == 128 ? g >> 1 : g >> 2)) * 2;
+        } else {
+            k = B::chunk(ra, 2 * t);
+            v0 = B::kVOff + B::chunk(rv, g);
+            v1 = B::kVOff + B::chunk(rv + 1, g);
+            sk = sv = 0;
+        }
+    }
+};
+
 // tail: the tile reaches past the context, so what a row sees is tested key by key
 template <int D, bool Q8, int NT>
-__device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const uint32_t (&q)[NT][D / 16][2],
-                                          float scale_log2, RowState<D, Q8, NT>& st, int ctx, int len,
-                                          const uint64_t* row_mask, bool tail)
+__device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const TilePlaces<D, Q8>& at,
+                                          const uint32_t (&q)[NT][D / 16][2], float scale_log2,
+                                          RowState<D, Q8, NT>& st, int ctx, int len, const uint64_t* row_mask, bool tail)
 {
     using B = KvBlock<D, Q8>;
+    constexpr int k8 = 8 * B::kRow;          // eight rows on
+    constexpr int s8 = 8 * (D / 32) * 2;     // their scales
+    constexpr int kPlane = kKvPage * 128;    // f16: the next 64 values
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t base = smem_u32(blk);
     // ---- S^T
     float s[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-    const int ra = r0 + g, rb = ra + 8;
     if constexpr (Q8) {
-        const __half* const sc = reinterpret_cast<const __half*>(blk + B::kScK);
-        constexpr int LD = D / 64;  // 16-byte chunks of a lane per row
-        const int sb = D == 128 ? t : t >> 1;
-        const __half2 da = __half2half2(sc[ra * (D / 32) + sb]), db = __half2half2(sc[rb * (D / 32) + sb]);
+        const uint32_t da = lds16u(base + at.sk) * 0x10001u, db = lds16u(base + at.sk + s8) * 0x10001u;
+        constexpr int LD = D / 64;  // 16-byte runs of a lane per row
 #pragma unroll
         for (int h = 0; h < LD; ++h) {
-            const uint4 xa = lds16(blk + B::chunk(ra, LD * t + h)), xb = lds16(blk + B::chunk(rb, LD * t + h));
+            const uint32_t ka = (base + at.k) ^ (h << 4);  // blocks start at multiples of 128
+            const uint4 xa = lds128(ka), xb = lds128(ka + k8);
             const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -214,8 +262,8 @@ __device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const 
     } else {
 #pragma unroll
         for (int h = 0; h < D / 32; ++h) {  // plane h/2, chunk 2t + h%2: 8 values, two MMA steps
-            const int c = 8 * (h >> 1) + 2 * t + (h & 1);
-            const uint4 xa = lds16(blk + B::chunk(ra, c)), xb = lds16(blk + B::chunk(rb, c));
+            const uint32_t ka = ((base + at.k) ^ ((h & 1) << 4)) + (h >> 1) * kPlane;
+            const uint4 xa = lds128(ka), xb = lds128(ka + k8);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 mma16816(s[n], xa.x, xb.x, xa.y, xb.y, q[n][2 * h][0], q[n][2 * h][1]);
@@ -268,8 +316,6 @@ __device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const 
         mma16816(st.l[n], one, one, one, one, pb[n][0], pb[n][1]);
     }
     // ---- O^T: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the tile
-    const int k0 = r0 + 2 * t;
-    const uint8_t* const vb = blk + B::kVOff;
     if (tail) {
         if (clean_values<D, Q8>(blk, r0, key0, len)) {
 #pragma unroll 1
@@ -302,23 +348,21 @@ __device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const 
         for (int n = 0; n < NT; ++n) mma16816(st.o[n][i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
     };
     if constexpr (Q8) {
-        const __half* const sc = reinterpret_cast<const __half*>(blk + B::kScK + B::kScBytes);
-        const int sb = D == 128 ? g >> 1 : g >> 2;
-        constexpr int SL = D / 32;
-        const __half2 d01 = __halves2half2(sc[k0 * SL + sb], sc[(k0 + 1) * SL + sb]);
-        const __half2 d23 = __halves2half2(sc[(k0 + 8) * SL + sb], sc[(k0 + 9) * SL + sb]);
+        const uint32_t sv = base + at.sv;
+        const uint32_t d01 = __byte_perm(lds16u(sv), lds16u(sv + (D / 32) * 2), 0x5410);
+        const uint32_t d23 = __byte_perm(lds16u(sv + s8), lds16u(sv + s8 + (D / 32) * 2), 0x5410);
         constexpr int NW = D / 32;  // words (4 head values) of a lane
         uint32_t v0[NW], v1[NW], v2[NW], v3[NW];
-        auto load = [&](int r, uint32_t(&v)[NW]) {
+        auto load = [&](uint32_t a, uint32_t(&v)[NW]) {
             if constexpr (D == 128) {
-                const uint4 x = lds16(vb + B::chunk(r, g));
+                const uint4 x = lds128(a);
                 v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
             } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(vb + B::chunk(r, g >> 1) + (g & 1) * 8);
+                const uint2 x = lds64(a);
                 v[0] = x.x, v[1] = x.y;
             }
         };
-        load(k0, v0), load(k0 + 1, v1), load(k0 + 8, v2), load(k0 + 9, v3);
+        load(base + at.v0, v0), load(base + at.v1, v1), load(base + at.v0 + k8, v2), load(base + at.v1 + k8, v3);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             const uint32_t pl = __byte_perm(v0[w], v1[w], 0x5140), ph = __byte_perm(v0[w], v1[w], 0x7362);
@@ -331,8 +375,8 @@ __device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const 
     } else {
 #pragma unroll
         for (int pl = 0; pl < D / 64; ++pl) {
-            const uint4 x0 = lds16(vb + B::chunk(k0, 8 * pl + g)), x1 = lds16(vb + B::chunk(k0 + 1, 8 * pl + g));
-            const uint4 x2 = lds16(vb + B::chunk(k0 + 8, 8 * pl + g)), x3 = lds16(vb + B::chunk(k0 + 9, 8 * pl + g));
+            const uint32_t va = base + at.v0 + pl * kPlane, vb = base + at.v1 + pl * kPlane;
+            const uint4 x0 = lds128(va), x1 = lds128(vb), x2 = lds128(va + k8), x3 = lds128(vb + k8);
             const uint32_t v0[4] = {x0.x, x0.y, x0.z, x0.w}, v1[4] = {x1.x, x1.y, x1.z, x1.w};
             const uint32_t v2[4] = {x2.x, x2.y, x2.z, x2.w}, v3[4] = {x3.x, x3.y, x3.z, x3.w};
 #pragma unroll
@@ -378,8 +422,8 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
     __shared__ AttnSegment split_s[2];
     __shared__ uint64_t mask_s[kSegs][RT];
     __shared__ float m_s[kWarps][RT], l_s[kWarps][RT], sum_s[RT];
-    __shared__ int2 at_s;
-    __shared__ int scratch[kWarps + 1], bad_s[kMaxStages], seen_s[kMaxStages], ok_s[kWarps], pages_bad_s[kWarps], last_s[2], gone_s;
+    __shared__ int2 at_s, scratch[kWarps + 1];
+    __shared__ int bad_s[kMaxStages], seen_s[kMaxStages], ok_s[kWarps], pages_bad_s[kWarps], last_s[2], gone_s;
     __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -406,6 +450,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
 
     // one outcome for the whole warp
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.limit_ns));
         if (!ok) abort_flag = 1;
         return ok;
@@ -414,11 +459,14 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
     if (warp == kWarps) {
         // ---- producer: lane 0 waits and copies, the warp reads page numbers 32 at a time
         AttnRange w = rg;
-        AttnSegment g;
-        int at = rg.first, it = 0, sg = 0, splits = 0;
-        bool ok = true;
-        for (; ok && attn_next(p, RT, &w, &at, &g); ++sg) {
-            const int ss = sg % kSegs, rows = min(RT, g.T * p.group - g.row0);
+        AttnSegment g = {};
+        int at = rg.first, it = 0, s = 0, sg = 0, splits = 0;
+        uint32_t phase = 0;
+        bool ok = true, more = true;
+        for (; ok && more; ++sg) {
+            more = attn_next(p, RT, &w, &at, &g);
+            if (!more) g.n = g.T = 0;
+            const int ss = sg % kSegs, rows = more ? min(RT, g.T * p.group - g.row0) : 0;
             const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0;
             int32_t page_l = lane < g.n ? __ldg(table + lane) : 0;
             uint64_t bits = 0;
@@ -426,7 +474,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
             if (lane < rows) bits = p.a.mask ? __ldg(p.a.mask + g.t0 + node) : ~0ull >> (63 - node);
             if (sg >= kSegs) ok = wait_all(&seg_empty[ss], uint32_t(sg / kSegs - 1) & 1u);
             if (!ok) break;
-            const int split = g.n_ctas > 1 ? splits++ : -1;
+            const int split = more && g.n_ctas > 1 ? splits++ : -1;
             if (lane < RT) mask_s[ss][lane] = bits;
             if (lane == 0) {
                 seg_s[ss].g = g;
@@ -448,9 +496,8 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
                 if (i0 + 32 + lane < g.n) page_l = __ldg(table + i0 + 32 + lane);
                 const int m = min(32, g.n - i0);
                 for (int i = 0; i < m; ++i, ++it) {
-                    const int s = it % stages;
                     const int32_t page = __shfl_sync(0xffffffffu, page_now, i);
-                    if (it >= stages) ok = wait_all(&empty[s], uint32_t(it / stages - 1) & 1u);
+                    if (it >= stages) ok = wait_all(&empty[s], phase ^ 1u);
                     if (!ok) break;
                     if (lane == 0) {
                         const bool bad = page < 0 || page >= p.c.n_pages;  // table entries are not trusted
@@ -464,6 +511,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
                                           &full[s]);
                         }
                     }
+                    if (++s == stages) s = 0, phase ^= 1u;
                 }
             }
         }
@@ -488,18 +536,20 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
     // ---- consumers
     const int team = warp / kTeam, wi = warp % kTeam, g8 = lane >> 2, t4 = lane & 3;
     auto wait_seen = [&](int* word, int value) {
-        bool ok = load_acquire(word) >= value;
+        bool ok = __all_sync(0xffffffffu, load_acquire(word) >= value);
         if (!ok) {
             const uint64_t t0 = global_timer_ns();
-            while (!(ok = load_acquire(word) >= value) && global_timer_ns() - t0 < p.limit_ns) {}
+            do {
+                ok = __all_sync(0xffffffffu, load_acquire(word) >= value);
+            } while (__any_sync(0xffffffffu, !ok && global_timer_ns() - t0 < p.limit_ns));
         }
-        ok = __all_sync(0xffffffffu, ok);
         if (!ok) abort_flag = 1;
         return ok;
     };
-    int it = 0, done = rg.first, splits = 0;
+    const TilePlaces<D, Q8> places(16 * wi, g8, t4);
+    int it = 0, splits = 0;
     bool all_ok = true;
-    for (int sg = 0; done < rg.last; ++sg) {
+    for (int sg = 0;; ++sg) {
         const int ss = sg % kSegs;
         bool ok = wait_all(&seg_full[ss], uint32_t(sg / kSegs) & 1u);
         const AttnSegment& g = seg_s[ss].g;  // stays until this warp's arrival at seg_empty
@@ -524,26 +574,29 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
             }
         }
         bool bad = false;
+        int s = (it + team) % stages;
+        uint32_t phase = uint32_t((it + team) / stages) & 1u;
 #pragma unroll 1
         for (int i = team; ok && i < seg_n; i += C::kTeams) {
-            const int n = it + i, s = n % stages;
+            const int n = it + i;
             // The stage's previous use was another team's page, which may not even have
             // landed; a wait by parity tells two successive uses apart only, so that team's
             // word that it has comes first.
             ok = n < stages || wait_seen(&seen_s[s], n - stages + 1);
-            ok = ok && wait_all(&full[s], uint32_t(n / stages) & 1u);
+            ok = ok && wait_all(&full[s], phase);
             if (ok && wi == 0 && lane == 0) store_release(&seen_s[s], n + 1);
             if (!ok) break;
             bad |= bad_s[s] != 0;
             uint8_t* const blk = ring + s * B::kBytes;
             const int key0 = first_key + i * kKvPage;
             if (key0 < len)
-                rows_tile<D, Q8, NT>(blk, 16 * wi, key0, q, p.scale_log2, st, ctx, len, mask_s[ss], key0 + 16 > ctx);
+                rows_tile<D, Q8, NT>(blk, 16 * wi, key0, places, q, p.scale_log2, st, ctx, len, mask_s[ss], key0 + 16 > ctx);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
+            s += C::kTeams;
+            if (s >= stages) s -= stages, phase ^= 1u;
         }
         it += seg_n;
-        done += seg_n;
 
         // ---- join the warps that had pages: each leaves its tiles as it holds them
         float* const mine = out_s + warp * S::kWarpOut;
@@ -570,7 +623,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
         const int flags = lane < kWarps ? (ok_s[lane] ? 0 : 1) | (pages_bad_s[lane] ? 2 : 0) : 0;
         all_ok = !__any_sync(0xffffffffu, flags & 1);
         const bool seg_bad = __any_sync(0xffffffffu, flags & 2);
-        if (!all_ok) break;
+        if (!all_ok || seg_n == 0) break;  // failed, or the end
         const int split = seg_s[ss].split, rows = min(RT, g.T * p.group - g.row0);
         const int nw = min(C::kTeams, seg_n) * kTeam;  // warps that had pages
         float* const slot = p.parts + (int64_t(blockIdx.x) * 2 + g.slot) * attn_slot_floats(RT, D);

@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(256)
         if (!Q8) {
             out[ch] = v;
         } else {
-            const __half2 d = __half2half2(*reinterpret_cast<const __half*>(
-                blk + B::kScK + is_v * B::kScBytes + (r * (D / 32) + (ch >> 1)) * 2));
+            const uint32_t d = *reinterpret_cast<const uint16_t*>(blk + B::kScK + is_v * B::kScBytes +
+                                                                  (r * (D / 32) + (ch >> 1)) * 2) * 0x10001u;
             uint32_t u[8];
             const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -22,6 +22,8 @@
 
 namespace mq {
 
+constexpr int kAttnGroupCost = 3;
+
 struct AttnParams {
     mq_attn_args a;
     KvView c;
@@ -50,16 +52,17 @@ __device__ __forceinline__ bool attn_seq(const AttnParams& p, int s, AttnSeq* q,
     return T > 0 && !*bad;
 }
 
-// units of sequence s with row blocks of RT rows
-__device__ __forceinline__ int attn_units(const AttnParams& p, const AttnSeq& q, int RT)
+// groups of sequence s with row blocks of RT rows; each has q.pages + (the group cost) units
+__device__ __forceinline__ int attn_groups(const AttnParams& p, const AttnSeq& q, int RT)
 {
-    return q.pages * p.c.n_kv_heads * ((q.T * p.group + RT - 1) / RT);
+    return p.c.n_kv_heads * ((q.T * p.group + RT - 1) / RT);
 }
 
 // The cut of the line, and where this CTA's stretch starts.
 struct AttnRange {
     int total, ctas;  // all units; the CTAs that take part (each has a unit at least)
     int quot, rem;    // total / ctas, total % ctas
+    int cost;         // units of a group beyond its pages
     int first, last;  // this CTA's units
     int seq;          // sequence that the walk is at, and its first unit
     int seq_first;
@@ -71,48 +74,53 @@ struct AttnRange {
     }
 };
 
-// Called by all threads of the CTA; scratch: an int per warp.
-__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status, int* scratch, int2* at_s)
+// Called by all threads of the CTA; scratch: an int2 per warp.
+__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status, int2* scratch, int2* at_s)
 {
     const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.c.n_seqs + nthr - 1) / nthr, s0 = min(tid * per, p.c.n_seqs), s1 = min(s0 + per, p.c.n_seqs);
-    int mine = 0;
+    int2 mine = make_int2(0, 0);  // pages of all groups, groups
     bool any_bad = false;
     for (int s = s0; s < s1; ++s) {
         AttnSeq q;
         bool bad;
-        if (attn_seq(p, s, &q, &bad)) mine += attn_units(p, q, RT);
+        if (attn_seq(p, s, &q, &bad)) {
+            const int n = attn_groups(p, q, RT);
+            mine.x += n * q.pages;
+            mine.y += n;
+        }
         any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-    int incl = mine;
+    int2 incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+        if (lane >= o) incl.x += x, incl.y += y;
     }
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
     AttnRange r;
-    int before = 0;
-    r.total = 0;
+    int2 before = make_int2(0, 0), total = before;
     for (int w = 0; w < nthr / 32; ++w) {
-        if (w == warp) before = r.total;
-        r.total += scratch[w];
+        if (w == warp) before = total;
+        total.x += scratch[w].x, total.y += scratch[w].y;
     }
+    r.cost = total.x > int(gridDim.x) ? kAttnGroupCost : 0;
+    r.total = total.x + total.y * r.cost;
     r.ctas = min(r.total, int(gridDim.x));
     const int c = blockIdx.x;
     r.quot = r.ctas ? r.total / r.ctas : 0;
     r.rem = r.total - r.quot * r.ctas;
     r.first = c < r.ctas ? r.begin(c) : r.total;
     r.last = c < r.ctas ? r.begin(c + 1) : r.total;
-    int at = before + incl - mine;
-    if (r.first >= at && r.first < at + mine) {
+    int at = before.x + incl.x - mine.x + (before.y + incl.y - mine.y) * r.cost;
+    if (r.first >= at && r.first < at + mine.x + mine.y * r.cost) {
         for (int s = s0; s < s1; ++s) {
             AttnSeq q;
             bool bad;
             if (!attn_seq(p, s, &q, &bad)) continue;
-            const int u = attn_units(p, q, RT);
+            const int u = attn_groups(p, q, RT) * (q.pages + r.cost);
             if (r.first < at + u) {
                 *at_s = make_int2(s, at);
                 break;
@@ -130,7 +138,7 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, uns
 struct AttnSegment {
     int seq, t0, T, ctx;
     int head, row0;   // key/value head; first query row of the block
-    int page0, n;     // its pages page0 .. page0 + n - 1
+    int page0, n;     // its pages page0 .. page0 + n - 1; n = 0: the stretch is done
     int group_index;  // of the counters
     int cta0, n_ctas; // the CTAs that share the group
     int slot0;        // workspace slot of the first of them (the others use 0)
@@ -138,37 +146,42 @@ struct AttnSegment {
 };
 
 // The next segment of a CTA's stretch, which starts at unit *at of sequence
-// w->seq or a later one; *at moves past it.
+// w->seq or a later one; *at moves past it.  False: there is none.
 __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange* w, int* at, AttnSegment* g)
 {
-    const int u = *at;
-    if (u >= w->last) return false;
-    AttnSeq q;
-    bool bad;
-    int units = 0;
-    for (;; ++w->seq, w->seq_first += units) {
-        if (w->seq >= p.c.n_seqs) return false;  // not reached unless the lengths change under the call
-        units = attn_seq(p, w->seq, &q, &bad) ? attn_units(p, q, RT) : 0;
-        if (u < w->seq_first + units) break;
+    for (int u = *at; u < w->last;) {
+        AttnSeq q;
+        bool bad;
+        const int units = attn_seq(p, w->seq, &q, &bad) ? attn_groups(p, q, RT) * (q.pages + w->cost) : 0;
+        if (u >= w->seq_first + units) {
+            w->seq_first += units;
+            if (++w->seq >= p.c.n_seqs) return false;  // not reached unless the lengths change under the call
+            continue;
+        }
+        const int blocks = (q.T * p.group + RT - 1) / RT, span = q.pages + w->cost;
+        const int k = (u - w->seq_first) / span;  // group within the sequence
+        const int g0 = w->seq_first + k * span, g1 = g0 + q.pages;
+        if (u >= g1) {
+            u = g0 + span;
+            continue;
+        }
+        g->seq = w->seq;
+        g->t0 = q.t0, g->T = q.T, g->ctx = q.ctx;
+        g->head = k / blocks;
+        g->row0 = (k - g->head * blocks) * RT;
+        g->page0 = u - g0;
+        g->n = min(g1, w->last) - u;
+        const int most = (p.a.max_tokens * p.group + RT - 1) / RT;
+        g->group_index = (w->seq * p.c.n_kv_heads + g->head) * most + k - g->head * blocks;
+        const bool whole = g0 >= w->first && g1 <= w->last;
+        g->cta0 = whole ? int(blockIdx.x) : w->owner(g0);
+        g->n_ctas = whole ? 1 : w->owner(g1 - 1) - g->cta0 + 1;
+        g->slot0 = g0 > w->begin(g->cta0) ? 1 : 0;
+        g->slot = u > w->first ? 1 : 0;
+        *at = u + g->n;
+        return true;
     }
-    const int blocks = (q.T * p.group + RT - 1) / RT;
-    const int k = (u - w->seq_first) / q.pages;  // group within the sequence
-    const int g0 = w->seq_first + k * q.pages, g1 = g0 + q.pages;
-    g->seq = w->seq;
-    g->t0 = q.t0, g->T = q.T, g->ctx = q.ctx;
-    g->head = k / blocks;
-    g->row0 = (k - g->head * blocks) * RT;
-    g->page0 = u - g0;
-    g->n = min(g1, w->last) - u;
-    const int most = (p.a.max_tokens * p.group + RT - 1) / RT;
-    g->group_index = (w->seq * p.c.n_kv_heads + g->head) * most + k - g->head * blocks;
-    const bool whole = g0 >= w->first && g1 <= w->last;
-    g->cta0 = whole ? int(blockIdx.x) : w->owner(g0);
-    g->n_ctas = whole ? 1 : w->owner(g1 - 1) - g->cta0 + 1;
-    g->slot0 = g0 > w->begin(g->cta0) ? 1 : 0;
-    g->slot = u > w->first ? 1 : 0;
-    *at = u + g->n;
-    return true;
+    return false;
 }
 
 // A segment's results in the workspace: m[RT], l[RT] (l < 0 in row 0: the

@@ -55,13 +55,14 @@ inline KvView kv_view(const mq_kv_cache& c)
 }
 
 // two codes, each in the low byte of a half of magic 0x64 (1024 + code + 128),
-// to f16(scale * code): the subtraction is exact, the product rounds once
-__device__ __forceinline__ uint32_t kv_pair(uint32_t u, __half2 scale)
+// to f16(scale * code), scale as a pair: the subtraction is exact, the product rounds once
+__device__ __forceinline__ uint32_t kv_pair(uint32_t u, uint32_t scale)
 {
-    const uint32_t bias = 0x64806480u;  // 1024 + 128
-    const __half2 h = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&bias)),
-                              scale);
-    return *reinterpret_cast<const uint32_t*>(&h);
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tsub.rn.f16x2 t, %1, %2;\n\tmul.rn.f16x2 %0, t, %3;\n\t}"
+        : "=r"(r)
+        : "r"(u), "r"(0x64806480u), "r"(scale));  // 1024 + 128
+    return r;
 }
 
 // one element of a block as fp32 (rare paths)
