@@ -8,25 +8,29 @@
 // What bounds it is the cache's bytes, each of which is used once; the query
 // rows of a key/value head (8 or 16 of them, tokens x group) ride along.  So:
 // * one CTA per SM and an equal share of all pages for each (mq_attn.cuh);
-//   a producer lane brings whole (page, head) blocks by one bulk copy each
+//   a producer warp brings whole (page, head) blocks by one bulk copy each
 //   into a ring that fills the shared memory, and runs ahead over segments;
-// * a page's 64 keys are four tiles of 16, one per warp of a team; the teams
-//   take a segment's pages in turn;
+// * the teams of four warps take the CTA's pages in turn.  In a page's 64 keys
+//   each warp forms the scores of 16; the probabilities go round the team
+//   through shared memory, and each warp sums a quarter of the head's values
+//   over all 64, so a team holds one set of outputs, not four;
 // * both products are formed transposed, keys and head values on the MMA's
 //   16-row side and the query rows on its 8-column side, so 7 rows of a group
 //   of 7 fill it: S^T[key][row] = K q^T, O^T[d][row] = V^T P^T.  The inner
 //   index of an MMA may be permuted freely, so a lane takes its K values as
-//   16-byte runs of two rows, and its V values as 16-byte runs of the four
-//   keys that its share of P needs; S^T becomes P's operand by one 8x8
-//   transpose per 8 keys.  q8_0 codes become f16 in registers on the way
-//   (byte permute, exact subtraction, one rounded product with the scale);
+//   16-byte runs of two rows; S^T becomes P's operand by one 8x8 transpose per
+//   8 keys.  q8_0 codes become f16 in registers on the way (byte permute,
+//   exact subtraction, one rounded product with the scale);
 // * the probabilities are rounded to f16 for the second product (2^-11 each,
 //   the output's own rounding), scaled by 2^10 so that a key at 2^-24 of the
 //   largest still has a normal number, and their sum is formed from the same
 //   rounded numbers by an MMA with ones, so the weights add up to one;
 // * the maximum is raised only when a score passes it by more than 5 (in
 //   powers of two; 2^15 still fits f16), which after the first tiles is rare:
-//   a vote per tile instead of a maximum over its lanes and a rescaling.
+//   a predicate on the barrier that the team needs anyway, instead of a
+//   maximum over its lanes and a rescaling;
+// * a team that is done with a segment leaves its outputs and goes on to the
+//   next; the last of them to leave joins them.  Nothing waits for all teams.
 // Scores, maxima, sums and outputs are fp32 throughout.
 #include "mq_attn.cuh"
 
@@ -34,18 +38,38 @@ namespace mq {
 
 namespace {
 
-constexpr int kTeam = 4;       // warps that share a page
-constexpr int kSegs = 4;       // segment descriptors in flight
+constexpr int kTeam = 4;  // warps that share a page
+constexpr int kSegs = 4;  // segment descriptors in flight
 constexpr int kMaxStages = 16;
-constexpr float kRaise = 5.0f, kShift = 10.0f;
+constexpr int kRowsSmem = 218 * 1024;  // dynamic; the kernel's static arrays come on top
+constexpr float kRaise = 5.0f, kShift = 10.0f, kLowest = -3.402823466e38f;
 
-// query rows 8*NT.  Registers set the warps: with the producer 13 (NT = 1) may have 128 each, 9 (NT = 2) 168
-template <int NT>
+// what the producer hands over with a segment, besides its query rows
+struct RowsSegment {
+    AttnSegment g;
+    int it0;    // number of its first page among the CTA's
+    int split;  // index among the CTA's groups that it shares with others (at most two), or -1
+                // (behind the last segment: how many there were)
+};
+
+// query rows 8*NT
+template <int D, bool Q8, int NT>
 struct RowsCfg {
+    using B = KvBlock<D, Q8>;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kTeams = NT == 1 ? 3 : 2;
+    // registers allow 16 warps of 8 rows or 12 of 16; the ring of 32 KB blocks is too short for four teams
+    static constexpr int kTeams = D == 128 && (NT == 2 || !Q8) ? 3 : 4;
     static constexpr int kWarps = kTeams * kTeam;
     static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kSlice = D / kTeam;                     // head values that a warp sums
+    static constexpr int kQ = kRows * D * 2;                     // a segment's query rows
+    static constexpr int kP = NT * kTeam * 32 * 8;               // a page's probabilities
+    static constexpr int kOut = kRows * D * 4;                   // a team's outputs
+    static constexpr int kFixed = kSegs * kQ + kTeams * 2 * kP + 2 * kTeams * kOut;
+    static constexpr int kFit = (kRowsSmem - kFixed) / B::kBytes;
+    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+    static constexpr int kSmem = kStages * B::kBytes + kFixed;
+    static_assert(kStages > kTeams, "the teams' pages and one on its way");
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -70,11 +94,23 @@ __device__ __forceinline__ uint2 lds64(uint32_t a)
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
 __device__ __forceinline__ uint32_t lds16u(uint32_t a)
 {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
     return v;
+}
+
+// more bytes to come in the barrier's phase, without an arrival
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ int load_acquire(const int* p)
@@ -110,27 +146,32 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return r;
 }
 
+// barrier over n threads; true for all of them where it was for one
+__device__ __forceinline__ bool barrier_any(int id, int n, bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(uint32_t(v)), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
 constexpr uint32_t k64 = 0x64646464u;
 
-// Lane (g = lane/4, t = lane%4).  K values of MMA step j: head values kdim(t, j) + 0..3;
-// output tile i: head values vdim(g, i), +1.
+// Lane (g = lane/4, t = lane%4).  K values of MMA step j: head values kdim(t, j) + 0..3.
 template <int D, bool Q8>
 __device__ __forceinline__ constexpr int kdim(int t, int j)
 {
     return Q8 && D == 128 ? 32 * t + 4 * j : 64 * (j / 4) + 16 * t + 4 * (j % 4);
 }
-template <int D, bool Q8>
-__device__ __forceinline__ constexpr int vdim(int g, int i)
-{
-    return Q8 && D == 128 ? 16 * g + 2 * i : 64 * (i / 4) + 8 * g + 2 * (i % 4);
-}
 
-// ---- one tile of 16 keys ----------------------------------------------------------------
-template <int D, bool Q8, int NT>
+template <int D, int NT>
 struct RowState {
-    float o[NT][D / 16][4];
-    float l[NT][4];      // every key row of the ones-product holds the same sums
-    float m[NT][2];      // running maxima of rows 2t, 2t + 1
+    float o[NT][D / 64][4];  // values of output tile i: slice + (D/32) g + 2i, +1, of rows 2t, 2t + 1
+    float l[NT][4];          // sums over the warp's own keys (every row of the ones-product is the same)
+    float m[NT][2];          // running maxima of rows 2t, 2t + 1, the same in the whole team
 };
 
 // A tile that reaches past the context, before its values are used: rows past
@@ -196,46 +237,62 @@ __device__ __noinline__ void drop_values(uint8_t* blk, int r0)
     __syncwarp();
 }
 
-// A lane's places in a tile of the warp's rows r0.. of a block, in bytes from
-// the block's start (the rows 8 further have the same permutation, so their
-// places are constants away).
+// A lane's places in a block, in bytes from its start, for the scores of rows
+// r0.. and the values of slice w of rows 0..15 (the rows 8 and 16 further have
+// the same permutation, so their places are constants away).
 template <int D, bool Q8>
-struct TilePlaces {
+struct PagePlaces {
     using B = KvBlock<D, Q8>;
-    uint32_t k;       // first 16-byte run of K row r0 + g; the next is at ^ 16 (where there is one)
-    uint32_t v0, v1;  // run of V rows r0 + 2t and r0 + 2t + 1
-    uint32_t sk, sv;  // q8_0: scales of those K and V rows
-    __device__ __forceinline__ TilePlaces(int r0, int g, int t)
+    uint32_t k, sk;   // first 16-byte run of K row r0 + g (the next is at ^ 16), its scale (q8_0)
+    uint32_t v0, v1;  // the lane's D/32 values of V rows 2t and 2t + 1
+    uint32_t sv;      // q8_0: scales of V rows 2 * lane, + 1
+    __device__ __forceinline__ PagePlaces(int r0, int w, int lane)
     {
-        const int ra = r0 + g, rv = r0 + 2 * t;
+        const int g = lane >> 2, t = lane & 3, ra = r0 + g;
         if (Q8) {
             k = B::chunk(ra, (D / 64) * t);
-            v0 = B::kVOff + B::chunk(rv, D == 128 ? g : g >> 1) + (D == 128 ? 0 : (g & 1) * 8);
-            v1 = B::kVOff + B::chunk(rv + 1, D == 128 ? g : g >> 1) + (D == 128 ? 0 : (g & 1) * 8);
             sk = B::kScK + (ra * (D / 32) + (D == 128 ? t : t >> 1)) * 2;
-            sv = B::kScK + B::kScBytes + (rv * (D / 32) + (D == 128 ? g >> 1 : g >> 2)) * 2;
+            const int d = w * (D / 4) + g * (D / 32);
+            v0 = B::kVOff + B::chunk(2 * t, d >> 4) + (d & 15);
+            v1 = B::kVOff + B::chunk(2 * t + 1, d >> 4) + (d & 15);
+            sv = B::kScK + B::kScBytes + (2 * lane * (D / 32) + (w * (D / 4) >> 5)) * 2;
         } else {
             k = B::chunk(ra, 2 * t);
-            v0 = B::kVOff + B::chunk(rv, g);
-            v1 = B::kVOff + B::chunk(rv + 1, g);
+            const int d = w * (D / 4) + g * (D / 32);
+            v0 = B::kVOff + B::chunk(2 * t, d >> 3) + (d & 7) * 2;
+            v1 = B::kVOff + B::chunk(2 * t + 1, d >> 3) + (d & 7) * 2;
             sk = sv = 0;
         }
     }
 };
 
-// tail: the tile reaches past the context, so what a row sees is tested key by key
+enum { kFlagRaise = 1, kFlagOdd = 2, kFlagFail = 4 };
+
+// a team's words in shared memory
+template <int NT>
+struct TeamWords {
+    float top[kTeam][8 * NT];  // the warps' maxima when the team's is raised
+    int flags;
+    int closed_last;
+};
+
+// ---- one page ------------------------------------------------------------------------------
+// ok: the page is there (false goes round the team, which gives up together).
+// p_at: the team's probabilities of this page (every other page has the other place).
 template <int D, bool Q8, int NT>
-__device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const TilePlaces<D, Q8>& at,
-                                          const uint32_t (&q)[NT][D / 16][2], float scale_log2,
-                                          RowState<D, Q8, NT>& st, int ctx, int len, const uint64_t* row_mask, bool tail)
+__device__ __forceinline__ bool rows_page(bool ok, uint8_t* blk, int wi, int team, int page_key, const PagePlaces<D, Q8>& at,
+                                          const uint32_t (&q)[NT][D / 16][2], float scale_log2, RowState<D, NT>& st,
+                                          int ctx, int len, const uint64_t* row_mask, uint2* p_at, TeamWords<NT>* words)
 {
     using B = KvBlock<D, Q8>;
     constexpr int k8 = 8 * B::kRow;          // eight rows on
     constexpr int s8 = 8 * (D / 32) * 2;     // their scales
     constexpr int kPlane = kKvPage * 128;    // f16: the next 64 values
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, id = 2 + team;
     const uint32_t base = smem_u32(blk);
-    // ---- S^T
+    const int r0 = 16 * wi, key0 = page_key + r0;
+    const bool tail = page_key + kKvPage > ctx;  // visibility is tested key by key
+    // ---- S^T of the warp's 16 keys
     float s[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -271,8 +328,7 @@ __device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const 
             }
         }
     }
-    // ---- softmax numerators
-    bool raise = false;
+    bool raise = false, odd = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -287,40 +343,33 @@ __device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const 
         }
         raise |= fmaxf(s[n][0], s[n][2]) > st.m[n][0] + kRaise || fmaxf(s[n][1], s[n][3]) > st.m[n][1] + kRaise;
     }
-    if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = fmaxf(s[n][e], s[n][e + 2]);
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                const float mn = fmaxf(st.m[n][e], x), f = ex2(st.m[n][e] - mn);
-                st.m[n][e] = mn;
-                st.l[n][e] *= f;
-                st.l[n][e + 2] *= f;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    st.o[n][i][e] *= f;
-                    st.o[n][i][e + 2] *= f;
-                }
-            }
-    }
+    if (tail && ok && key0 < len) odd = clean_values<D, Q8>(blk, r0, key0, len);
+    // ---- softmax numerators, round the team
     uint32_t pb[NT][2];
+    auto numerators = [&]() {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const float m0 = st.m[n][0] - kShift, m1 = st.m[n][1] - kShift;
-        pb[n][0] = transpose8x8(pack_f16(ex2(s[n][0] - m0), ex2(s[n][1] - m1)));
-        pb[n][1] = transpose8x8(pack_f16(ex2(s[n][2] - m0), ex2(s[n][3] - m1)));
-        constexpr uint32_t one = 0x3c003c00u;
-        mma16816(st.l[n], one, one, one, one, pb[n][0], pb[n][1]);
-    }
-    // ---- O^T: keys 2t, 2t + 1, 2t + 8, 2t + 9 of the tile
-    if (tail) {
-        if (clean_values<D, Q8>(blk, r0, key0, len)) {
+        for (int n = 0; n < NT; ++n) {
+            const float m0 = st.m[n][0] - kShift, m1 = st.m[n][1] - kShift;
+            pb[n][0] = transpose8x8(pack_f16(ex2(s[n][0] - m0), ex2(s[n][1] - m1)));
+            pb[n][1] = transpose8x8(pack_f16(ex2(s[n][2] - m0), ex2(s[n][3] - m1)));
+            p_at[(n * kTeam + wi) * 32 + lane] = make_uint2(pb[n][0], pb[n][1]);
+        }
+    };
+    numerators();
+    const int flags = (__any_sync(0xffffffffu, raise) ? kFlagRaise : 0) | (odd ? kFlagOdd : 0) | (ok ? 0 : kFlagFail);
+    if (flags && lane == 0) atomicOr(&words->flags, flags);
+    if (barrier_any(id, 32 * kTeam, flags != 0)) {
+        // ---- rare, and the whole team together
+        const int all = *const_cast<volatile int*>(&words->flags);
+        named_barrier_sync(id, 32 * kTeam);
+        if (wi == 0 && lane == 0) words->flags = 0;
+        if (all & kFlagFail) return false;
+        if (all & kFlagOdd) {
+            // whatever a key's weight is, a value that is not finite makes the outputs of the
+            // rows that see it what it is; then it is dropped, for the rows that do not
 #pragma unroll 1
-            for (int k = 0; k < min(16, len - key0); ++k) {
-                const int j = key0 + k, r = r0 + k;
+            for (int r = 0; r < min(kKvPage, len - page_key); ++r) {
+                const int j = page_key + r;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -328,125 +377,149 @@ __device__ __forceinline__ void rows_tile(uint8_t* blk, int r0, int key0, const 
                         const uint64_t bits = row_mask[8 * n + 2 * t + e];
                         if (!(j < ctx || ((bits >> (j - ctx)) & 1))) continue;
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i)
+                        for (int i = 0; i < D / 64; ++i)
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
-                                const float v = kv_value<D, Q8>(blk, r, vdim<D, Q8>(g, i) + x, 1);
+                                const float v = kv_value<D, Q8>(blk, r, wi * (D / 4) + (D / 32) * g + 2 * i + x, 1);
                                 if (!(v - v == 0.0f)) st.o[n][i][e + 2 * x] += v;
                             }
                     }
             }
-            __syncwarp();
-            drop_values<D, Q8>(blk, r0);
+            named_barrier_sync(id, 32 * kTeam);
+            if (key0 < len) drop_values<D, Q8>(blk, r0);
         }
-        // the next bulk copy into this stage comes after these writes
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-    }
-    auto product = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        if (all & kFlagRaise) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(st.o[n][i], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-    };
-    if constexpr (Q8) {
-        const uint32_t sv = base + at.sv;
-        const uint32_t d01 = __byte_perm(lds16u(sv), lds16u(sv + (D / 32) * 2), 0x5410);
-        const uint32_t d23 = __byte_perm(lds16u(sv + s8), lds16u(sv + s8 + (D / 32) * 2), 0x5410);
-        constexpr int NW = D / 32;  // words (4 head values) of a lane
-        uint32_t v0[NW], v1[NW], v2[NW], v3[NW];
-        auto load = [&](uint32_t a, uint32_t(&v)[NW]) {
-            if constexpr (D == 128) {
-                const uint4 x = lds128(a);
-                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-            } else {
-                const uint2 x = lds64(a);
-                v[0] = x.x, v[1] = x.y;
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = fmaxf(s[n][e], s[n][e + 2]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                    if (g == 0) words->top[wi][8 * n + 2 * t + e] = x;
+                }
+            named_barrier_sync(id, 32 * kTeam);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mn = st.m[n][e];
+#pragma unroll
+                    for (int w = 0; w < kTeam; ++w) mn = fmaxf(mn, words->top[w][8 * n + 2 * t + e]);
+                    const float f = ex2(st.m[n][e] - mn);
+                    st.m[n][e] = mn;
+                    st.l[n][e] *= f;
+                    st.l[n][e + 2] *= f;
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i) {
+                        st.o[n][i][e] *= f;
+                        st.o[n][i][e + 2] *= f;
+                    }
+                }
+            numerators();
+        }
+        named_barrier_sync(id, 32 * kTeam);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        constexpr uint32_t one = 0x3c003c00u;
+        mma16816(st.l[n], one, one, one, one, pb[n][0], pb[n][1]);
+    }
+    // ---- O^T of the warp's slice over the page's keys, 16 a step: keys 2t, 2t + 1, 2t + 8, 2t + 9
+    uint32_t dv = 0;
+    if (Q8) dv = __byte_perm(lds16u(base + at.sv), lds16u(base + at.sv + (D / 32) * 2), 0x5410);
+#pragma unroll
+    for (int ks = 0; ks < kTeam; ++ks) {
+        if (tail && page_key + 16 * ks >= len) break;  // rows that were not cleaned
+        uint2 p2[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) p2[n] = p_at[(n * kTeam + ks) * 32 + lane];
+        auto product = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(st.o[n][i], a0, a1, a2, a3, p2[n].x, p2[n].y);
         };
-        load(base + at.v0, v0), load(base + at.v1, v1), load(base + at.v0 + k8, v2), load(base + at.v1 + k8, v3);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const uint32_t pl = __byte_perm(v0[w], v1[w], 0x5140), ph = __byte_perm(v0[w], v1[w], 0x7362);
-            const uint32_t rl = __byte_perm(v2[w], v3[w], 0x5140), rh = __byte_perm(v2[w], v3[w], 0x7362);
-            product(2 * w, kv_pair(__byte_perm(pl, k64, 0x4140), d01), kv_pair(__byte_perm(pl, k64, 0x4342), d01),
-                    kv_pair(__byte_perm(rl, k64, 0x4140), d23), kv_pair(__byte_perm(rl, k64, 0x4342), d23));
-            product(2 * w + 1, kv_pair(__byte_perm(ph, k64, 0x4140), d01), kv_pair(__byte_perm(ph, k64, 0x4342), d01),
-                    kv_pair(__byte_perm(rh, k64, 0x4140), d23), kv_pair(__byte_perm(rh, k64, 0x4342), d23));
-        }
-    } else {
-#pragma unroll
-        for (int pl = 0; pl < D / 64; ++pl) {
-            const uint32_t va = base + at.v0 + pl * kPlane, vb = base + at.v1 + pl * kPlane;
-            const uint4 x0 = lds128(va), x1 = lds128(vb), x2 = lds128(va + k8), x3 = lds128(vb + k8);
-            const uint32_t v0[4] = {x0.x, x0.y, x0.z, x0.w}, v1[4] = {x1.x, x1.y, x1.z, x1.w};
-            const uint32_t v2[4] = {x2.x, x2.y, x2.z, x2.w}, v3[4] = {x3.x, x3.y, x3.z, x3.w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                product(4 * pl + w, __byte_perm(v0[w], v1[w], 0x5410), __byte_perm(v0[w], v1[w], 0x7632),
-                        __byte_perm(v2[w], v3[w], 0x5410), __byte_perm(v2[w], v3[w], 0x7632));
+        const uint32_t va = base + at.v0 + 2 * ks * k8, vb = base + at.v1 + 2 * ks * k8;
+        if constexpr (Q8) {
+            const uint32_t d01 = __shfl_sync(0xffffffffu, dv, 8 * ks + t), d23 = __shfl_sync(0xffffffffu, dv, 8 * ks + t + 4);
+            if constexpr (D == 128) {
+                const uint32_t x0 = lds32(va), x1 = lds32(vb), x2 = lds32(va + k8), x3 = lds32(vb + k8);
+                const uint32_t pl = __byte_perm(x0, x1, 0x5140), ph = __byte_perm(x0, x1, 0x7362);
+                const uint32_t rl = __byte_perm(x2, x3, 0x5140), rh = __byte_perm(x2, x3, 0x7362);
+                product(0, kv_pair(__byte_perm(pl, k64, 0x4140), d01), kv_pair(__byte_perm(pl, k64, 0x4342), d01),
+                        kv_pair(__byte_perm(rl, k64, 0x4140), d23), kv_pair(__byte_perm(rl, k64, 0x4342), d23));
+                product(D / 64 - 1, kv_pair(__byte_perm(ph, k64, 0x4140), d01), kv_pair(__byte_perm(ph, k64, 0x4342), d01),
+                        kv_pair(__byte_perm(rh, k64, 0x4140), d23), kv_pair(__byte_perm(rh, k64, 0x4342), d23));
+            } else {
+                const uint32_t pl = __byte_perm(lds16u(va), lds16u(vb), 0x5140);
+                const uint32_t rl = __byte_perm(lds16u(va + k8), lds16u(vb + k8), 0x5140);
+                product(0, kv_pair(__byte_perm(pl, k64, 0x4140), d01), kv_pair(__byte_perm(pl, k64, 0x4342), d01),
+                        kv_pair(__byte_perm(rl, k64, 0x4140), d23), kv_pair(__byte_perm(rl, k64, 0x4342), d23));
+            }
+        } else if constexpr (D == 128) {
+            const uint2 x0 = lds64(va), x1 = lds64(vb), x2 = lds64(va + k8), x3 = lds64(vb + k8);
+            product(0, __byte_perm(x0.x, x1.x, 0x5410), __byte_perm(x0.x, x1.x, 0x7632), __byte_perm(x2.x, x3.x, 0x5410),
+                    __byte_perm(x2.x, x3.x, 0x7632));
+            product(D / 64 - 1, __byte_perm(x0.y, x1.y, 0x5410), __byte_perm(x0.y, x1.y, 0x7632),
+                    __byte_perm(x2.y, x3.y, 0x5410), __byte_perm(x2.y, x3.y, 0x7632));
+        } else {
+            const uint32_t x0 = lds32(va), x1 = lds32(vb), x2 = lds32(va + k8), x3 = lds32(vb + k8);
+            product(0, __byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632), __byte_perm(x2, x3, 0x5410),
+                    __byte_perm(x2, x3, 0x7632));
         }
     }
+    // the next bulk copy into this stage comes after the cleaning's writes
+    if (tail) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    return true;
 }
 
 // ---- the kernel ----------------------------------------------------------------------------
-// what the producer hands over with a segment, besides its query rows
-struct RowsSegment {
-    AttnSegment g;
-    int split;  // index among the CTA's groups that it shares with others (at most two), or -1
-};
-
 template <int D, bool Q8, int NT>
-struct RowsSmem {
-    using B = KvBlock<D, Q8>;
-    using C = RowsCfg<NT>;
-    static constexpr int kQ = C::kRows * D * 2;            // a segment's query rows
-    static constexpr int kTile = 32 * 4 + 4;               // floats of one output tile of a warp, padded
-    static constexpr int kWarpOut = NT * (D / 16) * kTile; // floats of a warp's outputs
-    static constexpr int kFixed = kSegs * kQ + C::kWarps * kWarpOut * 4;
-};
-
-template <int D, bool Q8, int NT>
-__global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
-    attn_rows_kernel(const AttnParams p, const int stages, unsigned* status)
+__global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
+    attn_rows_kernel(const AttnParams p, unsigned* status)
 {
     using B = KvBlock<D, Q8>;
-    using C = RowsCfg<NT>;
-    using S = RowsSmem<D, Q8, NT>;
-    constexpr int RT = C::kRows, kWarps = C::kWarps, kCons = 32 * kWarps;
+    using C = RowsCfg<D, Q8, NT>;
+    constexpr int RT = C::kRows, kTeams = C::kTeams, kWarps = C::kWarps, kCons = 32 * kWarps, kStages = C::kStages;
     extern __shared__ __align__(128) uint8_t sm[];
     uint8_t* const ring = sm;
-    __half* const q_s = reinterpret_cast<__half*>(sm + stages * B::kBytes);
-    float* const out_s = reinterpret_cast<float*>(sm + stages * B::kBytes + kSegs * S::kQ);
-    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], seg_full[kSegs], seg_empty[kSegs];
-    __shared__ __align__(8) uint64_t part_full[2], part_done[2];
+    __half* const q_s = reinterpret_cast<__half*>(sm + kStages * B::kBytes);
+    uint2* const p_s = reinterpret_cast<uint2*>(sm + kStages * B::kBytes + kSegs * C::kQ);
+    float* const out_s = reinterpret_cast<float*>(sm + kStages * B::kBytes + kSegs * C::kQ + kTeams * 2 * C::kP);
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], seg_full[kSegs], seg_empty[kSegs];
+    __shared__ __align__(8) uint64_t out_free[2], part_full[2], part_done[2];
     __shared__ RowsSegment seg_s[kSegs];
     __shared__ AttnSegment split_s[2];
     __shared__ uint64_t mask_s[kSegs][RT];
-    __shared__ float m_s[kWarps][RT], l_s[kWarps][RT], sum_s[RT];
-    __shared__ int2 at_s, scratch[kWarps + 1];
-    __shared__ int bad_s[kMaxStages], seen_s[kMaxStages], ok_s[kWarps], pages_bad_s[kWarps], last_s[2], gone_s;
+    // a segment's teams (every other segment has the other place): maxima, sums, whether there were pages, bad ones
+    __shared__ float m_s[2][kTeams][RT], l_s[2][kTeams][kTeam][RT];
+    __shared__ int had_s[2][kTeams], closed_s[2];
+    __shared__ TeamWords<NT> words_s[kTeams];
+    __shared__ float cm_s[kWarps][RT], cl_s[kWarps][RT];
+    __shared__ int bad_s[kStages], seen_s[kStages], last_s[2];
     __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        abort_flag = 0;
-        gone_s = 0;
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], kTeam);
-            seen_s[s] = 0;
-        }
-        for (int s = 0; s < kSegs; ++s) {
-            mbar_init(&seg_full[s], 1);
-            mbar_init(&seg_empty[s], kWarps);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&part_full[s], kWarps);
-            mbar_init(&part_done[s], 1);
-        }
-        fence_barrier_init();
+    if (threadIdx.x < kStages) {
+        mbar_init(&full[threadIdx.x], 1);
+        mbar_init(&empty[threadIdx.x], kTeam);
+        seen_s[threadIdx.x] = 0;
+    } else if (threadIdx.x >= 32 && threadIdx.x < 32 + kSegs) {
+        mbar_init(&seg_full[threadIdx.x - 32], 1);
+        mbar_init(&seg_empty[threadIdx.x - 32], kWarps);
+    } else if (threadIdx.x >= 64 && threadIdx.x < 66) {
+        const int k = threadIdx.x - 64;
+        mbar_init(&out_free[k], kTeam);
+        mbar_init(&part_full[k], kTeam);
+        mbar_init(&part_done[k], 1);
+        closed_s[k] = 0;
+    } else if (threadIdx.x >= 96 && threadIdx.x < 96 + kTeams) {
+        words_s[threadIdx.x - 96].flags = 0;
+        if (threadIdx.x == 96) abort_flag = 0;
     }
-    const AttnRange rg = attn_range(p, RT, status, scratch, &at_s);  // synchronises the CTA
-    if (rg.first >= rg.last) return;
+    fence_barrier_init();
+    AttnRange w;
+    if (warp == kWarps) w = attn_range(p, RT, status);
+    __syncthreads();
 
     // one outcome for the whole warp
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
@@ -457,10 +530,9 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
     };
 
     if (warp == kWarps) {
-        // ---- producer: lane 0 waits and copies, the warp reads page numbers 32 at a time
-        AttnRange w = rg;
+        // ---- producer: lane 0 copies the pages, the warp reads their numbers 32 at a time
         AttnSegment g = {};
-        int at = rg.first, it = 0, s = 0, sg = 0, splits = 0;
+        int at = w.first, it = 0, s = 0, sg = 0, splits = 0;
         uint32_t phase = 0;
         bool ok = true, more = true;
         for (; ok && more; ++sg) {
@@ -470,34 +542,34 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
             const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0;
             int32_t page_l = lane < g.n ? __ldg(table + lane) : 0;
             uint64_t bits = 0;
-            const int node = (g.row0 + lane) / p.group;
+            const int row = g.row0 + lane, node = attn_row_token(p, row);
             if (lane < rows) bits = p.a.mask ? __ldg(p.a.mask + g.t0 + node) : ~0ull >> (63 - node);
             if (sg >= kSegs) ok = wait_all(&seg_empty[ss], uint32_t(sg / kSegs - 1) & 1u);
             if (!ok) break;
-            const int split = more && g.n_ctas > 1 ? splits++ : -1;
-            if (lane < RT) mask_s[ss][lane] = bits;
-            if (lane == 0) {
-                seg_s[ss].g = g;
-                seg_s[ss].split = split;
-                if (split >= 0) split_s[split] = g;
-            }
+            if (lane == 0) mbar_expect_tx(&seg_full[ss], uint32_t(rows) * D * 2);
             __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&seg_full[ss], uint32_t(rows) * D * 2);
-            __syncwarp();
-            if (lane < rows) {
-                const int row = g.row0 + lane;
+            if (lane < rows)
                 bulk_copy_g2s(q_s + (ss * RT + lane) * D,
                               static_cast<const __half*>(p.a.q) + int64_t(g.t0 + node) * p.a.q_ld +
-                                  (g.head * p.group + row - node * p.group) * D,
+                                  ((g.head - node) * p.group + row) * D,
                               D * 2, &seg_full[ss]);
+            const int split = more && g.n_ctas > 1 ? splits++ : -1;
+            if (lane == 0) {
+                seg_s[ss].g = g;
+                seg_s[ss].it0 = it;
+                seg_s[ss].split = more ? split : splits;
+                if (split >= 0) split_s[split] = g;
             }
+            if (lane < RT) mask_s[ss][lane] = bits;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_full[ss]);
             for (int i0 = 0; ok && i0 < g.n; i0 += 32) {
                 const int32_t page_now = page_l;
                 if (i0 + 32 + lane < g.n) page_l = __ldg(table + i0 + 32 + lane);
                 const int m = min(32, g.n - i0);
                 for (int i = 0; i < m; ++i, ++it) {
                     const int32_t page = __shfl_sync(0xffffffffu, page_now, i);
-                    if (it >= stages) ok = wait_all(&empty[s], phase ^ 1u);
+                    if (it >= kStages) ok = wait_all(&empty[s], phase ^ 1u);
                     if (!ok) break;
                     if (lane == 0) {
                         const bool bad = page < 0 || page >= p.c.n_pages;  // table entries are not trusted
@@ -511,7 +583,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
                                           &full[s]);
                         }
                     }
-                    if (++s == stages) s = 0, phase ^= 1u;
+                    if (++s == kStages) s = 0, phase ^= 1u;
                 }
             }
         }
@@ -524,8 +596,8 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
             }
         }
         // copies still in flight land before the CTA can exit
-        for (int j = it > stages ? it - stages : 0; j < it; ++j)
-            (void)mbar_wait_bounded(&full[j % stages], uint32_t(j / stages) & 1u, p.limit_ns);
+        for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
+            (void)mbar_wait_bounded(&full[j % kStages], uint32_t(j / kStages) & 1u, p.limit_ns);
         for (int j = sg > kSegs ? sg - kSegs : 0; j < sg; ++j)
             (void)mbar_wait_bounded(&seg_full[j % kSegs], uint32_t(j / kSegs) & 1u, p.limit_ns);
         __syncwarp();
@@ -534,7 +606,9 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
     }
 
     // ---- consumers
-    const int team = warp / kTeam, wi = warp % kTeam, g8 = lane >> 2, t4 = lane & 3;
+    const int team = warp / kTeam, wi = warp % kTeam, g8 = lane >> 2, t4 = lane & 3, id = 2 + team;
+    TeamWords<NT>* const words = &words_s[team];
+    const PagePlaces<D, Q8> places(16 * wi, wi, lane);
     auto wait_seen = [&](int* word, int value) {
         bool ok = __all_sync(0xffffffffu, load_acquire(word) >= value);
         if (!ok) {
@@ -546,239 +620,244 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, 1)
         if (!ok) abort_flag = 1;
         return ok;
     };
-    const TilePlaces<D, Q8> places(16 * wi, g8, t4);
-    int it = 0, splits = 0;
-    bool all_ok = true;
+    bool good = true;  // the whole team's
+    int it = team, s = team, splits = 0, flip = 0;
+    uint32_t phase = 0;
     for (int sg = 0;; ++sg) {
-        const int ss = sg % kSegs;
+        const int ss = sg % kSegs, os = sg & 1;
         bool ok = wait_all(&seg_full[ss], uint32_t(sg / kSegs) & 1u);
+        // the outputs' place is free once the segment before the last has been joined
+        if (sg >= 2) ok = wait_all(&out_free[os], uint32_t(sg / 2 - 1) & 1u) && ok;
+        good = !barrier_any(id, 32 * kTeam, !ok);
+        if (!good) break;
         const AttnSegment& g = seg_s[ss].g;  // stays until this warp's arrival at seg_empty
-        const int ctx = g.ctx, len = ctx + g.T, seg_n = g.n, first_key = g.page0 * kKvPage + 16 * wi;
-        RowState<D, Q8, NT> st;
-        uint32_t q[NT][D / 16][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            // rows past the block's hold what was there: they stay in their own columns
-            const __half* const src = q_s + (ss * RT + 8 * n + g8) * D;
-#pragma unroll
-            for (int j = 0; j < D / 16; j += 2) {
-                const uint4 v = *reinterpret_cast<const uint4*>(src + kdim<D, Q8>(t4, j));
-                q[n][j][0] = v.x, q[n][j][1] = v.y, q[n][j + 1][0] = v.z, q[n][j + 1][1] = v.w;
-            }
-            st.m[n][0] = st.m[n][1] = -3.402823466e38f;  // finite: a row without keys keeps zero sums
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                st.l[n][e] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) st.o[n][i][e] = 0.0f;
-            }
+        const int ctx = g.ctx, len = ctx + g.T, end = seg_s[ss].it0 + g.n, first_key = (g.page0 - seg_s[ss].it0) * kKvPage;
+        if (g.n == 0) {
+            splits = seg_s[ss].split;
+            break;
         }
+        const bool had = it < end;
         bool bad = false;
-        int s = (it + team) % stages;
-        uint32_t phase = uint32_t((it + team) / stages) & 1u;
+        if (had) {
+            RowState<D, NT> st;
+            uint32_t q[NT][D / 16][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                // rows past the block's hold what was there: they stay in their own columns
+                const __half* const src = q_s + (ss * RT + 8 * n + g8) * D;
+#pragma unroll
+                for (int j = 0; j < D / 16; j += 2) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + kdim<D, Q8>(t4, j));
+                    q[n][j][0] = v.x, q[n][j][1] = v.y, q[n][j + 1][0] = v.z, q[n][j + 1][1] = v.w;
+                }
+                st.m[n][0] = st.m[n][1] = kLowest;  // finite: a row without keys keeps zero sums
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    st.l[n][e] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i) st.o[n][i][e] = 0.0f;
+                }
+            }
 #pragma unroll 1
-        for (int i = team; ok && i < seg_n; i += C::kTeams) {
-            const int n = it + i;
-            // The stage's previous use was another team's page, which may not even have
-            // landed; a wait by parity tells two successive uses apart only, so that team's
-            // word that it has comes first.
-            ok = n < stages || wait_seen(&seen_s[s], n - stages + 1);
-            ok = ok && wait_all(&full[s], phase);
-            if (ok && wi == 0 && lane == 0) store_release(&seen_s[s], n + 1);
-            if (!ok) break;
-            bad |= bad_s[s] != 0;
-            uint8_t* const blk = ring + s * B::kBytes;
-            const int key0 = first_key + i * kKvPage;
-            if (key0 < len)
-                rows_tile<D, Q8, NT>(blk, 16 * wi, key0, places, q, p.scale_log2, st, ctx, len, mask_s[ss], key0 + 16 > ctx);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
-            s += C::kTeams;
-            if (s >= stages) s -= stages, phase ^= 1u;
-        }
-        it += seg_n;
-
-        // ---- join the warps that had pages: each leaves its tiles as it holds them
-        float* const mine = out_s + warp * S::kWarpOut;
-        if (team < seg_n) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    *reinterpret_cast<float4*>(mine + (n * (D / 16) + i) * S::kTile + 4 * lane) =
-                        make_float4(st.o[n][i][0], st.o[n][i][1], st.o[n][i][2], st.o[n][i][3]);
-        }
-        if (g8 == 0) {
+            for (; it < end; it += kTeams) {
+                // The stage's previous use may be another team's page, which may not even have
+                // landed; a wait by parity tells two successive uses apart only, so that team's
+                // word that it has comes first.
+                if (kStages % kTeams) ok = it < kStages || wait_seen(&seen_s[s], it - kStages + 1);
+                ok = ok && wait_all(&full[s], phase);
+                if (kStages % kTeams && ok && wi == 0 && lane == 0) store_release(&seen_s[s], it + 1);
+                bad |= ok && bad_s[s] != 0;
+                good = rows_page<D, Q8, NT>(ok, ring + s * B::kBytes, wi, team, first_key + it * kKvPage, places, q,
+                                            p.scale_log2, st, ctx, len, mask_s[ss],
+                                            p_s + (team * 2 + flip) * (C::kP / 8), words);
+                if (!good) break;
+                flip ^= 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
+                s += kTeams;
+                if (s >= kStages) s -= kStages, phase ^= 1u;
+            }
+            if (!good) break;
+            // ---- leave the team's results
+            float* const mine = out_s + (os * kTeams + team) * RT * D + wi * C::kSlice + g8 * (D / 32);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    m_s[warp][8 * n + 2 * t4 + e] = st.m[n][e];
-                    l_s[warp][8 * n + 2 * t4 + e] = st.l[n][e];
+                    const int r = 8 * n + 2 * t4 + e;
+#pragma unroll
+                    for (int i = 0; i < D / 64; ++i)
+                        *reinterpret_cast<float2*>(mine + r * D + 2 * i) = make_float2(st.o[n][i][e], st.o[n][i][e + 2]);
+                    if (g8 == 0) {
+                        if (wi == 0) m_s[os][team][r] = st.m[n][e];
+                        l_s[os][team][wi][r] = st.l[n][e];
+                    }
                 }
         }
-        if (lane == 0) ok_s[warp] = ok, pages_bad_s[warp] = bad;
-        named_barrier_sync(1, kCons);
-        // a wait that ran out in any warp ends all of them here, together
-        const int flags = lane < kWarps ? (ok_s[lane] ? 0 : 1) | (pages_bad_s[lane] ? 2 : 0) : 0;
-        all_ok = !__any_sync(0xffffffffu, flags & 1);
-        const bool seg_bad = __any_sync(0xffffffffu, flags & 2);
-        if (!all_ok || seg_n == 0) break;  // failed, or the end
-        const int split = seg_s[ss].split, rows = min(RT, g.T * p.group - g.row0);
-        const int nw = min(C::kTeams, seg_n) * kTeam;  // warps that had pages
-        float* const slot = p.parts + (int64_t(blockIdx.x) * 2 + g.slot) * attn_slot_floats(RT, D);
-#pragma unroll 1
-        for (int x = warp; x < rows * (D / 32); x += kWarps) {
-            const int r = x / (D / 32), d = (x % (D / 32)) * 32 + lane;
-            // lane w: warp w's maximum and weight
-            const float mw = lane < nw ? m_s[lane][r] : -3.402823466e38f;
-            float mm = mw;
+        if (wi == 0 && lane == 0) had_s[os][team] = had ? (bad ? 2 : 1) : 0;
+        named_barrier_sync(id, 32 * kTeam);
+        if (wi == 0 && lane == 0) {
+            __threadfence_block();
+            words->closed_last = atomicAdd(&closed_s[os], 1) == kTeams - 1;
+            __threadfence_block();
+        }
+        named_barrier_sync(id, 32 * kTeam);
+        if (words->closed_last) {
+            // ---- the last team to leave joins them
+            const int split = seg_s[ss].split, rows = min(RT, g.T * p.group - g.row0);
+            float* const slot = p.parts + (int64_t(blockIdx.x) * 2 + g.slot) * attn_slot_floats(RT, D);
+            bool seg_bad = false;
 #pragma unroll
-            for (int o = 8; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-            const float fw = ex2(mw - mm);
-            float sum = lane < nw ? l_s[lane][r] * fw : 0.0f;
+            for (int k = 0; k < kTeams; ++k) seg_bad |= had_s[os][k] == 2;
+            // lane l: row l % 8 (+ 8j) of team l / 8: its weight, and the row's maximum and sum
+            float fk[NT], top[NT], sum[NT];
 #pragma unroll
-            for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            mm = __shfl_sync(0xffffffffu, mm, 0);
-            sum = __shfl_sync(0xffffffffu, sum, 0);
-            // value d of row r in a warp's tiles
-            const int g_of = Q8 && D == 128 ? d / 16 : (d % 64) / 8;
-            const int i_of = Q8 && D == 128 ? (d % 16) / 2 : 4 * (d / 64) + (d % 8) / 2;
-            const float* const src = out_s + ((r / 8) * (D / 16) + i_of) * S::kTile +
-                                     4 * (4 * g_of + (r % 8) / 2) + (r & 1) + 2 * (d & 1);
-            float v = 0.0f;
-#pragma unroll 4
-            for (int w = 0; w < nw; ++w) v = fmaf(src[w * S::kWarpOut], __shfl_sync(0xffffffffu, fw, w), v);
-            if (split < 0) {
-                if (!seg_bad) attn_emit(p, g, g.row0 + r, D, d - lane, sum == 0.0f ? 0.0f : v / sum);
-            } else {
-                if (d == 0) {
-                    slot[r] = mm;
-                    slot[RT + r] = seg_bad ? -1.0f : sum;
+            for (int j = 0; j < NT; ++j) {
+                const int k = lane >> 3, r = 8 * j + (lane & 7);
+                const bool there = k < kTeams && had_s[os][k] != 0;
+                const float mk = there ? m_s[os][k][r] : kLowest;
+                float lk = 0.0f;
+#pragma unroll
+                for (int u = 0; u < kTeam; ++u) lk += there ? l_s[os][k][u][r] : 0.0f;
+                top[j] = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, 8));
+                top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
+                fk[j] = there ? ex2(mk - top[j]) : 0.0f;
+                sum[j] = lk * fk[j];
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
+                if (split >= 0 && wi == 0 && lane < 8 && r < rows) {
+                    slot[r] = top[j];
+                    slot[RT + r] = seg_bad ? -1.0f : sum[j];
                 }
-                slot[2 * RT + r * D + d] = v;
+                sum[j] = sum[j] == 0.0f ? 0.0f : 1.0f / sum[j];
+            }
+            constexpr int kBlocks = RT * D / 32 / kTeam;  // of 32 values
+#pragma unroll
+            for (int j = 0; j < kBlocks; ++j) {
+                // block wi of row j, or (64 values) block wi % 2 of row 2j + wi / 2
+                const int r = D == 128 ? j : 2 * j + (wi >> 1), d = (D == 128 ? wi : wi & 1) * 32 + lane;
+                constexpr int kRowsAStep = 128 / D;
+                float v = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kTeams; ++k) {
+                    const float f = __shfl_sync(0xffffffffu, fk[kRowsAStep * j / 8], 8 * k + (r & 7));
+                    // a team without pages left nothing: what lies there is not read as a number
+                    const float o = out_s[((os * kTeams + k) * RT + r) * D + d];
+                    v = f == 0.0f && !had_s[os][k] ? v : fmaf(o, f, v);
+                }
+                const float inv = __shfl_sync(0xffffffffu, sum[kRowsAStep * j / 8], r & 7);
+                if (r >= rows) continue;
+                if (split >= 0)
+                    slot[2 * RT + r * D + d] = v;
+                else if (!seg_bad)
+                    attn_emit(p, g, g.row0 + r, D, d - lane, v * inv);
+            }
+            __syncwarp();
+            if (wi == 0 && lane == 0) {
+                closed_s[os] = 0;
+                if (split < 0 && seg_bad) atomicOr(status, MQ_DEV_KV_RANGE);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                if (split >= 0) mbar_arrive(&part_full[split]);
+                mbar_arrive(&out_free[os]);
             }
         }
         __syncwarp();
-        if (lane == 0) {
-            if (split >= 0) mbar_arrive(&part_full[split]);
-            mbar_arrive(&seg_empty[ss]);
-        }
-        if (split < 0 && seg_bad && threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-        splits += split >= 0;
-        named_barrier_sync(1, kCons);  // out_s, m_s, l_s are free again
-    }
-    if (!all_ok) {
-        if (lane == 0)
-            for (int k = splits; k < 2; ++k) mbar_arrive(&part_full[k]);  // the producer finds abort_flag set
-        return;
+        if (lane == 0) mbar_arrive(&seg_empty[ss]);
     }
 
     // ---- the shared groups whose last CTA this is: their segments joined in CTA order
-    if (splits > 0) {
-        bool ok = true;
-        for (int k = 0; k < splits; ++k) ok = wait_all(&part_done[k], 0) && ok;
-        if (lane == 0) ok_s[warp] = ok;
-        named_barrier_sync(1, kCons);
-        if (__any_sync(0xffffffffu, lane < kWarps && !ok_s[lane])) return;
-    }
+    for (int k = 0; good && k < splits; ++k) good = wait_all(&part_done[k], 0);
+    if (barrier_any(1, kCons, !good)) return;  // a wait that ran out anywhere ends all
     for (int k = 0; k < splits; ++k) {
         if (!last_s[k]) continue;
         const AttnSegment& g = split_s[k];
         const int rows = min(RT, g.T * p.group - g.row0);
-        float* const wgt = reinterpret_cast<float*>(ring);  // [n_ctas][RT]; every copy has landed and been read
-        auto slot_of = [&](int c) {
-            return p.parts + (int64_t(g.cta0 + c) * 2 + (c == 0 ? g.slot0 : 0)) * attn_slot_floats(RT, D);
-        };
-        bool gone = false;
-        for (int r = warp; r < RT; r += kWarps) {
-            float mm = -3.402823466e38f, sum = 0.0f;
-            if (r < rows) {
-                for (int c = lane; c < g.n_ctas; c += 32) mm = fmaxf(mm, __ldcg(slot_of(c) + r));
-#pragma unroll
-                for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-            }
-            for (int c = lane; c < g.n_ctas; c += 32) {
-                float f1 = 0.0f;
-                if (r < rows) {
-                    const float l = __ldcg(slot_of(c) + RT + r);
-                    f1 = ex2(__ldcg(slot_of(c) + r) - mm);
-                    gone |= l < 0.0f;
-                    sum = fmaf(l, f1, sum);
-                }
-                wgt[c * RT + r] = f1;
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) sum_s[r] = sum;
-        }
-        if (gone) gone_s = 1 + k;
-        named_barrier_sync(1, kCons);
-        if (gone_s == 1 + k) {
-            if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-            continue;
-        }
-        // warp w adds up CTAs w, w + kWarps, ...; a lane holds four values of each 128 of the rows
+        // every copy has landed and been read: the ring is free
+        float* const sums = reinterpret_cast<float*>(ring);  // [kWarps][RT][D]
+        // warp w joins the parts of CTAs w, w + kWarps, ...: lane r has row r's maximum and sum, and a
+        // lane four values of each 128 of the rows
         constexpr int NV = RT * D / 128;
+        float mr = kLowest, lr = 0.0f;
+        bool gone = false;
         float4 acc[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
         for (int c = warp; c < g.n_ctas; c += kWarps) {
-            const float4* const src = reinterpret_cast<const float4*>(slot_of(c) + 2 * RT) + lane;
+            const float* const slot =
+                p.parts + (int64_t(g.cta0 + c) * 2 + (c == 0 ? g.slot0 : 0)) * attn_slot_floats(RT, D);
+            const float mc = lane < rows ? __ldcg(slot + lane) : kLowest;
+            const float lc = lane < rows ? __ldcg(slot + RT + lane) : 0.0f;
             float4 x[NV];
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-                x[v] = (v * 128 + lane * 4) / D < rows ? __ldcg(src + v * 32) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                x[v] = (v * 128 + lane * 4) / D < rows
+                           ? __ldcg(reinterpret_cast<const float4*>(slot + 2 * RT) + lane + v * 32)
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            gone |= lc < 0.0f;
+            const float mn = fmaxf(mr, mc), fr = ex2(mr - mn), fc = ex2(mc - mn);
+            mr = mn;
+            lr = lr * fr + lc * fc;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const float f1 = wgt[c * RT + (v * 128 + lane * 4) / D];
-                acc[v].x = fmaf(x[v].x, f1, acc[v].x);
-                acc[v].y = fmaf(x[v].y, f1, acc[v].y);
-                acc[v].z = fmaf(x[v].z, f1, acc[v].z);
-                acc[v].w = fmaf(x[v].w, f1, acc[v].w);
+                const int r = (v * 128 + lane * 4) / D;
+                const float a = __shfl_sync(0xffffffffu, fr, r), b = __shfl_sync(0xffffffffu, fc, r);
+                acc[v].x = fmaf(acc[v].x, a, x[v].x * b);
+                acc[v].y = fmaf(acc[v].y, a, x[v].y * b);
+                acc[v].z = fmaf(acc[v].z, a, x[v].z * b);
+                acc[v].w = fmaf(acc[v].w, a, x[v].w * b);
             }
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            *reinterpret_cast<float4*>(out_s + warp * RT * D + v * 128 + lane * 4) = acc[v];
-        named_barrier_sync(1, kCons);
+            *reinterpret_cast<float4*>(sums + warp * RT * D + v * 128 + lane * 4) = acc[v];
+        if (lane < RT) cm_s[warp][lane] = mr, cl_s[warp][lane] = lr;
+        if (barrier_any(1, kCons, gone)) {  // a page outside the cache: the group stays unwritten
+            if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+            continue;
+        }
+        const int nw = min(kWarps, g.n_ctas);
+#pragma unroll 1
         for (int x = warp; x < rows * (D / 32); x += kWarps) {
             const int r = x / (D / 32), d = (x % (D / 32)) * 32 + lane;
-            float v = 0.0f;
+            // lane w: warp w's maximum and weight
+            const float mw = lane < nw ? cm_s[lane][r] : kLowest;
+            float mm = mw;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += out_s[(w * RT + r) * D + d];
-            attn_emit(p, g, g.row0 + r, D, d - lane, sum_s[r] == 0.0f ? 0.0f : v / sum_s[r]);
+            for (int o = 8; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+            const float fw = ex2(mw - mm);
+            float sum = lane < nw ? cl_s[lane][r] * fw : 0.0f;
+#pragma unroll
+            for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            sum = __shfl_sync(0xffffffffu, sum, 0);
+            float v = 0.0f;
+#pragma unroll 8
+            for (int u = 0; u < nw; ++u) v = fmaf(sums[(u * RT + r) * D + d], __shfl_sync(0xffffffffu, fw, u), v);
+            attn_emit(p, g, g.row0 + r, D, d - lane, sum == 0.0f ? 0.0f : v / sum);
         }
         named_barrier_sync(1, kCons);
     }
 }
 
-constexpr int kRowsSmem = 222 * 1024;  // ring and merge buffers; the kernel's static arrays come on top
-
 template <int D, bool Q8, int NT>
-cudaError_t launch_rows(const AttnParams& p, int grid, int max_smem, unsigned* status, cudaStream_t s)
+cudaError_t launch_rows(const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
 {
-    using B = KvBlock<D, Q8>;
-    using S = RowsSmem<D, Q8, NT>;
-    int stages = (max_smem - S::kFixed) / B::kBytes;
-    if (stages > kMaxStages) stages = kMaxStages;
-    static_assert((kRowsSmem - S::kFixed) / B::kBytes >= RowsCfg<NT>::kTeams, "each team needs a page to work on");
-    const int smem = stages * B::kBytes + S::kFixed;
-    attn_rows_kernel<D, Q8, NT><<<grid, RowsCfg<NT>::kThreads, smem, s>>>(p, stages, status);
+    using C = RowsCfg<D, Q8, NT>;
+    attn_rows_kernel<D, Q8, NT><<<grid, C::kThreads, C::kSmem, s>>>(p, status);
     return cudaGetLastError();
 }
 
 template <int NT>
-cudaError_t launch_rows_nt(const mq_kv_cache& c, const AttnParams& p, int grid, int max_smem, unsigned* status,
-                           cudaStream_t s)
+cudaError_t launch_rows_nt(const mq_kv_cache& c, const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
 {
     if (c.type == MQ_TYPE_Q8_0)
-        return c.head_dim == 128 ? launch_rows<128, true, NT>(p, grid, max_smem, status, s)
-                                 : launch_rows<64, true, NT>(p, grid, max_smem, status, s);
-    return c.head_dim == 128 ? launch_rows<128, false, NT>(p, grid, max_smem, status, s)
-                             : launch_rows<64, false, NT>(p, grid, max_smem, status, s);
+        return c.head_dim == 128 ? launch_rows<128, true, NT>(p, grid, status, s)
+                                 : launch_rows<64, true, NT>(p, grid, status, s);
+    return c.head_dim == 128 ? launch_rows<128, false, NT>(p, grid, status, s)
+                             : launch_rows<64, false, NT>(p, grid, status, s);
 }
-
 
 }  // namespace
 
@@ -803,6 +882,7 @@ cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* w
     p.a = a;
     p.c = kv_view(cache);
     p.group = a.n_heads / cache.n_kv_heads;
+    p.group_inv = uint32_t((0x100000000ull + p.group - 1) / p.group);
     p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
     p.counters = static_cast<unsigned*>(ws);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + counters_bytes(cache, a.n_heads));
@@ -812,8 +892,8 @@ cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* w
     const int64_t most = int64_t(cache.n_seqs) * ((int64_t(a.max_len) + kKvPage - 1) / kKvPage) * cache.n_kv_heads *
                          ((rows + RT - 1) / RT);
     const int grid = int(most < 1 ? 1 : most < num_sms ? most : num_sms);
-    return RT == 8 ? launch_rows_nt<1>(cache, p, grid, kRowsSmem, status, s)
-                   : launch_rows_nt<2>(cache, p, grid, kRowsSmem, status, s);
+    return RT == 8 ? launch_rows_nt<1>(cache, p, grid, status, s)
+                   : launch_rows_nt<2>(cache, p, grid, status, s);
 }
 
 cudaError_t set_attn_attributes(int max_smem)

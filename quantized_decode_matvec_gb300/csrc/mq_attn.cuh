@@ -28,11 +28,18 @@ struct AttnParams {
     mq_attn_args a;
     KvView c;
     int group;           // query heads per key/value head
+    uint32_t group_inv;  // 2^32 / group rounded up: x / group = umulhi(x, group_inv) for x < 2^16
     float scale_log2;    // scale * log2(e): exp(x) = 2^(x log2 e)
     unsigned* counters;  // one per group
     float* parts;        // two slots of a segment's results per CTA
     uint64_t limit_ns;
 };
+
+// query row r of a sequence is head r % group of the group, of token r / group
+__device__ __forceinline__ int attn_row_token(const AttnParams& p, int r)
+{
+    return p.group == 1 ? r : int(__umulhi(uint32_t(r), p.group_inv));
+}
 
 // sequence s as the device data has it; false (and nothing to do) where it is
 // empty, *bad where it contradicts the call's bounds or the cache
@@ -74,63 +81,54 @@ struct AttnRange {
     }
 };
 
-// Called by all threads of the CTA; scratch: an int2 per warp.
-__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status, int2* scratch, int2* at_s)
+// Called by one whole warp.
+__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status)
 {
-    const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.c.n_seqs + nthr - 1) / nthr, s0 = min(tid * per, p.c.n_seqs), s1 = min(s0 + per, p.c.n_seqs);
-    int2 mine = make_int2(0, 0);  // pages of all groups, groups
+    const int lane = threadIdx.x & 31;
+    int pages = 0, groups = 0;
     bool any_bad = false;
-    for (int s = s0; s < s1; ++s) {
+    for (int s = lane; s < p.c.n_seqs; s += 32) {
         AttnSeq q;
         bool bad;
         if (attn_seq(p, s, &q, &bad)) {
             const int n = attn_groups(p, q, RT);
-            mine.x += n * q.pages;
-            mine.y += n;
+            pages += n * q.pages;
+            groups += n;
         }
         any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-    int2 incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
-        if (lane >= o) incl.x += x, incl.y += y;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
+    pages = __reduce_add_sync(0xffffffffu, pages);
+    groups = __reduce_add_sync(0xffffffffu, groups);
     AttnRange r;
-    int2 before = make_int2(0, 0), total = before;
-    for (int w = 0; w < nthr / 32; ++w) {
-        if (w == warp) before = total;
-        total.x += scratch[w].x, total.y += scratch[w].y;
-    }
-    r.cost = total.x > int(gridDim.x) ? kAttnGroupCost : 0;
-    r.total = total.x + total.y * r.cost;
+    r.cost = pages > int(gridDim.x) ? kAttnGroupCost : 0;
+    r.total = pages + groups * r.cost;
     r.ctas = min(r.total, int(gridDim.x));
     const int c = blockIdx.x;
     r.quot = r.ctas ? r.total / r.ctas : 0;
     r.rem = r.total - r.quot * r.ctas;
     r.first = c < r.ctas ? r.begin(c) : r.total;
     r.last = c < r.ctas ? r.begin(c + 1) : r.total;
-    int at = before.x + incl.x - mine.x + (before.y + incl.y - mine.y) * r.cost;
-    if (r.first >= at && r.first < at + mine.x + mine.y * r.cost) {
-        for (int s = s0; s < s1; ++s) {
-            AttnSeq q;
-            bool bad;
-            if (!attn_seq(p, s, &q, &bad)) continue;
-            const int u = attn_groups(p, q, RT) * (q.pages + r.cost);
-            if (r.first < at + u) {
-                *at_s = make_int2(s, at);
-                break;
-            }
-            at += u;
+    r.seq = 0, r.seq_first = 0;
+    // the sequence that holds unit r.first, 32 at a time
+    for (int s0 = 0; s0 < p.c.n_seqs && r.first < r.last; s0 += 32) {
+        AttnSeq q;
+        bool bad;
+        const int mine = s0 + lane < p.c.n_seqs && attn_seq(p, s0 + lane, &q, &bad)
+                             ? attn_groups(p, q, RT) * (q.pages + r.cost) : 0;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
         }
+        const unsigned past = __ballot_sync(0xffffffffu, r.first < r.seq_first + incl);
+        const int l = past ? __ffs(past) - 1 : 31;
+        const int upto = __shfl_sync(0xffffffffu, past ? incl - mine : incl, l);
+        r.seq_first += upto;
+        r.seq = s0 + l;
+        if (past) break;
     }
-    __syncthreads();
-    r.seq = at_s->x;
-    r.seq_first = at_s->y;
     return r;
 }
 
@@ -159,7 +157,7 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange
             continue;
         }
         const int blocks = (q.T * p.group + RT - 1) / RT, span = q.pages + w->cost;
-        const int k = (u - w->seq_first) / span;  // group within the sequence
+        const int k = u - w->seq_first < span ? 0 : (u - w->seq_first) / span;  // group within the sequence
         const int g0 = w->seq_first + k * span, g1 = g0 + q.pages;
         if (u >= g1) {
             u = g0 + span;
@@ -167,11 +165,11 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange
         }
         g->seq = w->seq;
         g->t0 = q.t0, g->T = q.T, g->ctx = q.ctx;
-        g->head = k / blocks;
+        g->head = blocks == 1 ? k : k / blocks;
         g->row0 = (k - g->head * blocks) * RT;
         g->page0 = u - g0;
         g->n = min(g1, w->last) - u;
-        const int most = (p.a.max_tokens * p.group + RT - 1) / RT;
+        const int most = (p.a.max_tokens * p.group + RT - 1) / RT;  // RT is a constant power of two
         g->group_index = (w->seq * p.c.n_kv_heads + g->head) * most + k - g->head * blocks;
         const bool whole = g0 >= w->first && g1 <= w->last;
         g->cta0 = whole ? int(blockIdx.x) : w->owner(g0);
@@ -192,7 +190,7 @@ __host__ __device__ constexpr int64_t attn_slot_floats(int RT, int D) { return i
 __device__ __forceinline__ void attn_emit(const AttnParams& p, const AttnSegment& g, int row, int D, int d0, float v)
 {
     const int lane = threadIdx.x & 31;
-    const int tok = g.t0 + row / p.group, h = g.head * p.group + row % p.group;
+    const int node = attn_row_token(p, row), tok = g.t0 + node, h = (g.head - node) * p.group + row;
     if (p.a.out_type == MQ_TYPE_F16) {
         static_cast<__half*>(p.a.out)[int64_t(tok) * p.a.out_ld + h * D + d0 + lane] = __float2half_rn(v);
     } else {
@@ -209,13 +207,11 @@ __device__ __forceinline__ void attn_emit(const AttnParams& p, const AttnSegment
 // (one thread calls it, after the CTA's results are written and synchronised)
 __device__ __forceinline__ bool attn_arrive(const AttnParams& p, const AttnSegment& g)
 {
-    __threadfence();
     unsigned* const c = p.counters + g.group_index;
-    const bool is_last = atomicAdd(c, 1u) == unsigned(g.n_ctas - 1);
-    if (is_last) {
-        *c = 0;  // nobody else of this call comes back to it
-        __threadfence();
-    }
+    unsigned before;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(c) : "memory");
+    const bool is_last = before == unsigned(g.n_ctas - 1);
+    if (is_last) *c = 0;  // nobody else of this call comes back to it
     return is_last;
 }
 
