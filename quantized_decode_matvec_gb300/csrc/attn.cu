@@ -146,18 +146,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     return r;
 }
 
-// barrier over n threads; true for all of them where it was for one
-__device__ __forceinline__ bool barrier_any(int id, int n, bool v)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(uint32_t(v)), "r"(id), "r"(n)
-        : "memory");
-    return r != 0;
-}
-
 constexpr uint32_t k64 = 0x64646464u;
 
 // Lane (g = lane/4, t = lane%4).  K values of MMA step j: head values kdim(t, j) + 0..3.
@@ -869,10 +857,13 @@ static size_t counters_bytes(const mq_kv_cache& c, int n_heads)
     return (groups * 4 + 127) / 128 * 128;
 }
 
+// the most query rows of a key/value head that the warp kernels take
+constexpr int kWarpRows = 16;
+
 size_t attn_workspace_bytes(const mq_kv_cache& c, int n_heads, int max_tokens, int num_sms)
 {
-    (void)max_tokens;
-    return counters_bytes(c, n_heads) + size_t(num_sms) * 2 * attn_slot_floats(16, c.head_dim) * 4;
+    const int RT = n_heads / c.n_kv_heads * max_tokens > kWarpRows ? attn_tc_rows() : kWarpRows;
+    return counters_bytes(c, n_heads) + size_t(num_sms) * 2 * attn_slot_floats(RT, c.head_dim) * 4;
 }
 
 cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* ws, int num_sms, unsigned* status,
@@ -887,13 +878,13 @@ cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* w
     p.counters = static_cast<unsigned*>(ws);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + counters_bytes(cache, a.n_heads));
     p.limit_ns = uint64_t(fault_policy() == FAULT_NONE ? 2000 : 50) * 1000000ull;
-    const int rows = p.group * a.max_tokens, RT = rows <= 8 ? 8 : 16;
+    const int rows = p.group * a.max_tokens, RT = rows <= 8 ? 8 : rows <= kWarpRows ? 16 : attn_tc_rows();
     // no more CTAs than the bounds allow units
     const int64_t most = int64_t(cache.n_seqs) * ((int64_t(a.max_len) + kKvPage - 1) / kKvPage) * cache.n_kv_heads *
                          ((rows + RT - 1) / RT);
     const int grid = int(most < 1 ? 1 : most < num_sms ? most : num_sms);
-    return RT == 8 ? launch_rows_nt<1>(cache, p, grid, status, s)
-                   : launch_rows_nt<2>(cache, p, grid, status, s);
+    if (RT > kWarpRows) return launch_attn_tc(cache, p, grid, status, s);
+    return RT == 8 ? launch_rows_nt<1>(cache, p, grid, status, s) : launch_rows_nt<2>(cache, p, grid, status, s);
 }
 
 cudaError_t set_attn_attributes(int max_smem)
@@ -906,6 +897,7 @@ cudaError_t set_attn_attributes(int max_smem)
     MQ_SET(128, true, 1) MQ_SET(64, true, 1) MQ_SET(128, false, 1) MQ_SET(64, false, 1)
     MQ_SET(128, true, 2) MQ_SET(64, true, 2) MQ_SET(128, false, 2) MQ_SET(64, false, 2)
 #undef MQ_SET
+    if (e == cudaSuccess) e = set_attn_tc_attributes();
     return e;
 }
 

@@ -22,7 +22,7 @@
 
 namespace mq {
 
-constexpr int kAttnGroupCost = 3;
+constexpr int kAttnGroupCost = 10;
 
 struct AttnParams {
     mq_attn_args a;
@@ -214,5 +214,22 @@ __device__ __forceinline__ bool attn_arrive(const AttnParams& p, const AttnSegme
     if (is_last) *c = 0;  // nobody else of this call comes back to it
     return is_last;
 }
+
+// barrier over n threads; true for all of them where it was for one
+__device__ __forceinline__ bool barrier_any(int id, int n, bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(uint32_t(v)), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
+// many query rows per key/value head (attn_tc.cu): rows of a block there, its launch and set-up
+int attn_tc_rows();
+cudaError_t launch_attn_tc(const mq_kv_cache& cache, const AttnParams& p, int grid, unsigned* status, cudaStream_t s);
+cudaError_t set_attn_tc_attributes();
 
 }  // namespace mq
