@@ -55,7 +55,6 @@ struct TcCfg {
 
 struct TcSegment {
     AttnSegment g;
-    int split;
     int odd, bad;  // a value that is not finite was dropped; a page outside the cache
 };
 
@@ -145,33 +144,44 @@ __device__ __forceinline__ bool tc_convert(const uint8_t* raw, uint8_t* op, cons
     bool odd = false;
     if (Q8) {
         constexpr int CH = D / 16;  // 16-code chunks of a row
+        constexpr int kBatch = 4;   // loads in flight before the first store (which might be to the same place, for all
+                                    // that the compiler knows)
+#pragma unroll 1
+        for (int i0 = 0; i0 < 2 * kKvPage * CH / 128; i0 += kBatch) {
+            uint4 in[kBatch];
+            uint32_t d[kBatch];
 #pragma unroll
-        for (int i = 0; i < 2 * kKvPage * CH / 128; ++i) {
-            const int item = i * 128 + x, is_v = item / (kKvPage * CH), r = item / CH % kKvPage, c = item % CH;
-            const uint4 in = lds16(raw + (is_v ? R::kVOff : 0) + R::chunk(r, c));
-            const uint32_t d = *reinterpret_cast<const uint16_t*>(raw + R::kScK + (is_v ? R::kScBytes : 0) +
-                                                                  (r * (D / 32) + (c >> 1)) * 2) * 0x10001u;
-            const uint32_t w[4] = {in.x, in.y, in.z, in.w};
-            uint32_t u[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                u[2 * k] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4140), d);
-                u[2 * k + 1] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4342), d);
+            for (int i = 0; i < kBatch; ++i) {
+                const int item = (i0 + i) * 128 + x, is_v = item / (kKvPage * CH), r = item / CH % kKvPage, c = item % CH;
+                in[i] = lds16(raw + (is_v ? R::kVOff : 0) + R::chunk(r, c));
+                d[i] = *reinterpret_cast<const uint16_t*>(raw + R::kScK + (is_v ? R::kScBytes : 0) +
+                                                          (r * (D / 32) + (c >> 1)) * 2) * 0x10001u;
             }
-            if (tail && is_v) {
-                const bool out = pg.key0 + r >= pg.len;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (out) u[k] = 0;
-                    if (pair_not_finite(u[k])) odd = true, u[k] = drop_pair(u[k]);
+            for (int i = 0; i < kBatch; ++i) {
+                const int item = (i0 + i) * 128 + x, is_v = item / (kKvPage * CH), r = item / CH % kKvPage, c = item % CH;
+                const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+                uint32_t u[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    u[2 * k] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4140), d[i]);
+                    u[2 * k + 1] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4342), d[i]);
                 }
+                if (tail && is_v) {
+                    const bool out = pg.key0 + r >= pg.len;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (out) u[k] = 0;
+                        if (pair_not_finite(u[k])) odd = true, u[k] = drop_pair(u[k]);
+                    }
+                }
+                uint8_t* const dst = op + (is_v ? O::kVOff : 0);
+                // the lanes of the second plane store their halves in the other order: no bank twice
+                const bool swap = (c & 4) != 0;
+                const uint4 lo = make_uint4(u[0], u[1], u[2], u[3]), hi = make_uint4(u[4], u[5], u[6], u[7]);
+                *reinterpret_cast<uint4*>(dst + O::chunk(r, 2 * c + (swap ? 1 : 0))) = swap ? hi : lo;
+                *reinterpret_cast<uint4*>(dst + O::chunk(r, 2 * c + (swap ? 0 : 1))) = swap ? lo : hi;
             }
-            uint8_t* const dst = op + (is_v ? O::kVOff : 0);
-            // the lanes of the second plane store their halves in the other order: no bank twice
-            const bool swap = (c & 4) != 0;
-            const uint4 lo = make_uint4(u[0], u[1], u[2], u[3]), hi = make_uint4(u[4], u[5], u[6], u[7]);
-            *reinterpret_cast<uint4*>(dst + O::chunk(r, 2 * c + (swap ? 1 : 0))) = swap ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + O::chunk(r, 2 * c + (swap ? 0 : 1))) = swap ? lo : hi;
         }
     } else if (tail) {
         for (int item = x; item < kKvPage * (D / 8); item += 128) {
@@ -255,12 +265,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     extern __shared__ uint8_t sm_raw[];
     __shared__ __align__(8) uint64_t raw_full[kStages], raw_free[kStages], kv_ready[kBufs], kv_free[kBufs];
     __shared__ __align__(8) uint64_t q_ready[2], s_ready[2], p_ready[2], o_done[2], seg_full[kTcSegs], seg_empty[kTcSegs];
-    __shared__ __align__(8) uint64_t part_full[2], part_done[2];
     __shared__ TcSegment seg_s[kTcSegs];
-    __shared__ AttnSegment split_s[2];
     __shared__ TcPage page_s[kStages];
     __shared__ float join_m[2][128], join_l[2][128];
-    __shared__ int last_s[2];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -282,14 +289,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         mbar_init(&s_ready[k], 1);
         mbar_init(&p_ready[k], 4);
         mbar_init(&o_done[k], 1);
-        mbar_init(&part_full[k], 8);
-        mbar_init(&part_done[k], 1);
     } else if (threadIdx.x >= 96 && threadIdx.x < 96 + kTcSegs) {
         mbar_init(&seg_full[threadIdx.x - 96], 1);
         mbar_init(&seg_empty[threadIdx.x - 96], 8 + 4 + 1);  // softmax and converter warps, the MMA warp
         if (threadIdx.x == 96) abort_flag = 0;
     }
     fence_barrier_init();
+    griddep_launch_dependents();  // the join may take its place; it waits for this grid's end
     AttnRange w;
     if (warp == 12) w = attn_range(p, kTcRows, status);
     if (warp == 13) tmem_alloc(&tmem_base, 512);
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     if (warp == 12) {
         // ---- producer
         AttnSegment g = {};
-        int at = w.first, it = 0, sg = 0, splits = 0, s = 0;
+        int at = w.first, it = 0, sg = 0, s = 0;
         uint32_t phase = 0;
         bool ok = true, more = true;
         for (; ok && more; ++sg) {
@@ -320,12 +326,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             int32_t page_l = lane < g.n ? __ldg(table + lane) : 0;
             if (sg >= kTcSegs) ok = wait_all(&seg_empty[ss], uint32_t(sg / kTcSegs - 1) & 1u);
             if (!ok) break;
-            const int split = more && g.n_ctas > 1 ? splits++ : -1;
             if (lane == 0) {
                 seg_s[ss].g = g;
-                seg_s[ss].split = more ? split : splits;
                 seg_s[ss].odd = seg_s[ss].bad = 0;
-                if (split >= 0) split_s[split] = g;
                 mbar_arrive(&seg_full[ss]);
             }
             __syncwarp();
@@ -352,13 +355,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                     }
                     if (++s == kStages) s = 0, phase ^= 1u;
                 }
-            }
-        }
-        for (int k = 0; k < splits; ++k) {
-            const bool there = mbar_wait_bounded(&part_full[k], 0, p.limit_ns) && !abort_flag;
-            if (lane == 0) {
-                last_s[k] = there && attn_arrive(p, split_s[k]);
-                mbar_arrive(&part_done[k]);
             }
         }
         // copies still in flight land before the CTA can exit
@@ -402,6 +398,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         if (lane == 0) {
             constexpr uint32_t idesc_s = umma_idesc_f16_f32(128, kKvPage);
             constexpr uint32_t idesc_o = umma_idesc_f16_f32(128, D) | kBMajorMn;
+            // operand buffer 0; an address within it or in another is added to the descriptor's address field
+            const uint64_t ops_k = umma_desc_sw128(smem_u32(ops)), ops_v = umma_desc_mn(smem_u32(ops) + Op::kVOff, kKvPage * 128);
             auto wait_one = [&](uint64_t* bar, uint32_t parity) {
                 if (!abort_flag && mbar_wait_bounded(bar, parity, p.limit_ns)) return true;
                 abort_flag = 1;
@@ -429,11 +427,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                         ready = pg + 1;
                     }
                     tc_fence_after();
-                    const uint32_t kb = smem_u32(ops + b * Op::kBytes);
+                    const uint64_t kd = ops_k + uint64_t(b * (Op::kBytes >> 4));
+                    umma_f16_ts(tmem + kColS + 64 * t, tmem + kColQ + 64 * t, kd, idesc_s, false);
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x)
+                    for (int x = 1; x < D / 16; ++x)
                         umma_f16_ts(tmem + kColS + 64 * t, tmem + kColQ + 64 * t + 8 * x,
-                                    umma_desc_sw128(kb + (x >> 2) * (kKvPage * 128) + 32 * (x & 3)), idesc_s, x > 0);
+                                    kd + (((x >> 2) * (kKvPage * 128) + 32 * (x & 3)) >> 4), idesc_s, true);
                     umma_commit(&s_ready[t]);
                     return true;
                 };
@@ -444,11 +443,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                     if (!ok) break;
                     pph[t] ^= 1u;
                     tc_fence_after();
-                    const uint32_t vb = smem_u32(ops + b * Op::kBytes + Op::kVOff);
+                    const uint64_t vd = ops_v + uint64_t(b * (Op::kBytes >> 4));
+                    umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 64 * t, vd, idesc_o, j > 1);
 #pragma unroll
-                    for (int x = 0; x < kKvPage / 16; ++x)
-                        umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 64 * t + 8 * x,
-                                    umma_desc_mn(vb + 2048u * x, kKvPage * 128), idesc_o, j > 1 || x > 0);
+                    for (int x = 1; x < kKvPage / 16; ++x)
+                        umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 64 * t + 8 * x, vd + ((2048 * x) >> 4), idesc_o,
+                                    true);
                     if (!halves || t == 1) umma_commit(&kv_free[b]);  // the page's last use
                     if (j + 2 < items)
                         ok = scores(j + 2);
@@ -469,7 +469,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;  // scores of -q, so that the scale is positive
         const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);     // not 0: -inf * 0 is no score
         uint32_t sph = 0, oph = 0;
-        int splits = 0;
         bool good = true;
         for (int sg = 0;; ++sg) {
             const int ss = sg % kTcSegs;
@@ -578,12 +577,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             join_l[t][r] = l;
             good = !barrier_any(1, 256, !ok);
             if (!good) break;
-            if (n == 0) {
-                splits = seg_s[ss].split;
-                break;
-            }
+            if (n == 0) break;
             // ---- the outputs: of its own rows, or (pages in turn) tile 1's handed to tile 0
-            const int split = seg_s[ss].split;
+            const bool split = g.n_ctas > 1;
             const bool odd = seg_s[ss].odd != 0, bad = seg_s[ss].bad != 0;
             float* const slot = p.parts + (int64_t(blockIdx.x) * 2 + g.slot) * attn_slot_floats(kTcRows, D);
             float f = 1.0f;
@@ -618,8 +614,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                     }
                     named_barrier_sync(1, 256);
                 }
-                if (odd && writes) tc_add_dropped<D, Q8>(p, g, mask, 32 * c, o);
-                if (writes && split >= 0) {
+                if (odd && writes) {
+                    float add[32];  // a copy, so that the outputs stay in registers
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) add[k] = 0.0f;
+                    tc_add_dropped<D, Q8>(p, g, mask, 32 * c, add);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] += add[k];
+                }
+                if (writes && split) {
                     // [D/4][row][4], so that a warp's rows lie together
                     float4* const dst = reinterpret_cast<float4*>(slot + 2 * kTcRows) + (8 * c) * kTcRows + at;
 #pragma unroll
@@ -629,66 +632,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                     tc_emit(p, g, row, D, 32 * c, o, inv);
                 }
             }
-            if (writes && split >= 0) {
+            if (writes && split) {
                 slot[at] = m;
                 slot[kTcRows + at] = bad ? -1.0f : l;
             }
-            if (split < 0 && bad && threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+            if (!split && bad && threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
             tc_fence_before();  // the outputs are read: the next segment's products may follow the queries
             __syncwarp();
-            if (lane == 0) {
-                if (split >= 0) mbar_arrive(&part_full[split]);
-                mbar_arrive(&seg_empty[ss]);
-            }
-        }
-        // ---- the shared groups whose last CTA this is: their parts joined in CTA order, a thread per row
-        for (int k = 0; good && k < splits; ++k) good = wait_all(&part_done[k], 0);
-        good = !barrier_any(1, 256, !good);
-        for (int k = 0; good && k < splits; ++k) {
-            if (!last_s[k]) continue;
-            const AttnSegment& g = split_s[k];
-            const int rr = threadIdx.x, rows = min(kTcRows, g.T * p.group - g.row0);
-            auto slot_of = [&](int c) {
-                return p.parts + (int64_t(g.cta0 + c) * 2 + (c == 0 ? g.slot0 : 0)) * attn_slot_floats(kTcRows, D);
-            };
-            float mm = kLowest, l = 0.0f;
-            bool gone = false;
-            if (rr < rows) {
-#pragma unroll 8
-                for (int c = 0; c < g.n_ctas; ++c) mm = fmaxf(mm, __ldcg(slot_of(c) + rr));
-#pragma unroll 4
-                for (int c = 0; c < g.n_ctas; ++c) {
-                    const float lc = __ldcg(slot_of(c) + kTcRows + rr);
-                    gone |= lc < 0.0f;
-                    l = fmaf(lc, ex2(__ldcg(slot_of(c) + rr) - mm), l);
-                }
-            }
-            if (barrier_any(1, 256, gone)) {  // a page outside the cache: the group stays unwritten
-                if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-                continue;
-            }
-            if (rr >= rows) continue;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll 1
-            for (int c4 = 0; c4 < D / 32; ++c4) {
-                float o[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-#pragma unroll 2
-                for (int c = 0; c < g.n_ctas; ++c) {
-                    const float f = ex2(__ldcg(slot_of(c) + rr) - mm);
-                    const float4* const src = reinterpret_cast<const float4*>(slot_of(c) + 2 * kTcRows) + (8 * c4) * kTcRows + rr;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 x = __ldcg(src + i * kTcRows);
-                        o[4 * i] = fmaf(x.x, f, o[4 * i]);
-                        o[4 * i + 1] = fmaf(x.y, f, o[4 * i + 1]);
-                        o[4 * i + 2] = fmaf(x.z, f, o[4 * i + 2]);
-                        o[4 * i + 3] = fmaf(x.w, f, o[4 * i + 3]);
-                    }
-                }
-                tc_emit(p, g, g.row0 + rr, D, 32 * c4, o, inv);
-            }
+            if (lane == 0) mbar_arrive(&seg_empty[ss]);
         }
     }
     __syncwarp();
@@ -701,11 +652,79 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     }
 }
 
+// ---- the groups that several CTAs share: their parts joined in CTA order -------------------------
+// CTA (group, 32 rows), a warp per 32 head values, a thread per row of them.  Bound by the parts' bytes,
+// which lie in L2; a kernel of its own, so that all SMs read them.
+template <int D>
+__global__ void __launch_bounds__(D) attn_tc_join_kernel(const AttnParams p, const int grid, unsigned* status)
+{
+    __shared__ AttnSegment g_s;
+    __shared__ int there_s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slab = blockIdx.x % (kTcRows / 32) * 32;
+    if (warp == 0) {
+        bool bad;
+        const AttnRange w = attn_cut(p, kTcRows, grid, 0, &bad);
+        AttnSegment g;
+        const bool there = attn_group(p, kTcRows, w, blockIdx.x / (kTcRows / 32), &g);
+        if (lane == 0) {
+            there_s = there && g.n_ctas > 1;
+            if (there_s) g_s = g;
+        }
+    }
+    griddep_wait();
+    __syncthreads();
+    if (!there_s) return;
+    const AttnSegment& g = g_s;
+    const int row = slab + lane, rows = min(kTcRows, g.T * p.group - g.row0);
+    if (row >= rows) return;
+    auto slot_of = [&](int c) {
+        return p.parts + (int64_t(g.cta0 + c) * 2 + (c == 0 ? g.slot0 : 0)) * attn_slot_floats(kTcRows, D);
+    };
+    float mm = kLowest, l = 0.0f, o[32];
+    bool gone = false;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+#pragma unroll 8
+    for (int c = 0; c < g.n_ctas; ++c) mm = fmaxf(mm, __ldcg(slot_of(c) + row));
+#pragma unroll 2
+    for (int c = 0; c < g.n_ctas; ++c) {
+        const float* const slot = slot_of(c);
+        const float lc = __ldcg(slot + kTcRows + row), f = ex2(__ldcg(slot + row) - mm);
+        const float4* const src = reinterpret_cast<const float4*>(slot + 2 * kTcRows) + 8 * warp * kTcRows + row;
+        gone |= lc < 0.0f;
+        l = fmaf(lc, f, l);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 x = __ldcg(src + i * kTcRows);
+            o[4 * i] = fmaf(x.x, f, o[4 * i]);
+            o[4 * i + 1] = fmaf(x.y, f, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(x.z, f, o[4 * i + 2]);
+            o[4 * i + 3] = fmaf(x.w, f, o[4 * i + 3]);
+        }
+    }
+    if (gone) {  // a page outside the cache: the group stays unwritten
+        atomicOr(status, MQ_DEV_KV_RANGE);
+        return;
+    }
+    tc_emit(p, g, g.row0 + row, D, 32 * warp, o, l == 0.0f ? 0.0f : 1.0f / l);
+}
+
 template <int D, bool Q8>
-cudaError_t launch_tc(const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
+cudaError_t launch_tc(const AttnParams& p, int grid, int64_t groups, unsigned* status, cudaStream_t s)
 {
     attn_tc_kernel<D, Q8><<<grid, kTcThreads, TcCfg<D, Q8>::kSmem, s>>>(p, status);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || grid == 1) return e;  // one CTA shares no group
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(groups * (kTcRows / 32)));
+    cfg.blockDim = dim3(D);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D>, p, grid, status);
 }
 
 }  // namespace
@@ -714,9 +733,12 @@ int attn_tc_rows() { return kTcRows; }
 
 cudaError_t launch_attn_tc(const mq_kv_cache& c, const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
 {
+    const int64_t groups = int64_t(c.n_seqs) * c.n_kv_heads * ((p.group * p.a.max_tokens + kTcRows - 1) / kTcRows);
     if (c.type == MQ_TYPE_Q8_0)
-        return c.head_dim == 128 ? launch_tc<128, true>(p, grid, status, s) : launch_tc<64, true>(p, grid, status, s);
-    return c.head_dim == 128 ? launch_tc<128, false>(p, grid, status, s) : launch_tc<64, false>(p, grid, status, s);
+        return c.head_dim == 128 ? launch_tc<128, true>(p, grid, groups, status, s)
+                                 : launch_tc<64, true>(p, grid, groups, status, s);
+    return c.head_dim == 128 ? launch_tc<128, false>(p, grid, groups, status, s)
+                             : launch_tc<64, false>(p, grid, groups, status, s);
 }
 
 cudaError_t set_attn_tc_attributes()
