@@ -4,23 +4,27 @@
 // The same sums as attn.cu; with dozens to hundreds of query rows per
 // key/value head every cached byte is used that often, and the products and
 // the exponentials bound it instead of the cache's bytes.  Per CTA (one per
-// SM, an equal share of all pages, mq_attn.cuh):
+// SM, an equal share of all pages, mq_attn.cuh), in steps of two pages:
 //   warps 0-3, 4-7  softmax of two tiles of 128 query rows, a thread per row
-//   warps 8-11      q8_0: codes to f16 in the tensor cores' layout; both
-//                   types: the values of pages that reach past the context
-//                   made finite
-//   warp 12         bulk copies of (page, head) blocks into a ring
+//   warps 8-11      the operands: q8_0 codes to f16 in the tensor cores'
+//                   layout; both types: the values of pages that reach past
+//                   the context made finite
+//   warp 12         segments, and bulk copies in the order of use: q8_0 into a
+//                   ring of half blocks, f16 into the operands themselves
 //   warp 13         tensor memory; one lane issues the MMAs
-// Tensor memory holds for each tile the queries (f16, the A operand), the
-// scores of one page (64 columns), in their place the probabilities (f16, the
-// A operand of the second product), and the fp32 outputs:
-//   S[128][64] = Q K^T        K from shared memory, K-major
+// Tensor memory holds for each tile the scores of a step (128 columns), in
+// their place the probabilities (f16, the A operand of the second product),
+// and the fp32 outputs:
+//   S[128][128] = Q K^T       Q and K from shared memory, K-major
 //   O[128][D] += P V          V from shared memory as it lies, MN-major
-// so that shared memory is read for one operand only.  While one tile's
-// probabilities are formed the other tile's products run: the issue order is
-// S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...  With more than 128 rows the
-// tiles are the rows' halves and both take every page; with fewer both hold
-// the same rows, take the pages in turn and are joined at the end.
+// Steps of 128 keys because an MMA of N = 64 takes as long as one of 128 (66
+// cycles measured).  While one tile's probabilities are formed the other
+// tile's products run: the issue order is
+//   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
+// and a step's second product starts when the first half of its probabilities
+// is there.  With more than 128 rows the tiles are the rows' halves and both
+// take every step; with fewer both hold the same rows, take the steps in turn
+// and are joined at the end.
 // Probabilities are 2^(s - m + 7) in f16, m the row's running maximum, which is
 // raised (and O rescaled in tensor memory) only when a score passes it by more
 // than 8, so they stay below 2^15; a key at 2^-21 of the largest is still a
@@ -34,34 +38,53 @@ namespace {
 
 constexpr int kTcRows = 256;  // query rows of a block
 constexpr int kTcSegs = 4;
-constexpr int kTcMaxStages = 12;
-constexpr int kTcThreads = 448;
-constexpr int kTcSmem = 218 * 1024;
+constexpr int kStep = 2 * kKvPage;  // keys
+constexpr int kConv = 4;  // operand warps
+constexpr int kConvThreads = 32 * kConv;
+constexpr int kWarpSeg = 8 + kConv, kWarpMma = kWarpSeg + 1;
+constexpr int kTcThreads = 32 * (kWarpMma + 1);
 constexpr float kTcRaise = 8.0f, kTcShift = 7.0f, kLowest = -3.402823466e38f;
-constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384;  // tensor memory columns of tile 0; of tile 1 behind
+constexpr uint32_t kColO = 0, kColS = 256;  // tensor memory columns of tile 0; of tile 1 128 further
 
+// Shared memory: a 128-row operand tile is D/64 planes of [128 rows][64 f16], each with the 128-byte swizzle.  K and V
+// tiles of a step pass through one ring, in the order of their use; q8_0 comes through a ring of units before, each
+// the codes and scales of a page's keys or values.
 template <int D, bool Q8>
 struct TcCfg {
-    using Raw = KvBlock<D, Q8>;
-    using Op = KvBlock<D, false>;  // the operands' layout: an f16 block
-    static constexpr int kJoin = 32 * 128 * 4;                // 32 outputs of 128 rows
-    // q8_0: a ring of blocks as they come, and buffers of operands; f16: the ring's blocks are the operands
-    static constexpr int kBufs = Q8 ? 3 : (kTcSmem - 1024 - kJoin) / Op::kBytes;
-    static constexpr int kFit = (kTcSmem - 1024 - kJoin - kBufs * Op::kBytes) / Raw::kBytes;
-    static constexpr int kStages = !Q8 ? kBufs : kFit < kTcMaxStages ? kFit : kTcMaxStages;
-    static constexpr int kSmem = 1024 + kBufs * Op::kBytes + (Q8 ? kStages * Raw::kBytes : 0) + kJoin;
-    static_assert(kStages >= 3 && kBufs <= 16 && kStages <= 16, "ring");
+    static constexpr int kPlane = 128 * 128;
+    static constexpr int kTile = D / 64 * kPlane;
+    static constexpr int kOps = D == 128 ? (Q8 ? 3 : 4) : 6;
+    static constexpr int kCodes = kKvPage * D, kUnit = kCodes + KvBlock<D, true>::kScBytes;
+    static constexpr int kUnits = !Q8 ? 0 : D == 128 ? 6 : 12;
+    static constexpr int kSmem = 1024 + 2 * kTile + kOps * kTile + kUnits * kUnit;
 };
+// byte of 16-byte chunk c of row r of an operand tile
+__device__ __forceinline__ int tc_chunk(int r, int c)
+{
+    return (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// The order of a segment's 2n tiles, by position: K(0) V(0) K(1) V(1) .. where both tiles of rows take every step, and
+// where they take the steps in turn the scores are a step further ahead: K(0) K(1) V(0) K(2) V(1) .. V(n-1).
+struct TcTile {
+    int is_v, step;
+};
+__device__ __forceinline__ TcTile tc_tile_at(int pos, int n, bool halves)
+{
+    if (halves) return TcTile{pos & 1, pos >> 1};
+    if (pos == 0) return TcTile{0, 0};
+    if (pos == 2 * n - 1) return TcTile{1, n - 1};
+    return pos & 1 ? TcTile{0, (pos + 1) >> 1} : TcTile{1, (pos - 2) >> 1};
+}
+__device__ __forceinline__ int tc_pos_k(int st, bool halves) { return halves ? 2 * st : st == 0 ? 0 : 2 * st - 1; }
+__device__ __forceinline__ int tc_pos_v(int st, int n, bool halves)
+{
+    return halves ? 2 * st + 1 : st == n - 1 ? 2 * n - 1 : 2 * st + 2;
+}
 
 struct TcSegment {
     AttnSegment g;
     int odd, bad;  // a value that is not finite was dropped; a page outside the cache
-};
-
-// what a ring stage holds
-struct TcPage {
-    int key0, ctx, len, seg;
-    int bad;
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -134,91 +157,108 @@ __device__ __forceinline__ uint32_t drop_pair(uint32_t v)
     return v;
 }
 
-// ---- the values of one page, made operands (warps 8-11, thread x of 128) -----------------------
-template <int D, bool Q8>
-__device__ __forceinline__ bool tc_convert(const uint8_t* raw, uint8_t* op, const TcPage& pg, int x)
+// ---- operands (warps 8-11, thread x of 128): 64 rows from row0 on of a tile ----------------------
+// q8_0 codes and scales of a unit; values (is_v) of a page from key key0 that reaches past the context are made
+// finite: true where some were not
+template <int D>
+__device__ __forceinline__ bool tc_convert(const uint8_t* unit, uint8_t* tile, int row0, bool tail, int key0, int len, int x)
 {
-    using R = KvBlock<D, Q8>;
-    using O = KvBlock<D, false>;
-    const bool tail = pg.key0 + kKvPage > pg.ctx;
+    using R = KvBlock<D, true>;
+    constexpr int N = D / 32;  // 16-byte chunks of codes per thread, all loaded before the first is stored
+    uint4 in[N];
+    uint32_t d[N];
     bool odd = false;
-    if (Q8) {
-        constexpr int CH = D / 16;  // 16-code chunks of a row
-        constexpr int kBatch = 4;   // loads in flight before the first store (which might be to the same place, for all
-                                    // that the compiler knows)
-#pragma unroll 1
-        for (int i0 = 0; i0 < 2 * kKvPage * CH / 128; i0 += kBatch) {
-            uint4 in[kBatch];
-            uint32_t d[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int item = (i0 + i) * 128 + x, is_v = item / (kKvPage * CH), r = item / CH % kKvPage, c = item % CH;
-                in[i] = lds16(raw + (is_v ? R::kVOff : 0) + R::chunk(r, c));
-                d[i] = *reinterpret_cast<const uint16_t*>(raw + R::kScK + (is_v ? R::kScBytes : 0) +
-                                                          (r * (D / 32) + (c >> 1)) * 2) * 0x10001u;
-            }
+    for (int i = 0; i < N; ++i) {
+        const int r = (i * kConvThreads + x) / (D / 16), c = x % (D / 16);
+        in[i] = lds16(unit + R::chunk(r, c));
+        d[i] = *reinterpret_cast<const uint16_t*>(unit + kKvPage * D + (r * (D / 32) + (c >> 1)) * 2) * 0x10001u;
+    }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int item = (i0 + i) * 128 + x, is_v = item / (kKvPage * CH), r = item / CH % kKvPage, c = item % CH;
-                const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-                uint32_t u[8];
+    for (int i = 0; i < N; ++i) {
+        const int r = (i * kConvThreads + x) / (D / 16), c = x % (D / 16);
+        const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+        uint32_t u[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    u[2 * k] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4140), d[i]);
-                    u[2 * k + 1] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4342), d[i]);
-                }
-                if (tail && is_v) {
-                    const bool out = pg.key0 + r >= pg.len;
+        for (int k = 0; k < 4; ++k) {
+            u[2 * k] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4140), d[i]);
+            u[2 * k + 1] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4342), d[i]);
+        }
+        if (tail) {
+            const bool out = key0 + r >= len;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        if (out) u[k] = 0;
-                        if (pair_not_finite(u[k])) odd = true, u[k] = drop_pair(u[k]);
-                    }
-                }
-                uint8_t* const dst = op + (is_v ? O::kVOff : 0);
-                // the lanes of the second plane store their halves in the other order: no bank twice
-                const bool swap = (c & 4) != 0;
-                const uint4 lo = make_uint4(u[0], u[1], u[2], u[3]), hi = make_uint4(u[4], u[5], u[6], u[7]);
-                *reinterpret_cast<uint4*>(dst + O::chunk(r, 2 * c + (swap ? 1 : 0))) = swap ? hi : lo;
-                *reinterpret_cast<uint4*>(dst + O::chunk(r, 2 * c + (swap ? 0 : 1))) = swap ? lo : hi;
+            for (int k = 0; k < 8; ++k) {
+                if (out) u[k] = 0;
+                if (pair_not_finite(u[k])) odd = true, u[k] = drop_pair(u[k]);
             }
         }
-    } else if (tail) {
-        for (int item = x; item < kKvPage * (D / 8); item += 128) {
-            const int r = item / (D / 8);
-            uint4* const v = reinterpret_cast<uint4*>(op + O::kVOff + O::chunk(r, item % (D / 8)));
-            if (pg.key0 + r >= pg.len) {
-                *v = make_uint4(0, 0, 0, 0);
-                continue;
-            }
-            uint4 y = *v;
-            if (pair_not_finite(y.x) || pair_not_finite(y.y) || pair_not_finite(y.z) || pair_not_finite(y.w)) {
-                odd = true;
-                y.x = drop_pair(y.x), y.y = drop_pair(y.y), y.z = drop_pair(y.z), y.w = drop_pair(y.w);
-                *v = y;
-            }
+        // the lanes of the second plane store their halves in the other order: no bank twice
+        const bool swap = (c & 4) != 0;
+        const uint4 lo = make_uint4(u[0], u[1], u[2], u[3]), hi = make_uint4(u[4], u[5], u[6], u[7]);
+        *reinterpret_cast<uint4*>(tile + tc_chunk(row0 + r, 2 * c + (swap ? 1 : 0))) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(tile + tc_chunk(row0 + r, 2 * c + (swap ? 0 : 1))) = swap ? lo : hi;
+    }
+    return odd;
+}
+// f16 values that are operands already
+template <int D>
+__device__ __forceinline__ bool tc_clean(uint8_t* tile, int row0, int key0, int len, int x)
+{
+    bool odd = false;
+    for (int i = x; i < kKvPage * (D / 8); i += kConvThreads) {
+        const int r = i / (D / 8);
+        uint4* const v = reinterpret_cast<uint4*>(tile + tc_chunk(row0 + r, i % (D / 8)));
+        if (key0 + r >= len) {
+            *v = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        uint4 y = *v;
+        if (pair_not_finite(y.x) || pair_not_finite(y.y) || pair_not_finite(y.z) || pair_not_finite(y.w)) {
+            odd = true;
+            y.x = drop_pair(y.x), y.y = drop_pair(y.y), y.z = drop_pair(y.z), y.w = drop_pair(y.w);
+            *v = y;
         }
     }
     return odd;
 }
-
-// the row's share of values that were dropped: what is not finite and seen makes the output what it is
-template <int D, bool Q8>
-__device__ __noinline__ void tc_add_dropped(const AttnParams& p, const AttnSegment& g, uint64_t mask, int d0,
-                                            float (&o)[32])
+// zeros
+template <int D>
+__device__ __forceinline__ void tc_zero(uint8_t* tile, int row0, int x)
 {
-    for (int pg = max(g.page0, g.ctx / kKvPage); pg < g.page0 + g.n; ++pg) {
-        const int64_t page = kv_page_of(p.c, g.seq, pg * kKvPage, int64_t(p.c.n_kv_heads) * KvBlock<D, Q8>::kBytes);
-        if (page < 0) continue;
-        const uint8_t* const blk = p.c.pages + page + int64_t(g.head) * KvBlock<D, Q8>::kBytes;
-        for (int r = 0; r < kKvPage; ++r) {
-            const int j = pg * kKvPage + r;
-            if (j >= g.ctx + g.T || (j >= g.ctx && !((mask >> (j - g.ctx)) & 1))) continue;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float v = kv_value<D, Q8>(blk, r, d0 + i, 1);
-                if (!(v - v == 0.0f)) o[i] += v;
+    for (int i = x; i < kKvPage * (D / 8); i += kConvThreads)
+        *reinterpret_cast<uint4*>(tile + tc_chunk(row0 + i / (D / 8), i % (D / 8))) = make_uint4(0, 0, 0, 0);
+}
+
+// A row's outputs d0 .. d0 + 31 are written (to slot, or where tc_emit puts them): what was dropped because it is
+// not finite, and the row sees, makes an output what it is (of a q8_0 block, its scale).
+template <int D, bool Q8>
+__device__ __noinline__ void tc_add_dropped(const AttnParams& p, const AttnSegment& g, int row, uint64_t mask, int d0,
+                                            float* slot)
+{
+    const int node = attn_row_token(p, row), h = (g.head - node) * p.group + row;
+    const int64_t tok = g.t0 + node;
+    for (int d = d0; d < d0 + 32; ++d) {
+        float add = 0.0f;
+        for (int pg = max(g.page0, g.ctx / kKvPage); pg < g.page0 + g.n; ++pg) {
+            const int64_t page = kv_page_of(p.c, g.seq, pg * kKvPage, int64_t(p.c.n_kv_heads) * KvBlock<D, Q8>::kBytes);
+            if (page < 0) continue;
+            const uint8_t* const blk = p.c.pages + page + int64_t(g.head) * KvBlock<D, Q8>::kBytes;
+            for (int r = 0; r < kKvPage; ++r) {
+                const int j = pg * kKvPage + r;
+                if (j >= g.ctx + g.T || (j >= g.ctx && !((mask >> (j - g.ctx)) & 1))) continue;
+                const float v = kv_value<D, Q8>(blk, r, d, 1);
+                if (!(v - v == 0.0f)) add += v;
             }
+        }
+        if (add == 0.0f) continue;
+        if (slot) {
+            slot[2 * kTcRows + (d / 4 * kTcRows + row - g.row0) * 4 + d % 4] += add;
+        } else if (p.a.out_type == MQ_TYPE_F16) {
+            __half* const o = static_cast<__half*>(p.a.out) + tok * p.a.out_ld + h * D + d;
+            *o = __float2half_rn(__half2float(*o) + add);
+        } else {
+            *reinterpret_cast<__half*>(static_cast<uint8_t*>(p.a.out) +
+                                       (tok * (p.a.n_heads * D / 32) + (h * D + d) / 32) * kQ8Bytes) = __float2half_rn(add);
         }
     }
 }
@@ -259,46 +299,48 @@ template <int D, bool Q8>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams p, unsigned* status)
 {
     using C = TcCfg<D, Q8>;
-    using Raw = typename C::Raw;
-    using Op = typename C::Op;
-    constexpr int kBufs = C::kBufs, kStages = C::kStages;
+    using B = KvBlock<D, Q8>;
+    constexpr int kOps = C::kOps, kUnits = Q8 ? C::kUnits : 1;
     extern __shared__ uint8_t sm_raw[];
-    __shared__ __align__(8) uint64_t raw_full[kStages], raw_free[kStages], kv_ready[kBufs], kv_free[kBufs];
-    __shared__ __align__(8) uint64_t q_ready[2], s_ready[2], p_ready[2], o_done[2], seg_full[kTcSegs], seg_empty[kTcSegs];
+    __shared__ __align__(8) uint64_t unit_full[kUnits], unit_free[kUnits], op_full[kOps], op_ready[kOps], op_free[kOps];
+    __shared__ int unit_bad[kUnits], op_bad[kOps];  // (page of the tile: bit) not in the cache, so not copied
+    __shared__ __align__(8) uint64_t q_ready[2], s_ready[2], p_ready[2][2], o_done[2], seg_full[kTcSegs], seg_empty[kTcSegs];
     __shared__ TcSegment seg_s[kTcSegs];
-    __shared__ TcPage page_s[kStages];
     __shared__ float join_m[2][128], join_l[2][128];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the swizzled tiles want 1024-byte alignment
     uint8_t* const sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
-    uint8_t* const ops = sm;                                          // operand buffers (f16: the ring)
-    uint8_t* const ring = Q8 ? sm + kBufs * Op::kBytes : sm;
-    float* const join = reinterpret_cast<float*>(sm + kBufs * Op::kBytes + (Q8 ? kStages * Raw::kBytes : 0));
+    uint8_t* const q_s = sm;
+    uint8_t* const op_s = sm + 2 * C::kTile;
+    uint8_t* const unit_s = op_s + kOps * C::kTile;
+    float* const join = reinterpret_cast<float*>(q_s + C::kTile);  // [32][128]; tile 1's queries are not used then
 
-    if (threadIdx.x < kStages) {
-        mbar_init(&raw_full[threadIdx.x], 1);
-        mbar_init(&raw_free[threadIdx.x], 4);
-    } else if (threadIdx.x >= 32 && threadIdx.x < 32 + kBufs) {
-        mbar_init(&kv_ready[threadIdx.x - 32], 4);
-        mbar_init(&kv_free[threadIdx.x - 32], 1);
+    if (threadIdx.x < kOps) {
+        mbar_init(&op_full[threadIdx.x], 1);
+        mbar_init(&op_ready[threadIdx.x], kConv);
+        mbar_init(&op_free[threadIdx.x], 1);
+    } else if (threadIdx.x >= 32 && threadIdx.x < 32 + kUnits) {
+        mbar_init(&unit_full[threadIdx.x - 32], 1);
+        mbar_init(&unit_free[threadIdx.x - 32], kConv);
     } else if (threadIdx.x >= 64 && threadIdx.x < 66) {
         const int k = threadIdx.x - 64;
         mbar_init(&q_ready[k], 4);
         mbar_init(&s_ready[k], 1);
-        mbar_init(&p_ready[k], 4);
+        mbar_init(&p_ready[k][0], 4);
+        mbar_init(&p_ready[k][1], 4);
         mbar_init(&o_done[k], 1);
     } else if (threadIdx.x >= 96 && threadIdx.x < 96 + kTcSegs) {
         mbar_init(&seg_full[threadIdx.x - 96], 1);
-        mbar_init(&seg_empty[threadIdx.x - 96], 8 + 4 + 1);  // softmax and converter warps, the MMA warp
+        mbar_init(&seg_empty[threadIdx.x - 96], 8 + kConv + 1);  // softmax and operand warps, the MMA warp
         if (threadIdx.x == 96) abort_flag = 0;
     }
     fence_barrier_init();
     griddep_launch_dependents();  // the join may take its place; it waits for this grid's end
     AttnRange w;
-    if (warp == 12) w = attn_range(p, kTcRows, status);
-    if (warp == 13) tmem_alloc(&tmem_base, 512);
+    if (warp == kWarpSeg) w = attn_range(p, kTcRows, status);
+    if (warp == kWarpMma) tmem_alloc(&tmem_base, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -312,18 +354,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         return ok;
     };
 
-    if (warp == 12) {
-        // ---- producer
+    if (warp == kWarpSeg) {
+        // ---- segments and copies; lane h: page h of a step
         AttnSegment g = {};
-        int at = w.first, it = 0, sg = 0, s = 0;
-        uint32_t phase = 0;
+        int at = w.first, sg = 0, k = 0, u = 0;  // k: tiles before; u: units before
         bool ok = true, more = true;
         for (; ok && more; ++sg) {
             more = attn_next(p, kTcRows, &w, &at, &g);
             if (!more) g.n = g.T = 0;
             const int ss = sg % kTcSegs;
-            const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0;
-            int32_t page_l = lane < g.n ? __ldg(table + lane) : 0;
             if (sg >= kTcSegs) ok = wait_all(&seg_empty[ss], uint32_t(sg / kTcSegs - 1) & 1u);
             if (!ok) break;
             if (lane == 0) {
@@ -332,140 +371,196 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 mbar_arrive(&seg_full[ss]);
             }
             __syncwarp();
-            for (int i0 = 0; ok && i0 < g.n; i0 += 32) {
-                const int32_t page_now = page_l;
-                if (i0 + 32 + lane < g.n) page_l = __ldg(table + i0 + 32 + lane);
-                const int m = min(32, g.n - i0);
-                for (int i = 0; i < m; ++i, ++it) {
-                    const int32_t page = __shfl_sync(0xffffffffu, page_now, i);
-                    // f16: the block is the operand, and the MMAs free it
-                    if (it >= kStages) ok = wait_all(Q8 ? &raw_free[s] : &kv_free[s], phase ^ 1u);
+            const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0;
+            const int n = (g.n + 1) / 2;
+            const bool halves = g.T * p.group - g.row0 > 128;
+            for (int pos = 0; ok && pos < 2 * n; ++pos, ++k) {
+                const TcTile tl = tc_tile_at(pos, n, halves);
+                const int i = 2 * tl.step + (lane & 1), pages = min(2, g.n - 2 * tl.step);
+                const int64_t page = i < g.n ? __ldg(table + i) : -1;
+                const bool there = page >= 0 && page < p.c.n_pages;  // table entries are not trusted
+                const unsigned both = __ballot_sync(0xffffffffu, there) & 3u;
+                const uint8_t* const src = p.c.pages + (there ? (page * p.c.n_kv_heads + g.head) * B::kBytes : 0);
+                if (Q8) {
+                    for (int h = 0; ok && h < pages; ++h, ++u) {
+                        const int s = u % kUnits;
+                        if (u >= kUnits) ok = wait_all(&unit_free[s], uint32_t(u / kUnits - 1) & 1u);
+                        if (!ok) break;
+                        if (lane == h) {
+                            uint8_t* const dst = unit_s + s * C::kUnit;
+                            unit_bad[s] = !there;
+                            if (there) {
+                                mbar_arrive_expect_tx(&unit_full[s], C::kUnit);
+                                bulk_copy_g2s(dst, src + (tl.is_v ? B::kVOff : 0), C::kCodes, &unit_full[s]);
+                                bulk_copy_g2s(dst + C::kCodes, src + B::kScK + (tl.is_v ? B::kScBytes : 0), B::kScBytes,
+                                              &unit_full[s]);
+                            } else {
+                                mbar_arrive(&unit_full[s]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    const int b = k % kOps;
+                    if (k >= kOps) ok = wait_all(&op_free[b], uint32_t(k / kOps - 1) & 1u);
                     if (!ok) break;
                     if (lane == 0) {
-                        const bool bad = page < 0 || page >= p.c.n_pages;  // table entries are not trusted
-                        page_s[s] = TcPage{(g.page0 + i0 + i) * kKvPage, g.ctx, g.ctx + g.T, ss, bad};
-                        if (bad) {
-                            mbar_arrive(&raw_full[s]);
-                        } else {
-                            mbar_arrive_expect_tx(&raw_full[s], Raw::kBytes);
-                            bulk_copy_g2s(ring + s * Raw::kBytes,
-                                          p.c.pages + (int64_t(page) * p.c.n_kv_heads + g.head) * Raw::kBytes,
-                                          Raw::kBytes, &raw_full[s]);
-                        }
+                        op_bad[b] = int(~both & (pages == 2 ? 3u : 1u));
+                        if (both)
+                            mbar_arrive_expect_tx(&op_full[b], uint32_t(__popc(both)) * (kKvPage * D * 2));
+                        else
+                            mbar_arrive(&op_full[b]);
                     }
-                    if (++s == kStages) s = 0, phase ^= 1u;
+                    __syncwarp();
+                    if (lane < 2 && there) {
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            bulk_copy_g2s(op_s + b * C::kTile + x * C::kPlane + lane * (kKvPage * 128),
+                                          src + (tl.is_v ? B::kVOff : 0) + x * (kKvPage * 128), kKvPage * 128, &op_full[b]);
+                    }
                 }
             }
         }
         // copies still in flight land before the CTA can exit
-        for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
-            (void)mbar_wait_bounded(&raw_full[j % kStages], uint32_t(j / kStages) & 1u, p.limit_ns);
-    } else if (warp >= 8 && warp < 12) {
-        // ---- operands: the pages in order, every segment's
-        int s = 0, b = 0, it = 0;
-        uint32_t phase = 0, bphase = 0;
+        if (Q8) {
+            for (int j = u > kUnits ? u - kUnits : 0; j < u; ++j)
+                (void)mbar_wait_bounded(&unit_full[j % kUnits], uint32_t(j / kUnits) & 1u, p.limit_ns);
+        } else {
+            for (int j = k > kOps ? k - kOps : 0; j < k; ++j)
+                (void)mbar_wait_bounded(&op_full[j % kOps], uint32_t(j / kOps) & 1u, p.limit_ns);
+        }
+    } else if (warp >= 8 && warp < kWarpSeg) {
+        // ---- operands, tile by tile
+        const int x = threadIdx.x - 256;
+        int k = 0, s = 0;  // tiles before; unit
+        uint32_t sph = 0;
         bool ok = true;
         for (int sg = 0; ok; ++sg) {
             const int ss = sg % kTcSegs;
             ok = wait_all(&seg_full[ss], uint32_t(sg / kTcSegs) & 1u);
             if (!ok) break;
-            const int n = seg_s[ss].g.n;
+            const AttnSegment& g = seg_s[ss].g;
+            const int n = (g.n + 1) / 2, gn = g.n, key_base = g.page0 * kKvPage, ctx = g.ctx, len = g.ctx + g.T;
+            const bool halves = g.T * p.group - g.row0 > 128;
             if (n == 0) break;
-            for (int i = 0; i < n; ++i, ++it) {
-                ok = wait_all(&raw_full[s], phase);
-                if (Q8 && it >= kBufs) ok = ok && wait_all(&kv_free[b], bphase ^ 1u);
+            for (int pos = 0; pos < 2 * n; ++pos, ++k) {
+                const TcTile tl = tc_tile_at(pos, n, halves);
+                const int b = k % kOps;
+                uint8_t* const tile = op_s + b * C::kTile;
+                if (Q8)
+                    ok = k < kOps || wait_all(&op_free[b], uint32_t(k / kOps - 1) & 1u);
+                else
+                    ok = wait_all(&op_full[b], uint32_t(k / kOps) & 1u);
                 if (!ok) break;
-                const TcPage pg = page_s[s];
-                uint8_t* const op = ops + (Q8 ? b * Op::kBytes : s * Op::kBytes);
-                bool odd = false;
-                if (!pg.bad) odd = tc_convert<D, Q8>(ring + s * Raw::kBytes, op, pg, (warp - 8) * 32 + lane);
+                bool odd = false, bad = false;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int pg = 2 * tl.step + h, key0 = key_base + pg * kKvPage;
+                    const bool tail = tl.is_v && key0 + kKvPage > ctx;
+                    bool there = pg < gn;
+                    if (Q8 && there) {
+                        ok = wait_all(&unit_full[s], sph);
+                        if (!ok) break;
+                        there = !unit_bad[s];
+                        bad |= !there;
+                        if (there) odd |= tc_convert<D>(unit_s + s * C::kUnit, tile, h * kKvPage, tail, key0, len, x);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&unit_free[s]);
+                        if (++s == kUnits) s = 0, sph ^= 1u;
+                    } else if (there) {
+                        there = !(op_bad[b] >> h & 1);
+                        bad |= !there;
+                        if (there && tail) odd |= tc_clean<D>(tile, h * kKvPage, key0, len, x);
+                    }
+                    // such values weigh nothing, but they are multiplied with the weight 0
+                    if (!there && tl.is_v) tc_zero<D>(tile, h * kKvPage, x);
+                }
+                if (!ok) break;
                 if (odd) seg_s[ss].odd = 1;
-                if (pg.bad && lane == 0) seg_s[ss].bad = 1;
+                if (bad && lane == 0) seg_s[ss].bad = 1;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) {
-                    if (Q8) mbar_arrive(&raw_free[s]);
-                    mbar_arrive(&kv_ready[Q8 ? b : s]);
-                }
-                if (++s == kStages) s = 0, phase ^= 1u;
-                if (++b == kBufs) b = 0, bphase ^= 1u;
+                if (lane == 0) mbar_arrive(&op_ready[b]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_empty[ss]);
         }
-    } else if (warp == 13) {
+    } else if (warp == kWarpMma) {
         // ---- MMA issuer
         if (lane == 0) {
-            constexpr uint32_t idesc_s = umma_idesc_f16_f32(128, kKvPage);
+            constexpr uint32_t idesc_s = umma_idesc_f16_f32(128, kStep);
             constexpr uint32_t idesc_o = umma_idesc_f16_f32(128, D) | kBMajorMn;
-            // operand buffer 0; an address within it or in another is added to the descriptor's address field
-            const uint64_t ops_k = umma_desc_sw128(smem_u32(ops)), ops_v = umma_desc_mn(smem_u32(ops) + Op::kVOff, kKvPage * 128);
+            // tile 0 of the queries, operand 0 as K and as V; an address within or in another is added to the
+            // descriptor's address field
+            const uint64_t q_d = umma_desc_sw128(smem_u32(q_s)), k_d = umma_desc_sw128(smem_u32(op_s)),
+                           v_d = umma_desc_mn(smem_u32(op_s), C::kPlane);
             auto wait_one = [&](uint64_t* bar, uint32_t parity) {
                 if (!abort_flag && mbar_wait_bounded(bar, parity, p.limit_ns)) return true;
                 abort_flag = 1;
                 return false;
             };
-            int it = 0;              // pages before this segment
+            int it = 0;  // tiles before this segment
             uint32_t pph[2] = {0, 0}, qph = 0;  // phases of p_ready and q_ready
             bool ok = true;
             for (int sg = 0; ok; ++sg) {
                 const int ss = sg % kTcSegs;
                 ok = wait_one(&seg_full[ss], uint32_t(sg / kTcSegs) & 1u);
                 if (!ok) break;
-                const int n = seg_s[ss].g.n;
+                const int n = (seg_s[ss].g.n + 1) / 2;  // steps
                 if (n == 0) break;
                 const bool halves = seg_s[ss].g.T * p.group - seg_s[ss].g.row0 > 128;
                 const int items = halves ? 2 * n : n;
                 mbar_arrive(&seg_empty[ss]);
                 ok = wait_one(&q_ready[0], qph) && wait_one(&q_ready[1], qph);
                 qph ^= 1u;
-                int ready = 0;  // pages of the segment known to be there
                 auto scores = [&](int j) {
-                    const int pg = halves ? j >> 1 : j, t = j & 1, k = it + pg, b = k % kBufs;
-                    if (pg >= ready) {
-                        if (!wait_one(&kv_ready[b], uint32_t(k / kBufs) & 1u)) return false;
-                        ready = pg + 1;
-                    }
+                    const int st = halves ? j >> 1 : j, t = j & 1, k = it + tc_pos_k(st, halves), b = k % kOps;
+                    if ((!halves || t == 0) && !wait_one(&op_ready[b], uint32_t(k / kOps) & 1u)) return false;
                     tc_fence_after();
-                    const uint64_t kd = ops_k + uint64_t(b * (Op::kBytes >> 4));
-                    umma_f16_ts(tmem + kColS + 64 * t, tmem + kColQ + 64 * t, kd, idesc_s, false);
+                    const uint64_t ad = q_d + (halves && t ? C::kTile >> 4 : 0), bd = k_d + uint64_t(b * (C::kTile >> 4));
+                    umma_f16(tmem + kColS + 128 * t, ad, bd, idesc_s, false);
 #pragma unroll
-                    for (int x = 1; x < D / 16; ++x)
-                        umma_f16_ts(tmem + kColS + 64 * t, tmem + kColQ + 64 * t + 8 * x,
-                                    kd + (((x >> 2) * (kKvPage * 128) + 32 * (x & 3)) >> 4), idesc_s, true);
+                    for (int x = 1; x < D / 16; ++x) {
+                        const uint32_t off = ((x >> 2) * C::kPlane + 32 * (x & 3)) >> 4;
+                        umma_f16(tmem + kColS + 128 * t, ad + off, bd + off, idesc_s, true);
+                    }
                     umma_commit(&s_ready[t]);
+                    if (!halves || t == 1) umma_commit(&op_free[b]);  // the tile's last use
                     return true;
                 };
                 for (int j = 0; ok && j < min(2, items); ++j) ok = scores(j);
                 for (int j = 0; ok && j < items; ++j) {
-                    const int pg = halves ? j >> 1 : j, t = j & 1, b = (it + pg) % kBufs;
-                    ok = wait_one(&p_ready[t], pph[t]);
+                    const int st = halves ? j >> 1 : j, t = j & 1, k = it + tc_pos_v(st, n, halves), b = k % kOps;
+                    const uint64_t bd = v_d + uint64_t(b * (C::kTile >> 4));
+                    if (!halves || t == 0) ok = wait_one(&op_ready[b], uint32_t(k / kOps) & 1u);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && wait_one(&p_ready[t][h], pph[t]);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int x = 4 * h; x < 4 * h + 4; ++x)
+                            umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * x, bd + ((2048 * x) >> 4),
+                                        idesc_o, x > 0 || j > 1);
+                    }
                     if (!ok) break;
                     pph[t] ^= 1u;
-                    tc_fence_after();
-                    const uint64_t vd = ops_v + uint64_t(b * (Op::kBytes >> 4));
-                    umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 64 * t, vd, idesc_o, j > 1);
-#pragma unroll
-                    for (int x = 1; x < kKvPage / 16; ++x)
-                        umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 64 * t + 8 * x, vd + ((2048 * x) >> 4), idesc_o,
-                                    true);
-                    if (!halves || t == 1) umma_commit(&kv_free[b]);  // the page's last use
+                    if (!halves || t == 1) umma_commit(&op_free[b]);
                     if (j + 2 < items)
                         ok = scores(j + 2);
                     else
                         umma_commit(&o_done[t]);
                 }
-                it += n;
+                it += 2 * n;
             }
             // what was issued completes before tensor memory is freed
-            if (it > 0) (void)mbar_wait_bounded(&kv_free[(it - 1) % kBufs], uint32_t((it - 1) / kBufs) & 1u, p.limit_ns);
+            if (it > 0) (void)mbar_wait_bounded(&op_free[(it - 1) % kOps], uint32_t((it - 1) / kOps) & 1u, p.limit_ns);
         }
     } else {
         // ---- softmax: tile t, thread = row = tensor memory lane
         const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
         const uint32_t lanes = uint32_t(wq * 32) << 16;
-        const uint32_t tS = tmem + lanes + kColS + 64 * t, tO = tmem + lanes + kColO + 128 * t,
-                       tQ = tmem + lanes + kColQ + 64 * t;
+        const uint32_t tS = tmem + lanes + kColS + 128 * t, tO = tmem + lanes + kColO + 128 * t;
         const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;  // scores of -q, so that the scale is positive
         const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);     // not 0: -inf * 0 is no score
         uint32_t sph = 0, oph = 0;
@@ -474,32 +569,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             const int ss = sg % kTcSegs;
             bool ok = good && wait_all(&seg_full[ss], uint32_t(sg / kTcSegs) & 1u);
             const AttnSegment& g = seg_s[ss].g;
-            const int n = ok ? g.n : 0, rows = n ? min(kTcRows, g.T * p.group - g.row0) : 0;
+            const int n = ok ? (g.n + 1) / 2 : 0, rows = n ? min(kTcRows, g.T * p.group - g.row0) : 0;
             const bool halves = rows > 128;
             const int row = g.row0 + r + (halves ? 128 * t : 0);
             const bool mine = r + (halves ? 128 * t : 0) < rows;  // a row of the block
-            const int ctx = g.ctx, len = ctx + g.T;
+            const int ctx = g.ctx, len = ctx + g.T, end = (g.page0 + g.n) * kKvPage;
             uint64_t mask = 0;
             float m = kLowest, l = 0.0f;
-            const int steps = n == 0 ? 0 : halves ? n : (n + 1 - t) / 2;  // pages of this tile
+            const int steps = n == 0 ? 0 : halves ? n : (n + 1 - t) / 2;  // of this tile
             if (n) {
                 const int node = attn_row_token(p, row);
                 if (mine) mask = p.a.mask ? __ldg(p.a.mask + g.t0 + node) : ~0ull >> (63 - node);
-                const uint4* const src = reinterpret_cast<const uint4*>(
-                    static_cast<const __half*>(p.a.q) + int64_t(g.t0 + node) * p.a.q_ld +
-                    ((g.head - node) * p.group + row) * D);
+                if (halves || t == 0) {
+                    const uint4* const src = reinterpret_cast<const uint4*>(
+                        static_cast<const __half*>(p.a.q) + int64_t(g.t0 + node) * p.a.q_ld +
+                        ((g.head - node) * p.group + row) * D);
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint4 x = mine ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
-                        v[4 * i] = x.x ^ flip, v[4 * i + 1] = x.y ^ flip, v[4 * i + 2] = x.z ^ flip, v[4 * i + 3] = x.w ^ flip;
+                    for (int c = 0; c < D / 8; ++c) {
+                        uint4 v = mine ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                        v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+                        *reinterpret_cast<uint4*>(q_s + t * C::kTile + tc_chunk(r, c)) = v;
                     }
-                    tmem_st32(tQ + 32 * c, v);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
-                tmem_st_wait();
-                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_ready[t]);
             }
@@ -508,27 +600,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 if (!ok) break;
                 sph ^= 1u;
                 tc_fence_after();
-                uint32_t v[2][32];
-                tmem_ld32(tS, v[0]);
-                tmem_ld32(tS + 32, v[1]);
-                tmem_ld_wait();
-                const int key0 = (g.page0 + (halves ? i : 2 * i + t)) * kKvPage;
-                if (key0 + kKvPage > ctx) {
-                    // bit k: the row sees key key0 + k
-                    uint64_t see = key0 >= ctx ? 0 : ~0ull >> (kKvPage - (ctx - key0));  // ctx - key0 is 1..63
-                    const int nodes = len - max(ctx, key0);  // tree nodes from the page's first on
-                    uint64_t tree = key0 >= ctx ? (key0 - ctx < 64 ? mask >> (key0 - ctx) : 0) : mask << (ctx - key0);
-                    if (nodes < 64) tree &= key0 >= ctx ? (1ull << nodes) - 1 : ((1ull << nodes) - 1) << (ctx - key0);
-                    see |= tree;
+                const int key0 = g.page0 * kKvPage + (halves ? i : 2 * i + t) * kStep;
+                // bit k of see[h]: the row sees key key0 + 64h + k
+                uint64_t see[2] = {~0ull, ~0ull};
+                const bool tail = key0 + kStep > ctx || key0 + kStep > end;
+                if (tail) {
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
-                        if (!((see >> k) & 1)) v[k >> 5][k & 31] = 0xff800000u;
+                    for (int h = 0; h < 2; ++h) {
+                        const int k0 = key0 + h * kKvPage, past = k0 - ctx;  // nodes before the page; < 0: context left
+                        if (k0 >= min(end, len)) {
+                            see[h] = 0;
+                        } else if (past < 0) {
+                            const uint64_t nodes = g.T < 64 ? mask & ((1ull << g.T) - 1) : mask;
+                            see[h] = past <= -kKvPage ? ~0ull : ~0ull >> (kKvPage + past) | nodes << -past;
+                        } else {  // past < 64, since k0 < len
+                            see[h] = (g.T < 64 ? mask & ((1ull << g.T) - 1) : mask) >> past;
+                        }
+                    }
                 }
+                // scores 64h .. 64h + 63 of the row
+                auto load = [&](int h, uint32_t (&v)[2][32]) {
+                    tmem_ld32(tS + 64 * h, v[0]);
+                    tmem_ld32(tS + 64 * h + 32, v[1]);
+                    tmem_ld_wait();
+                    if (tail) {
+#pragma unroll
+                        for (int k = 0; k < 64; ++k)
+                            if (!((see[h] >> k) & 1)) v[k >> 5][k & 31] = 0xff800000u;
+                    }
+                };
+                // the maximum first, then the numbers again: tensor memory is read faster than registers spill
                 float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    x0 = fmaxf(x0, __uint_as_float(v[0][k]));
-                    x1 = fmaxf(x1, __uint_as_float(v[1][k]));
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[2][32];
+                    load(h, v);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        x0 = fmaxf(x0, __uint_as_float(v[0][k]));
+                        x1 = fmaxf(x1, __uint_as_float(v[1][k]));
+                    }
                 }
                 // raised for the lanes that need it; a row without keys so far keeps the lowest number
                 const float top = fmaxf(x0, x1) * scale;
@@ -551,22 +662,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                     }
                 }
                 const float base = kTcShift - m;
-                float l0 = 0.0f, l1 = 0.0f;
-                uint32_t pk[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float a = ex2(fmaf(__uint_as_float(v[k >> 4][2 * (k & 15)]), scale, base));
-                    const float b = ex2(fmaf(__uint_as_float(v[k >> 4][2 * (k & 15) + 1]), scale, base));
-                    l0 += a;
-                    l1 += b;
-                    pk[k] = pack_f16(a, b);
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[2][32], pk[32];
+                    load(h, v);
+                    float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float a = ex2(fmaf(__uint_as_float(v[k >> 4][2 * (k & 15)]), scale, base));
+                        const float b = ex2(fmaf(__uint_as_float(v[k >> 4][2 * (k & 15) + 1]), scale, base));
+                        l0 += a;
+                        l1 += b;
+                        pk[k] = pack_f16(a, b);
+                    }
+                    l += l0 + l1;
+                    tmem_st32(tS + 32 * h, pk);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_ready[t][h]);
                 }
-                l += l0 + l1;
-                tmem_st32(tS, pk);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[t]);
             }
             if (ok && steps > 0) {
                 ok = wait_all(&o_done[t], oph);
@@ -576,14 +691,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             join_m[t][r] = m;
             join_l[t][r] = l;
             good = !barrier_any(1, 256, !ok);
-            if (!good) break;
-            if (n == 0) break;
-            // ---- the outputs: of its own rows, or (pages in turn) tile 1's handed to tile 0
-            const bool split = g.n_ctas > 1;
+            if (!good || n == 0) break;
+            // ---- the outputs: of its own rows, or (steps in turn) tile 1's handed to tile 0
+            const bool split = g.n_ctas > 1, both = !halves && n > 1;
             const bool odd = seg_s[ss].odd != 0, bad = seg_s[ss].bad != 0;
             float* const slot = p.parts + (int64_t(blockIdx.x) * 2 + g.slot) * attn_slot_floats(kTcRows, D);
             float f = 1.0f;
-            if (!halves && n > 1) {
+            if (both) {
                 const float mo = join_m[t ^ 1][r], mm = fmaxf(m, mo);
                 f = ex2(m - mm);
                 l = l * f + join_l[t ^ 1][r] * ex2(mo - mm);
@@ -602,7 +716,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(v[k]) * f;
                 }
-                if (!halves && n > 1) {
+                if (both) {
                     if (t == 1) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k) join[k * 128 + r] = o[k];
@@ -614,14 +728,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                     }
                     named_barrier_sync(1, 256);
                 }
-                if (odd && writes) {
-                    float add[32];  // a copy, so that the outputs stay in registers
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) add[k] = 0.0f;
-                    tc_add_dropped<D, Q8>(p, g, mask, 32 * c, add);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] += add[k];
-                }
                 if (writes && split) {
                     // [D/4][row][4], so that a warp's rows lie together
                     float4* const dst = reinterpret_cast<float4*>(slot + 2 * kTcRows) + (8 * c) * kTcRows + at;
@@ -631,6 +737,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 } else if (writes && !bad) {
                     tc_emit(p, g, row, D, 32 * c, o, inv);
                 }
+                if (odd && writes && (split || !bad)) tc_add_dropped<D, Q8>(p, g, row, mask, 32 * c, split ? slot : nullptr);
             }
             if (writes && split) {
                 slot[at] = m;
@@ -638,6 +745,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             }
             if (!split && bad && threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
             tc_fence_before();  // the outputs are read: the next segment's products may follow the queries
+            // the joining's plain writes come before the next queries', which the tensor cores read
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_empty[ss]);
         }
@@ -646,7 +754,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     tc_fence_before();
     __syncthreads();
     if (abort_flag && threadIdx.x == 0) atomicOr(status, MQ_DEV_TIMEOUT);
-    if (warp == 13) {
+    if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
