@@ -158,25 +158,29 @@ __device__ __forceinline__ uint32_t drop_pair(uint32_t v)
 }
 
 // ---- operands (warps 8-11, thread x of 128): 64 rows from row0 on of a tile ----------------------
-// q8_0 codes and scales of a unit; values (is_v) of a page from key key0 that reaches past the context are made
-// finite: true where some were not
+// The loops that every page passes are kept short: with all their rare cases in line they and the
+// softmax's outgrew the instruction cache, and warps waited for instructions 40 % of the time.
+
+// q8_0 codes and scales of a unit
 template <int D>
-__device__ __forceinline__ bool tc_convert(const uint8_t* unit, uint8_t* tile, int row0, bool tail, int key0, int len, int x)
+__device__ __forceinline__ void tc_convert(const uint8_t* unit, uint8_t* tile, int row0, int x)
 {
     using R = KvBlock<D, true>;
     constexpr int N = D / 32;  // 16-byte chunks of codes per thread, all loaded before the first is stored
     uint4 in[N];
     uint32_t d[N];
-    bool odd = false;
+    const int r0 = x / (D / 16), c = x % (D / 16);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int r = (i * kConvThreads + x) / (D / 16), c = x % (D / 16);
+        const int r = i * (kConvThreads / (D / 16)) + r0;
         in[i] = lds16(unit + R::chunk(r, c));
         d[i] = *reinterpret_cast<const uint16_t*>(unit + kKvPage * D + (r * (D / 32) + (c >> 1)) * 2) * 0x10001u;
     }
+    // the lanes of the second plane store their halves in the other order: no bank twice
+    const int swap = c >> 2 & 1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int r = (i * kConvThreads + x) / (D / 16), c = x % (D / 16);
+        const int r = row0 + i * (kConvThreads / (D / 16)) + r0;
         const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
         uint32_t u[8];
 #pragma unroll
@@ -184,25 +188,16 @@ __device__ __forceinline__ bool tc_convert(const uint8_t* unit, uint8_t* tile, i
             u[2 * k] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4140), d[i]);
             u[2 * k + 1] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4342), d[i]);
         }
-        if (tail) {
-            const bool out = key0 + r >= len;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (out) u[k] = 0;
-                if (pair_not_finite(u[k])) odd = true, u[k] = drop_pair(u[k]);
-            }
-        }
-        // the lanes of the second plane store their halves in the other order: no bank twice
-        const bool swap = (c & 4) != 0;
         const uint4 lo = make_uint4(u[0], u[1], u[2], u[3]), hi = make_uint4(u[4], u[5], u[6], u[7]);
-        *reinterpret_cast<uint4*>(tile + tc_chunk(row0 + r, 2 * c + (swap ? 1 : 0))) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(tile + tc_chunk(row0 + r, 2 * c + (swap ? 0 : 1))) = swap ? lo : hi;
+        uint8_t* const at = tile + tc_chunk(r, 2 * c);
+        uint8_t* const at1 = tile + tc_chunk(r, 2 * c + 1);
+        *reinterpret_cast<uint4*>(swap ? at1 : at) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(swap ? at : at1) = swap ? lo : hi;
     }
-    return odd;
 }
-// f16 values that are operands already
+// values of a page that reaches past the context: rows past the sequence zeroed, what is not finite dropped (true)
 template <int D>
-__device__ __forceinline__ bool tc_clean(uint8_t* tile, int row0, int key0, int len, int x)
+__device__ __noinline__ bool tc_clean(uint8_t* tile, int row0, int key0, int len, int x)
 {
     bool odd = false;
     for (int i = x; i < kKvPage * (D / 8); i += kConvThreads) {
@@ -223,7 +218,7 @@ __device__ __forceinline__ bool tc_clean(uint8_t* tile, int row0, int key0, int 
 }
 // zeros
 template <int D>
-__device__ __forceinline__ void tc_zero(uint8_t* tile, int row0, int x)
+__device__ __noinline__ void tc_zero(uint8_t* tile, int row0, int x)
 {
     for (int i = x; i < kKvPage * (D / 8); i += kConvThreads)
         *reinterpret_cast<uint4*>(tile + tc_chunk(row0 + i / (D / 8), i % (D / 8))) = make_uint4(0, 0, 0, 0);
@@ -463,14 +458,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                         if (!ok) break;
                         there = !unit_bad[s];
                         bad |= !there;
-                        if (there) odd |= tc_convert<D>(unit_s + s * C::kUnit, tile, h * kKvPage, tail, key0, len, x);
+                        if (there) tc_convert<D>(unit_s + s * C::kUnit, tile, h * kKvPage, x);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&unit_free[s]);
                         if (++s == kUnits) s = 0, sph ^= 1u;
                     } else if (there) {
                         there = !(op_bad[b] >> h & 1);
                         bad |= !there;
-                        if (there && tail) odd |= tc_clean<D>(tile, h * kKvPage, key0, len, x);
+                    }
+                    if (there && tail) {
+                        if (Q8) named_barrier_sync(2, kConvThreads);  // the rows that other warps stored
+                        odd |= tc_clean<D>(tile, h * kKvPage, key0, len, x);
                     }
                     // such values weigh nothing, but they are multiplied with the weight 0
                     if (!there && tl.is_v) tc_zero<D>(tile, h * kKvPage, x);
@@ -602,7 +600,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 tc_fence_after();
                 const int key0 = g.page0 * kKvPage + (halves ? i : 2 * i + t) * kStep;
                 // bit k of see[h]: the row sees key key0 + 64h + k
-                uint64_t see[2] = {~0ull, ~0ull};
+                uint64_t see[2];
                 const bool tail = key0 + kStep > ctx || key0 + kStep > end;
                 if (tail) {
 #pragma unroll
@@ -618,23 +616,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                         }
                     }
                 }
-                // scores 64h .. 64h + 63 of the row
-                auto load = [&](int h, uint32_t (&v)[2][32]) {
+                if (tail) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(tS + 32 * c, v);
+                        tmem_ld_wait();
+                        const uint32_t bits = uint32_t(see[c >> 1] >> (32 * (c & 1)));
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!((bits >> k) & 1)) v[k] = 0xff800000u;
+                        tmem_st32(tS + 32 * c, v);
+                    }
+                    tmem_st_wait();
+                }
+                // the maximum first, then the numbers again: tensor memory is read faster than registers spill
+                float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t v[2][32];
                     tmem_ld32(tS + 64 * h, v[0]);
                     tmem_ld32(tS + 64 * h + 32, v[1]);
                     tmem_ld_wait();
-                    if (tail) {
-#pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (!((see[h] >> k) & 1)) v[k >> 5][k & 31] = 0xff800000u;
-                    }
-                };
-                // the maximum first, then the numbers again: tensor memory is read faster than registers spill
-                float x0 = -INFINITY, x1 = -INFINITY;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t v[2][32];
-                    load(h, v);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
                         x0 = fmaxf(x0, __uint_as_float(v[0][k]));
@@ -662,10 +665,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                     }
                 }
                 const float base = kTcShift - m;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     uint32_t v[2][32], pk[32];
-                    load(h, v);
+                    tmem_ld32(tS + 64 * h, v[0]);
+                    tmem_ld32(tS + 64 * h + 32, v[1]);
+                    tmem_ld_wait();
                     float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
