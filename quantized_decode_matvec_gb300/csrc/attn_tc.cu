@@ -48,14 +48,14 @@ constexpr uint32_t kColO = 0, kColS = 256;  // tensor memory columns of tile 0; 
 
 // Shared memory: a 128-row operand tile is D/64 planes of [128 rows][64 f16], each with the 128-byte swizzle.  K and V
 // tiles of a step pass through one ring, in the order of their use; q8_0 comes through a ring of units before, each
-// the codes and scales of a page's keys or values.
+// the codes and scales of the keys or values of a step's two pages.
 template <int D, bool Q8>
 struct TcCfg {
     static constexpr int kPlane = 128 * 128;
     static constexpr int kTile = D / 64 * kPlane;
     static constexpr int kOps = D == 128 ? (Q8 ? 3 : 4) : 6;
-    static constexpr int kCodes = kKvPage * D, kUnit = kCodes + KvBlock<D, true>::kScBytes;
-    static constexpr int kUnits = !Q8 ? 0 : D == 128 ? 6 : 12;
+    static constexpr int kCodes = kKvPage * D, kHalf = kCodes + KvBlock<D, true>::kScBytes;  // of a page
+    static constexpr int kUnit = 2 * kHalf, kUnits = !Q8 ? 0 : D == 128 ? 3 : 6;
     static constexpr int kSmem = 1024 + 2 * kTile + kOps * kTile + kUnits * kUnit;
 };
 // byte of 16-byte chunk c of row r of an operand tile
@@ -161,38 +161,47 @@ __device__ __forceinline__ uint32_t drop_pair(uint32_t v)
 // The loops that every page passes are kept short: with all their rare cases in line they and the
 // softmax's outgrew the instruction cache, and warps waited for instructions 40 % of the time.
 
-// q8_0 codes and scales of a unit
+// q8_0 codes and scales of a unit, both pages or (pages = 1) the first
 template <int D>
-__device__ __forceinline__ void tc_convert(const uint8_t* unit, uint8_t* tile, int row0, int x)
+__device__ __forceinline__ void tc_convert(const uint8_t* unit, uint8_t* tile, int pages, int x)
 {
     using R = KvBlock<D, true>;
-    constexpr int N = D / 32;  // 16-byte chunks of codes per thread, all loaded before the first is stored
-    uint4 in[N];
-    uint32_t d[N];
+    using C = TcCfg<D, true>;
+    constexpr int N = D / 32;  // 16-byte chunks of codes per thread and page, loaded a page ahead of their use
     const int r0 = x / (D / 16), c = x % (D / 16);
+    uint4 in[2][N];
+    uint32_t d[2][N];
+    auto load = [&](int h) {
+        const uint8_t* const u = unit + h * C::kHalf;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int r = i * (kConvThreads / (D / 16)) + r0;
-        in[i] = lds16(unit + R::chunk(r, c));
-        d[i] = *reinterpret_cast<const uint16_t*>(unit + kKvPage * D + (r * (D / 32) + (c >> 1)) * 2) * 0x10001u;
-    }
-    // the lanes of the second plane store their halves in the other order: no bank twice
-    const int swap = c >> 2 & 1;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int r = row0 + i * (kConvThreads / (D / 16)) + r0;
-        const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-        uint32_t u[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            u[2 * k] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4140), d[i]);
-            u[2 * k + 1] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4342), d[i]);
+        for (int i = 0; i < N; ++i) {
+            const int r = i * (kConvThreads / (D / 16)) + r0;
+            in[h][i] = lds16(u + R::chunk(r, c));
+            d[h][i] = *reinterpret_cast<const uint16_t*>(u + C::kCodes + (r * (D / 32) + (c >> 1)) * 2) * 0x10001u;
         }
-        const uint4 lo = make_uint4(u[0], u[1], u[2], u[3]), hi = make_uint4(u[4], u[5], u[6], u[7]);
-        uint8_t* const at = tile + tc_chunk(r, 2 * c);
-        uint8_t* const at1 = tile + tc_chunk(r, 2 * c + 1);
-        *reinterpret_cast<uint4*>(swap ? at1 : at) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(swap ? at : at1) = swap ? lo : hi;
+    };
+    // a chunk of codes is two of f16; the lanes of the second plane store theirs in the other order: no bank twice
+    const bool swap = (c & 4) != 0;
+    const int c0 = 2 * c + swap;
+    load(0);
+    if (pages > 1) load(1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h >= pages) break;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int r = h * kKvPage + i * (kConvThreads / (D / 16)) + r0;
+            const uint4 v = in[h][i];
+            const uint32_t w[4] = {swap ? v.z : v.x, swap ? v.w : v.y, swap ? v.x : v.z, swap ? v.y : v.w};
+            uint32_t u[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                u[2 * k] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4140), d[h][i]);
+                u[2 * k + 1] = kv_pair(__byte_perm(w[k], 0x64646464u, 0x4342), d[h][i]);
+            }
+            *reinterpret_cast<uint4*>(tile + tc_chunk(r, c0)) = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(tile + tc_chunk(r, c0 ^ 1)) = make_uint4(u[4], u[5], u[6], u[7]);
+        }
     }
 }
 // values of a page that reaches past the context: rows past the sequence zeroed, what is not finite dropped (true)
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     constexpr int kOps = C::kOps, kUnits = Q8 ? C::kUnits : 1;
     extern __shared__ uint8_t sm_raw[];
     __shared__ __align__(8) uint64_t unit_full[kUnits], unit_free[kUnits], op_full[kOps], op_ready[kOps], op_free[kOps];
-    __shared__ int unit_bad[kUnits], op_bad[kOps];  // (page of the tile: bit) not in the cache, so not copied
+    __shared__ int op_bad[Q8 ? kUnits : kOps];  // bit h: the step's page h is not in the cache, so not copied
     __shared__ __align__(8) uint64_t q_ready[2], s_ready[2], p_ready[2][2], o_done[2], seg_full[kTcSegs], seg_empty[kTcSegs];
     __shared__ TcSegment seg_s[kTcSegs];
     __shared__ float join_m[2][128], join_l[2][128];
@@ -352,7 +361,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     if (warp == kWarpSeg) {
         // ---- segments and copies; lane h: page h of a step
         AttnSegment g = {};
-        int at = w.first, sg = 0, k = 0, u = 0;  // k: tiles before; u: units before
+        int at = w.first, sg = 0, k = 0;  // k: tiles before
         bool ok = true, more = true;
         for (; ok && more; ++sg) {
             more = attn_next(p, kTcRows, &w, &at, &g);
@@ -376,59 +385,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 const bool there = page >= 0 && page < p.c.n_pages;  // table entries are not trusted
                 const unsigned both = __ballot_sync(0xffffffffu, there) & 3u;
                 const uint8_t* const src = p.c.pages + (there ? (page * p.c.n_kv_heads + g.head) * B::kBytes : 0);
-                if (Q8) {
-                    for (int h = 0; ok && h < pages; ++h, ++u) {
-                        const int s = u % kUnits;
-                        if (u >= kUnits) ok = wait_all(&unit_free[s], uint32_t(u / kUnits - 1) & 1u);
-                        if (!ok) break;
-                        if (lane == h) {
-                            uint8_t* const dst = unit_s + s * C::kUnit;
-                            unit_bad[s] = !there;
-                            if (there) {
-                                mbar_arrive_expect_tx(&unit_full[s], C::kUnit);
-                                bulk_copy_g2s(dst, src + (tl.is_v ? B::kVOff : 0), C::kCodes, &unit_full[s]);
-                                bulk_copy_g2s(dst + C::kCodes, src + B::kScK + (tl.is_v ? B::kScBytes : 0), B::kScBytes,
-                                              &unit_full[s]);
-                            } else {
-                                mbar_arrive(&unit_full[s]);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                } else {
-                    const int b = k % kOps;
-                    if (k >= kOps) ok = wait_all(&op_free[b], uint32_t(k / kOps - 1) & 1u);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        op_bad[b] = int(~both & (pages == 2 ? 3u : 1u));
-                        if (both)
-                            mbar_arrive_expect_tx(&op_full[b], uint32_t(__popc(both)) * (kKvPage * D * 2));
-                        else
-                            mbar_arrive(&op_full[b]);
-                    }
-                    __syncwarp();
-                    if (lane < 2 && there) {
+                // q8_0: the next unit; f16: the tile itself
+                const int b = k % (Q8 ? kUnits : kOps);
+                uint64_t* const full = Q8 ? &unit_full[b] : &op_full[b];
+                if (k >= (Q8 ? kUnits : kOps))
+                    ok = wait_all(Q8 ? &unit_free[b] : &op_free[b], uint32_t(k / (Q8 ? kUnits : kOps) - 1) & 1u);
+                if (!ok) break;
+                if (lane == 0) {
+                    op_bad[b] = int(~both & (pages == 2 ? 3u : 1u));
+                    if (both)
+                        mbar_arrive_expect_tx(full, uint32_t(__popc(both)) * (Q8 ? C::kHalf : kKvPage * D * 2));
+                    else
+                        mbar_arrive(full);
+                }
+                __syncwarp();
+                if (lane < 2 && there) {
+                    if (Q8) {
+                        uint8_t* const dst = unit_s + b * C::kUnit + lane * C::kHalf;
+                        bulk_copy_g2s(dst, src + (tl.is_v ? B::kVOff : 0), C::kCodes, full);
+                        bulk_copy_g2s(dst + C::kCodes, src + B::kScK + (tl.is_v ? B::kScBytes : 0), B::kScBytes, full);
+                    } else {
 #pragma unroll
                         for (int x = 0; x < D / 64; ++x)
                             bulk_copy_g2s(op_s + b * C::kTile + x * C::kPlane + lane * (kKvPage * 128),
-                                          src + (tl.is_v ? B::kVOff : 0) + x * (kKvPage * 128), kKvPage * 128, &op_full[b]);
+                                          src + (tl.is_v ? B::kVOff : 0) + x * (kKvPage * 128), kKvPage * 128, full);
                     }
                 }
             }
         }
         // copies still in flight land before the CTA can exit
-        if (Q8) {
-            for (int j = u > kUnits ? u - kUnits : 0; j < u; ++j)
-                (void)mbar_wait_bounded(&unit_full[j % kUnits], uint32_t(j / kUnits) & 1u, p.limit_ns);
-        } else {
-            for (int j = k > kOps ? k - kOps : 0; j < k; ++j)
-                (void)mbar_wait_bounded(&op_full[j % kOps], uint32_t(j / kOps) & 1u, p.limit_ns);
-        }
+        constexpr int kRing = Q8 ? kUnits : kOps;
+        for (int j = k > kRing ? k - kRing : 0; j < k; ++j)
+            (void)mbar_wait_bounded(Q8 ? &unit_full[j % kRing] : &op_full[j % kRing], uint32_t(j / kRing) & 1u, p.limit_ns);
     } else if (warp >= 8 && warp < kWarpSeg) {
         // ---- operands, tile by tile
         const int x = threadIdx.x - 256;
-        int k = 0, s = 0;  // tiles before; unit
-        uint32_t sph = 0;
+        int k = 0;  // tiles before
         bool ok = true;
         for (int sg = 0; ok; ++sg) {
             const int ss = sg % kTcSegs;
@@ -442,38 +434,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 const TcTile tl = tc_tile_at(pos, n, halves);
                 const int b = k % kOps;
                 uint8_t* const tile = op_s + b * C::kTile;
-                if (Q8)
-                    ok = k < kOps || wait_all(&op_free[b], uint32_t(k / kOps - 1) & 1u);
-                else
+                const int s = k % kUnits;
+                if (Q8) {
+                    ok = wait_all(&unit_full[s], uint32_t(k / kUnits) & 1u);
+                    ok = ok && (k < kOps || wait_all(&op_free[b], uint32_t(k / kOps - 1) & 1u));
+                } else {
                     ok = wait_all(&op_full[b], uint32_t(k / kOps) & 1u);
-                if (!ok) break;
-                bool odd = false, bad = false;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    const int pg = 2 * tl.step + h, key0 = key_base + pg * kKvPage;
-                    const bool tail = tl.is_v && key0 + kKvPage > ctx;
-                    bool there = pg < gn;
-                    if (Q8 && there) {
-                        ok = wait_all(&unit_full[s], sph);
-                        if (!ok) break;
-                        there = !unit_bad[s];
-                        bad |= !there;
-                        if (there) tc_convert<D>(unit_s + s * C::kUnit, tile, h * kKvPage, x);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&unit_free[s]);
-                        if (++s == kUnits) s = 0, sph ^= 1u;
-                    } else if (there) {
-                        there = !(op_bad[b] >> h & 1);
-                        bad |= !there;
-                    }
-                    if (there && tail) {
-                        if (Q8) named_barrier_sync(2, kConvThreads);  // the rows that other warps stored
-                        odd |= tc_clean<D>(tile, h * kKvPage, key0, len, x);
-                    }
-                    // such values weigh nothing, but they are multiplied with the weight 0
-                    if (!there && tl.is_v) tc_zero<D>(tile, h * kKvPage, x);
                 }
                 if (!ok) break;
+                const int bad = op_bad[Q8 ? s : b], pages = min(2, gn - 2 * tl.step);
+                if (Q8) {
+                    tc_convert<D>(unit_s + s * C::kUnit, tile, pages, x);  // of a page that is not there, whatever it is
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&unit_free[s]);
+                }
+                bool odd = false;
+                const int key0 = key_base + tl.step * kStep;
+                if (tl.is_v && (bad || pages < 2 || key0 + kStep > ctx)) {
+                    if (Q8) named_barrier_sync(2, kConvThreads);  // the rows that other warps stored
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        // such values weigh nothing, but they are multiplied with the weight 0
+                        if (h >= pages || (bad >> h & 1))
+                            tc_zero<D>(tile, h * kKvPage, x);
+                        else if (key0 + (h + 1) * kKvPage > ctx)
+                            odd |= tc_clean<D>(tile, h * kKvPage, key0 + h * kKvPage, len, x);
+                    }
+                }
                 if (odd) seg_s[ss].odd = 1;
                 if (bad && lane == 0) seg_s[ss].bad = 1;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
