@@ -784,22 +784,47 @@ __global__ void __launch_bounds__(D) attn_tc_join_kernel(const AttnParams p, con
     bool gone = false;
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-#pragma unroll 8
-    for (int c = 0; c < g.n_ctas; ++c) mm = fmaxf(mm, __ldcg(slot_of(c) + row));
-#pragma unroll 2
-    for (int c = 0; c < g.n_ctas; ++c) {
-        const float* const slot = slot_of(c);
-        const float lc = __ldcg(slot + kTcRows + row), f = ex2(__ldcg(slot + row) - mm);
-        const float4* const src = reinterpret_cast<const float4*>(slot + 2 * kTcRows) + 8 * warp * kTcRows + row;
-        gone |= lc < 0.0f;
-        l = fmaf(lc, f, l);
+    // loads of eight parts, then of two parts' 32 values, are on their way together: a loop over an unknown number
+    // of parts would wait for each (22 us where this takes 5, six parts of 32 groups)
+    for (int c0 = 0; c0 < g.n_ctas; c0 += 8) {
+        float m8[8], l8[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float4 x = __ldcg(src + i * kTcRows);
-            o[4 * i] = fmaf(x.x, f, o[4 * i]);
-            o[4 * i + 1] = fmaf(x.y, f, o[4 * i + 1]);
-            o[4 * i + 2] = fmaf(x.z, f, o[4 * i + 2]);
-            o[4 * i + 3] = fmaf(x.w, f, o[4 * i + 3]);
+            const bool there = c0 + i < g.n_ctas;
+            m8[i] = there ? __ldcg(slot_of(c0 + i) + row) : kLowest;
+            l8[i] = there ? __ldcg(slot_of(c0 + i) + kTcRows + row) : 0.0f;
+        }
+        const float before = mm;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mm = fmaxf(mm, m8[i]);
+        l *= ex2(before - mm);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            gone |= l8[i] < 0.0f;
+            l = fmaf(l8[i], ex2(m8[i] - mm), l);
+        }
+    }
+    for (int c = 0; c < g.n_ctas; c += 2) {
+        float4 x[2][8];
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float* const slot = slot_of(min(c + h, g.n_ctas - 1));
+            f[h] = c + h < g.n_ctas ? ex2(__ldcg(slot + row) - mm) : 0.0f;
+            const float4* const src = reinterpret_cast<const float4*>(slot + 2 * kTcRows) + 8 * warp * kTcRows + row;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[h][i] = c + h < g.n_ctas ? __ldcg(src + i * kTcRows) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                o[4 * i] = fmaf(x[h][i].x, f[h], o[4 * i]);
+                o[4 * i + 1] = fmaf(x[h][i].y, f[h], o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(x[h][i].z, f[h], o[4 * i + 2]);
+                o[4 * i + 3] = fmaf(x[h][i].w, f[h], o[4 * i + 3]);
+            }
         }
     }
     if (gone) {  // a page outside the cache: the group stays unwritten
