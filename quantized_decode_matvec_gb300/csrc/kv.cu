@@ -11,13 +11,15 @@ namespace mq {
 
 // ---- append -------------------------------------------------------------------------------
 // Per head x[0..D): x' = x * rsqrt(mean(x^2) + eps) * w, then each pair (a, b)
-// turned by pos * inv_freq: a' = a cos - b sin, b' = b cos + a sin.  One warp
-// per (token, run of heads): lane l holds elements 64j + 2l, +1, so loads and
-// f16 stores are coalesced, a q8_0 block is half a warp's row, and the lane's
-// cosines and sines (of the token alone) are formed once for all its heads.
-// The partner of a pair comes through a row of shared memory, which serves
-// every rot_dims and both pairings.  Statistics, products and rotation are
-// fp32; each output is rounded once, to f16 or to its q8_0 code.
+// turned by pos * inv_freq: a' = a cos - b sin, b' = b cos + a sin.  Half a
+// warp per head: lane l of 16 holds elements 4l..4l+3 (and 64 + 4l.. of 128),
+// so loads and f16 stores are coalesced, a q8_0 block is eight lanes' share,
+// and a pair lies in one lane (adjacent pairs; halves of 128), in lanes eight
+// apart (halves of 64), or, where only part of the head turns by halves, comes
+// through a row of shared memory.  A warp takes a run of heads of one token,
+// two at a time, and forms the token's cosines and sines once.  Statistics,
+// products and rotation are fp32; each output is rounded once, to f16 or to
+// its q8_0 code.
 //
 // The angle: pos * f / 2pi modulo one turn, with f = m 2^(e-23) (m the 24-bit
 // mantissa): m * floor(2^64 / 2pi) is a 128-bit integer, shifted by e - 23 it
@@ -47,22 +49,42 @@ __device__ __forceinline__ uint64_t turn_per_pos(float f)
 struct AppendArgs {
     mq_kv_append_args a;
     KvView c;
-    int heads_per_warp, parts;  // runs of heads per token
+    int heads_per_warp, parts;  // runs of heads per token (heads_per_warp is even)
+    int wide;                   // rows of qkv may be read 16 bytes at a time, rows of q written 8
 };
 
-template <int D, bool Q8>
+enum { kRotNone = 0, kRotHalves = 1, kRotAdjacent = 2, kRotPart = 3 };
+
+template <int D, bool Q8, int ROT>
 __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsigned* status)
 {
     using B = KvBlock<D, Q8>;
-    constexpr int NJ = D / 64;  // element pairs per lane
-    __shared__ float2 row_s[4][D / 2];
+    constexpr int NV = D / 16, NG = NV / 4;  // values of a lane, groups of four
+    __shared__ float row_s[ROT == kRotPart ? 8 : 1][D];
     const mq_kv_append_args& a = p.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 15, hw = lane >> 4;
     const int64_t w = int64_t(blockIdx.x) * 4 + warp;
     const int n = int(w / p.parts), part = int(w - int64_t(n) * p.parts);
     if (n >= a.n_tokens) return;
     const int Hq = a.n_heads, Hkv = p.c.n_kv_heads, H = Hq + 2 * Hkv;
     const int h0 = part * p.heads_per_warp, h1 = min(h0 + p.heads_per_warp, H);
+
+    const float* const src = a.qkv + size_t(n) * a.qkv_ld;
+    auto load = [&](int h, float (&x)[NV]) {
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const float* const at = src + h * D + 64 * j + 4 * l;
+            if (p.wide) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(at));
+                x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
+            } else {
+                const float2 u = __ldg(reinterpret_cast<const float2*>(at)), v = __ldg(reinterpret_cast<const float2*>(at) + 1);
+                x[4 * j] = u.x, x[4 * j + 1] = u.y, x[4 * j + 2] = v.x, x[4 * j + 3] = v.y;
+            }
+        }
+    };
+    float x[NV], nx[NV];
+    load(min(h0 + hw, h1 - 1), nx);
 
     // where K and V go: -1 writes q only
     int64_t page = -1;
@@ -76,146 +98,207 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
         }
     }
 
-    // cosine and signed sine of this lane's elements
-    float cs[NJ][2], sn[NJ][2];
-    int mate[NJ][2];
-    const int R = a.rot_dims;
-    const bool inter = (a.flags & MQ_ROPE_INTERLEAVED) != 0;
+    // cosine and signed sine of this lane's elements (halves of 128: of its first four, which its others share)
+    constexpr int NC = ROT == kRotHalves && D == 128 ? 4 : NV;
+    float cs[NC], sn[NC];
+    int mate[ROT == kRotPart ? NV : 1];
+    if (ROT != kRotNone && h0 < Hq + Hkv) {
+        const int R = a.rot_dims, half = R / 2;
+        const int64_t pos = __ldg(a.pos + n);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int d = 64 * j + 2 * lane + k;
-            cs[j][k] = 1.0f, sn[j][k] = 0.0f, mate[j][k] = d;
-            if (d < R && h0 < Hq + Hkv) {
-                const int half = R / 2;
-                const bool first = inter ? k == 0 : d < half;
-                const int i = inter ? d / 2 : (first ? d : d - half);
-                mate[j][k] = inter ? d ^ 1 : (first ? d + half : d - half);
-                const uint64_t turn = turn_per_pos(__ldg(a.inv_freq + i)) * uint64_t(int64_t(__ldg(a.pos + n)));
-                float s, c;
-                sincospif(float(int(turn >> 32)) * 0x1p-31f, &s, &c);  // signed half turns
-                cs[j][k] = c;
-                sn[j][k] = first ? -s : s;
-            }
-        }
-
-    const float2* const src = reinterpret_cast<const float2*>(a.qkv + size_t(n) * a.qkv_ld);
-    float2 x[NJ], nx[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) nx[j] = __ldg(src + h0 * (D / 2) + 32 * j + lane);
-    for (int h = h0; h < h1; ++h) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            x[j] = nx[j];
-            if (h + 1 < h1) nx[j] = __ldg(src + (h + 1) * (D / 2) + 32 * j + lane);
-        }
-        const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
-        if (!is_v) {
-            const float* const wn = is_q ? a.q_norm : a.k_norm;
-            if (wn) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) ss = fmaf(x[j].x, x[j].x, fmaf(x[j].y, x[j].y, ss));
-#pragma unroll
-                for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const float2 g = __ldg(reinterpret_cast<const float2*>(wn) + 32 * j + lane);
-                    x[j].x = x[j].x * rs * g.x;
-                    x[j].y = x[j].y * rs * g.y;
-                }
-            }
-            if (R > 0) {
-                float2* const row = row_s[warp];
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) row[32 * j + lane] = x[j];
-                __syncwarp();
-                const float* const rowf = reinterpret_cast<const float*>(row);
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    x[j].x = fmaf(x[j].x, cs[j][0], rowf[mate[j][0]] * sn[j][0]);
-                    x[j].y = fmaf(x[j].y, cs[j][1], rowf[mate[j][1]] * sn[j][1]);
-                }
-                __syncwarp();
-            }
-        }
-        if (is_q) {
-            __half2* const q = reinterpret_cast<__half2*>(static_cast<__half*>(a.q_out) + size_t(n) * a.q_ld + h * D);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) q[32 * j + lane] = __floats2half2_rn(x[j].x, x[j].y);
-            continue;
-        }
-        if (page < 0) continue;
-        uint8_t* const blk = p.c.pages + page + size_t(is_v ? h - Hq - Hkv : h - Hq) * B::kBytes;
-        uint8_t* const rows = blk + (is_v ? B::kVOff : 0);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int d = 64 * j + 2 * lane;
-            if (!Q8) {
-                *reinterpret_cast<__half2*>(rows + B::chunk(r, d >> 3) + (d & 7) * 2) =
-                    __floats2half2_rn(x[j].x, x[j].y);
+        for (int e = 0; e < NC; ++e) {
+            const int d = 64 * (e / 4) + 4 * l + e % 4;
+            cs[e] = 1.0f, sn[e] = 0.0f;
+            if (ROT == kRotPart) mate[e] = d;
+            // an adjacent pair shares its angle
+            if (ROT == kRotAdjacent && (e & 1)) {
+                cs[e] = cs[e - 1], sn[e] = -sn[e - 1];
                 continue;
             }
-            // a block of 32 values lies in 16 lanes; the bits of non-negative floats order like the values
-            unsigned m = max(__float_as_uint(fabsf(x[j].x)), __float_as_uint(fabsf(x[j].y)));
+            if (d < R) {
+                const bool first = ROT == kRotAdjacent || d < half;
+                const int i = ROT == kRotAdjacent ? d / 2 : (first ? d : d - half);
+                if (ROT == kRotPart) mate[e] = first ? d + half : d - half;
+                const uint64_t turn = turn_per_pos(__ldg(a.inv_freq + i)) * uint64_t(pos);
+                float s, c;
+                sincospif(float(int(turn >> 32)) * 0x1p-31f, &s, &c);  // signed half turns
+                cs[e] = c;
+                sn[e] = first ? -s : s;
+            }
+        }
+    }
+
+    for (int h = h0; h < h1; h += 2) {
+        const int hh = h + hw;
+        const bool there = hh < h1, is_q = hh < Hq, is_v = hh >= Hq + Hkv;
 #pragma unroll
-            for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int e = 0; e < NV; ++e) x[e] = nx[e];
+        if (h + 2 < h1) load(min(hh + 2, h1 - 1), nx);
+        if (a.q_norm || a.k_norm) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int e = 0; e < NV; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float* const wn = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
+            if (wn) {
+                const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+                for (int e = 0; e < NV; e += 2) {
+                    const float2 g = __ldg(reinterpret_cast<const float2*>(wn + 64 * (e / 4) + 4 * l + e % 4));
+                    x[e] = x[e] * rs * g.x;
+                    x[e + 1] = x[e + 1] * rs * g.y;
+                }
+            }
+        }
+        if (ROT == kRotHalves && D == 128) {
+            if (!is_v) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float u = x[e], v = x[e + NV - 4];  // sn[e] is the first of the pair's: -sin
+                    x[e] = fmaf(u, cs[e], v * sn[e]);
+                    x[e + NV - 4] = fmaf(v, cs[e], -(u * sn[e]));
+                }
+            }
+        } else if (ROT == kRotHalves) {
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                const float v = __shfl_xor_sync(0xffffffffu, x[e], 8);
+                if (!is_v) x[e] = fmaf(x[e], cs[e % NC], v * sn[e % NC]);
+            }
+        } else if (ROT == kRotAdjacent) {
+            if (!is_v) {
+#pragma unroll
+                for (int e = 0; e < NV; e += 2) {
+                    const float u = x[e], v = x[e + 1];
+                    x[e] = fmaf(u, cs[e % NC], v * sn[e % NC]);
+                    x[e + 1] = fmaf(v, cs[(e + 1) % NC], u * sn[(e + 1) % NC]);
+                }
+            }
+        } else if (ROT == kRotPart) {
+            float* const row = row_s[2 * warp + hw];
+#pragma unroll
+            for (int e = 0; e < NV; ++e) row[64 * (e / 4) + 4 * l + e % 4] = x[e];
+            __syncwarp();
+            if (!is_v) {
+#pragma unroll
+                for (int e = 0; e < NV; ++e) x[e] = fmaf(x[e], cs[e % NC], row[mate[e]] * sn[e % NC]);
+            }
+            __syncwarp();
+        }
+        if (is_q && there) {
+            __half* const q = static_cast<__half*>(a.q_out) + size_t(n) * a.q_ld + hh * D;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const __half2 u = __floats2half2_rn(x[4 * j], x[4 * j + 1]), v = __floats2half2_rn(x[4 * j + 2], x[4 * j + 3]);
+                __half2* const at = reinterpret_cast<__half2*>(q + 64 * j + 4 * l);
+                if (p.wide) {
+                    *reinterpret_cast<uint2*>(at) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+                } else {
+                    at[0] = u, at[1] = v;
+                }
+            }
+        }
+        if (page < 0 || h + 1 < Hq) continue;  // the warp as one: no key or value head here
+        const bool store = there && !is_q;
+        uint8_t* const blk =
+            p.c.pages + page + size_t(!store ? 0 : is_v ? hh - Hq - Hkv : hh - Hq) * B::kBytes;
+        uint8_t* const rows = blk + (is_v ? B::kVOff : 0);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const int d = 64 * j + 4 * l;
+            if (!Q8) {
+                const __half2 u = __floats2half2_rn(x[4 * j], x[4 * j + 1]), v = __floats2half2_rn(x[4 * j + 2], x[4 * j + 3]);
+                if (store)
+                    *reinterpret_cast<uint2*>(rows + B::chunk(r, d >> 3) + (d & 7) * 2) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
+                continue;
+            }
+            // a block of 32 values lies in eight lanes; the bits of non-negative floats order like the values
+            unsigned m = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = max(m, __float_as_uint(fabsf(x[4 * j + e])));
+#pragma unroll
+            for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             const Q8Scale s = q8_scale_of(__uint_as_float(m));
-            int q0, q1;
-            if (!q8_code_fast(x[j].x, s, &q0)) q0 = q8_code_exact(x[j].x, s.d);
-            if (!q8_code_fast(x[j].y, s, &q1)) q1 = q8_code_exact(x[j].y, s.d);
-            *reinterpret_cast<uchar2*>(rows + B::chunk(r, d >> 4) + (d & 15)) =
-                make_uchar2(uint8_t(q0 + 128), uint8_t(q1 + 128));
-            if ((lane & 15) == 0)
-                *reinterpret_cast<__half*>(blk + B::kScK + (is_v ? B::kScBytes : 0) + (r * (D / 32) + (d >> 5)) * 2) =
-                    __float2half_rn(s.d);
+            uint32_t code = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                int q;
+                if (!q8_code_fast(x[4 * j + e], s, &q)) q = q8_code_exact(x[4 * j + e], s.d);
+                code |= uint32_t(q + 128) << (8 * e);
+            }
+            if (store) {
+                *reinterpret_cast<uint32_t*>(rows + B::chunk(r, d >> 4) + (d & 15)) = code;
+                if ((l & 7) == 0)
+                    *reinterpret_cast<__half*>(blk + B::kScK + (is_v ? B::kScBytes : 0) + (r * (D / 32) + (d >> 5)) * 2) =
+                        __float2half_rn(s.d);
+            }
         }
     }
 }
 
 // ---- read ---------------------------------------------------------------------------------
-// One thread per 16-byte chunk of a cached row: 16 bytes in, 16 (f16) or 32
+// A thread per U 16-byte chunks of cached rows: 16 bytes in, 16 (f16) or 32
 // (q8_0, scale applied and rounded once) out, neighbouring threads on
-// neighbouring chunks.  Bound by the bytes it moves.
-template <int D, bool Q8>
-__global__ void __launch_bounds__(256)
-    kv_read_kernel(const KvView c, const int32_t* __restrict__ seq, const int32_t* __restrict__ slot, int n,
-                   uint4* __restrict__ k_out, uint4* __restrict__ v_out, unsigned* status)
+// neighbouring chunks of a token's heads.  Bound by the bytes it moves once
+// enough of them are under way; U = 4 where that still fills the chip twice
+// (32768 tokens of 4 heads of 128, q8_0), U = 1 for few tokens (latency).
+struct ReadArgs {
+    KvView c;
+    const int32_t *seq, *slot;
+    uint4 *k_out, *v_out;
+    int n, per, tokens;  // pairs; chunks of a token, tokens of a CTA
+    uint32_t per_inv;    // 2^32 / per rounded up
+};
+template <int D, bool Q8, int U>
+__global__ void __launch_bounds__(256) kv_read_kernel(const ReadArgs p, unsigned* status)
 {
     using B = KvBlock<D, Q8>;
     constexpr int CH = B::kChunks;
-    const int64_t total = int64_t(n) * c.n_kv_heads * (2 * CH);
-    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += int64_t(gridDim.x) * blockDim.x) {
-        const int ch = int(i % CH), is_v = int(i / CH) & 1;
-        const int64_t th = i / (2 * CH);
-        const int h = int(th % c.n_kv_heads), t = int(th / c.n_kv_heads);
-        const int sl = __ldg(slot + t);
-        const int64_t page = kv_page_of(c, __ldg(seq + t), sl, int64_t(c.n_kv_heads) * B::kBytes);
+    const int base = blockIdx.y * (256 * U) + threadIdx.x;
+    uint4 v[U];
+    uint32_t d[U];
+    uint4* out[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        out[i] = nullptr;
+        const int x = base + 256 * i;
+        // x / per, exact: x < 2^16 where a CTA has several tokens, and one token is all of x otherwise
+        const int tl = p.tokens > 1 ? int(__umulhi(uint32_t(x), p.per_inv)) : 0, u = x - tl * p.per;
+        const int64_t t = int64_t(blockIdx.x) * p.tokens + tl;
+        if (tl >= p.tokens || u >= p.per || t >= p.n) continue;
+        const int sl = __ldg(p.slot + t), r = sl & (kKvPage - 1);
+        const int64_t page = kv_page_of(p.c, __ldg(p.seq + t), sl, int64_t(p.c.n_kv_heads) * B::kBytes);
         if (page < 0) {
-            atomicOr(status, MQ_DEV_KV_RANGE);
+            if (u == 0) atomicOr(status, MQ_DEV_KV_RANGE);
             continue;
         }
-        const int r = sl % kKvPage;
-        const uint8_t* const blk = c.pages + page + size_t(h) * B::kBytes;
-        const uint4 v = *reinterpret_cast<const uint4*>(blk + (is_v ? B::kVOff : 0) + B::chunk(r, ch));
-        uint4* const out = (is_v ? v_out : k_out) + th * (D / 8);
-        if (!Q8) {
-            out[ch] = v;
-        } else {
-            const uint32_t d = *reinterpret_cast<const uint16_t*>(blk + B::kScK + is_v * B::kScBytes +
-                                                                  (r * (D / 32) + (ch >> 1)) * 2) * 0x10001u;
-            uint32_t u[8];
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        const int ch = u % CH, is_v = u / CH & 1, h = u / (2 * CH);
+        const uint8_t* const blk = p.c.pages + page + size_t(h) * B::kBytes;
+        v[i] = *reinterpret_cast<const uint4*>(blk + (is_v ? B::kVOff : 0) + B::chunk(r, ch));
+        if (Q8)
+            d[i] = *reinterpret_cast<const uint16_t*>(blk + B::kScK + is_v * B::kScBytes +
+                                                      (r * (D / 32) + (ch >> 1)) * 2) * 0x10001u;
+        out[i] = (is_v ? p.v_out : p.k_out) + (t * p.c.n_kv_heads + h) * (D / 8) + (Q8 ? 2 * ch : ch);
+    }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                u[2 * k] = kv_pair(__byte_perm(in[k], 0x64646464u, 0x4140), d);
-                u[2 * k + 1] = kv_pair(__byte_perm(in[k], 0x64646464u, 0x4342), d);
-            }
-            out[2 * ch] = make_uint4(u[0], u[1], u[2], u[3]);
-            out[2 * ch + 1] = make_uint4(u[4], u[5], u[6], u[7]);
+    for (int i = 0; i < U; ++i) {
+        if (!out[i]) continue;
+        if (!Q8) {
+            *out[i] = v[i];
+            continue;
         }
+        uint32_t o[8];
+        const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            o[2 * k] = kv_pair(__byte_perm(in[k], 0x64646464u, 0x4140), d[i]);
+            o[2 * k + 1] = kv_pair(__byte_perm(in[k], 0x64646464u, 0x4342), d[i]);
+        }
+        out[i][0] = make_uint4(o[0], o[1], o[2], o[3]);
+        out[i][1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
@@ -307,14 +390,22 @@ cudaError_t launch_kv_append(const mq_kv_cache& cache, const mq_kv_append_args& 
     AppendArgs p;
     p.a = a;
     p.c = kv_view(cache);
-    // one head per warp while that leaves the chip room (few tokens: latency), then
+    // two heads per warp while that leaves the chip room (few tokens: latency), then
     // longer runs, which form a token's cosines and sines fewer times
     const int H = a.n_heads + 2 * cache.n_kv_heads;
-    const int64_t per = int64_t(a.n_tokens) * H / (int64_t(num_sms) * 32);
-    p.heads_per_warp = per < 1 ? 1 : per > 12 ? 12 : int(per);
+    const int64_t per = int64_t(a.n_tokens) * H / (int64_t(num_sms) * 32) / 2 * 2;
+    p.heads_per_warp = per < 2 ? 2 : per > 12 ? 12 : int(per);
     p.parts = (H + p.heads_per_warp - 1) / p.heads_per_warp;
-    const int64_t grid = (int64_t(a.n_tokens) * p.parts + 3) / 4;
-#define MQ_CALL(D, Q) kv_append_kernel<D, Q><<<unsigned(grid), 128, 0, s>>>(p, status)
+    p.wide = (reinterpret_cast<uintptr_t>(a.qkv) & 15) == 0 && a.qkv_ld % 4 == 0 &&
+             (reinterpret_cast<uintptr_t>(a.q_out) & 7) == 0 && a.q_ld % 4 == 0;
+    const unsigned grid = unsigned((int64_t(a.n_tokens) * p.parts + 3) / 4);
+    const int rot = a.rot_dims == 0 ? kRotNone : a.flags & MQ_ROPE_INTERLEAVED ? kRotAdjacent
+                    : a.rot_dims == cache.head_dim ? kRotHalves : kRotPart;
+#define MQ_CALL(D, Q)                                                                                           \
+    rot == kRotNone ? kv_append_kernel<D, Q, kRotNone><<<grid, 128, 0, s>>>(p, status)                          \
+    : rot == kRotHalves ? kv_append_kernel<D, Q, kRotHalves><<<grid, 128, 0, s>>>(p, status)                    \
+    : rot == kRotAdjacent ? kv_append_kernel<D, Q, kRotAdjacent><<<grid, 128, 0, s>>>(p, status)                \
+                          : kv_append_kernel<D, Q, kRotPart><<<grid, 128, 0, s>>>(p, status)
     MQ_KV_DISPATCH(cache, MQ_CALL);
 #undef MQ_CALL
     return cudaGetLastError();
@@ -323,13 +414,20 @@ cudaError_t launch_kv_append(const mq_kv_cache& cache, const mq_kv_append_args& 
 cudaError_t launch_kv_read(const mq_kv_cache& cache, const int32_t* seq, const int32_t* slot, int n, void* k_out,
                            void* v_out, int num_sms, unsigned* status, cudaStream_t s)
 {
-    const int ch = cache.head_dim / (cache.type == MQ_TYPE_Q8_0 ? 16 : 8);
-    const int64_t total = int64_t(n) * cache.n_kv_heads * 2 * ch;
-    int64_t grid = (total + 255) / 256;
-    if (grid > int64_t(num_sms) * 64) grid = int64_t(num_sms) * 64;
-#define MQ_CALL(D, Q)                                                                                              \
-    kv_read_kernel<D, Q><<<unsigned(grid), 256, 0, s>>>(kv_view(cache), seq, slot, n, static_cast<uint4*>(k_out),  \
-                                                        static_cast<uint4*>(v_out), status)
+    ReadArgs p;
+    p.c = kv_view(cache);
+    p.seq = seq, p.slot = slot;
+    p.k_out = static_cast<uint4*>(k_out), p.v_out = static_cast<uint4*>(v_out);
+    p.n = n;
+    p.per = cache.n_kv_heads * 2 * (cache.head_dim / (cache.type == MQ_TYPE_Q8_0 ? 16 : 8));
+    p.per_inv = uint32_t((0x100000000ull + p.per - 1) / p.per);
+    const bool many = int64_t(n) * p.per >= int64_t(num_sms) * 2048 * 8;
+    const int chunks = many ? 1024 : 256;  // of a CTA
+    p.tokens = p.per < chunks ? chunks / p.per : 1;
+    const dim3 grid(unsigned((int64_t(n) + p.tokens - 1) / p.tokens), unsigned((p.per + chunks - 1) / chunks));
+#define MQ_CALL(D, Q)                                                           \
+    many ? kv_read_kernel<D, Q, 4><<<grid, 256, 0, s>>>(p, status)              \
+         : kv_read_kernel<D, Q, 1><<<grid, 256, 0, s>>>(p, status)
     MQ_KV_DISPATCH(cache, MQ_CALL);
 #undef MQ_CALL
     return cudaGetLastError();
