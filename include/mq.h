@@ -452,7 +452,7 @@ mq_status mq_kv_accept(const mq_kv_cache* h_cache, const int32_t* ctx_len, const
  * columns [n_tokens][n_heads*head_dim/32 blocks] (out_ld not read), the xq of
  * an o projection.  Tokens outside every sequence are not written.
  * max_len bounds ctx_len[s] + T, max_tokens bounds T (host values; they size
- * the launch and pick its kernel); n_seqs * (max_len/64 + 8) * n_kv_heads *
+ * the launch and pick its kernel); n_seqs * (max_len/64 + 12) * n_kv_heads *
  * ceil(max_tokens * n_heads/n_kv_heads / 8) must stay below 2^31
  * (MQ_ERR_UNSUPPORTED).
  * workspace: mq_attn_workspace_bytes bytes, 128-byte aligned, zeroed once by

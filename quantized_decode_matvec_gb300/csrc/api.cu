@@ -946,8 +946,9 @@ mq_status mq_attn_tree(const mq_kv_cache* cache, const mq_attn_args* a, void* wo
     if (a->q_ld < width || a->q_ld % 8) return MQ_ERR_SHAPE;
     if (a->out_type == MQ_TYPE_F16 && (a->out_ld < width || a->out_ld % 8)) return MQ_ERR_SHAPE;
     if (!(a->scale - a->scale == 0.0f)) return MQ_ERR_INVALID_ARG;  // not finite
-    // the work is counted in 31 bits: pages of a row block of eight rows and a head, over all sequences
-    const double units = double(cache->n_seqs) * cache->n_kv_heads * (a->max_len / MQ_KV_PAGE_TOKENS + 8.0) *
+    // the work is counted in 31 bits: pages of a row block of eight rows and a head, begun ones and what a block
+    // counts for besides its pages included, over all sequences
+    const double units = double(cache->n_seqs) * cache->n_kv_heads * (a->max_len / MQ_KV_PAGE_TOKENS + 12.0) *
                          ((a->n_heads / cache->n_kv_heads * a->max_tokens + 7) / 8);
     if (units >= 2147483648.0) return MQ_ERR_UNSUPPORTED;
     if (a->n_tokens == 0 || cache->n_seqs == 0) return MQ_OK;

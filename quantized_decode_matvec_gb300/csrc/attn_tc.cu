@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     __shared__ __align__(8) uint64_t unit_full[kUnits], unit_free[kUnits], op_full[kOps], op_ready[kOps], op_free[kOps];
     __shared__ int op_bad[Q8 ? kUnits : kOps];  // bit h: the step's page h is not in the cache, so not copied
     __shared__ __align__(8) uint64_t q_ready[2], s_ready[2], p_ready[2][2], o_done[2], seg_full[kTcSegs], seg_empty[kTcSegs];
+    __shared__ __align__(8) uint64_t tile_done;  // the converters' stores to a tile that one of them corrects
     __shared__ TcSegment seg_s[kTcSegs];
     __shared__ float join_m[2][128], join_l[2][128];
     __shared__ uint32_t tmem_base;
@@ -338,7 +339,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     } else if (threadIdx.x >= 96 && threadIdx.x < 96 + kTcSegs) {
         mbar_init(&seg_full[threadIdx.x - 96], 1);
         mbar_init(&seg_empty[threadIdx.x - 96], 8 + kConv + 1);  // softmax and operand warps, the MMA warp
-        if (threadIdx.x == 96) abort_flag = 0;
+        if (threadIdx.x == 96) {
+            mbar_init(&tile_done, kConv);
+            abort_flag = 0;
+        }
     }
     fence_barrier_init();
     griddep_launch_dependents();  // the join may take its place; it waits for this grid's end
@@ -421,6 +425,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         // ---- operands, tile by tile
         const int x = threadIdx.x - 256;
         int k = 0;  // tiles before
+        uint32_t done_ph = 0;
         bool ok = true;
         for (int sg = 0; ok; ++sg) {
             const int ss = sg % kTcSegs;
@@ -451,7 +456,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 bool odd = false;
                 const int key0 = key_base + tl.step * kStep;
                 if (tl.is_v && (bad || pages < 2 || key0 + kStep > ctx)) {
-                    if (Q8) named_barrier_sync(2, kConvThreads);  // the rows that other warps stored
+                    if (Q8) {  // the rows that other warps stored; a warp that gave up does not come
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tile_done);
+                        ok = wait_all(&tile_done, done_ph);
+                        done_ph ^= 1u;
+                        if (!ok) break;
+                    }
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         // such values weigh nothing, but they are multiplied with the weight 0

@@ -16,8 +16,9 @@ namespace mq {
 // so loads and f16 stores are coalesced, a q8_0 block is eight lanes' share,
 // and a pair lies in one lane (adjacent pairs; halves of 128), in lanes eight
 // apart (halves of 64), or, where only part of the head turns by halves, comes
-// through a row of shared memory.  A warp takes a run of heads of one token,
-// two at a time, and forms the token's cosines and sines once.  Statistics,
+// through a row of shared memory.  A warp takes a run of pairs of heads of one
+// token (query, key or value heads, so that its lanes agree on what to do) and
+// forms the token's cosines and sines once.  Statistics,
 // products and rotation are fp32; each output is rounded once, to f16 or to
 // its q8_0 code.
 //
@@ -49,7 +50,7 @@ __device__ __forceinline__ uint64_t turn_per_pos(float f)
 struct AppendArgs {
     mq_kv_append_args a;
     KvView c;
-    int heads_per_warp, parts;  // runs of heads per token (heads_per_warp is even)
+    int per_warp, parts;  // pairs of heads of a run, runs per token
     int wide;                   // rows of qkv may be read 16 bytes at a time, rows of q written 8
 };
 
@@ -66,14 +67,20 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
     const int64_t w = int64_t(blockIdx.x) * 4 + warp;
     const int n = int(w / p.parts), part = int(w - int64_t(n) * p.parts);
     if (n >= a.n_tokens) return;
-    const int Hq = a.n_heads, Hkv = p.c.n_kv_heads, H = Hq + 2 * Hkv;
-    const int h0 = part * p.heads_per_warp, h1 = min(h0 + p.heads_per_warp, H);
+    const int Hq = a.n_heads, Hkv = p.c.n_kv_heads;
+    const int PQ = (Hq + 1) / 2, PK = (Hkv + 1) / 2;  // pairs
+    const int p0 = part * p.per_warp, p1 = min(p0 + p.per_warp, PQ + 2 * PK);
+    // pair i: 0 query, 1 key, 2 value heads; this half's head of that kind
+    auto kind_of = [&](int i) { return i < PQ ? 0 : i < PQ + PK ? 1 : 2; };
+    auto head_of = [&](int i, int kind) { return 2 * (i - (kind == 0 ? 0 : kind == 1 ? PQ : PQ + PK)) + hw; };
 
-    const float* const src = a.qkv + size_t(n) * a.qkv_ld;
-    auto load = [&](int h, float (&x)[NV]) {
+    const float* const src = a.qkv + size_t(n) * a.qkv_ld + 4 * l;
+    auto load = [&](int i, float (&x)[NV]) {
+        const int kind = kind_of(i), head = min(head_of(i, kind), (kind == 0 ? Hq : Hkv) - 1);
+        const float* const from = src + (kind == 0 ? head : kind == 1 ? Hq + head : Hq + Hkv + head) * D;
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            const float* const at = src + h * D + 64 * j + 4 * l;
+            const float* const at = from + 64 * j;
             if (p.wide) {
                 const float4 v = __ldg(reinterpret_cast<const float4*>(at));
                 x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
@@ -84,12 +91,12 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
         }
     };
     float x[NV], nx[NV];
-    load(min(h0 + hw, h1 - 1), nx);
+    load(p0, nx);
 
     // where K and V go: -1 writes q only
     int64_t page = -1;
     int r = 0;
-    if (h1 > Hq) {
+    if (p1 > PQ) {
         const int slot = __ldg(a.slot + n);
         if (slot >= 0) {
             page = kv_page_of(p.c, __ldg(a.seq + n), slot, int64_t(Hkv) * B::kBytes);
@@ -102,7 +109,7 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
     constexpr int NC = ROT == kRotHalves && D == 128 ? 4 : NV;
     float cs[NC], sn[NC];
     int mate[ROT == kRotPart ? NV : 1];
-    if (ROT != kRotNone && h0 < Hq + Hkv) {
+    if (ROT != kRotNone && p0 < PQ + PK) {
         const int R = a.rot_dims, half = R / 2;
         const int64_t pos = __ldg(a.pos + n);
 #pragma unroll
@@ -128,70 +135,72 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
         }
     }
 
-    for (int h = h0; h < h1; h += 2) {
-        const int hh = h + hw;
-        const bool there = hh < h1, is_q = hh < Hq, is_v = hh >= Hq + Hkv;
+    int wk = -1;  // kind whose weights are held
+    float wt[NV];
+#pragma unroll 1
+    for (int i = p0; i < p1; ++i) {
+        const int kind = kind_of(i), head = head_of(i, kind);
+        const bool there = head < (kind == 0 ? Hq : Hkv);  // an odd number of heads leaves half a pair
 #pragma unroll
         for (int e = 0; e < NV; ++e) x[e] = nx[e];
-        if (h + 2 < h1) load(min(hh + 2, h1 - 1), nx);
-        if (a.q_norm || a.k_norm) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int e = 0; e < NV; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-            for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float* const wn = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
+        if (i + 1 < p1) load(i + 1, nx);
+        if (kind < 2) {
+            const float* const wn = kind == 0 ? a.q_norm : a.k_norm;
             if (wn) {
+                if (wk != kind) {
+                    wk = kind;
+#pragma unroll
+                    for (int e = 0; e < NV; e += 2) {
+                        const float2 g = __ldg(reinterpret_cast<const float2*>(wn + 64 * (e / 4) + 4 * l + e % 4));
+                        wt[e] = g.x, wt[e + 1] = g.y;
+                    }
+                }
+                float ss = 0.0f;
+#pragma unroll
+                for (int e = 0; e < NV; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+                for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
 #pragma unroll
-                for (int e = 0; e < NV; e += 2) {
-                    const float2 g = __ldg(reinterpret_cast<const float2*>(wn + 64 * (e / 4) + 4 * l + e % 4));
-                    x[e] = x[e] * rs * g.x;
-                    x[e + 1] = x[e + 1] * rs * g.y;
-                }
+                for (int e = 0; e < NV; ++e) x[e] = x[e] * rs * wt[e];
             }
-        }
-        if (ROT == kRotHalves && D == 128) {
-            if (!is_v) {
+            if (ROT == kRotHalves && D == 128) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float u = x[e], v = x[e + NV - 4];  // sn[e] is the first of the pair's: -sin
                     x[e] = fmaf(u, cs[e], v * sn[e]);
                     x[e + NV - 4] = fmaf(v, cs[e], -(u * sn[e]));
                 }
-            }
-        } else if (ROT == kRotHalves) {
+            } else if (ROT == kRotHalves) {
 #pragma unroll
-            for (int e = 0; e < NV; ++e) {
-                const float v = __shfl_xor_sync(0xffffffffu, x[e], 8);
-                if (!is_v) x[e] = fmaf(x[e], cs[e % NC], v * sn[e % NC]);
-            }
-        } else if (ROT == kRotAdjacent) {
-            if (!is_v) {
+                for (int e = 0; e < NV; ++e) {
+                    const float v = __shfl_xor_sync(0xffffffffu, x[e], 8);
+                    x[e] = fmaf(x[e], cs[e % NC], v * sn[e % NC]);
+                }
+            } else if (ROT == kRotAdjacent) {
 #pragma unroll
                 for (int e = 0; e < NV; e += 2) {
                     const float u = x[e], v = x[e + 1];
                     x[e] = fmaf(u, cs[e % NC], v * sn[e % NC]);
                     x[e + 1] = fmaf(v, cs[(e + 1) % NC], u * sn[(e + 1) % NC]);
                 }
-            }
-        } else if (ROT == kRotPart) {
-            float* const row = row_s[2 * warp + hw];
+            } else if (ROT == kRotPart) {
+                float* const row = row_s[2 * warp + hw];
 #pragma unroll
-            for (int e = 0; e < NV; ++e) row[64 * (e / 4) + 4 * l + e % 4] = x[e];
-            __syncwarp();
-            if (!is_v) {
+                for (int e = 0; e < NV; ++e) row[64 * (e / 4) + 4 * l + e % 4] = x[e];
+                __syncwarp();
 #pragma unroll
                 for (int e = 0; e < NV; ++e) x[e] = fmaf(x[e], cs[e % NC], row[mate[e]] * sn[e % NC]);
+                __syncwarp();
             }
-            __syncwarp();
         }
-        if (is_q && there) {
-            __half* const q = static_cast<__half*>(a.q_out) + size_t(n) * a.q_ld + hh * D;
+        if (kind == 0) {
+            if (!there) continue;
+            __half* const q = static_cast<__half*>(a.q_out) + size_t(n) * a.q_ld + head * D + 4 * l;
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
                 const __half2 u = __floats2half2_rn(x[4 * j], x[4 * j + 1]), v = __floats2half2_rn(x[4 * j + 2], x[4 * j + 3]);
-                __half2* const at = reinterpret_cast<__half2*>(q + 64 * j + 4 * l);
+                __half2* const at = reinterpret_cast<__half2*>(q + 64 * j);
                 if (p.wide) {
                     *reinterpret_cast<uint2*>(at) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
@@ -199,18 +208,17 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
                     at[0] = u, at[1] = v;
                 }
             }
+            continue;
         }
-        if (page < 0 || h + 1 < Hq) continue;  // the warp as one: no key or value head here
-        const bool store = there && !is_q;
-        uint8_t* const blk =
-            p.c.pages + page + size_t(!store ? 0 : is_v ? hh - Hq - Hkv : hh - Hq) * B::kBytes;
-        uint8_t* const rows = blk + (is_v ? B::kVOff : 0);
+        if (page < 0) continue;
+        uint8_t* const blk = p.c.pages + page + size_t(there ? head : 0) * B::kBytes;
+        uint8_t* const rows = blk + (kind == 2 ? B::kVOff : 0);
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             const int d = 64 * j + 4 * l;
             if (!Q8) {
                 const __half2 u = __floats2half2_rn(x[4 * j], x[4 * j + 1]), v = __floats2half2_rn(x[4 * j + 2], x[4 * j + 3]);
-                if (store)
+                if (there)
                     *reinterpret_cast<uint2*>(rows + B::chunk(r, d >> 3) + (d & 7) * 2) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
                 continue;
@@ -223,17 +231,23 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
             for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             const Q8Scale s = q8_scale_of(__uint_as_float(m));
             uint32_t code = 0;
+            bool sure = true;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 int q;
-                if (!q8_code_fast(x[4 * j + e], s, &q)) q = q8_code_exact(x[4 * j + e], s.d);
+                sure &= q8_code_fast(x[4 * j + e], s, &q);
                 code |= uint32_t(q + 128) << (8 * e);
             }
-            if (store) {
+            if (!sure) {
+                code = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) code |= uint32_t(q8_code_exact(x[4 * j + e], s.d) + 128) << (8 * e);
+            }
+            if (there) {
                 *reinterpret_cast<uint32_t*>(rows + B::chunk(r, d >> 4) + (d & 15)) = code;
                 if ((l & 7) == 0)
-                    *reinterpret_cast<__half*>(blk + B::kScK + (is_v ? B::kScBytes : 0) + (r * (D / 32) + (d >> 5)) * 2) =
-                        __float2half_rn(s.d);
+                    *reinterpret_cast<__half*>(blk + B::kScK + (kind == 2 ? B::kScBytes : 0) +
+                                               (r * (D / 32) + (d >> 5)) * 2) = __float2half_rn(s.d);
             }
         }
     }
@@ -390,12 +404,15 @@ cudaError_t launch_kv_append(const mq_kv_cache& cache, const mq_kv_append_args& 
     AppendArgs p;
     p.a = a;
     p.c = kv_view(cache);
-    // two heads per warp while that leaves the chip room (few tokens: latency), then
-    // longer runs, which form a token's cosines and sines fewer times
-    const int H = a.n_heads + 2 * cache.n_kv_heads;
-    const int64_t per = int64_t(a.n_tokens) * H / (int64_t(num_sms) * 32) / 2 * 2;
-    p.heads_per_warp = per < 2 ? 2 : per > 12 ? 12 : int(per);
-    p.parts = (H + p.heads_per_warp - 1) / p.heads_per_warp;
+    // a pair of heads per warp while that leaves the chip room (few tokens: latency), then longer runs, which
+    // form a token's cosines and sines fewer times: 2048 tokens of 36 heads take 33, 26, 24, 20 and 25 us in
+    // runs of one, two, four, nine and 18 pairs
+    const int pairs = (a.n_heads + 1) / 2 + 2 * ((cache.n_kv_heads + 1) / 2);
+    const int64_t per = int64_t(a.n_tokens) * pairs / (int64_t(num_sms) * 16);
+    p.per_warp = per < 1 ? 1 : per > 9 ? 9 : int(per);
+    p.parts = (pairs + p.per_warp - 1) / p.per_warp;
+    p.per_warp = (pairs + p.parts - 1) / p.parts;  // runs of the same length, and none of length zero
+    p.parts = (pairs + p.per_warp - 1) / p.per_warp;
     p.wide = (reinterpret_cast<uintptr_t>(a.qkv) & 15) == 0 && a.qkv_ld % 4 == 0 &&
              (reinterpret_cast<uintptr_t>(a.q_out) & 7) == 0 && a.q_ld % 4 == 0;
     const unsigned grid = unsigned((int64_t(a.n_tokens) * p.parts + 3) / 4);
