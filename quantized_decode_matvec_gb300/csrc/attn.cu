@@ -863,7 +863,8 @@ constexpr int kWarpRows = 16;
 size_t attn_workspace_bytes(const mq_kv_cache& c, int n_heads, int max_tokens, int num_sms)
 {
     const int RT = n_heads / c.n_kv_heads * max_tokens > kWarpRows ? attn_tc_rows() : kWarpRows;
-    return counters_bytes(c, n_heads) + size_t(num_sms) * 2 * attn_slot_floats(RT, c.head_dim) * 4;
+    return counters_bytes(c, n_heads) + size_t(num_sms) * 2 * attn_slot_floats(RT, c.head_dim) * 4 +
+           size_t(num_sms) * kAttnSharedBytes;
 }
 
 cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* ws, int num_sms, unsigned* status,
@@ -877,13 +878,17 @@ cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* w
     p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
     p.counters = static_cast<unsigned*>(ws);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + counters_bytes(cache, a.n_heads));
+    p.shared = nullptr;  // of the kernel that has one: behind the parts
     p.limit_ns = uint64_t(fault_policy() == FAULT_NONE ? 2000 : 50) * 1000000ull;
     const int rows = p.group * a.max_tokens, RT = rows <= 8 ? 8 : rows <= kWarpRows ? 16 : attn_tc_rows();
     // no more CTAs than the bounds allow units
     const int64_t most = int64_t(cache.n_seqs) * ((int64_t(a.max_len) + kKvPage - 1) / kKvPage) * cache.n_kv_heads *
                          ((rows + RT - 1) / RT);
     const int grid = int(most < 1 ? 1 : most < num_sms ? most : num_sms);
-    if (RT > kWarpRows) return launch_attn_tc(cache, p, grid, status, s);
+    if (RT > kWarpRows) {
+        p.shared = reinterpret_cast<int4*>(p.parts + int64_t(num_sms) * 2 * attn_slot_floats(RT, cache.head_dim));
+        return launch_attn_tc(cache, p, grid, status, s);
+    }
     return RT == 8 ? launch_rows_nt<1>(cache, p, grid, status, s) : launch_rows_nt<2>(cache, p, grid, status, s);
 }
 

@@ -367,9 +367,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         AttnSegment g = {};
         int at = w.first, sg = 0, k = 0;  // k: tiles before
         bool ok = true, more = true;
+        int4 start[2] = {};  // the last segment's group, if it starts here and others go on with it
         for (; ok && more; ++sg) {
             more = attn_next(p, kTcRows, &w, &at, &g);
             if (!more) g.n = g.T = 0;
+            if (more && g.n_ctas > 1 && g.cta0 == int(blockIdx.x)) {
+                start[0] = make_int4(g.t0, g.T, g.head, g.row0);
+                start[1] = make_int4(g.n_ctas, g.slot0, 0, 0);
+            }
             const int ss = sg % kTcSegs;
             if (sg >= kTcSegs) ok = wait_all(&seg_empty[ss], uint32_t(sg / kTcSegs - 1) & 1u);
             if (!ok) break;
@@ -417,6 +422,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 }
             }
         }
+        // every CTA says so in every call, one that gave up too: the join finds nothing of another call
+        if (lane < 2) p.shared[2 * blockIdx.x + lane] = lane == 0 ? start[0] : start[1];
         // copies still in flight land before the CTA can exit
         constexpr int kRing = Q8 ? kUnits : kOps;
         for (int j = k > kRing ? k - kRing : 0; j < k; ++j)
@@ -764,103 +771,131 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
 }
 
 // ---- the groups that several CTAs share: their parts joined in CTA order -------------------------
-// CTA (group, 32 rows), a warp per 32 head values, a thread per row of them.  Bound by the parts' bytes,
-// which lie in L2; a kernel of its own, so that all SMs read them.
+// CTA (first CTA of the group, 32 rows): a warp per 8 head values, a lane per row.  Bound by the parts' bytes, which
+// lie in L2, where there are many rows, and by the latency of its loads where a group has many parts (38 of 14 rows
+// for one sequence of 16000 tokens): so the values of four parts are on their way together, and before the maxima
+// that they wait for; these go through shared memory, where all warps find them.  A kernel of its own, so that all
+// SMs read them.
+constexpr int kJoinAhead = 4;
+
 template <int D>
-__global__ void __launch_bounds__(D) attn_tc_join_kernel(const AttnParams p, const int grid, unsigned* status)
+__global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(const AttnParams p, unsigned* status)
 {
-    __shared__ AttnSegment g_s;
-    __shared__ int there_s;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slab = blockIdx.x % (kTcRows / 32) * 32;
-    if (warp == 0) {
-        bool bad;
-        const AttnRange w = attn_cut(p, kTcRows, grid, 0, &bad);
-        AttnSegment g;
-        const bool there = attn_group(p, kTcRows, w, blockIdx.x / (kTcRows / 32), &g);
-        if (lane == 0) {
-            there_s = there && g.n_ctas > 1;
-            if (there_s) g_s = g;
-        }
-    }
+    extern __shared__ float part_s[];  // [parts][32] maxima, then sums
+    __shared__ float top_s[D / 8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta0 = blockIdx.x;
     griddep_wait();
-    __syncthreads();
-    if (!there_s) return;
-    const AttnSegment& g = g_s;
-    const int row = slab + lane, rows = min(kTcRows, g.T * p.group - g.row0);
-    if (row >= rows) return;
-    auto slot_of = [&](int c) {
-        return p.parts + (int64_t(g.cta0 + c) * 2 + (c == 0 ? g.slot0 : 0)) * attn_slot_floats(kTcRows, D);
+    const int4 s0 = __ldcg(p.shared + 2 * cta0), s1 = __ldcg(p.shared + 2 * cta0 + 1);
+    const int n = s1.x, slab = blockIdx.y * 32, rows = min(kTcRows, s0.y * p.group - s0.w);
+    if (n < 2 || slab >= rows) return;
+    const bool mine = slab + lane < rows;
+    const int row = min(slab + lane, rows - 1);
+    const float* const first = p.parts + (int64_t(cta0) * 2 + s1.y) * attn_slot_floats(kTcRows, D);
+    const float* const others = p.parts + int64_t(cta0) * 2 * attn_slot_floats(kTcRows, D);
+    auto slot_of = [&](int c) { return c == 0 ? first : others + int64_t(c) * 2 * attn_slot_floats(kTcRows, D); };
+    float4 x[kJoinAhead][2];
+    auto load = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i) {
+            const float4* const src =
+                reinterpret_cast<const float4*>(slot_of(min(c0 + i, n - 1)) + 2 * kTcRows) + 2 * warp * kTcRows + row;
+            x[i][0] = __ldcg(src);
+            x[i][1] = __ldcg(src + kTcRows);
+        }
     };
-    float mm = kLowest, l = 0.0f, o[32];
-    bool gone = false;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-    // loads of eight parts, then of two parts' 32 values, are on their way together: a loop over an unknown number
-    // of parts would wait for each (22 us where this takes 5, six parts of 32 groups)
-    for (int c0 = 0; c0 < g.n_ctas; c0 += 8) {
-        float m8[8], l8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool there = c0 + i < g.n_ctas;
-            m8[i] = there ? __ldcg(slot_of(c0 + i) + row) : kLowest;
-            l8[i] = there ? __ldcg(slot_of(c0 + i) + kTcRows + row) : 0.0f;
-        }
-        const float before = mm;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mm = fmaxf(mm, m8[i]);
-        l *= ex2(before - mm);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            gone |= l8[i] < 0.0f;
-            l = fmaf(l8[i], ex2(m8[i] - mm), l);
-        }
+    load(0);
+    float* const m_s = part_s;
+    float* const l_s = part_s + n * 32;
+    for (int c = warp; c < n; c += D / 8) {
+        m_s[c * 32 + lane] = __ldcg(slot_of(c) + row);
+        l_s[c * 32 + lane] = __ldcg(slot_of(c) + kTcRows + row);
     }
-    for (int c = 0; c < g.n_ctas; c += 2) {
-        float4 x[2][8];
-        float f[2];
+    __syncthreads();
+    float mm = kLowest, l = 0.0f, o[8];
+    bool gone = false;
+    for (int c = 0; c < n; ++c) mm = fmaxf(mm, m_s[c * 32 + lane]);
+    for (int c = 0; c < n; ++c) {
+        const float lc = l_s[c * 32 + lane];
+        gone |= lc < 0.0f;
+        l = fmaf(lc, ex2(m_s[c * 32 + lane] - mm), l);
+    }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float* const slot = slot_of(min(c + h, g.n_ctas - 1));
-            f[h] = c + h < g.n_ctas ? ex2(__ldcg(slot + row) - mm) : 0.0f;
-            const float4* const src = reinterpret_cast<const float4*>(slot + 2 * kTcRows) + 8 * warp * kTcRows + row;
+    for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+    for (int c0 = 0;;) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[h][i] = c + h < g.n_ctas ? __ldcg(src + i * kTcRows) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
+        for (int i = 0; i < kJoinAhead; ++i) {
+            if (c0 + i >= n) break;
+            const float f = ex2(m_s[(c0 + i) * 32 + lane] - mm);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                o[4 * i] = fmaf(x[h][i].x, f[h], o[4 * i]);
-                o[4 * i + 1] = fmaf(x[h][i].y, f[h], o[4 * i + 1]);
-                o[4 * i + 2] = fmaf(x[h][i].z, f[h], o[4 * i + 2]);
-                o[4 * i + 3] = fmaf(x[h][i].w, f[h], o[4 * i + 3]);
+            for (int h = 0; h < 2; ++h) {
+                o[4 * h] = fmaf(x[i][h].x, f, o[4 * h]);
+                o[4 * h + 1] = fmaf(x[i][h].y, f, o[4 * h + 1]);
+                o[4 * h + 2] = fmaf(x[i][h].z, f, o[4 * h + 2]);
+                o[4 * h + 3] = fmaf(x[i][h].w, f, o[4 * h + 3]);
             }
         }
+        c0 += kJoinAhead;
+        if (c0 >= n) break;
+        load(c0);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= inv;
+    const int r = s0.w + row, node = attn_row_token(p, r), h = (s0.z - node) * p.group + r;
+    const int64_t tok = s0.x + node;
+    const int d0 = h * D + 8 * warp;
+    const bool q8 = p.a.out_type != MQ_TYPE_F16;
+    if (q8) {  // a block of 32 values lies in four warps
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(fabsf(o[i]))));
+        top_s[warp][lane] = top;
+        __syncthreads();
     }
     if (gone) {  // a page outside the cache: the group stays unwritten
-        atomicOr(status, MQ_DEV_KV_RANGE);
+        if (warp == 0) atomicOr(status, MQ_DEV_KV_RANGE);
         return;
     }
-    tc_emit(p, g, g.row0 + row, D, 32 * warp, o, l == 0.0f ? 0.0f : 1.0f / l);
+    if (!mine) return;
+    if (!q8) {
+        *reinterpret_cast<uint4*>(static_cast<__half*>(p.a.out) + tok * p.a.out_ld + d0) =
+            make_uint4(pack_f16(o[0], o[1]), pack_f16(o[2], o[3]), pack_f16(o[4], o[5]), pack_f16(o[6], o[7]));
+        return;
+    }
+    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(top_s[warp / 4 * 4 + i][lane]));
+    const Q8Scale s = q8_scale_of(__uint_as_float(top));
+    uint16_t* const dst = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.a.out) +
+                                                      (tok * (p.a.n_heads * D / 32) + d0 / 32) * kQ8Bytes);
+    if (warp % 4 == 0) dst[0] = __half_as_ushort(__float2half_rn(s.d));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int a, b;
+        if (!q8_code_fast(o[2 * i], s, &a)) a = q8_code_exact(o[2 * i], s.d);
+        if (!q8_code_fast(o[2 * i + 1], s, &b)) b = q8_code_exact(o[2 * i + 1], s.d);
+        dst[1 + warp % 4 * 4 + i] = uint16_t((a & 255) | (b & 255) << 8);
+    }
 }
 
 template <int D, bool Q8>
-cudaError_t launch_tc(const AttnParams& p, int grid, int64_t groups, unsigned* status, cudaStream_t s)
+cudaError_t launch_tc(const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
 {
     attn_tc_kernel<D, Q8><<<grid, kTcThreads, TcCfg<D, Q8>::kSmem, s>>>(p, status);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;  // one CTA shares no group
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(groups * (kTcRows / 32)));
-    cfg.blockDim = dim3(D);
+    const int rows = p.group * p.a.max_tokens;
+    cfg.gridDim = dim3(grid, ((rows < kTcRows ? rows : kTcRows) + 31) / 32);
+    cfg.blockDim = dim3(4 * D);
+    cfg.dynamicSmemBytes = size_t(grid) * 2 * 32 * sizeof(float);  // 39 KB for 152 SMs
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D>, p, grid, status);
+    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D>, p, status);
 }
 
 }  // namespace
@@ -869,12 +904,11 @@ int attn_tc_rows() { return kTcRows; }
 
 cudaError_t launch_attn_tc(const mq_kv_cache& c, const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
 {
-    const int64_t groups = int64_t(c.n_seqs) * c.n_kv_heads * ((p.group * p.a.max_tokens + kTcRows - 1) / kTcRows);
     if (c.type == MQ_TYPE_Q8_0)
-        return c.head_dim == 128 ? launch_tc<128, true>(p, grid, groups, status, s)
-                                 : launch_tc<64, true>(p, grid, groups, status, s);
-    return c.head_dim == 128 ? launch_tc<128, false>(p, grid, groups, status, s)
-                             : launch_tc<64, false>(p, grid, groups, status, s);
+        return c.head_dim == 128 ? launch_tc<128, true>(p, grid, status, s)
+                                 : launch_tc<64, true>(p, grid, status, s);
+    return c.head_dim == 128 ? launch_tc<128, false>(p, grid, status, s)
+                             : launch_tc<64, false>(p, grid, status, s);
 }
 
 cudaError_t set_attn_tc_attributes()

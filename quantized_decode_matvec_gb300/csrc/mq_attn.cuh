@@ -37,6 +37,7 @@ struct AttnParams {
     float scale_log2;    // scale * log2(e): exp(x) = 2^(x log2 e)
     unsigned* counters;  // one per group
     float* parts;        // two slots of a segment's results per CTA
+    int4* shared;        // per CTA: the group that it starts and the next one goes on with (attn_tc.cu)
     uint64_t limit_ns;
 };
 
@@ -86,12 +87,12 @@ struct AttnRange {
     }
 };
 
-// The cut for a grid of n CTAs, and CTA c's stretch; called by one whole warp.
-__device__ __forceinline__ AttnRange attn_cut(const AttnParams& p, int RT, int n, int c, bool* any_bad)
+// The cut, and where this CTA's stretch starts; called by one whole warp.
+__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, n = gridDim.x, c = blockIdx.x;
     int pages = 0, groups = 0;
-    *any_bad = false;
+    bool any_bad = false;
     for (int s = lane; s < p.c.n_seqs; s += 32) {
         AttnSeq q;
         bool bad;
@@ -100,8 +101,9 @@ __device__ __forceinline__ AttnRange attn_cut(const AttnParams& p, int RT, int n
             pages += k * q.pages;
             groups += k;
         }
-        *any_bad |= bad;
+        any_bad |= bad;
     }
+    if (any_bad && c == 0) atomicOr(status, MQ_DEV_KV_RANGE);
     pages = __reduce_add_sync(0xffffffffu, pages);
     groups = __reduce_add_sync(0xffffffffu, groups);
     AttnRange r;
@@ -113,16 +115,6 @@ __device__ __forceinline__ AttnRange attn_cut(const AttnParams& p, int RT, int n
     r.first = c < r.ctas ? r.begin(c) : r.total;
     r.last = c < r.ctas ? r.begin(c + 1) : r.total;
     r.seq = 0, r.seq_first = 0;
-    return r;
-}
-
-// Where this CTA's stretch starts; called by one whole warp.
-__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status)
-{
-    const int lane = threadIdx.x & 31;
-    bool any_bad;
-    AttnRange r = attn_cut(p, RT, gridDim.x, blockIdx.x, &any_bad);
-    if (any_bad && blockIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
     // the sequence that holds unit r.first, 32 at a time
     for (int s0 = 0; s0 < p.c.n_seqs && r.first < r.last; s0 += 32) {
         AttnSeq q;
@@ -195,50 +187,6 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange
     return false;
 }
 
-// Group gi of a call whose cut is w (as a segment of all its pages, with the CTAs that
-// share it); called by one whole warp.  False: there are fewer groups.
-__device__ __forceinline__ bool attn_group(const AttnParams& p, int RT, const AttnRange& w, int gi, AttnSegment* g)
-{
-    const int lane = threadIdx.x & 31;
-    int groups = 0, units = 0;  // of the sequences before
-    for (int s0 = 0; s0 < p.c.n_seqs; s0 += 32) {
-        AttnSeq q;
-        bool bad;
-        const bool there = s0 + lane < p.c.n_seqs && attn_seq(p, s0 + lane, &q, &bad);
-        const int mine = there ? attn_groups(p, q, RT) : 0, span = there ? q.pages + w.cost : 0;
-        int gs = mine, us = mine * span;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, gs, o), y = __shfl_up_sync(0xffffffffu, us, o);
-            if (lane >= o) gs += x, us += y;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, gi < groups + gs);
-        if (!past) {
-            groups += __shfl_sync(0xffffffffu, gs, 31);
-            units += __shfl_sync(0xffffffffu, us, 31);
-            continue;
-        }
-        const int l = __ffs(past) - 1;
-        const int k = gi - groups - __shfl_sync(0xffffffffu, gs - mine, l);  // within the sequence
-        g->seq = s0 + l;
-        g->t0 = __shfl_sync(0xffffffffu, there ? q.t0 : 0, l);
-        g->T = __shfl_sync(0xffffffffu, there ? q.T : 0, l);
-        g->ctx = __shfl_sync(0xffffffffu, there ? q.ctx : 0, l);
-        const int pages = __shfl_sync(0xffffffffu, there ? q.pages : 0, l);
-        const int g0 = units + __shfl_sync(0xffffffffu, us - mine * span, l) + k * (pages + w.cost);
-        const int blocks = (g->T * p.group + RT - 1) / RT;
-        g->head = blocks == 1 ? k : k / blocks;
-        g->row0 = (k - g->head * blocks) * RT;
-        g->page0 = 0, g->n = pages;
-        g->group_index = 0, g->slot = 0;
-        g->cta0 = w.owner(g0);
-        g->n_ctas = w.owner(g0 + pages - 1) - g->cta0 + 1;
-        g->slot0 = g0 > w.begin(g->cta0) ? 1 : 0;
-        return true;
-    }
-    return false;
-}
-
 // A segment's results in the workspace: m[RT], l[RT] (l < 0 in row 0: the
 // segment met a page outside the cache), then RT rows of D outputs.
 __host__ __device__ constexpr int64_t attn_slot_floats(int RT, int D) { return int64_t(RT) * (D + 2); }
@@ -286,6 +234,7 @@ __device__ __forceinline__ bool barrier_any(int id, int n, bool v)
 
 // many query rows per key/value head (attn_tc.cu): rows of a block there, its launch and set-up
 int attn_tc_rows();
+constexpr int kAttnSharedBytes = 32;  // of AttnParams::shared, per CTA
 cudaError_t launch_attn_tc(const mq_kv_cache& cache, const AttnParams& p, int grid, unsigned* status, cudaStream_t s);
 cudaError_t set_attn_tc_attributes();
 
