@@ -60,7 +60,7 @@ def run_case(mq, rng, ctx, new, Hq, Hkv, D, ctype, out_type="f16", masks="tree",
                                   ctx[s], bits[s], D**-0.5 if scale is None else scale)
         tol = bound(ref, A, big)
         if out_type == "q8_0":
-            top = (np.abs(ref) + tol).reshape(b - a, Hq, -1, 32).max(-1).repeat(32, -1)
+            top = (np.abs(ref) + tol).reshape(b - a, Hq, D // 32, 32).max(-1).repeat(32, -1)
             tol = tol + top / 127 * (0.5 + 2 * 127 * 2**-11)
         err = np.abs(got[a:b] - ref)
         assert (err <= tol).all(), (s, ctx[s], new[s], float((err / tol).max()), np.argwhere(err > tol)[:3])
@@ -268,3 +268,50 @@ def test_bad_device_data_is_skipped_and_reported(cuda_ready):
         # tokens outside every sequence are not written
         out, st = call([0, T, T], [100, 50], table)
         assert st == 0 and torch.equal(out[:T], good[:T]) and (out[T:] == 3).all()
+
+
+@pytest.mark.parametrize("ctype", ["q8_0", "f16"])
+@pytest.mark.parametrize("Hq,Hkv,D,T", [(14, 2, 128, 3), (14, 2, 64, 18), (8, 2, 128, 64), (14, 2, 128, 33), (16, 2, 64, 48)])
+def test_many_pages_of_trees(cuda_ready, ctype, Hq, Hkv, D, T):
+    # more pages than SMs, of one long sequence (many parts of a group) and short ones; blocks of up to 128 rows and more
+    run_case(cuda_ready, np.random.default_rng(T), [20000, 3, 0, 700], [T, T, 1, T // 2], Hq, Hkv, D, ctype)
+
+
+@pytest.mark.parametrize("ctype", ["q8_0", "f16"])
+@pytest.mark.parametrize("T", [2, 33])
+def test_many_sequences(cuda_ready, ctype, T):
+    # more groups than SMs: most are one CTA's own, in one kernel's call and in the other's
+    rng = np.random.default_rng(T + 5)
+    ctx = [int(c) for c in rng.integers(0, 200, 50)]
+    run_case(cuda_ready, rng, ctx, [int(t) for t in rng.integers(0, T + 1, 50)], 16, 4, 64, ctype, out_type="q8_0")
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_not_finite_values_in_a_q8_0_output(cuda_ready, T):
+    # a value that is not finite: the blocks of the rows that see it say so by their scale, the others are untouched
+    import torch
+    mq, D, Hkv, Hq = cuda_ready, 64, 1, 4
+    rng = np.random.default_rng(T)
+    ctx = 4000
+    K = rng.standard_normal((ctx + T, Hkv, D)).astype(np.float32)
+    V = rng.standard_normal((ctx + T, Hkv, D)).astype(np.float32)
+    masks = tree_masks(rng, T)
+    masks[T - 1] = 1 << (T - 1)
+    bad = V.copy()
+    bad[ctx + 1, 0, 40] = np.inf  # node 1
+    start, lens = dev(np.array([0, T], np.int32)), dev(np.array([ctx], np.int32))
+    q = dev(rng.standard_normal((T, Hq * D)).astype(np.float16))
+    got = []
+    for v in (V, bad):
+        pages, table = P.build([K], [v], "f16", np.random.default_rng(1))
+        out = mq.attn_tree(mq.KVCache(dev(pages), dev(table), "f16", Hkv, D), q, start, lens, mask=dev(as_i64(masks)),
+                           max_len=ctx + T, max_tokens=T, out_type="q8_0")
+        got.append(out.cpu().numpy().reshape(T, Hq, D // 32, 34))
+    ok_status(mq)
+    for i in range(T):
+        scale = got[1][i, :, 1, :2].copy().view(np.float16)
+        assert np.array_equal(got[0][i, :, 0], got[1][i, :, 0])
+        if masks[i] >> 1 & 1:
+            assert not np.isfinite(scale).any()
+        else:
+            assert np.array_equal(got[0][i], got[1][i])

@@ -267,3 +267,60 @@ def test_pages_beyond_4_gib(cuda_ready):
     at, voff, _, _ = P.places("f16", D)
     tail = cache.pages[-Hkv * P.block_bytes("f16", D):].cpu().numpy().view(np.float16).reshape(Hkv, -1)
     assert np.array_equal(tail[:, at[63] // 2], x[0, 4:8])
+
+
+@pytest.mark.parametrize("ctype", ["q8_0", "f16"])
+@pytest.mark.parametrize("Hq,Hkv,D", HEADS)
+def test_append_of_many_tokens_is_the_same_as_of_few(cuda_ready, ctype, Hq, Hkv, D):
+    # long runs of heads per warp, rows on and off a 16-byte boundary: the same bits as token by token
+    import torch
+    mq = cuda_ready
+    rng = np.random.default_rng(Hq + D)
+    n, H = 900, Hq + 2 * Hkv
+    x = dev(rng.standard_normal((n, H * D + 2)).astype(np.float32))
+    even = x[:, :H * D].contiguous()
+    freq = dev((1e5 ** (-np.arange(0, D, 2) / D)).astype(np.float32))
+    w = dev(rng.uniform(0.5, 1.5, D).astype(np.float32))
+    table = dev(rng.permutation(15).reshape(1, 15).astype(np.int32))
+    at = dev(np.arange(n, dtype=np.int32))
+    seq = torch.zeros_like(at)
+    got = []
+    for rows, step in ((x[:, :H * D], n), (even, n), (even, 7)):
+        cache = mq.KVCache(torch.zeros(15 * mq.mq_kv_page_bytes(mq.KV_TYPES[ctype], Hkv, D), dtype=torch.uint8,
+                                       device="cuda"), table, ctype, Hkv, D)
+        q = [mq.kv_append(cache, rows[a:a + step], at[a:a + step], seq[a:a + step], at[a:a + step], Hq, inv_freq=freq,
+                          q_norm=w, k_norm=w) for a in range(0, n, step)]
+        got.append((torch.cat(q), cache.pages))
+    ok_status(mq)
+    for q, pages in got[1:]:
+        assert torch.equal(q, got[0][0]) and torch.equal(pages, got[0][1])
+    ref = P.norm_rope(even.cpu().numpy().reshape(n, H, D)[:, :Hq], w.cpu().numpy(), 1e-6, np.arange(n),
+                      freq.cpu().numpy(), False)
+    q = got[0][0].cpu().numpy().reshape(n, Hq, D).astype(np.float64)
+    assert (np.abs(q - ref) <= 2**-11 * np.abs(ref) + 2**-19 * np.abs(ref).max(-1, keepdims=True) + 2**-24).all()
+
+
+@pytest.mark.parametrize("ctype,Hkv,D", [("q8_0", 3, 128), ("f16", 5, 64), ("q8_0", 40, 64), ("f16", 20, 128)])
+def test_read_of_many_tokens_is_the_same_as_of_few(cuda_ready, ctype, Hkv, D):
+    # a read of several chunks per thread; a row of more chunks than a CTA has threads; an odd number of heads
+    import torch
+    mq = cuda_ready
+    rng = np.random.default_rng(Hkv)
+    n_pages = 24
+    size = mq.mq_kv_page_bytes(mq.KV_TYPES[ctype], Hkv, D)
+    pages = dev(rng.integers(0, 120, n_pages * size, dtype=np.uint8))  # high bytes below 0x78: finite f16 values
+    cache = mq.KVCache(pages, dev(rng.permutation(n_pages).reshape(2, -1).astype(np.int32)), ctype, Hkv, D)
+    n = 70001
+    seq, slot = dev(rng.integers(0, 2, n).astype(np.int32)), dev(rng.integers(0, 12 * 64, n).astype(np.int32))
+    k, v = mq.kv_read(cache, seq, slot)
+    for a in range(0, n, 997):
+        ks, vs = mq.kv_read(cache, seq[a:a + 997], slot[a:a + 997])
+        assert torch.equal(ks, k[a:a + 997]) and torch.equal(vs, v[a:a + 997])
+    ok_status(mq)
+    table = cache.table.cpu().numpy()
+    blocks = cache.pages.cpu().numpy().reshape(n_pages, Hkv, -1)
+    for i in [0, 1, n // 2, n - 1]:
+        p, r = table[int(seq[i]), int(slot[i]) // 64], int(slot[i]) % 64
+        for h in range(Hkv):
+            for got, want in zip((k, v), P.unpack(blocks[p, h], ctype, D)):
+                assert np.array_equal(got[i, h].cpu().numpy().view(np.uint16), want[r].view(np.uint16))

@@ -154,3 +154,13 @@ def test_tensor_helpers_refuse_what_they_would_misread(mq_lib):
         m.attn_tree(c, q, i, i[:2], out=q[:2], workspace=ws)
     with pytest.raises(ValueError):
         m.attn_tree(c, q, i, i[:2], out_type="f32", workspace=ws)
+
+
+def test_attention_work_is_counted_with_its_groups(mq_lib):
+    # pages and the cost of a group together pass 31 bits where the pages alone do not
+    m = mq_lib
+    c = m.KvCacheStruct(0x10000, 0x20000, 10, 4096, 2**20, m.MQ_TYPE_Q8_0, 256, 64, 0)
+    a = m.AttnArgs(0x1000, 0x2000, 0x3000, 0x4000, 0x5000, 1024 * 64, 1024 * 64, 64, 1024, 0, 64, m.MQ_TYPE_F16, 1.0)
+    for max_len, want in ((64 * 51, m.MQ_OK), (64 * 52, m.MQ_ERR_UNSUPPORTED)):
+        a.max_len, a.n_tokens = max_len, 0
+        assert m._lib.mq_attn_tree(c, a, 0, 0, 0) == want
