@@ -29,8 +29,9 @@
 //   powers of two; 2^15 still fits f16), which after the first tiles is rare:
 //   a predicate on the barrier that the team needs anyway, instead of a
 //   maximum over its lanes and a rescaling;
-// * a team that is done with a segment leaves its outputs and goes on to the
-//   next; the last of them to leave joins them.  Nothing waits for all teams.
+// * a team that is done with a segment leaves its outputs in shared memory and
+//   goes on to the next; a warp of its own joins them.  (Joined by the last team
+//   to leave, the slowest fell behind further with every segment.)
 // Scores, maxima, sums and outputs are fp32 throughout.
 #include "mq_attn.cuh"
 
@@ -60,7 +61,7 @@ struct RowsCfg {
     // registers allow 16 warps of 8 rows or 12 of 16; the ring of 32 KB blocks is too short for four teams
     static constexpr int kTeams = D == 128 && (NT == 2 || !Q8) ? 3 : 4;
     static constexpr int kWarps = kTeams * kTeam;
-    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kThreads = 32 * (kWarps + 2);
     static constexpr int kSlice = D / kTeam;                     // head values that a warp sums
     static constexpr int kQ = kRows * D * 2;                     // a segment's query rows
     static constexpr int kP = NT * kTeam * 32 * 8;               // a page's probabilities
@@ -261,7 +262,6 @@ template <int NT>
 struct TeamWords {
     float top[kTeam][8 * NT];  // the warps' maxima when the team's is raised
     int flags;
-    int closed_last;
 };
 
 // ---- one page ------------------------------------------------------------------------------
@@ -474,13 +474,13 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
     uint2* const p_s = reinterpret_cast<uint2*>(sm + kStages * B::kBytes + kSegs * C::kQ);
     float* const out_s = reinterpret_cast<float*>(sm + kStages * B::kBytes + kSegs * C::kQ + kTeams * 2 * C::kP);
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], seg_full[kSegs], seg_empty[kSegs];
-    __shared__ __align__(8) uint64_t out_free[2], part_full[2], part_done[2];
+    __shared__ __align__(8) uint64_t out_full[2], out_free[2], part_done[2];
     __shared__ RowsSegment seg_s[kSegs];
     __shared__ AttnSegment split_s[2];
     __shared__ uint64_t mask_s[kSegs][RT];
     // a segment's teams (every other segment has the other place): maxima, sums, whether there were pages, bad ones
     __shared__ float m_s[2][kTeams][RT], l_s[2][kTeams][kTeam][RT];
-    __shared__ int had_s[2][kTeams], closed_s[2];
+    __shared__ int had_s[2][kTeams];
     __shared__ TeamWords<NT> words_s[kTeams];
     __shared__ float cm_s[kWarps][RT], cl_s[kWarps][RT];
     __shared__ int bad_s[kStages], seen_s[kStages], last_s[2];
@@ -493,13 +493,12 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
         seen_s[threadIdx.x] = 0;
     } else if (threadIdx.x >= 32 && threadIdx.x < 32 + kSegs) {
         mbar_init(&seg_full[threadIdx.x - 32], 1);
-        mbar_init(&seg_empty[threadIdx.x - 32], kWarps);
+        mbar_init(&seg_empty[threadIdx.x - 32], kWarps + 1);
     } else if (threadIdx.x >= 64 && threadIdx.x < 66) {
         const int k = threadIdx.x - 64;
-        mbar_init(&out_free[k], kTeam);
-        mbar_init(&part_full[k], kTeam);
+        mbar_init(&out_full[k], kWarps);
+        mbar_init(&out_free[k], 1);
         mbar_init(&part_done[k], 1);
-        closed_s[k] = 0;
     } else if (threadIdx.x >= 96 && threadIdx.x < 96 + kTeams) {
         words_s[threadIdx.x - 96].flags = 0;
         if (threadIdx.x == 96) abort_flag = 0;
@@ -575,14 +574,6 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                 }
             }
         }
-        // the shared groups' arrivals, once the consumers have written their parts
-        for (int k = 0; k < splits; ++k) {
-            const bool there = mbar_wait_bounded(&part_full[k], 0, p.limit_ns) && !abort_flag;
-            if (lane == 0) {
-                last_s[k] = there && attn_arrive(p, split_s[k]);
-                mbar_arrive(&part_done[k]);
-            }
-        }
         // copies still in flight land before the CTA can exit
         for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
             (void)mbar_wait_bounded(&full[j % kStages], uint32_t(j / kStages) & 1u, p.limit_ns);
@@ -590,6 +581,92 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
             (void)mbar_wait_bounded(&seg_full[j % kSegs], uint32_t(j / kSegs) & 1u, p.limit_ns);
         __syncwarp();
         if (abort_flag && lane == 0) atomicOr(status, MQ_DEV_TIMEOUT);
+        return;
+    }
+
+    if (warp == kWarps + 1) {
+        // ---- the segments' joins, in order, while the teams are at later ones
+        int splits = 0;
+        for (int sg = 0;; ++sg) {
+            const int ss = sg % kSegs, os = sg & 1;
+            bool ok = wait_all(&seg_full[ss], uint32_t(sg / kSegs) & 1u);
+            if (!ok || seg_s[ss].g.n == 0) break;
+            ok = wait_all(&out_full[os], uint32_t(sg / 2) & 1u);
+            if (!ok) break;
+            const AttnSegment& g = seg_s[ss].g;
+            const bool split = g.n_ctas > 1;
+            const int rows = min(RT, g.T * p.group - g.row0);
+            float* const slot = p.parts + (int64_t(blockIdx.x) * 2 + g.slot) * attn_slot_floats(RT, D);
+            int had = 0;  // the teams that had pages
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < kTeams; ++k) {
+                had |= had_s[os][k] != 0 ? 1 << k : 0;
+                bad |= had_s[os][k] == 2;
+            }
+            // lane l: row l % 8 (+ 8j) of team l / 8: its weight, and the row's maximum and sum
+            float fk[NT], top[NT], sum[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int k = lane >> 3, r = 8 * j + (lane & 7);
+                const bool there = had >> k & 1;
+                const float mk = there ? m_s[os][k][r] : kLowest;
+                float lk = 0.0f;
+#pragma unroll
+                for (int u = 0; u < kTeam; ++u) lk += there ? l_s[os][k][u][r] : 0.0f;
+                top[j] = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, 8));
+                top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
+                fk[j] = there ? ex2(mk - top[j]) : 0.0f;
+                sum[j] = lk * fk[j];
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
+                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
+                if (split && lane < 8 && r < rows) {
+                    slot[r] = top[j];
+                    slot[RT + r] = bad ? -1.0f : sum[j];
+                }
+                sum[j] = sum[j] == 0.0f ? 0.0f : 1.0f / sum[j];
+            }
+            constexpr int kLanes = D / 4, kStep = 32 / kLanes;  // lanes of a row with four values each, rows at a time
+            const int d = lane % kLanes * 4;
+#pragma unroll
+            for (int j = 0; j < RT; j += kStep) {
+                if (j >= rows) break;
+                const int r = j + lane / kLanes;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < kTeams; ++k) {
+                    const float f = __shfl_sync(0xffffffffu, fk[j / 8], 8 * k + (r & 7));
+                    if (!(had >> k & 1)) continue;  // what lies there is not read as a number
+                    const float4 o = *reinterpret_cast<const float4*>(out_s + ((os * kTeams + k) * RT + r) * D + d);
+                    v.x = fmaf(o.x, f, v.x), v.y = fmaf(o.y, f, v.y), v.z = fmaf(o.z, f, v.z), v.w = fmaf(o.w, f, v.w);
+                }
+                const float inv = __shfl_sync(0xffffffffu, sum[j / 8], r & 7);
+                if (split) {
+                    if (r < rows) *reinterpret_cast<float4*>(slot + 2 * RT + r * D + d) = v;
+                } else if (!bad) {
+                    v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+                    attn_emit4(p, g, g.row0 + r, r < rows, D, d, v);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&out_free[os]);
+                if (split) {
+                    last_s[splits] = attn_arrive(p, g);
+                    mbar_arrive(&part_done[splits]);
+                } else if (bad) {
+                    atomicOr(status, MQ_DEV_KV_RANGE);
+                }
+                mbar_arrive(&seg_empty[ss]);
+            }
+            splits += split;
+        }
+        if (abort_flag && lane == 0) {  // the teams wait for none that does not come
+            for (; splits < 2; ++splits) {
+                last_s[splits] = 0;
+                mbar_arrive(&part_done[splits]);
+            }
+        }
         return;
     }
 
@@ -683,76 +760,11 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                 }
         }
         if (wi == 0 && lane == 0) had_s[os][team] = had ? (bad ? 2 : 1) : 0;
-        named_barrier_sync(id, 32 * kTeam);
-        if (wi == 0 && lane == 0) {
-            __threadfence_block();
-            words->closed_last = atomicAdd(&closed_s[os], 1) == kTeams - 1;
-            __threadfence_block();
-        }
-        named_barrier_sync(id, 32 * kTeam);
-        if (words->closed_last) {
-            // ---- the last team to leave joins them
-            const int split = seg_s[ss].split, rows = min(RT, g.T * p.group - g.row0);
-            float* const slot = p.parts + (int64_t(blockIdx.x) * 2 + g.slot) * attn_slot_floats(RT, D);
-            bool seg_bad = false;
-#pragma unroll
-            for (int k = 0; k < kTeams; ++k) seg_bad |= had_s[os][k] == 2;
-            // lane l: row l % 8 (+ 8j) of team l / 8: its weight, and the row's maximum and sum
-            float fk[NT], top[NT], sum[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int k = lane >> 3, r = 8 * j + (lane & 7);
-                const bool there = k < kTeams && had_s[os][k] != 0;
-                const float mk = there ? m_s[os][k][r] : kLowest;
-                float lk = 0.0f;
-#pragma unroll
-                for (int u = 0; u < kTeam; ++u) lk += there ? l_s[os][k][u][r] : 0.0f;
-                top[j] = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, 8));
-                top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-                fk[j] = there ? ex2(mk - top[j]) : 0.0f;
-                sum[j] = lk * fk[j];
-                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
-                sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
-                if (split >= 0 && wi == 0 && lane < 8 && r < rows) {
-                    slot[r] = top[j];
-                    slot[RT + r] = seg_bad ? -1.0f : sum[j];
-                }
-                sum[j] = sum[j] == 0.0f ? 0.0f : 1.0f / sum[j];
-            }
-            constexpr int kBlocks = RT * D / 32 / kTeam;  // of 32 values
-#pragma unroll
-            for (int j = 0; j < kBlocks; ++j) {
-                // block wi of row j, or (64 values) block wi % 2 of row 2j + wi / 2
-                const int r = D == 128 ? j : 2 * j + (wi >> 1), d = (D == 128 ? wi : wi & 1) * 32 + lane;
-                constexpr int kRowsAStep = 128 / D;
-                float v = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kTeams; ++k) {
-                    const float f = __shfl_sync(0xffffffffu, fk[kRowsAStep * j / 8], 8 * k + (r & 7));
-                    // a team without pages left nothing: what lies there is not read as a number
-                    const float o = out_s[((os * kTeams + k) * RT + r) * D + d];
-                    v = f == 0.0f && !had_s[os][k] ? v : fmaf(o, f, v);
-                }
-                const float inv = __shfl_sync(0xffffffffu, sum[kRowsAStep * j / 8], r & 7);
-                if (r >= rows) continue;
-                if (split >= 0)
-                    slot[2 * RT + r * D + d] = v;
-                else if (!seg_bad)
-                    attn_emit(p, g, g.row0 + r, D, d - lane, v * inv);
-            }
-            __syncwarp();
-            if (wi == 0 && lane == 0) {
-                closed_s[os] = 0;
-                if (split < 0 && seg_bad) atomicOr(status, MQ_DEV_KV_RANGE);
-            }
-            __syncwarp();
-            if (lane == 0) {
-                if (split >= 0) mbar_arrive(&part_full[split]);
-                mbar_arrive(&out_free[os]);
-            }
-        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_empty[ss]);
+        if (lane == 0) {
+            mbar_arrive(&out_full[os]);
+            mbar_arrive(&seg_empty[ss]);
+        }
     }
 
     // ---- the shared groups whose last CTA this is: their segments joined in CTA order

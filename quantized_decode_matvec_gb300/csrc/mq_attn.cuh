@@ -208,6 +208,42 @@ __device__ __forceinline__ void attn_emit(const AttnParams& p, const AttnSegment
     }
 }
 
+// a warp writes rows, four values d .. d + 3 per lane (the eight lanes of a block of 32 lie together)
+__device__ __forceinline__ void attn_emit4(const AttnParams& p, const AttnSegment& g, int row, bool there, int D, int d,
+                                           float4 v)
+{
+    const int lane = threadIdx.x & 31;
+    const int node = attn_row_token(p, row), h = (g.head - node) * p.group + row;
+    const int64_t tok = g.t0 + node;
+    if (p.a.out_type == MQ_TYPE_F16) {
+        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+        if (there)
+            *reinterpret_cast<uint2*>(static_cast<__half*>(p.a.out) + tok * p.a.out_ld + h * D + d) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        return;
+    }
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(fabsf(x[i])));
+#pragma unroll
+    for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const Q8Scale s = q8_scale_of(__uint_as_float(top));
+    uint32_t code = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int c;
+        if (!q8_code_fast(x[i], s, &c)) c = q8_code_exact(x[i], s.d);
+        code |= uint32_t(c & 255) << (8 * i);
+    }
+    if (!there) return;
+    uint16_t* const ob = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.a.out) +
+                                                     (tok * (p.a.n_heads * D / 32) + (h * D + d) / 32) * kQ8Bytes);
+    if (lane % 8 == 0) ob[0] = __half_as_ushort(__float2half_rn(s.d));
+    ob[1 + d % 32 / 2] = uint16_t(code);
+    ob[2 + d % 32 / 2] = uint16_t(code >> 16);
+}
+
 // a segment's arrival at its group's counter; true in the CTA that came last
 // (one thread calls it, after the CTA's results are written and synchronised)
 __device__ __forceinline__ bool attn_arrive(const AttnParams& p, const AttnSegment& g)
