@@ -61,7 +61,7 @@ struct RowsCfg {
     // registers allow 16 warps of 8 rows or 12 of 16; the ring of 32 KB blocks is too short for four teams
     static constexpr int kTeams = D == 128 && (NT == 2 || !Q8) ? 3 : 4;
     static constexpr int kWarps = kTeams * kTeam;
-    static constexpr int kThreads = 32 * (kWarps + 2);
+    static constexpr int kThreads = 32 * (kWarps + 3);  // and the warps that plan, copy and join
     static constexpr int kSlice = D / kTeam;                     // head values that a warp sums
     static constexpr int kQ = kRows * D * 2;                     // a segment's query rows
     static constexpr int kP = NT * kTeam * 32 * 8;               // a page's probabilities
@@ -473,11 +473,12 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
     __half* const q_s = reinterpret_cast<__half*>(sm + kStages * B::kBytes);
     uint2* const p_s = reinterpret_cast<uint2*>(sm + kStages * B::kBytes + kSegs * C::kQ);
     float* const out_s = reinterpret_cast<float*>(sm + kStages * B::kBytes + kSegs * C::kQ + kTeams * 2 * C::kP);
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], seg_full[kSegs], seg_empty[kSegs];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], seg_planned[kSegs], seg_full[kSegs], seg_empty[kSegs];
     __shared__ __align__(8) uint64_t out_full[2], out_free[2], part_done[2];
     __shared__ RowsSegment seg_s[kSegs];
     __shared__ AttnSegment split_s[2];
     __shared__ uint64_t mask_s[kSegs][RT];
+    __shared__ int32_t pages_s[kSegs][32];  // a segment's first ones
     // a segment's teams (every other segment has the other place): maxima, sums, whether there were pages, bad ones
     __shared__ float m_s[2][kTeams][RT], l_s[2][kTeams][kTeam][RT];
     __shared__ int had_s[2][kTeams];
@@ -492,8 +493,9 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
         mbar_init(&empty[threadIdx.x], kTeam);
         seen_s[threadIdx.x] = 0;
     } else if (threadIdx.x >= 32 && threadIdx.x < 32 + kSegs) {
+        mbar_init(&seg_planned[threadIdx.x - 32], 1);
         mbar_init(&seg_full[threadIdx.x - 32], 1);
-        mbar_init(&seg_empty[threadIdx.x - 32], kWarps + 1);
+        mbar_init(&seg_empty[threadIdx.x - 32], kWarps + 2);
     } else if (threadIdx.x >= 64 && threadIdx.x < 66) {
         const int k = threadIdx.x - 64;
         mbar_init(&out_full[k], kWarps);
@@ -508,38 +510,34 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
     if (warp == kWarps) w = attn_range(p, RT, status);
     __syncthreads();
 
+    auto give_up = [&]() {
+        abort_flag = 1;
+        if (lane == 0) atomicOr(status, MQ_DEV_TIMEOUT);
+    };
     // one outcome for the whole warp
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.limit_ns));
-        if (!ok) abort_flag = 1;
+        if (!ok) give_up();
         return ok;
     };
 
     if (warp == kWarps) {
-        // ---- producer: lane 0 copies the pages, the warp reads their numbers 32 at a time
+        // ---- the segments, ahead of the copies (a segment's set-up takes some microseconds: divisions, the page
+        // table's latency, code that left the instruction cache)
         AttnSegment g = {};
-        int at = w.first, it = 0, s = 0, sg = 0, splits = 0;
-        uint32_t phase = 0;
+        int at = w.first, it = 0, sg = 0, splits = 0;
         bool ok = true, more = true;
         for (; ok && more; ++sg) {
             more = attn_next(p, RT, &w, &at, &g);
             if (!more) g.n = g.T = 0;
             const int ss = sg % kSegs, rows = more ? min(RT, g.T * p.group - g.row0) : 0;
-            const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0;
-            int32_t page_l = lane < g.n ? __ldg(table + lane) : 0;
+            const int32_t page = lane < g.n ? __ldg(p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0 + lane) : 0;
             uint64_t bits = 0;
             const int row = g.row0 + lane, node = attn_row_token(p, row);
             if (lane < rows) bits = p.a.mask ? __ldg(p.a.mask + g.t0 + node) : ~0ull >> (63 - node);
             if (sg >= kSegs) ok = wait_all(&seg_empty[ss], uint32_t(sg / kSegs - 1) & 1u);
             if (!ok) break;
-            if (lane == 0) mbar_expect_tx(&seg_full[ss], uint32_t(rows) * D * 2);
-            __syncwarp();
-            if (lane < rows)
-                bulk_copy_g2s(q_s + (ss * RT + lane) * D,
-                              static_cast<const __half*>(p.a.q) + int64_t(g.t0 + node) * p.a.q_ld +
-                                  ((g.head - node) * p.group + row) * D,
-                              D * 2, &seg_full[ss]);
             const int split = more && g.n_ctas > 1 ? splits++ : -1;
             if (lane == 0) {
                 seg_s[ss].g = g;
@@ -547,13 +545,48 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                 seg_s[ss].split = more ? split : splits;
                 if (split >= 0) split_s[split] = g;
             }
+            pages_s[ss][lane] = page;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&seg_planned[ss]);
+                mbar_expect_tx(&seg_full[ss], uint32_t(rows) * D * 2);
+            }
+            __syncwarp();
+            if (lane < rows)
+                bulk_copy_g2s(q_s + (ss * RT + lane) * D,
+                              static_cast<const __half*>(p.a.q) + int64_t(g.t0 + node) * p.a.q_ld +
+                                  ((g.head - node) * p.group + row) * D,
+                              D * 2, &seg_full[ss]);
             if (lane < RT) mask_s[ss][lane] = bits;
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_full[ss]);
-            for (int i0 = 0; ok && i0 < g.n; i0 += 32) {
+            it += g.n;
+        }
+        // copies still in flight land before the CTA can exit
+        for (int j = sg > kSegs ? sg - kSegs : 0; j < sg; ++j)
+            (void)mbar_wait_bounded(&seg_full[j % kSegs], uint32_t(j / kSegs) & 1u, p.limit_ns);
+        return;
+    }
+
+    if (warp == kWarps + 2) {
+        // ---- the pages' copies, by lane 0; the warp reads their numbers 32 at a time
+        int it = 0, s = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int sg = 0; ok; ++sg) {
+            const int ss = sg % kSegs;
+            ok = wait_all(&seg_planned[ss], uint32_t(sg / kSegs) & 1u);
+            if (!ok) break;
+            const AttnSegment& g = seg_s[ss].g;
+            const int n = g.n;
+            if (n == 0) break;
+            const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0;
+            const uint8_t* const src = p.c.pages + int64_t(g.head) * B::kBytes;
+            int32_t page_l = pages_s[ss][lane];
+            for (int i0 = 0; ok && i0 < n; i0 += 32) {
                 const int32_t page_now = page_l;
-                if (i0 + 32 + lane < g.n) page_l = __ldg(table + i0 + 32 + lane);
-                const int m = min(32, g.n - i0);
+                if (i0 + 32 + lane < n) page_l = __ldg(table + i0 + 32 + lane);
+                const int m = min(32, n - i0);
                 for (int i = 0; i < m; ++i, ++it) {
                     const int32_t page = __shfl_sync(0xffffffffu, page_now, i);
                     if (it >= kStages) ok = wait_all(&empty[s], phase ^ 1u);
@@ -565,22 +598,19 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                             mbar_arrive(&full[s]);
                         } else {
                             mbar_arrive_expect_tx(&full[s], B::kBytes);
-                            bulk_copy_g2s(ring + s * B::kBytes,
-                                          p.c.pages + (int64_t(page) * p.c.n_kv_heads + g.head) * B::kBytes, B::kBytes,
+                            bulk_copy_g2s(ring + s * B::kBytes, src + int64_t(page) * p.c.n_kv_heads * B::kBytes, B::kBytes,
                                           &full[s]);
                         }
                     }
                     if (++s == kStages) s = 0, phase ^= 1u;
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_empty[ss]);
         }
         // copies still in flight land before the CTA can exit
         for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
             (void)mbar_wait_bounded(&full[j % kStages], uint32_t(j / kStages) & 1u, p.limit_ns);
-        for (int j = sg > kSegs ? sg - kSegs : 0; j < sg; ++j)
-            (void)mbar_wait_bounded(&seg_full[j % kSegs], uint32_t(j / kSegs) & 1u, p.limit_ns);
-        __syncwarp();
-        if (abort_flag && lane == 0) atomicOr(status, MQ_DEV_TIMEOUT);
         return;
     }
 
@@ -682,7 +712,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                 ok = __all_sync(0xffffffffu, load_acquire(word) >= value);
             } while (__any_sync(0xffffffffu, !ok && global_timer_ns() - t0 < p.limit_ns));
         }
-        if (!ok) abort_flag = 1;
+        if (!ok) give_up();
         return ok;
     };
     bool good = true;  // the whole team's

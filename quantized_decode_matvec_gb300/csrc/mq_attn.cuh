@@ -27,7 +27,7 @@ namespace mq {
 
 // 64 sequences of 300 to 8000 tokens with one query each (q8_0, 4 key/value heads of 128): 79, 76, 71, 66, 69 and
 // 70 us at a cost of 2, 5, 8, 11, 14 and 18 pages.  The entry check's bound on the units counts on at most 11.
-constexpr int kAttnGroupCost = 10;
+constexpr int kAttnGroupCost = 8;
 
 struct AttnParams {
     mq_attn_args a;
