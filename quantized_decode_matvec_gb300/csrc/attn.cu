@@ -48,9 +48,7 @@ constexpr float kRaise = 5.0f, kShift = 10.0f, kLowest = -3.402823466e38f;
 // what the producer hands over with a segment, besides its query rows
 struct RowsSegment {
     AttnSegment g;
-    int it0;    // number of its first page among the CTA's
-    int split;  // index among the CTA's groups that it shares with others (at most two), or -1
-                // (behind the last segment: how many there were)
+    int it0;  // number of its first page among the CTA's
 };
 
 // query rows 8*NT
@@ -58,6 +56,7 @@ template <int D, bool Q8, int NT>
 struct RowsCfg {
     using B = KvBlock<D, Q8>;
     static constexpr int kRows = 8 * NT;
+    static constexpr bool kJoins = NT == 1;  // the CTA that comes last joins a shared group
     // registers allow 16 warps of 8 rows or 12 of 16; the ring of 32 KB blocks is too short for four teams
     static constexpr int kTeams = D == 128 && (NT == 2 || !Q8) ? 3 : 4;
     static constexpr int kWarps = kTeams * kTeam;
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
 {
     using B = KvBlock<D, Q8>;
     using C = RowsCfg<D, Q8, NT>;
-    constexpr int RT = C::kRows, kTeams = C::kTeams, kWarps = C::kWarps, kCons = 32 * kWarps, kStages = C::kStages;
+    constexpr int RT = C::kRows, kTeams = C::kTeams, kWarps = C::kWarps, kStages = C::kStages;
     extern __shared__ __align__(128) uint8_t sm[];
     uint8_t* const ring = sm;
     __half* const q_s = reinterpret_cast<__half*>(sm + kStages * B::kBytes);
@@ -475,16 +474,16 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
     float* const out_s = reinterpret_cast<float*>(sm + kStages * B::kBytes + kSegs * C::kQ + kTeams * 2 * C::kP);
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], seg_planned[kSegs], seg_full[kSegs], seg_empty[kSegs];
     __shared__ __align__(8) uint64_t out_full[2], out_free[2], part_done[2];
+    __shared__ AttnSegment split_s[2];  // the groups that it shares
+    __shared__ int last_s[2];
     __shared__ RowsSegment seg_s[kSegs];
-    __shared__ AttnSegment split_s[2];
     __shared__ uint64_t mask_s[kSegs][RT];
     __shared__ int32_t pages_s[kSegs][32];  // a segment's first ones
     // a segment's teams (every other segment has the other place): maxima, sums, whether there were pages, bad ones
     __shared__ float m_s[2][kTeams][RT], l_s[2][kTeams][kTeam][RT];
     __shared__ int had_s[2][kTeams];
     __shared__ TeamWords<NT> words_s[kTeams];
-    __shared__ float cm_s[kWarps][RT], cl_s[kWarps][RT];
-    __shared__ int bad_s[kStages], seen_s[kStages], last_s[2];
+    __shared__ int bad_s[kStages], seen_s[kStages];
     __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -506,6 +505,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
         if (threadIdx.x == 96) abort_flag = 0;
     }
     fence_barrier_init();
+    if (!C::kJoins) griddep_launch_dependents();  // the join may take its place; it waits for this grid's end
     AttnRange w;
     if (warp == kWarps) w = attn_range(p, RT, status);
     __syncthreads();
@@ -526,8 +526,9 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
         // ---- the segments, ahead of the copies (a segment's set-up takes some microseconds: divisions, the page
         // table's latency, code that left the instruction cache)
         AttnSegment g = {};
-        int at = w.first, it = 0, sg = 0, splits = 0;
+        int at = w.first, it = 0, sg = 0;
         bool ok = true, more = true;
+        int4 start[2] = {};  // the last segment's group, if it starts here and others go on with it
         for (; ok && more; ++sg) {
             more = attn_next(p, RT, &w, &at, &g);
             if (!more) g.n = g.T = 0;
@@ -538,12 +539,10 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
             if (lane < rows) bits = p.a.mask ? __ldg(p.a.mask + g.t0 + node) : ~0ull >> (63 - node);
             if (sg >= kSegs) ok = wait_all(&seg_empty[ss], uint32_t(sg / kSegs - 1) & 1u);
             if (!ok) break;
-            const int split = more && g.n_ctas > 1 ? splits++ : -1;
+            if (more && g.n_ctas > 1 && g.cta0 == int(blockIdx.x)) attn_shared(g, start);
             if (lane == 0) {
                 seg_s[ss].g = g;
                 seg_s[ss].it0 = it;
-                seg_s[ss].split = more ? split : splits;
-                if (split >= 0) split_s[split] = g;
             }
             pages_s[ss][lane] = page;
             __syncwarp();
@@ -562,6 +561,8 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
             if (lane == 0) mbar_arrive(&seg_full[ss]);
             it += g.n;
         }
+        // every CTA says so in every call, one that gave up too: the join finds nothing of another call
+        if (!C::kJoins && lane < 2) p.shared[2 * blockIdx.x + lane] = lane == 0 ? start[0] : start[1];
         // copies still in flight land before the CTA can exit
         for (int j = sg > kSegs ? sg - kSegs : 0; j < sg; ++j)
             (void)mbar_wait_bounded(&seg_full[j % kSegs], uint32_t(j / kSegs) & 1u, p.limit_ns);
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
         for (int sg = 0;; ++sg) {
             const int ss = sg % kSegs, os = sg & 1;
             bool ok = wait_all(&seg_full[ss], uint32_t(sg / kSegs) & 1u);
-            if (!ok || seg_s[ss].g.n == 0) break;
+            if (!ok || seg_s[ss].g.n == 0) break;  // (behind the last segment: no pages)
             ok = wait_all(&out_full[os], uint32_t(sg / 2) & 1u);
             if (!ok) break;
             const AttnSegment& g = seg_s[ss].g;
@@ -681,17 +682,17 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&out_free[os]);
-                if (split) {
+                if (!split && bad) atomicOr(status, MQ_DEV_KV_RANGE);
+                if (C::kJoins && split) {
+                    split_s[splits] = g;
                     last_s[splits] = attn_arrive(p, g);
                     mbar_arrive(&part_done[splits]);
-                } else if (bad) {
-                    atomicOr(status, MQ_DEV_KV_RANGE);
                 }
                 mbar_arrive(&seg_empty[ss]);
             }
             splits += split;
         }
-        if (abort_flag && lane == 0) {  // the teams wait for none that does not come
+        if (C::kJoins && lane == 0) {  // the teams wait for two
             for (; splits < 2; ++splits) {
                 last_s[splits] = 0;
                 mbar_arrive(&part_done[splits]);
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
         return ok;
     };
     bool good = true;  // the whole team's
-    int it = team, s = team, splits = 0, flip = 0;
+    int it = team, s = team, flip = 0;
     uint32_t phase = 0;
     for (int sg = 0;; ++sg) {
         const int ss = sg % kSegs, os = sg & 1;
@@ -727,10 +728,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
         if (!good) break;
         const AttnSegment& g = seg_s[ss].g;  // stays until this warp's arrival at seg_empty
         const int ctx = g.ctx, len = ctx + g.T, end = seg_s[ss].it0 + g.n, first_key = (g.page0 - seg_s[ss].it0) * kKvPage;
-        if (g.n == 0) {
-            splits = seg_s[ss].split;
-            break;
-        }
+        if (g.n == 0) break;
         const bool had = it < end;
         bool bad = false;
         if (had) {
@@ -798,14 +796,18 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
     }
 
     // ---- the shared groups whose last CTA this is: their segments joined in CTA order
-    for (int k = 0; good && k < splits; ++k) good = wait_all(&part_done[k], 0);
+    if (!C::kJoins) return;
+    constexpr int kCons = 32 * kWarps;
+    for (int k = 0; good && k < 2; ++k) good = wait_all(&part_done[k], 0);
     if (barrier_any(1, kCons, !good)) return;  // a wait that ran out anywhere ends all
-    for (int k = 0; k < splits; ++k) {
+    for (int k = 0; k < 2; ++k) {
         if (!last_s[k]) continue;
         const AttnSegment& g = split_s[k];
         const int rows = min(RT, g.T * p.group - g.row0);
         // every copy has landed and been read: the ring is free
-        float* const sums = reinterpret_cast<float*>(ring);  // [kWarps][RT][D]
+        float* const sums = reinterpret_cast<float*>(ring);  // [kWarps][RT][D], then maxima and sums [kWarps][RT]
+        float* const cm = sums + kWarps * RT * D;
+        float* const cl = cm + kWarps * RT;
         // warp w joins the parts of CTAs w, w + kWarps, ...: lane r has row r's maximum and sum, and a
         // lane four values of each 128 of the rows
         constexpr int NV = RT * D / 128;
@@ -843,32 +845,109 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
 #pragma unroll
         for (int v = 0; v < NV; ++v)
             *reinterpret_cast<float4*>(sums + warp * RT * D + v * 128 + lane * 4) = acc[v];
-        if (lane < RT) cm_s[warp][lane] = mr, cl_s[warp][lane] = lr;
+        if (lane < RT) cm[warp * RT + lane] = mr, cl[warp * RT + lane] = lr;
         if (barrier_any(1, kCons, gone)) {  // a page outside the cache: the group stays unwritten
             if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
             continue;
         }
+        // a warp per 128 values, four of a lane
         const int nw = min(kWarps, g.n_ctas);
-#pragma unroll 1
-        for (int x = warp; x < rows * (D / 32); x += kWarps) {
-            const int r = x / (D / 32), d = (x % (D / 32)) * 32 + lane;
-            // lane w: warp w's maximum and weight
-            const float mw = lane < nw ? cm_s[lane][r] : kLowest;
-            float mm = mw;
-#pragma unroll
-            for (int o = 8; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-            const float fw = ex2(mw - mm);
-            float sum = lane < nw ? cl_s[lane][r] * fw : 0.0f;
-#pragma unroll
-            for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            sum = __shfl_sync(0xffffffffu, sum, 0);
-            float v = 0.0f;
+        for (int x = warp * 128 + lane * 4; x - lane * 4 < rows * D; x += kWarps * 128) {
+            const int r = x / D;
+            float top = kLowest, sum = 0.0f;
 #pragma unroll 8
-            for (int u = 0; u < nw; ++u) v = fmaf(sums[(u * RT + r) * D + d], __shfl_sync(0xffffffffu, fw, u), v);
-            attn_emit(p, g, g.row0 + r, D, d - lane, sum == 0.0f ? 0.0f : v / sum);
+            for (int u = 0; u < nw; ++u) top = fmaxf(top, cm[u * RT + r]);
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int u = 0; u < nw; ++u) {
+                const float f = ex2(cm[u * RT + r] - top);
+                const float4 y = *reinterpret_cast<const float4*>(sums + u * RT * D + x);
+                sum = fmaf(cl[u * RT + r], f, sum);
+                v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+            attn_emit4(p, g, g.row0 + r, r < rows, D, x % D, v);
         }
         named_barrier_sync(1, kCons);
     }
+}
+
+// ---- the groups that several CTAs share: their parts joined in CTA order -------------------------
+// A CTA per first CTA of a group.  A thread has four values of a row, of every kSplit-th of kJoinAhead parts; a
+// group has some parts of 4 KB (16 at 1000 tokens, 38 at 16000 and more, with four key/value heads), which lie in
+// L2, so what it costs is latency: all of a round's loads are on their way together, and before the maxima.
+constexpr int kJoinAhead = 4;
+
+template <int D, int NT>
+struct RowsJoin {
+    static constexpr int kRows = 8 * NT, kPart = kRows * D / 4;  // threads of a part
+    static constexpr int kSplit = 1024 / kPart, kThreads = kPart * kSplit;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(RowsJoin<D, NT>::kThreads) attn_rows_join_kernel(const AttnParams p, unsigned* status)
+{
+    using J = RowsJoin<D, NT>;
+    constexpr int RT = J::kRows;
+    constexpr int64_t kSlot = attn_slot_floats(RT, D);
+    extern __shared__ float part_s[];  // [parts][RT] maxima, then sums
+    __shared__ float4 sum_s[J::kSplit][J::kPart];
+    const int cta0 = blockIdx.x, x = threadIdx.x % J::kPart, part = threadIdx.x / J::kPart;
+    const int row = x / (D / 4), d = x % (D / 4) * 4;
+    griddep_wait();
+    const int4 s0 = __ldcg(p.shared + 2 * cta0), s1 = __ldcg(p.shared + 2 * cta0 + 1);
+    const int n = s1.x;
+    if (n < 2) return;
+    AttnSegment g;
+    g.t0 = s0.x, g.T = s0.y, g.head = s0.z, g.row0 = s0.w;
+    const bool there = row < min(RT, g.T * p.group - g.row0);
+    auto slot_of = [&](int c) { return p.parts + (int64_t(cta0 + c) * 2 + (c == 0 ? s1.y : 0)) * kSlot; };
+    float4 v[kJoinAhead];
+    auto load = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i)
+            v[i] = c0 + i < n && there ? __ldcg(reinterpret_cast<const float4*>(slot_of(c0 + i) + 2 * RT) + x)
+                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    load(part * kJoinAhead);
+    for (int i = threadIdx.x; i < 2 * RT * n; i += J::kThreads) {
+        const int c = i / (2 * RT), k = i % (2 * RT);  // rows past the block's hold what was there, and stay theirs
+        part_s[k < RT ? c * RT + k : n * RT + c * RT + k - RT] = __ldcg(slot_of(c) + k);
+    }
+    __syncthreads();
+    float mm = kLowest, l = 0.0f;
+    bool gone = false;
+    for (int c = 0; c < n; ++c) mm = fmaxf(mm, part_s[c * RT + row]);
+    for (int c = 0; c < n; ++c) {
+        const float lc = part_s[(n + c) * RT + row];
+        gone |= there && lc < 0.0f;
+        l = fmaf(lc, ex2(part_s[c * RT + row] - mm), l);
+    }
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c0 = part * kJoinAhead; c0 < n;) {
+#pragma unroll
+        for (int i = 0; i < kJoinAhead; ++i) {
+            if (c0 + i >= n) break;
+            const float f = ex2(part_s[(c0 + i) * RT + row] - mm);
+            o.x = fmaf(v[i].x, f, o.x), o.y = fmaf(v[i].y, f, o.y), o.z = fmaf(v[i].z, f, o.z), o.w = fmaf(v[i].w, f, o.w);
+        }
+        c0 += J::kSplit * kJoinAhead;
+        if (c0 < n) load(c0);
+    }
+    sum_s[part][x] = o;
+    if (__syncthreads_or(gone)) {  // a page outside the cache: the group stays unwritten
+        if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+        return;
+    }
+    if (part > 0) return;
+    for (int i = 1; i < min(J::kSplit, (n + kJoinAhead - 1) / kJoinAhead); ++i) {
+        const float4 y = sum_s[i][x];
+        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    attn_emit4(p, g, g.row0 + row, there, D, d, o);
 }
 
 template <int D, bool Q8, int NT>
@@ -876,7 +955,13 @@ cudaError_t launch_rows(const AttnParams& p, int grid, unsigned* status, cudaStr
 {
     using C = RowsCfg<D, Q8, NT>;
     attn_rows_kernel<D, Q8, NT><<<grid, C::kThreads, C::kSmem, s>>>(p, status);
-    return cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if constexpr (!C::kJoins) {
+        if (e == cudaSuccess && grid > 1)  // one CTA shares no group
+            e = attn_launch_join(attn_rows_join_kernel<D, NT>, dim3(grid), RowsJoin<D, NT>::kThreads,
+                                 size_t(grid) * 2 * C::kRows * sizeof(float), p, status, s);
+    }
+    return e;
 }
 
 template <int NT>
@@ -891,12 +976,10 @@ cudaError_t launch_rows_nt(const mq_kv_cache& c, const AttnParams& p, int grid, 
 
 }  // namespace
 
-// counters of the most groups any call with these heads has, then the partial results
-static size_t counters_bytes(const mq_kv_cache& c, int n_heads)
+// Workspace: what the join kernels read of the CTAs, counters of the groups (of one row block each: 8 rows), parts.
+static size_t counters_bytes(const mq_kv_cache& c)
 {
-    const int rows = n_heads / c.n_kv_heads * MQ_TREE_MAX_TOKENS;
-    const size_t groups = size_t(c.n_seqs) * c.n_kv_heads * ((rows + 7) / 8);
-    return (groups * 4 + 127) / 128 * 128;
+    return (size_t(c.n_seqs) * c.n_kv_heads * sizeof(unsigned) + 127) / 128 * 128;
 }
 
 // the most query rows of a key/value head that the warp kernels take
@@ -905,8 +988,7 @@ constexpr int kWarpRows = 16;
 size_t attn_workspace_bytes(const mq_kv_cache& c, int n_heads, int max_tokens, int num_sms)
 {
     const int RT = n_heads / c.n_kv_heads * max_tokens > kWarpRows ? attn_tc_rows() : kWarpRows;
-    return counters_bytes(c, n_heads) + size_t(num_sms) * 2 * attn_slot_floats(RT, c.head_dim) * 4 +
-           size_t(num_sms) * kAttnSharedBytes;
+    return size_t(num_sms) * (kAttnSharedBytes + 2 * attn_slot_floats(RT, c.head_dim) * sizeof(float)) + counters_bytes(c);
 }
 
 cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* ws, int num_sms, unsigned* status,
@@ -918,19 +1000,16 @@ cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* w
     p.group = a.n_heads / cache.n_kv_heads;
     p.group_inv = uint32_t((0x100000000ull + p.group - 1) / p.group);
     p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
-    p.counters = static_cast<unsigned*>(ws);
-    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + counters_bytes(cache, a.n_heads));
-    p.shared = nullptr;  // of the kernel that has one: behind the parts
+    p.shared = static_cast<int4*>(ws);
+    p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + size_t(num_sms) * kAttnSharedBytes);
+    p.parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.counters) + counters_bytes(cache));
     p.limit_ns = uint64_t(fault_policy() == FAULT_NONE ? 2000 : 50) * 1000000ull;
     const int rows = p.group * a.max_tokens, RT = rows <= 8 ? 8 : rows <= kWarpRows ? 16 : attn_tc_rows();
     // no more CTAs than the bounds allow units
     const int64_t most = int64_t(cache.n_seqs) * ((int64_t(a.max_len) + kKvPage - 1) / kKvPage) * cache.n_kv_heads *
                          ((rows + RT - 1) / RT);
     const int grid = int(most < 1 ? 1 : most < num_sms ? most : num_sms);
-    if (RT > kWarpRows) {
-        p.shared = reinterpret_cast<int4*>(p.parts + int64_t(num_sms) * 2 * attn_slot_floats(RT, cache.head_dim));
-        return launch_attn_tc(cache, p, grid, status, s);
-    }
+    if (RT > kWarpRows) return launch_attn_tc(cache, p, grid, status, s);
     return RT == 8 ? launch_rows_nt<1>(cache, p, grid, status, s) : launch_rows_nt<2>(cache, p, grid, status, s);
 }
 

@@ -371,10 +371,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         for (; ok && more; ++sg) {
             more = attn_next(p, kTcRows, &w, &at, &g);
             if (!more) g.n = g.T = 0;
-            if (more && g.n_ctas > 1 && g.cta0 == int(blockIdx.x)) {
-                start[0] = make_int4(g.t0, g.T, g.head, g.row0);
-                start[1] = make_int4(g.n_ctas, g.slot0, 0, 0);
-            }
+            if (more && g.n_ctas > 1 && g.cta0 == int(blockIdx.x)) attn_shared(g, start);
             const int ss = sg % kTcSegs;
             if (sg >= kTcSegs) ok = wait_all(&seg_empty[ss], uint32_t(sg / kTcSegs - 1) & 1u);
             if (!ok) break;
@@ -884,18 +881,9 @@ cudaError_t launch_tc(const AttnParams& p, int grid, unsigned* status, cudaStrea
     attn_tc_kernel<D, Q8><<<grid, kTcThreads, TcCfg<D, Q8>::kSmem, s>>>(p, status);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1) return e;  // one CTA shares no group
-    cudaLaunchConfig_t cfg = {};
     const int rows = p.group * p.a.max_tokens;
-    cfg.gridDim = dim3(grid, ((rows < kTcRows ? rows : kTcRows) + 31) / 32);
-    cfg.blockDim = dim3(4 * D);
-    cfg.dynamicSmemBytes = size_t(grid) * 2 * 32 * sizeof(float);  // 39 KB for 152 SMs
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_tc_join_kernel<D>, p, status);
+    return attn_launch_join(attn_tc_join_kernel<D>, dim3(grid, ((rows < kTcRows ? rows : kTcRows) + 31) / 32), 4 * D,
+                            size_t(grid) * 2 * 32 * sizeof(float), p, status, s);  // 39 KB for 152 SMs
 }
 
 }  // namespace
