@@ -60,14 +60,20 @@ struct RowsCfg {
     // registers allow 16 warps of 8 rows or 12 of 16; the ring of 32 KB blocks is too short for four teams
     static constexpr int kTeams = D == 128 && (NT == 2 || !Q8) ? 3 : 4;
     static constexpr int kWarps = kTeams * kTeam;
-    static constexpr int kThreads = 32 * (kWarps + 3);  // and the warps that plan, copy and join
+    // Warps that copy pages, in turn: a page takes one 500 to 700 cycles whatever its size is, which is more than the
+    // teams take for one of 9 or 17 KB, and less than one of 32 KB takes to come.
+    static constexpr int kCopiers = B::kBytes < 32768 ? 2 : 1;
+    static constexpr int kThreads = 32 * (kWarps + 2 + kCopiers);  // and the warps that plan, join and copy
     static constexpr int kSlice = D / kTeam;                     // head values that a warp sums
     static constexpr int kQ = kRows * D * 2;                     // a segment's query rows
     static constexpr int kP = NT * kTeam * 32 * 8;               // a page's probabilities
     static constexpr int kOut = kRows * D * 4;                   // a team's outputs
     static constexpr int kFixed = kSegs * kQ + kTeams * 2 * kP + 2 * kTeams * kOut;
     static constexpr int kFit = (kRowsSmem - kFixed) / B::kBytes;
-    static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+    // A place belongs to one copier, so their number is even: teams of odd pages do not wait for those of even ones,
+    // so the odd pages' copier can be a whole round of the ring ahead, where a wait by parity would not see that the
+    // other's page has not even been there.
+    static constexpr int kStages = (kFit < kMaxStages ? kFit : kMaxStages) / kCopiers * kCopiers;
     static constexpr int kSmem = kStages * B::kBytes + kFixed;
     static_assert(kStages > kTeams, "the teams' pages and one on its way");
 };
@@ -466,7 +472,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
 {
     using B = KvBlock<D, Q8>;
     using C = RowsCfg<D, Q8, NT>;
-    constexpr int RT = C::kRows, kTeams = C::kTeams, kWarps = C::kWarps, kStages = C::kStages;
+    constexpr int RT = C::kRows, kCopiers = C::kCopiers, kTeams = C::kTeams, kWarps = C::kWarps, kStages = C::kStages;
     extern __shared__ __align__(128) uint8_t sm[];
     uint8_t* const ring = sm;
     __half* const q_s = reinterpret_cast<__half*>(sm + kStages * B::kBytes);
@@ -494,7 +500,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
     } else if (threadIdx.x >= 32 && threadIdx.x < 32 + kSegs) {
         mbar_init(&seg_planned[threadIdx.x - 32], 1);
         mbar_init(&seg_full[threadIdx.x - 32], 1);
-        mbar_init(&seg_empty[threadIdx.x - 32], kWarps + 2);
+        mbar_init(&seg_empty[threadIdx.x - 32], kWarps + 1 + kCopiers);
     } else if (threadIdx.x >= 64 && threadIdx.x < 66) {
         const int k = threadIdx.x - 64;
         mbar_init(&out_full[k], kWarps);
@@ -569,9 +575,9 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
         return;
     }
 
-    if (warp == kWarps + 2) {
+    if (warp >= kWarps + 2) {
         // ---- the pages' copies, by lane 0; the warp reads their numbers 32 at a time
-        int it = 0, s = 0;
+        int it = warp - (kWarps + 2), s = it, total = -1;
         uint32_t phase = 0;
         bool ok = true;
         for (int sg = 0; ok; ++sg) {
@@ -579,38 +585,43 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
             ok = wait_all(&seg_planned[ss], uint32_t(sg / kSegs) & 1u);
             if (!ok) break;
             const AttnSegment& g = seg_s[ss].g;
-            const int n = g.n;
-            if (n == 0) break;
-            const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0;
+            const int n = g.n, it0 = seg_s[ss].it0;
+            if (n == 0) {
+                total = it0;
+                break;
+            }
+            const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0 + lane;
             const uint8_t* const src = p.c.pages + int64_t(g.head) * B::kBytes;
-            int32_t page_l = pages_s[ss][lane];
-            for (int i0 = 0; ok && i0 < n; i0 += 32) {
-                const int32_t page_now = page_l;
-                if (i0 + 32 + lane < n) page_l = __ldg(table + i0 + 32 + lane);
-                const int m = min(32, n - i0);
-                for (int i = 0; i < m; ++i, ++it) {
-                    const int32_t page = __shfl_sync(0xffffffffu, page_now, i);
-                    if (it >= kStages) ok = wait_all(&empty[s], phase ^ 1u);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        const bool bad = page < 0 || page >= p.c.n_pages;  // table entries are not trusted
-                        bad_s[s] = bad;
-                        if (bad) {
-                            mbar_arrive(&full[s]);
-                        } else {
-                            mbar_arrive_expect_tx(&full[s], B::kBytes);
-                            bulk_copy_g2s(ring + s * B::kBytes, src + int64_t(page) * p.c.n_kv_heads * B::kBytes, B::kBytes,
-                                          &full[s]);
-                        }
-                    }
-                    if (++s == kStages) s = 0, phase ^= 1u;
+            int at = 0;  // the pages at .. at + 31 are in the lanes
+            int32_t page_l = pages_s[ss][lane], next_l = 32 + lane < n ? __ldg(table + 32) : 0;
+            for (; it < it0 + n; it += kCopiers) {
+                if (it - it0 >= at + 32) {
+                    at += 32;
+                    page_l = next_l;
+                    if (at + 32 + lane < n) next_l = __ldg(table + at + 32);
                 }
+                const int32_t page = __shfl_sync(0xffffffffu, page_l, it - it0 - at);
+                if (it >= kStages) ok = wait_all(&empty[s], phase ^ 1u);
+                if (!ok) break;
+                if (lane == 0) {
+                    const bool bad = page < 0 || page >= p.c.n_pages;  // table entries are not trusted
+                    bad_s[s] = bad;
+                    if (bad) {
+                        mbar_arrive(&full[s]);
+                    } else {
+                        mbar_arrive_expect_tx(&full[s], B::kBytes);
+                        bulk_copy_g2s(ring + s * B::kBytes, src + int64_t(page) * p.c.n_kv_heads * B::kBytes, B::kBytes,
+                                      &full[s]);
+                    }
+                }
+                s += kCopiers;
+                if (s >= kStages) s -= kStages, phase ^= 1u;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&seg_empty[ss]);
         }
-        // copies still in flight land before the CTA can exit
-        for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
+        // its copies still in flight land before the CTA can exit (older ones' places have been used again)
+        for (int j = it - kCopiers; j >= 0 && j >= (total < 0 ? it + 1 : total) - kStages; j -= kCopiers)
             (void)mbar_wait_bounded(&full[j % kStages], uint32_t(j / kStages) & 1u, p.limit_ns);
         return;
     }
