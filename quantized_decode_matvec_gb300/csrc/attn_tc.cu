@@ -11,7 +11,7 @@
 //                   the context made finite
 //   warp 12         segments, and bulk copies in the order of use: q8_0 into a
 //                   ring of half blocks, f16 into the operands themselves
-//   warp 13         tensor memory; one lane issues the MMAs
+//   warp 13         tensor memory and the MMAs
 // Tensor memory holds for each tile the scores of a step (128 columns), in
 // their place the probabilities (f16, the A operand of the second product),
 // and the fp32 outputs:
@@ -117,6 +117,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 __device__ __forceinline__ void tmem_st_wait()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// true in one lane of the warp, always the same one
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], one MMA of M x N x 16 (issued by one thread)
@@ -486,76 +494,82 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             if (lane == 0) mbar_arrive(&seg_empty[ss]);
         }
     } else if (warp == kWarpMma) {
-        // ---- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = umma_idesc_f16_f32(128, kStep);
-            constexpr uint32_t idesc_o = umma_idesc_f16_f32(128, D) | kBMajorMn;
-            // tile 0 of the queries, operand 0 as K and as V; an address within or in another is added to the
-            // descriptor's address field
-            const uint64_t q_d = umma_desc_sw128(smem_u32(q_s)), k_d = umma_desc_sw128(smem_u32(op_s)),
-                           v_d = umma_desc_mn(smem_u32(op_s), C::kPlane);
-            auto wait_one = [&](uint64_t* bar, uint32_t parity) {
-                if (!abort_flag && mbar_wait_bounded(bar, parity, p.limit_ns)) return true;
-                abort_flag = 1;
-                return false;
-            };
-            int it = 0;  // tiles before this segment
-            uint32_t pph[2] = {0, 0}, qph = 0;  // phases of p_ready and q_ready
-            bool ok = true;
-            for (int sg = 0; ok; ++sg) {
-                const int ss = sg % kTcSegs;
-                ok = wait_one(&seg_full[ss], uint32_t(sg / kTcSegs) & 1u);
-                if (!ok) break;
-                const int n = (seg_s[ss].g.n + 1) / 2;  // steps
-                if (n == 0) break;
-                const bool halves = seg_s[ss].g.T * p.group - seg_s[ss].g.row0 > 128;
-                const int items = halves ? 2 * n : n;
-                mbar_arrive(&seg_empty[ss]);
-                ok = wait_one(&q_ready[0], qph) && wait_one(&q_ready[1], qph);
-                qph ^= 1u;
-                auto scores = [&](int j) {
-                    const int st = halves ? j >> 1 : j, t = j & 1, k = it + tc_pos_k(st, halves), b = k % kOps;
-                    if ((!halves || t == 0) && !wait_one(&op_ready[b], uint32_t(k / kOps) & 1u)) return false;
-                    tc_fence_after();
-                    const uint64_t ad = q_d + (halves && t ? C::kTile >> 4 : 0), bd = k_d + uint64_t(b * (C::kTile >> 4));
-                    umma_f16(tmem + kColS + 128 * t, ad, bd, idesc_s, false);
+        // ---- MMA issuer.  The whole warp goes through the loops with values that the compiler knows to be the same
+        // in all lanes, and one lane issues: with the loops in one lane's branch every operand went through a vector
+        // register, and an MMA of 66 cycles took 92 to issue.
+        constexpr uint32_t idesc_s = umma_idesc_f16_f32(128, kStep);
+        constexpr uint32_t idesc_o = umma_idesc_f16_f32(128, D) | kBMajorMn;
+        const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+        // tile 0 of the queries, operand 0 as K and as V; an address within or in another is added to the
+        // descriptor's address field
+        const uint64_t q_d = umma_desc_sw128(smem_u32(q_s)), k_d = umma_desc_sw128(smem_u32(op_s)),
+                       v_d = umma_desc_mn(smem_u32(op_s), C::kPlane);
+        int it = 0;  // tiles before this segment
+        uint32_t pph[2] = {0, 0}, qph = 0;  // phases of p_ready and q_ready
+        bool ok = true;
+        for (int sg = 0; ok; ++sg) {
+            const int ss = sg % kTcSegs;
+            ok = wait_all(&seg_full[ss], uint32_t(sg / kTcSegs) & 1u);
+            if (!ok) break;
+            const int n = __reduce_max_sync(0xffffffffu, (seg_s[ss].g.n + 1) / 2);  // steps
+            if (n == 0) break;
+            const bool halves = __reduce_max_sync(0xffffffffu, seg_s[ss].g.T * p.group - seg_s[ss].g.row0) > 128;
+            const int items = halves ? 2 * n : n;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&seg_empty[ss]);
+            ok = wait_all(&q_ready[0], qph) && wait_all(&q_ready[1], qph);
+            qph ^= 1u;
+            auto scores = [&](int j) {
+                const int st = halves ? j >> 1 : j, t = j & 1, k = it + tc_pos_k(st, halves), b = k % kOps;
+                if ((!halves || t == 0) && !wait_all(&op_ready[b], uint32_t(k / kOps) & 1u)) return false;
+                tc_fence_after();
+                const uint64_t ad = q_d + (halves && t ? C::kTile >> 4 : 0), bd = k_d + uint64_t(b * (C::kTile >> 4));
+                if (elect_one()) {
+                    umma_f16(tm + kColS + 128 * t, ad, bd, idesc_s, false);
 #pragma unroll
                     for (int x = 1; x < D / 16; ++x) {
                         const uint32_t off = ((x >> 2) * C::kPlane + 32 * (x & 3)) >> 4;
-                        umma_f16(tmem + kColS + 128 * t, ad + off, bd + off, idesc_s, true);
+                        umma_f16(tm + kColS + 128 * t, ad + off, bd + off, idesc_s, true);
                     }
                     umma_commit(&s_ready[t]);
                     if (!halves || t == 1) umma_commit(&op_free[b]);  // the tile's last use
-                    return true;
-                };
-                for (int j = 0; ok && j < min(2, items); ++j) ok = scores(j);
-                for (int j = 0; ok && j < items; ++j) {
-                    const int st = halves ? j >> 1 : j, t = j & 1, k = it + tc_pos_v(st, n, halves), b = k % kOps;
-                    const uint64_t bd = v_d + uint64_t(b * (C::kTile >> 4));
-                    if (!halves || t == 0) ok = wait_one(&op_ready[b], uint32_t(k / kOps) & 1u);
+                }
+                __syncwarp();
+                return true;
+            };
+            for (int j = 0; ok && j < min(2, items); ++j) ok = scores(j);
+            for (int j = 0; ok && j < items; ++j) {
+                const int st = halves ? j >> 1 : j, t = j & 1, k = it + tc_pos_v(st, n, halves), b = k % kOps;
+                const uint64_t bd = v_d + uint64_t(b * (C::kTile >> 4));
+                if (!halves || t == 0) ok = wait_all(&op_ready[b], uint32_t(k / kOps) & 1u);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && wait_one(&p_ready[t][h], pph[t]);
-                        if (!ok) break;
-                        tc_fence_after();
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && wait_all(&p_ready[t][h], t ? pph[1] : pph[0]);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
                         for (int x = 4 * h; x < 4 * h + 4; ++x)
-                            umma_f16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * x, bd + ((2048 * x) >> 4),
+                            umma_f16_ts(tm + kColO + 128 * t, tm + kColS + 128 * t + 8 * x, bd + ((2048 * x) >> 4),
                                         idesc_o, x > 0 || j > 1);
+                        if (h == 1) {
+                            if (!halves || t == 1) umma_commit(&op_free[b]);
+                            if (j + 2 >= items) umma_commit(&o_done[t]);
+                        }
                     }
-                    if (!ok) break;
-                    pph[t] ^= 1u;
-                    if (!halves || t == 1) umma_commit(&op_free[b]);
-                    if (j + 2 < items)
-                        ok = scores(j + 2);
-                    else
-                        umma_commit(&o_done[t]);
+                    __syncwarp();
                 }
-                it += 2 * n;
+                if (!ok) break;
+                if (t)
+                    pph[1] ^= 1u;
+                else
+                    pph[0] ^= 1u;
+                if (j + 2 < items) ok = scores(j + 2);
             }
-            // what was issued completes before tensor memory is freed
-            if (it > 0) (void)mbar_wait_bounded(&op_free[(it - 1) % kOps], uint32_t((it - 1) / kOps) & 1u, p.limit_ns);
+            it += 2 * n;
         }
+        // what was issued completes before tensor memory is freed
+        if (it > 0) (void)mbar_wait_bounded(&op_free[(it - 1) % kOps], uint32_t((it - 1) / kOps) & 1u, p.limit_ns);
     } else {
         // ---- softmax: tile t, thread = row = tensor memory lane
         const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;
