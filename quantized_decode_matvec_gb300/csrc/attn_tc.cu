@@ -29,6 +29,13 @@
 // raised (and O rescaled in tensor memory) only when a score passes it by more
 // than 8, so they stay below 2^15; a key at 2^-21 of the largest is still a
 // normal number.  Scores, maxima, sums and outputs are fp32.
+//
+// Measured (28 query heads on 4 of 128, q8_0): four trees of 64 nodes over 8190
+// to 32700 tokens 78 us, 715 TFLOP/s, 0.37 of the dense f16 rate.  The tensor
+// pipe is busy 40 % of the time: a step's probabilities stand between its two
+// products, and of the time per tile and step (about 2000 cycles; the MMAs take
+// 1056) the rest is waiting for them, for operands, and the commits.  Start, the
+// segments' ends and the join take about 15 us of a call.
 #include "mq_attn.cuh"
 #include "mq_umma.cuh"
 
