@@ -37,9 +37,9 @@
 //
 // Measured (28 query heads on 4 of 128, one token per sequence): 131071 tokens
 // in f16 49.5 us, 5.4 TB/s, and 64 sequences of 128 to 8191 in f16 87 us,
-// 6.2 TB/s: the cache's bytes.  The same 64 in q8_0 70 us, 4.1 TB/s: the
-// conversion's instructions (about 300 of a warp's 500 a page; an SM issues
-// 2.9 a cycle while pages are there, and three teams are as fast as four).
+// 6.2 TB/s: the cache's bytes.  The same 64 in q8_0 59 us, 4.9 TB/s: start
+// and end of the call (about 10 us) and the conversion's instructions (about
+// 300 of a warp's 500 a page; three teams are as fast as four).
 // 1000 tokens 9.9 us: latencies, of which the launch and the split take about
 // 4, a page's copy 1, a page's products 1, and the two joins 4.
 #include "mq_attn.cuh"

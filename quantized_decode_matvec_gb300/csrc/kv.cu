@@ -21,9 +21,9 @@ namespace mq {
 // forms the token's cosines and sines once.  Statistics, products and rotation
 // are fp32; each output is rounded once, to f16 or to its q8_0 code.
 //
-// Measured (28 + 4 + 4 heads of 128, q8_0): one token 5.3 us, which is launch
-// and one chain of loads, angles, norm and stores; 2048 tokens 19.7 us,
-// 3.1 TB/s: between instructions (the angles' sines, the q8_0 codes) and one
+// Measured (28 + 4 + 4 heads of 128, q8_0): one token 3.8 us, which is launch
+// and one chain of loads, angles, norm and stores; 2048 tokens 16.1 us,
+// 3.4 TB/s: between instructions (the angles' sines, the q8_0 codes) and one
 // wave's latency.
 //
 // The angle: pos * f / 2pi modulo one turn, with f = m 2^(e-23) (m the 24-bit
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const ReadArgs p, unsigned
 // ---- accept -------------------------------------------------------------------------------
 // One CTA per (sequence, head): every row of the path is read into registers
 // before any is written, so the path may overlap its destination in any way.
-// Bound by latency: one sequence 4.3 us, 64 of them 5.3 us (11 nodes, f16).
+// Bound by latency: one sequence 2.7 us, 64 of them 3.2 us (11 nodes, f16).
 template <int D, bool Q8>
 __global__ void __launch_bounds__(256)
     kv_accept_kernel(const KvView c, const int32_t* __restrict__ ctx_len, const int32_t* __restrict__ path,
@@ -409,7 +409,7 @@ cudaError_t launch_kv_append(const mq_kv_cache& cache, const mq_kv_append_args& 
     p.a = a;
     p.c = kv_view(cache);
     // a pair of heads per warp while that leaves the chip room (few tokens: latency), then longer runs, which
-    // form a token's cosines and sines fewer times: 2048 tokens of 36 heads take 33, 26, 24, 20 and 25 us in
+    // form a token's cosines and sines fewer times: 2048 tokens of 36 heads take 30, 22, 20, 16 and 21 us in
     // runs of one, two, four, nine and 18 pairs
     const int pairs = (a.n_heads + 1) / 2 + 2 * ((cache.n_kv_heads + 1) / 2);
     const int64_t per = int64_t(a.n_tokens) * pairs / (int64_t(num_sms) * 16);

@@ -29,7 +29,7 @@
 namespace mq {
 
 // In pages.  One query token per sequence, q8_0, D 128, at a cost of 2, 4, 6, 8, 10 and 14: 64 sequences of 128 to 8191
-// tokens, 4 key/value heads: 77, 76, 72, 70, 70 and 70 us; 256 of 100 to 1000, 8 heads: 83, 81, 82, 84, 84 and 87; 16
+// tokens, 4 key/value heads: 67, 66, 61, 60, 59 and 59 us; 256 of 100 to 1000, 8 heads: 83, 81, 82, 84, 84 and 87; 16
 // trees of 16 nodes over 128 to 8000 tokens, 8 heads: 90, 76, 61, 60, 62 and 65.  The entry check's bound on the units
 // counts on at most 11.
 constexpr int kAttnGroupCost = 8;
