@@ -32,7 +32,7 @@
 //
 // Measured (28 query heads on 4 of 128, q8_0): four trees of 64 nodes over 8190
 // to 32700 tokens 78 us, 715 TFLOP/s, 0.37 of the dense f16 rate.  The tensor
-// pipe is busy 40 % of the time: a step's probabilities stand between its two
+// pipe is busy 37 % of the time: a step's probabilities stand between its two
 // products, and of the time per tile and step (about 2000 cycles; the MMAs take
 // 1056) the rest is waiting for them, for operands, and the commits.  Start, the
 // segments' ends and the join take about 15 us of a call.
