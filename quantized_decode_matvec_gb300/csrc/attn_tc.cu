@@ -31,9 +31,9 @@
 // normal number.  Scores, maxima, sums and outputs are fp32.
 //
 // Measured (28 query heads on 4 of 128, q8_0): four trees of 64 nodes over 8190
-// to 32700 tokens 78 us, 715 TFLOP/s, 0.37 of the dense f16 rate.  The tensor
+// to 32700 tokens 76 us, 730 TFLOP/s, 0.38 of the dense f16 rate.  The tensor
 // pipe is busy 37 % of the time: a step's probabilities stand between its two
-// products, and of the time per tile and step (about 2000 cycles; the MMAs take
+// products, and of the time per tile and step (about 1800 cycles; the MMAs take
 // 1056) the rest is waiting for them, for operands, and the commits.  Start, the
 // segments' ends and the join take about 15 us of a call.
 #include "mq_attn.cuh"
@@ -526,9 +526,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             if (lane == 0) mbar_arrive(&seg_empty[ss]);
             ok = wait_all(&q_ready[0], qph) && wait_all(&q_ready[1], qph);
             qph ^= 1u;
+            // K of item j's step is there, where item j is the first to use it, and so is what `bar` stands for: one
+            // wait, half of the lanes at each barrier (a wait takes 100 cycles when nothing is left to wait for)
+            auto wait_keys = [&](int j, uint64_t* bar, uint32_t parity) {
+                const int st = halves ? j >> 1 : j, k = it + tc_pos_k(st, halves), b = k % kOps;
+                const bool keys = j < items && (!halves || (j & 1) == 0) && (!bar || (lane & 1));
+                return (!keys && !bar) || wait_all(keys ? &op_ready[b] : bar, keys ? uint32_t(k / kOps) & 1u : parity);
+            };
             auto scores = [&](int j) {
                 const int st = halves ? j >> 1 : j, t = j & 1, k = it + tc_pos_k(st, halves), b = k % kOps;
-                if ((!halves || t == 0) && !wait_all(&op_ready[b], uint32_t(k / kOps) & 1u)) return false;
                 tc_fence_after();
                 const uint64_t ad = q_d + (halves && t ? C::kTile >> 4 : 0), bd = k_d + uint64_t(b * (C::kTile >> 4));
                 if (elect_one()) {
@@ -542,17 +548,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                     if (!halves || t == 1) umma_commit(&op_free[b]);  // the tile's last use
                 }
                 __syncwarp();
-                return true;
             };
-            for (int j = 0; ok && j < min(2, items); ++j) ok = scores(j);
+            for (int j = 0; ok && j < min(2, items); ++j) {
+                ok = wait_keys(j, nullptr, 0);
+                if (ok) scores(j);
+            }
             for (int j = 0; ok && j < items; ++j) {
                 const int st = halves ? j >> 1 : j, t = j & 1, k = it + tc_pos_v(st, n, halves), b = k % kOps;
                 const uint64_t bd = v_d + uint64_t(b * (C::kTile >> 4));
-                if (!halves || t == 0) ok = wait_all(&op_ready[b], uint32_t(k / kOps) & 1u);
+                const uint32_t pp = t ? pph[1] : pph[0];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    ok = ok && wait_all(&p_ready[t][h], t ? pph[1] : pph[0]);
+                    // before the first half the values, before the second the keys of the scores behind
+                    const bool values = (!halves || t == 0) && (lane & 1);
+                    ok = h == 0 ? wait_all(values ? &op_ready[b] : &p_ready[t][0], values ? uint32_t(k / kOps) & 1u : pp)
+                                : wait_keys(j + 2, &p_ready[t][1], pp);
                     if (!ok) break;
+                    __syncwarp();  // what one half of the lanes waited for, the issuing lane sees
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -571,7 +583,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                     pph[1] ^= 1u;
                 else
                     pph[0] ^= 1u;
-                if (j + 2 < items) ok = scores(j + 2);
+                if (j + 2 < items) scores(j + 2);
             }
             it += 2 * n;
         }
