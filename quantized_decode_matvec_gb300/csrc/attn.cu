@@ -996,10 +996,11 @@ cudaError_t launch_rows_nt(const mq_kv_cache& c, const AttnParams& p, int grid, 
 
 }  // namespace
 
-// Workspace: what the join kernels read of the CTAs, counters of the groups (of one row block each: 8 rows), parts.
-static size_t counters_bytes(const mq_kv_cache& c)
+// Workspace: what the join kernels read of the CTAs, the counters, parts.  Where each begins goes by the device alone,
+// so a call finds the counters at zero whatever cache, sequences and rows the call before had.
+static size_t parts_offset(int num_sms)
 {
-    return (size_t(c.n_seqs) * c.n_kv_heads * sizeof(unsigned) + 127) / 128 * 128;
+    return (size_t(num_sms) * (kAttnSharedBytes + sizeof(unsigned)) + 127) / 128 * 128;
 }
 
 // The most query rows of a key/value head that the warp kernels take.  16 rows, 8 key/value heads of 128, here and by
@@ -1011,7 +1012,7 @@ constexpr int kWarpRows = 16;
 size_t attn_workspace_bytes(const mq_kv_cache& c, int n_heads, int max_tokens, int num_sms)
 {
     const int RT = n_heads / c.n_kv_heads * max_tokens > kWarpRows ? attn_tc_rows() : kWarpRows;
-    return size_t(num_sms) * (kAttnSharedBytes + 2 * attn_slot_floats(RT, c.head_dim) * sizeof(float)) + counters_bytes(c);
+    return parts_offset(num_sms) + size_t(num_sms) * 2 * attn_slot_floats(RT, c.head_dim) * sizeof(float);
 }
 
 cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* ws, int num_sms, unsigned* status,
@@ -1025,7 +1026,7 @@ cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* w
     p.scale_log2 = float(double(a.scale) * 1.4426950408889634);
     p.shared = static_cast<int4*>(ws);
     p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + size_t(num_sms) * kAttnSharedBytes);
-    p.parts = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.counters) + counters_bytes(cache));
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + parts_offset(num_sms));
     p.limit_ns = uint64_t(fault_policy() == FAULT_NONE ? 2000 : 50) * 1000000ull;
     const int rows = p.group * a.max_tokens, RT = rows <= 8 ? 8 : rows <= kWarpRows ? 16 : attn_tc_rows();
     // no more CTAs than the bounds allow units

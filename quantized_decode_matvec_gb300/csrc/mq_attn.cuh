@@ -41,7 +41,7 @@ struct AttnParams {
     uint32_t group_inv;  // 2^32 / group rounded up: x / group = umulhi(x, group_inv) for x < 2^16
     float scale_log2;    // scale * log2(e): exp(x) = 2^(x log2 e)
     int4* shared;        // per CTA: the group that it starts and the next one goes on with (attn_shared)
-    unsigned* counters;  // one per (sequence, key/value head), where a head's rows are one block
+    unsigned* counters;  // one per CTA: arrivals at the group that it starts and the next one goes on with
     float* parts;        // two slots of a segment's results per CTA
     uint64_t limit_ns;
 };
@@ -237,11 +237,12 @@ __device__ __forceinline__ void attn_emit4(const AttnParams& p, const AttnSegmen
     ob[2 + d % 32 / 2] = uint16_t(code >> 16);
 }
 
-// a segment's arrival at its group's counter; true in the CTA that came last
+// a segment's arrival at its group's counter, which is that of the group's first CTA (a CTA is the first of one
+// shared group at most: the one that reaches past its stretch); true in the CTA that came last
 // (one thread calls it, after the CTA's results are written and synchronised)
 __device__ __forceinline__ bool attn_arrive(const AttnParams& p, const AttnSegment& g)
 {
-    unsigned* const c = p.counters + g.seq * p.c.n_kv_heads + g.head;
+    unsigned* const c = p.counters + g.cta0;
     unsigned before;
     asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(c) : "memory");
     const bool is_last = before == unsigned(g.n_ctas - 1);

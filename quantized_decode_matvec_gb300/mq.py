@@ -740,8 +740,8 @@ def kv_accept(cache: KVCache, ctx_len, path, n_path, stream=None) -> None:
 
 
 def attn_workspace(cache: KVCache, n_heads: int, max_tokens: int = MQ_TREE_MAX_TOKENS, stream=None):
-    """A zeroed workspace for attn_tree calls on caches of this one's n_seqs and n_kv_heads, with up to max_tokens tokens
-    per sequence (one per stream that runs them)."""
+    """A zeroed workspace for attn_tree calls with up to max_tokens tokens per sequence (one per stream that runs them).
+    It serves any number of sequences, and any cache and heads whose workspace is no larger."""
     out = _new(mq_attn_workspace_bytes(cache.struct, n_heads, max_tokens), _torch().uint8, cache.device, stream)
     torch = _torch()
     with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(_stream_on(stream, cache.device),

@@ -315,3 +315,21 @@ def test_not_finite_values_in_a_q8_0_output(cuda_ready, T):
             assert not np.isfinite(scale).any()
         else:
             assert np.array_equal(got[0][i], got[1][i])
+
+
+def test_one_workspace_for_batches_that_grow_and_shrink(cuda_ready):
+    # a few long sequences, many short ones, other heads, other row counts: each call finds the workspace ready
+    import torch
+    mq = cuda_ready
+    rng = np.random.default_rng(61)
+    many = [int(c) for c in rng.integers(100, 700, 64)]
+    calls = [([4000, 100, 2500], 28, 4, 128, 1), (many, 28, 4, 128, 1), ([4000, 100, 2500], 28, 4, 128, 1),
+             (many[:20], 16, 8, 64, 4), ([3000, 2000], 28, 4, 128, 30), (many, 28, 4, 128, 1), ([5000], 8, 1, 128, 1)]
+    size = 0
+    for ctx, Hq, Hkv, D, T in calls:
+        table = torch.zeros((len(ctx), 1), dtype=torch.int32, device="cuda")
+        cache = mq.KVCache.alloc(1, table, "q8_0", Hkv, D)
+        size = max(size, mq.attn_workspace(cache, Hq, T).numel())
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for ctx, Hq, Hkv, D, T in calls:
+        run_case(mq, rng, ctx, [T] * len(ctx), Hq, Hkv, D, "q8_0", workspace=ws)
