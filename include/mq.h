@@ -448,6 +448,9 @@ mq_status mq_kv_accept(const mq_kv_cache* h_cache, const int32_t* ctx_len, const
  *   out = sum_j softmax_j(scale * q . k_j) v_j     over the keys it sees
  * in fp32 sums and statistics; a node that sees no key gives zeros, and what
  * it does not see never reaches it, NaN and infinities included.
+ * An infinite value that it sees makes the output infinite; NaN where infinities
+ * of both signs meet, and possibly where the infinity's key is one of the
+ * context's with under 2^-31 of the largest key's weight.
  * out_type MQ_TYPE_F16: out f16 [n_tokens][out_ld]; MQ_TYPE_Q8_0: dense q8_0
  * columns [n_tokens][n_heads*head_dim/32 blocks] (out_ld not read), the xq of
  * an o projection.  Tokens outside every sequence are not written.

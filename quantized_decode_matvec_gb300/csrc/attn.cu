@@ -147,13 +147,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
     return r;
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     uint32_t r;
@@ -408,7 +401,7 @@ __device__ __forceinline__ bool rows_page(bool ok, uint8_t* blk, int wi, int tea
                     float mn = st.m[n][e];
 #pragma unroll
                     for (int w = 0; w < kTeam; ++w) mn = fmaxf(mn, words->top[w][8 * n + 2 * t + e]);
-                    const float f = ex2(st.m[n][e] - mn);
+                    const float f = attn_factor(st.m[n][e] - mn);
                     st.m[n][e] = mn;
                     st.l[n][e] *= f;
                     st.l[n][e + 2] *= f;
@@ -667,7 +660,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                 for (int u = 0; u < kTeam; ++u) lk += there ? l_s[os][k][u][r] : 0.0f;
                 top[j] = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, 8));
                 top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-                fk[j] = there ? ex2(mk - top[j]) : 0.0f;
+                fk[j] = there ? attn_factor(mk - top[j]) : 0.0f;
                 sum[j] = lk * fk[j];
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
@@ -849,7 +842,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                            ? __ldcg(reinterpret_cast<const float4*>(slot + 2 * RT) + lane + v * 32)
                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             gone |= lc < 0.0f;
-            const float mn = fmaxf(mr, mc), fr = ex2(mr - mn), fc = ex2(mc - mn);
+            const float mn = fmaxf(mr, mc), fr = attn_factor(mr - mn), fc = attn_factor(mc - mn);
             mr = mn;
             lr = lr * fr + lc * fc;
 #pragma unroll
@@ -880,7 +873,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
             for (int u = 0; u < nw; ++u) {
-                const float f = ex2(cm[u * RT + r] - top);
+                const float f = attn_factor(cm[u * RT + r] - top);
                 const float4 y = *reinterpret_cast<const float4*>(sums + u * RT * D + x);
                 sum = fmaf(cl[u * RT + r], f, sum);
                 v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
@@ -942,14 +935,14 @@ __global__ void __launch_bounds__(RowsJoin<D, NT>::kThreads) attn_rows_join_kern
     for (int c = 0; c < n; ++c) {
         const float lc = part_s[(n + c) * RT + row];
         gone |= there && lc < 0.0f;
-        l = fmaf(lc, ex2(part_s[c * RT + row] - mm), l);
+        l = fmaf(lc, attn_factor(part_s[c * RT + row] - mm), l);
     }
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int c0 = part * kJoinAhead; c0 < n;) {
 #pragma unroll
         for (int i = 0; i < kJoinAhead; ++i) {
             if (c0 + i >= n) break;
-            const float f = ex2(part_s[(c0 + i) * RT + row] - mm);
+            const float f = attn_factor(part_s[(c0 + i) * RT + row] - mm);
             o.x = fmaf(v[i].x, f, o.x), o.y = fmaf(v[i].y, f, o.y), o.z = fmaf(v[i].z, f, o.z), o.w = fmaf(v[i].w, f, o.w);
         }
         c0 += J::kSplit * kJoinAhead;

@@ -94,13 +94,6 @@ struct TcSegment {
     int odd, bad;  // a value that is not finite was dropped; a page outside the cache
 };
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     uint32_t r;
@@ -683,7 +676,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 const float top = fmaxf(x0, x1) * scale;
                 const bool raise = top > m + kTcRaise;
                 if (__any_sync(0xffffffffu, raise)) {
-                    const float mn = raise ? top : m, f = ex2(m - mn);
+                    const float mn = raise ? top : m, f = attn_factor(m - mn);
                     m = mn;
                     l *= f;
                     if (i > 0) {  // S is complete, so the product before it is: O is at rest
@@ -739,8 +732,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             float f = 1.0f;
             if (both) {
                 const float mo = join_m[t ^ 1][r], mm = fmaxf(m, mo);
-                f = ex2(m - mm);
-                l = l * f + join_l[t ^ 1][r] * ex2(mo - mm);
+                f = attn_factor(m - mm);
+                l = l * f + join_l[t ^ 1][r] * attn_factor(mo - mm);
                 m = mm;
             }
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -847,7 +840,7 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(con
     for (int c = 0; c < n; ++c) {
         const float lc = l_s[c * 32 + lane];
         gone |= lc < 0.0f;
-        l = fmaf(lc, ex2(m_s[c * 32 + lane] - mm), l);
+        l = fmaf(lc, attn_factor(m_s[c * 32 + lane] - mm), l);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = 0.0f;
@@ -855,7 +848,7 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(con
 #pragma unroll
         for (int i = 0; i < kJoinAhead; ++i) {
             if (c0 + i >= n) break;
-            const float f = ex2(m_s[(c0 + i) * 32 + lane] - mm);
+            const float f = attn_factor(m_s[(c0 + i) * 32 + lane] - mm);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 o[4 * h] = fmaf(x[i][h].x, f, o[4 * h]);

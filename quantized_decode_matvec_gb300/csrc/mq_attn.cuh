@@ -34,6 +34,21 @@ namespace mq {
 // counts on at most 11.
 constexpr int kAttnGroupCost = 8;
 
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^x (x <= 0) as the factor of sums and outputs that a larger maximum scales down.  It does not go to zero: an
+// infinite value in a sum stays infinite, where 0 * inf is NaN, and 2^-126 of a finite one is nothing beside the key
+// with the maximum.
+__device__ __forceinline__ float attn_factor(float x)
+{
+    return fmaxf(ex2(x), 0x1p-126f);
+}
+
 struct AttnParams {
     mq_attn_args a;
     KvView c;

@@ -333,3 +333,36 @@ def test_one_workspace_for_batches_that_grow_and_shrink(cuda_ready):
     ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
     for ctx, Hq, Hkv, D, T in calls:
         run_case(mq, rng, ctx, [T] * len(ctx), Hq, Hkv, D, "q8_0", workspace=ws)
+
+
+@pytest.mark.parametrize("ctype", ["q8_0", "f16"])
+@pytest.mark.parametrize("T", [1, 2, 4, 20, 64])
+@pytest.mark.parametrize("ctx", [100, 4000])
+def test_an_infinite_value_makes_an_infinite_output(cuda_ready, ctype, T, ctx):
+    # on both kernels, in groups of one CTA and of several: a value of a node that is infinite (a q8_0 product that
+    # overflows f16), whatever the node weighs, and one of the context that weighs like the others
+    mq = cuda_ready
+    rng = np.random.default_rng(T + ctx)
+    Hq, Hkv, D = 28, 4, 128
+    q = (np.abs(rng.standard_normal((T, Hq * D))) + 0.5).astype(np.float16)
+    masks = tree_masks(rng, T)
+    for kind, slot in (("node", ctx + T // 2), ("faint node", ctx + T // 2), ("context", 5)):
+        K = (rng.standard_normal((ctx + T, Hkv, D)) * 0.3).astype(np.float32)
+        V = rng.standard_normal((ctx + T, Hkv, D)).astype(np.float32)
+        big = np.inf if ctype == "f16" else 7.6e6  # scale 59843, code 127
+        V[slot, 1, 5], V[slot, 1, 70] = big, -big
+        if kind == "faint node":
+            K[slot] = -8.0  # 2^-150 of the others and less: q is positive
+        with np.errstate(over="ignore"):
+            pages, table = P.build([K], [V], ctype, rng)
+            k, v = P.stored(K, ctype), P.stored(V, ctype)
+        cache = mq.KVCache(dev(pages), dev(table), ctype, Hkv, D)
+        out = mq.attn_tree(cache, dev(q), dev(np.array([0, T], np.int32)), dev(np.array([ctx], np.int32)),
+                           mask=dev(as_i64(masks)), max_tokens=T, max_len=ctx + T)
+        ok_status(mq)
+        got = out.cpu().numpy().reshape(T, Hq, D).astype(np.float64)
+        ref, A, largest = P.attention(q.reshape(T, Hq, D), k, v, ctx, masks, D**-0.5)
+        assert np.isinf(ref[T // 2, 7:14, 5]).all()
+        inf = np.isinf(ref)
+        assert np.array_equal(got[inf], ref[inf]), kind
+        assert (np.abs(got[~inf] - ref[~inf]) <= bound(ref, A, largest)[~inf]).all(), kind
