@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
         }
     }
 
-    // cosine and signed sine of this lane's elements (halves of 128: of its first four, which its others share)
+    // cosine and signed sine of this lane's elements (halves of 128: of its first four, which its others share); what
+    // lies beyond the rotated part is not multiplied by 1 and 0: an infinity would become NaN, and reach its neighbour
     constexpr int NC = ROT == kRotHalves && D == 128 ? 4 : NV;
     float cs[NC], sn[NC];
     int mate[ROT == kRotPart ? NV : 1];
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
             } else if (ROT == kRotAdjacent) {
 #pragma unroll
                 for (int e = 0; e < NV; e += 2) {
+                    if (64 * (e / 4) + 4 * l + e % 4 >= a.rot_dims) continue;
                     const float u = x[e], v = x[e + 1];
                     x[e] = fmaf(u, cs[e % NC], v * sn[e % NC]);
                     x[e + 1] = fmaf(v, cs[(e + 1) % NC], u * sn[(e + 1) % NC]);
@@ -194,7 +196,10 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
                 for (int e = 0; e < NV; ++e) row[64 * (e / 4) + 4 * l + e % 4] = x[e];
                 __syncwarp();
 #pragma unroll
-                for (int e = 0; e < NV; ++e) x[e] = fmaf(x[e], cs[e % NC], row[mate[e]] * sn[e % NC]);
+                for (int e = 0; e < NV; ++e) {
+                    const int d = 64 * (e / 4) + 4 * l + e % 4;
+                    if (d < a.rot_dims) x[e] = fmaf(x[e], cs[e % NC], row[mate[e]] * sn[e % NC]);
+                }
                 __syncwarp();
             }
         }

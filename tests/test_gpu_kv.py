@@ -324,3 +324,37 @@ def test_read_of_many_tokens_is_the_same_as_of_few(cuda_ready, ctype, Hkv, D):
         for h in range(Hkv):
             for got, want in zip((k, v), P.unpack(blocks[p, h], ctype, D)):
                 assert np.array_equal(got[i, h].cpu().numpy().view(np.uint16), want[r].view(np.uint16))
+
+
+@pytest.mark.parametrize("ctype", ["q8_0", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_leaves_elements_that_are_not_rotated_alone(cuda_ready, ctype, D, inter):
+    # half of the head rotated; in the other half infinities, a NaN and -0 of queries and keys stay where they are
+    mq = cuda_ready
+    rng = np.random.default_rng(D + inter)
+    Hq, Hkv, n, R = 3, 2, 5, D // 2
+    K, V, pages, table = make(rng, [64], Hkv, D, ctype)
+    cache = cache_of(mq, pages, table, ctype, Hkv, D)
+    freq = (1e4 ** (-np.arange(0, R, 2) / R)).astype(np.float32)
+    pos = np.arange(7, 7 + n, dtype=np.int32)
+    qkv = rng.standard_normal((n, (Hq + 2 * Hkv) * D)).astype(np.float32)
+    x = qkv.reshape(n, Hq + 2 * Hkv, D)
+    for h in (1, Hq):  # a query and a key head
+        x[2, h, R + 2], x[2, h, R + 5], x[2, h, D - 1], x[2, h, D - 4] = np.inf, np.nan, -np.inf, -0.0
+    ids = dev(np.arange(n, dtype=np.int32))
+    q = mq.kv_append(cache, dev(qkv), dev(pos), dev(np.zeros(n, np.int32)), ids, Hq, inv_freq=dev(freq), interleaved=inter)
+    k, _ = mq.kv_read(cache, dev(np.zeros(n, np.int32)), ids)
+    ok_status(mq)
+    q, k = q.cpu().numpy().reshape(n, Hq, D), k.cpu().numpy()
+    assert np.array_equal(q[..., R:], x[:, :Hq, R:].astype(np.float16), equal_nan=True)
+    assert np.signbit(q[2, 1, D - 4]) and q[2, 1, D - 4] == 0
+    assert np.isfinite(q[..., :R]).all() and np.isfinite(k[..., :R]).all()
+    if ctype == "f16":
+        assert np.array_equal(k[..., R:], x[:, Hq:Hq + Hkv, R:].astype(np.float16), equal_nan=True)
+    else:
+        same = np.ones((n, Hkv, D), bool)
+        same[2, 0, R:] = False  # the blocks with values that are not finite
+        want = P.stored(x[:, Hq:Hq + Hkv], ctype)
+        same[..., :R] = False
+        assert np.array_equal(k[same], want[same])
