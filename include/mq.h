@@ -401,7 +401,8 @@ mq_status mq_check_kv_cache(const mq_kv_cache* h_cache);
  * rotation of its first rot_dims values by the angles pos[n] * inv_freq[i]:
  * pairs (i, i + rot_dims/2), or (2i, 2i+1) with MQ_ROPE_INTERLEAVED.  The
  * angle is the exact product of the integer position and the fp32 frequency
- * (reduced to a turn in 64-bit fixed point), so long positions lose nothing.
+ * (reduced to a turn in 64-bit fixed point), so long positions lose nothing;
+ * a frequency of 2^64 or more, an infinity or NaN turns its pairs to NaN.
  * q goes to q_out, K and V into slot[n] of sequence seq[n].  A negative slot
  * writes q only (padding).  Two tokens of one call must not name the same slot.
  * n_tokens == 0 launches nothing. */

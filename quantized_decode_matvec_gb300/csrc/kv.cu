@@ -29,16 +29,18 @@ namespace mq {
 // The angle: pos * f / 2pi modulo one turn, with f = m 2^(e-23) (m the 24-bit
 // mantissa): m * floor(2^64 / 2pi) is a 128-bit integer, shifted by e - 23 it
 // is the turn per position as a 64-bit binary fraction, and the product with
-// pos wraps exactly.  The fraction errs by about f units of 2^-64 per
-// position, so the angle is good to fp32 at any position (pos * f rounded to
-// fp32 is off by 4e-3 rad at position 131071).
+// pos wraps exactly.  The fraction errs by at most f + 1 units of 2^-64 per
+// position, so the angle is good to fp32 at any position for the frequencies
+// of a rotation, 1 and below (pos * f rounded to fp32 is off by 4e-3 rad at
+// position 131071).  From 2^64 on the product's low 64 bits say nothing: such
+// a frequency, an infinity or NaN gives NaN (has_angle).
 __device__ __forceinline__ uint64_t turn_per_pos(float f)
 {
     constexpr uint64_t kInv2Pi = 0x28be60db9391054aull;  // floor(2^64 / (2 pi))
     const uint32_t u = __float_as_uint(f);
     const int e = int((u >> 23) & 255u) - 127;
     uint64_t m = (u & 0x7fffffu) | 0x800000u;
-    if (e < -100 || e > 63) return 0;  // zero, subnormal (no turn in 2^31 positions) or not a frequency
+    if (e < -100 || e > 63) return 0;  // zero, subnormal (no turn in 2^31 positions); without an angle
     const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
     const int sh = e - 23;  // left shift of hi:lo, modulo 2^64
     uint64_t t;
@@ -50,6 +52,8 @@ __device__ __forceinline__ uint64_t turn_per_pos(float f)
         t = sh > -128 ? hi >> (-sh - 64) : 0;
     return u >> 31 ? 0 - t : t;
 }
+
+__device__ __forceinline__ bool has_angle(float f) { return fabsf(f) < 0x1p64f; }
 
 struct AppendArgs {
     mq_kv_append_args a;
@@ -131,9 +135,11 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs p, unsi
                 const bool first = ROT == kRotAdjacent || d < half;
                 const int i = ROT == kRotAdjacent ? d / 2 : (first ? d : d - half);
                 if (ROT == kRotPart) mate[e] = first ? d + half : d - half;
-                const uint64_t turn = turn_per_pos(__ldg(a.inv_freq + i)) * uint64_t(pos);
+                const float f = __ldg(a.inv_freq + i);
+                const uint64_t turn = turn_per_pos(f) * uint64_t(pos);
                 float s, c;
                 sincospif(float(int(turn >> 32)) * 0x1p-31f, &s, &c);  // signed half turns
+                if (!has_angle(f)) s = c = __uint_as_float(0x7fffffffu);
                 cs[e] = c;
                 sn[e] = first ? -s : s;
             }

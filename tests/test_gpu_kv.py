@@ -358,3 +358,30 @@ def test_append_leaves_elements_that_are_not_rotated_alone(cuda_ready, ctype, D,
         want = P.stored(x[:, Hq:Hq + Hkv], ctype)
         same[..., :R] = False
         assert np.array_equal(k[same], want[same])
+
+
+@pytest.mark.parametrize("inter,R", [(False, 64), (True, 64), (False, 32)])
+def test_append_with_frequencies_that_have_no_angle(cuda_ready, inter, R):
+    # NaN, an infinity or 2^64 and more in inv_freq: NaN in the pairs that it turns, and nowhere else
+    mq = cuda_ready
+    rng = np.random.default_rng(R + inter)
+    n, D = 3, 64
+    K, V, pages, table = make(rng, [64], 1, D, "f16")
+    cache = cache_of(mq, pages, table, "f16", 1, D)
+    freq = (1e4 ** (-np.arange(0, R, 2) / R)).astype(np.float32)
+    bad = {3: np.nan, 7: np.inf, 9: -np.inf, 11: np.float32(2.0**64)}
+    for i, f in bad.items():
+        freq[i] = f
+    freq[5] = 2.0**63  # the largest binade that is taken
+    pos = np.array([0, 1, 131071], np.int32)
+    qkv = rng.standard_normal((n, 3 * D)).astype(np.float32)
+    ids = dev(np.arange(n, dtype=np.int32))
+    q = mq.kv_append(cache, dev(qkv), dev(pos), dev(np.zeros(n, np.int32)), ids, 1, inv_freq=dev(freq), interleaved=inter)
+    k, _ = mq.kv_read(cache, dev(np.zeros(n, np.int32)), ids)
+    ok_status(mq)
+    i = np.array(list(bad))
+    pair = np.concatenate([2 * i, 2 * i + 1] if inter else [i, i + R // 2])
+    nan = np.zeros(D, bool)
+    nan[pair] = True
+    for x in (q.cpu().numpy(), k.cpu().numpy()[:, 0]):
+        assert (np.isnan(x) == nan).all()
