@@ -641,10 +641,18 @@ def _new(shape, dtype, device, stream):
 
 
 def _stream_on(stream, device) -> int:
-    """The stream handle of a call on ``device`` (None: torch's current stream there)."""
-    if stream is not None:
-        return stream if isinstance(stream, int) else stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+    """The stream handle of a call on ``device`` (None: torch's current stream there).  The library launches on the
+    current CUDA device, so a call whose memory is anywhere else is refused."""
+    torch = _torch()
+    if device.type != "cuda" or torch.cuda.current_device() != device.index:
+        raise ValueError(f"the cache is on {device}: the current CUDA device is wanted")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if isinstance(stream, int):
+        return stream
+    if stream.device != device:
+        raise ValueError(f"a stream of {stream.device}, the cache is on {device}")
+    return stream.cuda_stream
 
 
 class KVCache:
@@ -652,7 +660,7 @@ class KVCache:
 
     ``pages``: uint8 cuda tensor of n_pages * mq_kv_page_bytes bytes; ``table``: int32
     [n_seqs, pages per sequence].  ``type`` is "f16" or "q8_0".  The tensors are the
-    caller's; the handle keeps references to them.
+    caller's; the handle keeps references to them.  Calls on a cache are made with its device current.
     """
 
     def __init__(self, pages, table, type: str, n_kv_heads: int, head_dim: int):
@@ -742,10 +750,10 @@ def kv_accept(cache: KVCache, ctx_len, path, n_path, stream=None) -> None:
 def attn_workspace(cache: KVCache, n_heads: int, max_tokens: int = MQ_TREE_MAX_TOKENS, stream=None):
     """A zeroed workspace for attn_tree calls with up to max_tokens tokens per sequence (one per stream that runs them).
     It serves any number of sequences, and any cache and heads whose workspace is no larger."""
-    out = _new(mq_attn_workspace_bytes(cache.struct, n_heads, max_tokens), _torch().uint8, cache.device, stream)
     torch = _torch()
-    with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(_stream_on(stream, cache.device),
-                                                                                 device=cache.device)):
+    handle = _stream_on(stream, cache.device)  # before the size, which goes by the current device
+    out = _new(mq_attn_workspace_bytes(cache.struct, n_heads, max_tokens), torch.uint8, cache.device, stream)
+    with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(handle, device=cache.device)):
         return out.zero_()
 
 

@@ -164,3 +164,54 @@ def test_attention_work_is_counted_with_its_groups(mq_lib):
     for max_len, want in ((64 * 51, m.MQ_OK), (64 * 52, m.MQ_ERR_UNSUPPORTED)):
         a.max_len, a.n_tokens = max_len, 0
         assert m._lib.mq_attn_tree(c, a, 0, 0, 0) == want
+
+
+def test_calls_refuse_a_cache_that_is_not_on_the_current_device(mq_lib, monkeypatch):
+    # the library launches on the current device: a cache elsewhere, or in host memory, must not reach it
+    import torch
+    m = mq_lib
+    page = m.mq_kv_page_bytes(m.MQ_TYPE_F16, 2, 64)
+    pool = torch.zeros(4 * page + 128, dtype=torch.uint8)
+    c = m.KVCache(pool[(-pool.data_ptr()) % 128:][:4 * page], torch.zeros((2, 3), dtype=torch.int32), "f16", 2, 64)
+    i = torch.zeros(3, dtype=torch.int32)
+    q = torch.zeros((3, 4 * 64), dtype=torch.float16)
+    kv = torch.zeros((3, 2, 64), dtype=torch.float16)
+    ws = torch.zeros(128, dtype=torch.uint8)
+
+    class Stream:
+        def __init__(self, index):
+            self.device, self.cuda_stream = torch.device("cuda", index), 0x1000
+
+    class Library:  # what a call would launch
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or m.MQ_OK
+
+    calls = []
+    monkeypatch.setattr(m, "_lib", Library())
+    run = [lambda **k: m.kv_append(c, torch.zeros((3, 8 * 64)), i, i, i, 4, q_out=q, **k),
+           lambda **k: m.kv_read(c, i, i, k_out=kv, v_out=kv.clone(), **k),
+           lambda **k: m.kv_accept(c, i[:2], torch.zeros((2, 4), dtype=torch.int32), i[:2], **k),
+           lambda **k: m.attn_tree(c, q, i, i[:2], max_len=64, out=q.clone(), workspace=ws, **k),
+           lambda **k: m.attn_workspace(c, 4, **k)]
+    for f in run:  # host memory, whatever the stream
+        for stream in (0x1000, Stream(0)):
+            with pytest.raises(ValueError):
+                f(stream=stream)
+    # device memory, as far as the calls can tell
+    c.device = torch.device("cuda", 1)
+    monkeypatch.setattr(m, "_want", lambda t, *a, **k: t.data_ptr())
+    monkeypatch.setattr(m, "_rows", lambda t, *a, **k: (t.data_ptr(), t.shape[1]))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for f in run:
+        for stream in (0x1000, Stream(0), Stream(1), None):
+            with pytest.raises(ValueError):
+                f(stream=stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for f in run:  # the right device, a stream of another
+        with pytest.raises(ValueError):
+            f(stream=Stream(0))
+    assert not calls
+    for f in run[:4]:
+        f(stream=Stream(1))
+        f(stream=0x1000)
+    assert calls == [n for n in ("mq_kv_append", "mq_kv_read", "mq_kv_accept", "mq_attn_tree") for _ in range(2)]
