@@ -366,3 +366,45 @@ def test_an_infinite_value_makes_an_infinite_output(cuda_ready, ctype, T, ctx):
         inf = np.isinf(ref)
         assert np.array_equal(got[inf], ref[inf]), kind
         assert (np.abs(got[~inf] - ref[~inf]) <= bound(ref, A, largest)[~inf]).all(), kind
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_calls_on_a_given_stream(cuda_ready, handle):
+    # stream= as a torch stream or its handle: work and new outputs are that stream's, behind what it is doing
+    import torch
+    mq = cuda_ready
+    rng = np.random.default_rng(71)
+    Hq, Hkv, D, n = 8, 2, 64, 200
+    table = dev(np.arange(8, dtype=np.int32).reshape(1, 8))
+    cache = mq.KVCache.alloc(8, table, "q8_0", Hkv, D)
+    qkv = dev(rng.standard_normal((n, (Hq + 2 * Hkv) * D)).astype(np.float32))
+    at = dev(np.arange(n, dtype=np.int32))
+    seq, start, ctx = torch.zeros_like(at), dev(np.array([0, 1], np.int32)), dev(np.array([n - 1], np.int32))
+    path, one = dev(np.array([[2, 5]], np.int32)), dev(np.array([2], np.int32))
+    from_ = dev(np.array([100], np.int32))
+
+    def step(**kw):
+        q = mq.kv_append(cache, qkv, None, seq, at, Hq, **kw)
+        out = mq.attn_tree(cache, q[-1:], start, ctx, max_len=n, max_tokens=1, **kw)
+        mq.kv_accept(cache, from_, path, one, **kw)
+        return (q, out) + mq.kv_read(cache, seq, at, **kw)
+
+    want = [t.clone() for t in step()]
+    cache.pages.zero_()
+    side = torch.cuda.Stream()
+    on = side.cuda_stream if handle else side
+    torch.cuda.synchronize()
+    step(stream=on)  # what has to be loaded is loaded
+    torch.cuda.synchronize()
+    assert not (cache.pages == 0).all()
+    cache.pages.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(int(1e9))  # some 0.5 s
+    got = step(stream=on)
+    assert (cache.pages == 0).all()  # on the current stream, which did not wait
+    assert not side.query()
+    side.synchronize()
+    ok_status(mq)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
