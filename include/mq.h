@@ -541,7 +541,8 @@ mq_status mq_debug_set_variant(int32_t policy);
  * delivers each CTA's last tile and every wait is limited to 50 ms, so the
  * consumers' bounded waits run out: the kernels record MQ_DEV_TIMEOUT in the
  * device status word, write no output and return; the GPU context stays
- * usable.  MQ_FAULT_WITHHOLD_RECORDS: in the persistent step kernel the last
+ * usable.  In the attention kernels it is the last page of each CTA's first
+ * stretch of a sequence.  MQ_FAULT_WITHHOLD_RECORDS: in the persistent step kernel the last
  * CTA (which always owns h blocks) never writes its h records and every wait is limited to 50 ms, so every
  * CTA's down phase runs out of time waiting for them: the kernel records
  * MQ_DEV_TIMEOUT, the abort word stops every CTA, and the launch returns.

@@ -592,6 +592,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                 total = it0;
                 break;
             }
+            const int withheld = p.withhold && sg == 0 ? it0 + n - 1 : -1;  // test-only fault
             const int32_t* const table = p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0 + lane;
             const uint8_t* const src = p.c.pages + int64_t(g.head) * B::kBytes;
             int at = 0;  // the pages at .. at + 31 are in the lanes
@@ -605,7 +606,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                 const int32_t page = __shfl_sync(0xffffffffu, page_l, it - it0 - at);
                 if (it >= kStages) ok = wait_all(&empty[s], phase ^ 1u);
                 if (!ok) break;
-                if (lane == 0) {
+                if (lane == 0 && it != withheld) {
                     const bool bad = page < 0 || page >= p.c.n_pages;  // table entries are not trusted
                     bad_s[s] = bad;
                     if (bad) {
@@ -1021,6 +1022,7 @@ cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* w
     p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + size_t(num_sms) * kAttnSharedBytes);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + parts_offset(num_sms));
     p.limit_ns = uint64_t(fault_policy() == FAULT_NONE ? 2000 : 50) * 1000000ull;
+    p.withhold = fault_policy() == FAULT_WITHHOLD_TILE;
     const int rows = p.group * a.max_tokens, RT = rows <= 8 ? 8 : rows <= kWarpRows ? 16 : attn_tc_rows();
     // no more CTAs than the bounds allow units
     const int64_t most = int64_t(cache.n_seqs) * ((int64_t(a.max_len) + kKvPage - 1) / kKvPage) * cache.n_kv_heads *

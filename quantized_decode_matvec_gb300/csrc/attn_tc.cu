@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     __shared__ int op_bad[Q8 ? kUnits : kOps];  // bit h: the step's page h is not in the cache, so not copied
     __shared__ __align__(8) uint64_t q_ready[2], s_ready[2], p_ready[2][2], o_done[2], seg_full[kTcSegs], seg_empty[kTcSegs];
     __shared__ __align__(8) uint64_t tile_done;  // the converters' stores to a tile that one of them corrects
+    __shared__ __align__(8) uint64_t mma_done;   // all that was issued
     __shared__ TcSegment seg_s[kTcSegs];
     __shared__ float join_m[2][128], join_l[2][128];
     __shared__ uint32_t tmem_base;
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         mbar_init(&seg_empty[threadIdx.x - 96], 8 + kConv + 1);  // softmax and operand warps, the MMA warp
         if (threadIdx.x == 96) {
             mbar_init(&tile_done, kConv);
+            mbar_init(&mma_done, 1);
             abort_flag = 0;
         }
     }
@@ -399,13 +401,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                 const bool there = page >= 0 && page < p.c.n_pages;  // table entries are not trusted
                 const unsigned both = __ballot_sync(0xffffffffu, there) & 3u;
                 const uint8_t* const src = p.c.pages + (there ? (page * p.c.n_kv_heads + g.head) * B::kBytes : 0);
+                const bool withheld = p.withhold && sg == 0 && pos == 2 * n - 1;  // test-only fault
                 // q8_0: the next unit; f16: the tile itself
                 const int b = k % (Q8 ? kUnits : kOps);
                 uint64_t* const full = Q8 ? &unit_full[b] : &op_full[b];
                 if (k >= (Q8 ? kUnits : kOps))
                     ok = wait_all(Q8 ? &unit_free[b] : &op_free[b], uint32_t(k / (Q8 ? kUnits : kOps) - 1) & 1u);
                 if (!ok) break;
-                if (lane == 0) {
+                if (lane == 0 && !withheld) {
                     op_bad[b] = int(~both & (pages == 2 ? 3u : 1u));
                     if (both)
                         mbar_arrive_expect_tx(full, uint32_t(__popc(both)) * (Q8 ? C::kHalf : kKvPage * D * 2));
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
                         mbar_arrive(full);
                 }
                 __syncwarp();
-                if (lane < 2 && there) {
+                if (lane < 2 && there && !withheld) {
                     if (Q8) {
                         uint8_t* const dst = unit_s + b * C::kUnit + lane * C::kHalf;
                         bulk_copy_g2s(dst, src + (tl.is_v ? B::kVOff : 0), C::kCodes, full);
@@ -580,8 +583,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             }
             it += 2 * n;
         }
-        // what was issued completes before tensor memory is freed
-        if (it > 0) (void)mbar_wait_bounded(&op_free[(it - 1) % kOps], uint32_t((it - 1) / kOps) & 1u, p.limit_ns);
+        // what was issued completes before tensor memory is freed, in a segment that was given up too
+        __syncwarp();
+        if (elect_one()) umma_commit(&mma_done);
+        __syncwarp();
+        (void)mbar_wait_bounded(&mma_done, 0, p.limit_ns);
     } else {
         // ---- softmax: tile t, thread = row = tensor memory lane
         const int t = warp >> 2, wq = warp & 3, r = wq * 32 + lane;

@@ -59,6 +59,7 @@ struct AttnParams {
     unsigned* counters;  // one per CTA: arrivals at the group that it starts and the next one goes on with
     float* parts;        // two slots of a segment's results per CTA
     uint64_t limit_ns;
+    int withhold;  // test-only: the last page of a CTA's first segment is never delivered
 };
 
 // query row r of a sequence is head r % group of the group, of token r / group

@@ -86,3 +86,39 @@ def test_persistent_step_dependency_wait_runs_out_and_reports(cuda_ready, fault)
     for k in ("y_qkv", "y_o", "y_ffn", "h_q8"):
         x, y = getattr(bufs[0], k).cpu().numpy(), getattr(bufs[1], k).cpu().numpy()
         assert np.array_equal(x.view(np.uint8), y.view(np.uint8)), k
+
+
+# the attention kernels: warp MMAs (joined by the last CTA, joined by a kernel) and tcgen05; 28 heads on 4
+@pytest.mark.parametrize("ctype", ["q8_0", "f16"])
+@pytest.mark.parametrize("T", [1, 2, 9, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_wait_runs_out_and_reports(cuda_ready, ctype, T, D):
+    import torch
+    from tests import kv_plain as P
+    mq = cuda_ready
+    rng = np.random.default_rng(T)
+    ctx = [3000, 40, 9000]
+    K = [rng.standard_normal((c + T, 4, D)).astype(np.float32) for c in ctx]
+    pages, table = P.build(K, K, ctype, rng)
+    cache = mq.KVCache(torch.from_numpy(pages).cuda(), torch.from_numpy(table).cuda(), ctype, 4, D)
+    q = torch.from_numpy(rng.standard_normal((3 * T, 28 * D)).astype(np.float16)).cuda()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    ws = mq.attn_workspace(cache, 28, T)
+
+    def call():
+        out = torch.full((3 * T, 28 * D), 3.0, dtype=torch.float16, device="cuda")
+        mq.attn_tree(cache, q, i32(0, T, 2 * T, 3 * T), i32(*ctx), max_len=9100, max_tokens=T, out=out, workspace=ws)
+        torch.cuda.synchronize()                     # returns: the waits are bounded
+        return out, mq.mq_read_device_status(0)
+
+    want, st = call()
+    assert st == 0 and not (want == 3).all(1).any()
+    assert mq.mq_debug_set_fault(mq.MQ_FAULT_WITHHOLD_TILE) == mq.MQ_OK
+    try:
+        out, st = call()
+    finally:
+        assert mq.mq_debug_set_fault(mq.MQ_FAULT_NONE) == mq.MQ_OK
+    assert st == mq.MQ_DEV_TIMEOUT
+    ws.zero_()
+    out, st = call()
+    assert st == 0 and torch.equal(out, want)
