@@ -632,9 +632,10 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
     if (warp == kWarps + 1) {
         // ---- the segments' joins, in order, while the teams are at later ones
         int splits = 0;
+        bool ok = true;
         for (int sg = 0;; ++sg) {
             const int ss = sg % kSegs, os = sg & 1;
-            bool ok = wait_all(&seg_full[ss], uint32_t(sg / kSegs) & 1u);
+            ok = wait_all(&seg_full[ss], uint32_t(sg / kSegs) & 1u);
             if (!ok || seg_s[ss].g.n == 0) break;  // (behind the last segment: no pages)
             ok = wait_all(&out_full[os], uint32_t(sg / 2) & 1u);
             if (!ok) break;
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                 sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
                 if (split && lane < 8 && r < rows) {
                     slot[r] = top[j];
-                    slot[RT + r] = bad ? -1.0f : sum[j];
+                    slot[RT + r] = bad ? kAttnBadPage : sum[j];
                 }
                 sum[j] = sum[j] == 0.0f ? 0.0f : 1.0f / sum[j];
             }
@@ -705,6 +706,10 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
                 mbar_arrive(&seg_empty[ss]);
             }
             splits += split;
+        }
+        if (!C::kJoins && !ok && lane < RT) {  // where the last CTA joins, a group without this one's arrival is not
+            float* const slots = p.parts + int64_t(blockIdx.x) * 2 * attn_slot_floats(RT, D);
+            slots[RT + lane] = slots[attn_slot_floats(RT, D) + RT + lane] = kAttnGaveUp;
         }
         if (C::kJoins && lane == 0) {  // the teams wait for two
             for (; splits < 2; ++splits) {
@@ -931,11 +936,12 @@ __global__ void __launch_bounds__(RowsJoin<D, NT>::kThreads) attn_rows_join_kern
     }
     __syncthreads();
     float mm = kLowest, l = 0.0f;
-    bool gone = false;
+    bool gone = false, bad = false;
     for (int c = 0; c < n; ++c) mm = fmaxf(mm, part_s[c * RT + row]);
     for (int c = 0; c < n; ++c) {
         const float lc = part_s[(n + c) * RT + row];
         gone |= there && lc < 0.0f;
+        bad |= there && lc == kAttnBadPage;
         l = fmaf(lc, attn_factor(part_s[c * RT + row] - mm), l);
     }
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -950,8 +956,8 @@ __global__ void __launch_bounds__(RowsJoin<D, NT>::kThreads) attn_rows_join_kern
         if (c0 < n) load(c0);
     }
     sum_s[part][x] = o;
-    if (__syncthreads_or(gone)) {  // a page outside the cache: the group stays unwritten
-        if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+    if (__syncthreads_or(gone)) {  // the group stays unwritten
+        if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
         return;
     }
     if (part > 0) return;

@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
             }
             if (writes && split) {
                 slot[at] = m;
-                slot[kTcRows + at] = bad ? -1.0f : l;
+                slot[kTcRows + at] = bad ? kAttnBadPage : l;
             }
             if (!split && bad && threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
             tc_fence_before();  // the outputs are read: the next segment's products may follow the queries
@@ -792,7 +792,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (abort_flag && threadIdx.x == 0) atomicOr(status, MQ_DEV_TIMEOUT);
+    if (abort_flag) {
+        if (threadIdx.x == 0) atomicOr(status, MQ_DEV_TIMEOUT);
+        float* const slots = p.parts + int64_t(blockIdx.x) * 2 * attn_slot_floats(kTcRows, D);
+        if (threadIdx.x < kTcRows)
+            slots[kTcRows + threadIdx.x] = slots[attn_slot_floats(kTcRows, D) + kTcRows + threadIdx.x] = kAttnGaveUp;
+    }
     if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -841,11 +846,12 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(con
     }
     __syncthreads();
     float mm = kLowest, l = 0.0f, o[8];
-    bool gone = false;
+    bool gone = false, bad = false;
     for (int c = 0; c < n; ++c) mm = fmaxf(mm, m_s[c * 32 + lane]);
     for (int c = 0; c < n; ++c) {
         const float lc = l_s[c * 32 + lane];
         gone |= lc < 0.0f;
+        bad |= lc == kAttnBadPage;
         l = fmaf(lc, attn_factor(m_s[c * 32 + lane] - mm), l);
     }
 #pragma unroll
@@ -881,8 +887,8 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(con
         top_s[warp][lane] = top;
         __syncthreads();
     }
-    if (gone) {  // a page outside the cache: the group stays unwritten
-        if (warp == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+    if (gone) {  // the group stays unwritten
+        if (warp == 0 && bad) atomicOr(status, MQ_DEV_KV_RANGE);
         return;
     }
     if (!mine) return;

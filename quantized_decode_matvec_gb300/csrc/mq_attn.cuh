@@ -205,9 +205,12 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange
     return false;
 }
 
-// A segment's results in the workspace: m[RT], l[RT] (l < 0 in row 0: the
-// segment met a page outside the cache), then RT rows of D outputs.
+// A segment's results in the workspace: m[RT], l[RT], then RT rows of D
+// outputs.  A negative l says that there are none, and the group stays
+// unwritten: the segment met a page outside the cache, or its CTA gave up
+// (the slot may hold another call's results then).
 __host__ __device__ constexpr int64_t attn_slot_floats(int RT, int D) { return int64_t(RT) * (D + 2); }
+constexpr float kAttnBadPage = -1.0f, kAttnGaveUp = -2.0f;
 
 // what the join has to know of a group (n_ctas = 0: nothing to join)
 constexpr int kAttnSharedBytes = 32;

@@ -122,3 +122,34 @@ def test_attention_wait_runs_out_and_reports(cuda_ready, ctype, T, D):
     ws.zero_()
     out, st = call()
     assert st == 0 and torch.equal(out, want)
+
+
+# what is joined by a kernel: 9 rows and more
+@pytest.mark.parametrize("ctype", ["q8_0", "f16"])
+@pytest.mark.parametrize("T", [1, 2, 40])
+def test_attention_whose_wait_ran_out_writes_nothing(cuda_ready, ctype, T):
+    import torch
+    from tests import kv_plain as P
+    mq = cuda_ready
+    rng = np.random.default_rng(T)
+    D, ctx = 128, [20000, 40, 9000]  # pages enough that every CTA has one of a shared group first
+    K = [rng.standard_normal((c + T, 4, D)).astype(np.float32) for c in ctx]
+    pages, table = P.build(K, K, ctype, rng)
+    cache = mq.KVCache(torch.from_numpy(pages).cuda(), torch.from_numpy(table).cuda(), ctype, 4, D)
+    q = torch.from_numpy(rng.standard_normal((3 * T, 28 * D)).astype(np.float16)).cuda()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    ws = mq.attn_workspace(cache, 28, T)
+
+    def call(out):
+        mq.attn_tree(cache, q, i32(0, T, 2 * T, 3 * T), i32(*ctx), max_len=20100, max_tokens=T, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        return mq.mq_read_device_status(0)
+
+    assert call(torch.empty_like(q)) == 0            # leaves its partial results in the workspace
+    out = torch.full((3 * T, 28 * D), 3.0, dtype=torch.float16, device="cuda")
+    assert mq.mq_debug_set_fault(mq.MQ_FAULT_WITHHOLD_TILE) == mq.MQ_OK
+    try:
+        st = call(out)
+    finally:
+        assert mq.mq_debug_set_fault(mq.MQ_FAULT_NONE) == mq.MQ_OK
+    assert st == mq.MQ_DEV_TIMEOUT and (out == 3).all()
