@@ -522,10 +522,10 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
         abort_flag = 1;
         if (lane == 0) atomicOr(status, MQ_DEV_TIMEOUT);
     };
-    // one outcome for the whole warp
+    // one outcome for the whole warp; after one wait that ran out, what is not there yet is not waited for
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.limit_ns));
+        const bool ok = __all_sync(0xffffffffu, !abort_flag && mbar_wait_bounded(bar, parity, p.limit_ns));
         if (!ok) give_up();
         return ok;
     };
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
             const uint64_t t0 = global_timer_ns();
             do {
                 ok = __all_sync(0xffffffffu, load_acquire(word) >= value);
-            } while (__any_sync(0xffffffffu, !ok && global_timer_ns() - t0 < p.limit_ns));
+            } while (__any_sync(0xffffffffu, !ok && !abort_flag && global_timer_ns() - t0 < p.limit_ns));
         }
         if (!ok) give_up();
         return ok;
