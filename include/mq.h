@@ -462,9 +462,10 @@ mq_status mq_kv_accept(const mq_kv_cache* h_cache, const int32_t* ctx_len, const
  * One launch up to 8 query rows (max_tokens * n_heads/n_kv_heads), two above.
  * workspace: mq_attn_workspace_bytes bytes or more, 128-byte aligned, zeroed
  * once by the caller; every call leaves it ready for the next one on the same
- * device, whatever that one's cache, sequences, heads and tokens are.  After a
- * call that set MQ_DEV_TIMEOUT it has to be zeroed again.  Two calls that
- * overlap on the GPU must not share one. */
+ * device, whatever that one's cache, sequences, heads and tokens are.  A call
+ * that sets MQ_DEV_TIMEOUT leaves the outputs that it did not finish unwritten,
+ * and the workspace has to be zeroed again.  Two calls that overlap on the GPU
+ * must not share one. */
 typedef struct mq_attn_args {
     const void* q;            /* f16 [n_tokens][q_ld], 16-byte aligned, q_ld % 8 == 0 */
     void* out;                /* 16-byte aligned (q8_0: 2-byte) */

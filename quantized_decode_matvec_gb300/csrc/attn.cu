@@ -23,9 +23,12 @@
 //   8 keys.  q8_0 codes become f16 in registers on the way (byte permute,
 //   exact subtraction, one rounded product with the scale);
 // * the probabilities are rounded to f16 for the second product (2^-11 each,
-//   the output's own rounding), scaled by 2^10 so that a key at 2^-24 of the
-//   largest still has a normal number, and their sum is formed from the same
-//   rounded numbers by an MMA with ones, so the weights add up to one;
+//   the output's own rounding; a 32-bit operand would halve the MMAs' rate and
+//   double what goes round the team), scaled by 2^10 so that a key at 2^-24 of
+//   the largest still has a normal number, and their sum is formed from the
+//   same rounded numbers by an MMA with ones, so the weights add up to one.
+//   Root mean square error against 64 bits, relative: 2.6e-4 over 1000 keys,
+//   2.9e-4 over 131071, where a result that is only rounded once has 2.1e-4;
 // * the maximum is raised only when a score passes it by more than 5 (in
 //   powers of two; 2^15 still fits f16), which after the first tiles is rare:
 //   a predicate on the barrier that the team needs anyway, instead of a
@@ -36,12 +39,14 @@
 // Scores, maxima, sums and outputs are fp32 throughout.
 //
 // Measured (28 query heads on 4 of 128, one token per sequence): 131071 tokens
-// in f16 49.5 us, 5.4 TB/s, and 64 sequences of 128 to 8191 in f16 87 us,
-// 6.2 TB/s: the cache's bytes.  The same 64 in q8_0 59 us, 4.9 TB/s: start
-// and end of the call (about 10 us) and the conversion's instructions (about
-// 300 of a warp's 500 a page; three teams are as fast as four).
-// 1000 tokens 9.9 us: latencies, of which the launch and the split take about
-// 4, a page's copy 1, a page's products 1, and the two joins 4.
+// in f16 49.7 us, 5.4 TB/s, and 64 sequences of 128 to 8191 in f16 87 us,
+// 6.2 TB/s: the cache's bytes.  The same 64 in q8_0 58 us, 5.0 TB/s: start
+// and end of the call (about 10 us), and between them a page's instructions
+// (about 300 of a warp's 500 convert; three teams are as fast as four), 0.53
+// issued per cycle and scheduler: of a warp's waits per issue 1.6 are for
+// loads, 1.5 for fixed latencies, 1.0 for instructions.  1000 tokens 9.9 us:
+// latencies, of which the launch and the split take about 4, a page's copy 1,
+// a page's products 1, and the two joins 4.
 #include "mq_attn.cuh"
 
 namespace mq {

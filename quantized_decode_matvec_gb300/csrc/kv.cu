@@ -21,9 +21,9 @@ namespace mq {
 // forms the token's cosines and sines once.  Statistics, products and rotation
 // are fp32; each output is rounded once, to f16 or to its q8_0 code.
 //
-// Measured (28 + 4 + 4 heads of 128, q8_0): one token 3.8 us, which is launch
-// and one chain of loads, angles, norm and stores; 2048 tokens 16.1 us,
-// 3.4 TB/s: between instructions (the angles' sines, the q8_0 codes) and one
+// Measured (28 + 4 + 4 heads of 128, q8_0): one token 3.6 us, which is launch
+// and one chain of loads, angles, norm and stores; 2048 tokens 16.0 us,
+// 3.4 TB/s (f16 15.0): between instructions (the angles' sines, the q8_0 codes) and one
 // wave's latency.
 //
 // The angle: pos * f / 2pi modulo one turn, with f = m 2^(e-23) (m the 24-bit
@@ -421,7 +421,8 @@ cudaError_t launch_kv_append(const mq_kv_cache& cache, const mq_kv_append_args& 
     p.c = kv_view(cache);
     // a pair of heads per warp while that leaves the chip room (few tokens: latency), then longer runs, which
     // form a token's cosines and sines fewer times: 2048 tokens of 36 heads take 30, 22, 20, 16 and 21 us in
-    // runs of one, two, four, nine and 18 pairs
+    // runs of one, two, four, nine and 18 pairs.  Measured with those 18 pairs alone, which nine halves; other
+    // numbers of heads get the fewest runs of at most nine, of one length
     const int pairs = (a.n_heads + 1) / 2 + 2 * ((cache.n_kv_heads + 1) / 2);
     const int64_t per = int64_t(a.n_tokens) * pairs / (int64_t(num_sms) * 16);
     p.per_warp = per < 1 ? 1 : per > 9 ? 9 : int(per);
@@ -455,7 +456,7 @@ cudaError_t launch_kv_read(const mq_kv_cache& cache, const int32_t* seq, const i
     p.per_inv = uint32_t((0x100000000ull + p.per - 1) / p.per);
     // Four chunks per thread once the chip has plenty of them; with 4 heads of 128 and one or four: f16, 4096 tokens
     // 3.9 and 4.6 us, 16384 17.6 and 13.5, 131072 119 and 84 (6.4 TB/s); q8_0, 32768 22.3 (4.6 TB/s) and 24.1, 131072 79
-    // and 76.
+    // and 76.  Other head counts and heads of 64 were not measured; the rule counts their chunks alike.
     const bool many = int64_t(n) * p.per >= int64_t(num_sms) * (cache.type == MQ_TYPE_Q8_0 ? 20480 : 8192);
     const int chunks = many ? 1024 : 256;  // of a CTA
     p.tokens = p.per < chunks ? chunks / p.per : 1;

@@ -763,9 +763,10 @@ def attn_tree(cache: KVCache, q, tok_start, ctx_len, mask=None, scale: Optional[
     """Attention of every tree's nodes (q: f16 [n, n_heads * head_dim], rows may be strided) over the cache.
 
     ``mask``: int64 [n], bit j = node j of the token's tree is seen (None: a chain).  ``max_len`` bounds context plus
-    tree of any sequence (default: what the table can hold).  Returns f16 [n, n_heads * head_dim], or with
-    ``out_type="q8_0"`` uint8 [n, n_heads * head_dim / 32 * 34], the ``xq`` of a projection.  A program that calls
-    this every step keeps the workspace (attn_workspace)."""
+    tree of any sequence (default: what the table can hold).  ``max_tokens`` bounds the tokens of any sequence, picks the
+    kernel and sizes the workspace: a decode step says 1, with the default it takes the kernel for large trees.  Returns
+    f16 [n, n_heads * head_dim], or with ``out_type="q8_0"`` uint8 [n, n_heads * head_dim / 32 * 34], the ``xq`` of a
+    projection.  A program that calls this every step keeps the workspace (attn_workspace)."""
     torch = _torch()
     dev, D, S, i32 = cache.device, cache.head_dim, cache.n_seqs, torch.int32
     if q.dim() != 2 or q.shape[1] % D:
