@@ -72,6 +72,7 @@ typedef int mq_status;
                                     the MQ_STEP_CHAINED pattern; nothing was written */
 #define MQ_DEV_KV_RANGE 16u      /* a sequence, slot, page, length or tree node outside the key/value cache or
                                     the call's host bounds; what it concerns was skipped */
+#define MQ_DEV_KV_FULL 32u       /* a pool has fewer free pages than a call needs; nothing was changed */
 
 /* quantization types (mq_concat_rows*) */
 #define MQ_TYPE_Q4_K 1
@@ -485,6 +486,149 @@ typedef struct mq_attn_args {
 mq_status mq_attn_workspace_bytes(const mq_kv_cache* h_cache, int32_t n_heads, int32_t max_tokens, size_t* bytes);
 mq_status mq_attn_tree(const mq_kv_cache* h_cache, const mq_attn_args* h_args, void* workspace, size_t ws_bytes,
                        void* stream);
+
+/* ---- several continuations of one prompt ------------------------------------------------
+ * A pool hands out a cache's pages (mq_kv_grow, mq_kv_fork, mq_kv_free,
+ * mq_kv_compact): a continuation shares its prompt's full pages.
+ * mq_attn_shared attends over such pages once for all who share them;
+ * mq_softmax and mq_verify_tree end a step that drafted trees: the target's
+ * probabilities, and from them each tree's accepted path, which mq_kv_accept
+ * takes, and the token behind it. */
+
+/* Attention as mq_attn_tree, of a batch whose sequences have the pages of a
+ * prefix in common.  Group g are the sequences grp_start[g]..grp_start[g+1]-1:
+ * the first grp_pages[g] pages of the table are the same for all of them (those
+ * of the group's first sequence are read), and each has at least 64 *
+ * grp_pages[g] tokens of context.  grp_start must not decrease; sequences in no
+ * group, and those of a group with 0 pages, have no prefix in common.  The
+ * result is mq_attn_tree's up to rounding, and so are the rules for what a node
+ * sees, for masks, infinities and NaN.  A sequence that contradicts its group,
+ * and every sequence of a group that contradicts the bounds, is skipped
+ * (MQ_DEV_KV_RANGE).
+ * max_pages bounds grp_pages[g].  n_tokens * (n_heads/n_kv_heads)^2 must stay
+ * below 2^32, mq_attn_tree's bound holds, and (n_tokens *
+ * (n_heads/n_kv_heads) / 256 + n_groups) * (max_pages + 12) * n_kv_heads stays
+ * below 2^31 (MQ_ERR_UNSUPPORTED).  Three or four launches; without groups or
+ * pages, mq_attn_tree's.
+ * workspace: as mq_attn_tree's, of mq_attn_shared_workspace_bytes; it serves
+ * any call whose own size is no larger. */
+typedef struct mq_attn_groups {
+    const int32_t* grp_start; /* device [n_groups + 1] */
+    const int32_t* grp_pages; /* device [n_groups] */
+    int32_t n_groups;
+    int32_t max_pages;
+} mq_attn_groups;
+/* needs mq_init for the current device (the size goes by its SMs) */
+mq_status mq_attn_shared_workspace_bytes(const mq_kv_cache* h_cache, int32_t n_heads, int32_t n_tokens,
+                                         int32_t max_tokens, int32_t n_groups, size_t* bytes);
+mq_status mq_attn_shared(const mq_kv_cache* h_cache, const mq_attn_args* h_args, const mq_attn_groups* h_groups,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/* y[r][i] = exp(scale * x[r][i]) / sum_j exp(scale * x[r][j]), fp32 [rows][vocab]
+ * with row strides x_ld, y_ld >= vocab; scale > 0 (one over the temperature).
+ * y may be x with the same stride, and otherwise does not overlap it.  -inf
+ * weighs nothing; a row of -inf alone, or with +inf or NaN in it, becomes NaN.
+ * 4-byte aligned (rows that start at the same place in 16 bytes are fastest).
+ * vocab <= 2^28, rows <= 2^24 (MQ_ERR_UNSUPPORTED).  rows == 0 or vocab == 0
+ * launches nothing. */
+mq_status mq_softmax(const float* x, float* y, int32_t rows, int32_t vocab, int64_t x_ld, int64_t y_ld, float scale,
+                     void* stream);
+
+/* Verification of drafted trees.  Sequence s owns the nodes
+ * tok_start[s]..tok_start[s+1]-1 (0..MQ_TREE_MAX_TOKENS), node 0 of them the
+ * root: the token that the step before ended with.  Node i >= 1 holds the drafted
+ * token[i], a continuation of node parent[i] (0..i-1).  Row i of target has the
+ * target's probabilities of the token behind node i, row i of draft those that
+ * the tokens of i's children were drawn from, independently of one another;
+ * without draft every drafted token is its own distribution (looked up, not
+ * drawn).  The walk starts at the root.  At a node, with p and q its rows, a = 0,
+ * W = 1, its children x are tried in the order of their numbers:
+ *   accepted   u[x] q(x) W < S(x) and S(x) > 0, where S = max(p - a q, 0): the
+ *              walk goes on at x
+ *   refused    a += W; then W = the sum of S over the vocabulary
+ * (without draft: q(x) = 1; a refused token's S is 0 from then on, and W is less
+ * by what it was).  Where no child is accepted the walk ends, and next is the
+ * first index at which the running sum of S passes u[root] times the whole sum;
+ * where S is zero everywhere, p takes its place; where that is zero too, next
+ * is -1.  So next and the path are distributed as if drawn from the target.
+ * With MQ_VERIFY_GREEDY next is the index of the largest target value at the
+ * node (the lowest of equals; -1 where none is above -inf), and the first child
+ * that holds it is accepted; target may be logits then, and draft and u are not
+ * read.
+ * path[s][0..n_path[s]-1] are the accepted nodes, root first, and n_path[s] their
+ * number, as mq_kv_accept takes them; entries behind are not written.  A path
+ * ends at path_ld nodes (>= 1), at the last as if it had no children.  A sequence
+ * without nodes has n_path 0 and next -1.
+ * Probabilities are >= 0 (what is not counts as 0, above 1 as 1) and u in [0, 1).
+ * Sums are integers in units of 2^-60; a test of a child is made in fp64.
+ * A node whose parent or token is outside its range is never accepted, a
+ * sequence whose nodes are is not written: MQ_DEV_KV_RANGE.
+ * vocab <= 2^28.  One launch. */
+#define MQ_VERIFY_GREEDY 1u
+typedef struct mq_verify_args {
+    const float* target;      /* [n_tokens][target_ld], target_ld >= vocab */
+    const float* draft;       /* [n_tokens][draft_ld], or NULL */
+    const int32_t* tok_start; /* [n_seqs + 1] */
+    const int32_t* token;     /* [n_tokens]; a root's is not read as one */
+    const int32_t* parent;    /* [n_tokens]; a root's is not read as one */
+    const float* u;           /* [n_tokens]; not read with MQ_VERIFY_GREEDY */
+    int32_t* path;            /* [n_seqs][path_ld] */
+    int32_t* n_path;          /* [n_seqs] */
+    int32_t* next;            /* [n_seqs] */
+    int64_t target_ld;
+    int64_t draft_ld;
+    int32_t n_tokens;
+    int32_t n_seqs;
+    int32_t vocab;
+    int32_t path_ld;
+    uint32_t flags;           /* MQ_VERIFY_* */
+    int32_t reserved;         /* 0 */
+} mq_verify_args;
+mq_status mq_verify_tree(const mq_verify_args* h_args, void* stream);
+
+/* A cache's pages as a pool.  free_list[0..n_free-1] are the free pages, the one
+ * at the end is taken next; what lies behind n_free is not read.  refs[p] counts
+ * the table entries that name page p; seq_pages[s] is the number of pages of
+ * sequence s, table[s][0..seq_pages[s]-1].  All of it is device memory that the
+ * caller fills once (every page free: refs and seq_pages zero, free_list any
+ * order, *n_free = n_pages) and the calls keep; they write the cache's table too.
+ * A call does what its list says as if entry by entry, in the list's order.  An
+ * entry outside the cache or the pool's state is left out and sets
+ * MQ_DEV_KV_RANGE.  Lists have up to MQ_MAX_SEQS entries, and n_seqs * table_ld
+ * is below 2^31 (MQ_ERR_UNSUPPORTED).
+ *  - mq_kv_grow: sequence s gets pages behind its own until it has ceil(length[s]
+ *    / 64) of them, for every s of the cache; one that has as many keeps them.
+ *    A page it gets has a count of one.  Too few free pages: nothing is changed,
+ *    MQ_DEV_KV_FULL.
+ *  - mq_kv_fork: sequence dst[i], which has no pages, continues the first
+ *    length[i] tokens of src[i]: it shares src's full pages among them, and where
+ *    the last is not full it takes a free one, into which the page's written
+ *    tokens are copied (length[i] % 64 of them; the rest stays as it was).  A dst
+ *    is named once, and is no src of the same call.  Too few free pages: nothing
+ *    is changed, MQ_DEV_KV_FULL.
+ *  - mq_kv_free: sequence seq[i] gives up its pages but the first keep[i] (all of
+ *    them where keep is NULL); their table entries become -1, and a page that no
+ *    entry names any more goes onto the stack, where its last reference in the
+ *    call was given up.  A sequence named again is left out.
+ *  - mq_kv_compact: with U pages in use, the k-th of those from page U on (in
+ *    ascending order) moves to the k-th free page before U, bytes and count, and
+ *    the table follows; free_list becomes n_pages - 1 down to U.
+ * One launch (grow, free), two (fork, compact). */
+typedef struct mq_kv_pool {
+    int32_t* refs;      /* [n_pages] */
+    int32_t* free_list; /* [n_pages] */
+    int32_t* n_free;    /* [1] */
+    int32_t* seq_pages; /* [n_seqs] */
+    int32_t* scratch;   /* [mq_kv_pool_scratch(...)], the calls' own; nothing is kept there */
+} mq_kv_pool;
+/* int32 values of a pool's scratch */
+int64_t mq_kv_pool_scratch(const mq_kv_cache* h_cache);
+mq_status mq_kv_grow(const mq_kv_cache* h_cache, const mq_kv_pool* h_pool, const int32_t* length, void* stream);
+mq_status mq_kv_fork(const mq_kv_cache* h_cache, const mq_kv_pool* h_pool, const int32_t* src, const int32_t* dst,
+                     const int32_t* length, int32_t n, void* stream);
+mq_status mq_kv_free(const mq_kv_cache* h_cache, const mq_kv_pool* h_pool, const int32_t* seq, const int32_t* keep,
+                     int32_t n, void* stream);
+mq_status mq_kv_compact(const mq_kv_cache* h_cache, const mq_kv_pool* h_pool, void* stream);
 
 /* ---- the FFN without caller scratch --------------------------------------------------
  * No counterpart in the pages: they describe the FFN kernels, not how a

@@ -3,6 +3,7 @@
 // mq_init, no synchronization and no host read of device memory inside a
 // compute call, so every compute call can be captured into a CUDA graph.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -20,6 +21,7 @@ cudaError_t set_ring_split_attributes(int max_smem);
 cudaError_t set_gemm_attributes(int max_smem);
 cudaError_t set_mmq_attributes(int max_smem);
 cudaError_t set_attn_attributes(int max_smem);
+cudaError_t set_attn_shared_attributes();
 void plan_ring(MvPlan& q, int64_t units, int kind, int nc, const DeviceInfo& dev, int64_t unit_bytes,
                bool allow_cols);
 }  // namespace mq
@@ -446,6 +448,7 @@ cudaError_t set_kernel_attributes(int max_smem)
     if (e == cudaSuccess) e = set_gemm_attributes(max_smem);
     if (e == cudaSuccess) e = set_mmq_attributes(max_smem);
     if (e == cudaSuccess) e = set_attn_attributes(max_smem);
+    if (e == cudaSuccess) e = set_attn_shared_attributes();
     return e;
 }
 
@@ -934,8 +937,10 @@ mq_status mq_attn_workspace_bytes(const mq_kv_cache* cache, int32_t n_heads, int
     return MQ_OK;
 }
 
-mq_status mq_attn_tree(const mq_kv_cache* cache, const mq_attn_args* a, void* workspace, size_t ws_bytes, void* stream)
+// what mq_attn_tree and mq_attn_shared ask of their arguments; *none: there is nothing to do
+static mq_status check_attn(const mq_kv_cache* cache, const mq_attn_args* a, const void* workspace, bool* none)
 {
+    *none = false;
     mq_status st = mq_check_kv_cache(cache);
     if (st != MQ_OK) return st;
     if (!a) return MQ_ERR_INVALID_ARG;
@@ -951,15 +956,191 @@ mq_status mq_attn_tree(const mq_kv_cache* cache, const mq_attn_args* a, void* wo
     const double units = double(cache->n_seqs) * cache->n_kv_heads * (a->max_len / MQ_KV_PAGE_TOKENS + 12.0) *
                          ((a->n_heads / cache->n_kv_heads * a->max_tokens + 7) / 8);
     if (units >= 2147483648.0) return MQ_ERR_UNSUPPORTED;
-    if (a->n_tokens == 0 || cache->n_seqs == 0) return MQ_OK;
+    if (a->n_tokens == 0 || cache->n_seqs == 0) {
+        *none = true;
+        return MQ_OK;
+    }
     if (!a->q || !a->out || !a->tok_start || !a->ctx_len || !workspace) return MQ_ERR_INVALID_ARG;
     if (!aligned(a->q, 16) || !aligned(a->out, a->out_type == MQ_TYPE_F16 ? 16 : 2) || !aligned(a->tok_start, 4) ||
         !aligned(a->ctx_len, 4) || !aligned(a->mask, 8) || !aligned(workspace, 128))
         return MQ_ERR_ALIGN;
+    return MQ_OK;
+}
+
+mq_status mq_attn_tree(const mq_kv_cache* cache, const mq_attn_args* a, void* workspace, size_t ws_bytes, void* stream)
+{
+    bool none;
+    mq_status st = check_attn(cache, a, workspace, &none);
+    if (st != MQ_OK || none) return st;
     const mq::DeviceInfo* dev = nullptr;
     if ((st = current_dev(&dev)) != MQ_OK) return st;
     if (ws_bytes < mq::attn_workspace_bytes(*cache, a->n_heads, a->max_tokens, dev->num_sms)) return MQ_ERR_INVALID_ARG;
     cudaError_t e = mq::launch_attn(*cache, *a, workspace, dev->num_sms, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+// ---- several continuations of one prompt ----------------------------------------------------
+
+static mq_status check_shared_shape(const mq_kv_cache* cache, int32_t n_heads, int32_t n_tokens, int32_t n_groups)
+{
+    if (n_tokens < 0 || n_groups < 0) return MQ_ERR_SHAPE;
+    if (n_groups > MQ_MAX_SEQS) return MQ_ERR_UNSUPPORTED;
+    const double group = n_heads / cache->n_kv_heads;
+    // query rows of a group are divided by the heads with 32-bit factors, and counted in 31 bits
+    return n_tokens * group * group >= 4294967296.0 || n_tokens * group >= 2147483648.0 ? MQ_ERR_UNSUPPORTED : MQ_OK;
+}
+
+mq_status mq_attn_shared_workspace_bytes(const mq_kv_cache* cache, int32_t n_heads, int32_t n_tokens, int32_t max_tokens,
+                                         int32_t n_groups, size_t* bytes)
+{
+    mq_status st = mq_check_kv_cache(cache);
+    if (st != MQ_OK) return st;
+    if (!bytes) return MQ_ERR_INVALID_ARG;
+    if ((st = check_attn_shape(cache, n_heads, max_tokens)) != MQ_OK) return st;
+    if ((st = check_shared_shape(cache, n_heads, n_tokens, n_groups)) != MQ_OK) return st;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    *bytes = mq::attn_shared_workspace_bytes(*cache, n_heads, n_tokens, max_tokens, n_groups, dev->num_sms);
+    return MQ_OK;
+}
+
+mq_status mq_attn_shared(const mq_kv_cache* cache, const mq_attn_args* a, const mq_attn_groups* g, void* workspace,
+                         size_t ws_bytes, void* stream)
+{
+    bool none;
+    mq_status st = check_attn(cache, a, workspace, &none);
+    if (st != MQ_OK) return st;
+    if (!g) return MQ_ERR_INVALID_ARG;
+    if (g->max_pages < 0) return MQ_ERR_SHAPE;
+    if ((st = check_shared_shape(cache, a->n_heads, a->n_tokens, g->n_groups)) != MQ_OK) return st;
+    const double group = a->n_heads / cache->n_kv_heads;
+    if ((a->n_tokens * group / 256 + g->n_groups) * (g->max_pages + 12.0) * cache->n_kv_heads >= 2147483648.0)
+        return MQ_ERR_UNSUPPORTED;
+    if (none) return MQ_OK;
+    if (g->n_groups > 0 && (!g->grp_start || !g->grp_pages)) return MQ_ERR_INVALID_ARG;
+    if (!aligned(g->grp_start, 4) || !aligned(g->grp_pages, 4)) return MQ_ERR_ALIGN;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    if (ws_bytes < mq::attn_shared_workspace_bytes(*cache, a->n_heads, a->n_tokens, a->max_tokens, g->n_groups, dev->num_sms))
+        return MQ_ERR_INVALID_ARG;
+    cudaError_t e = mq::launch_attn_shared(*cache, *a, *g, workspace, dev->num_sms, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+mq_status mq_softmax(const float* x, float* y, int32_t rows, int32_t vocab, int64_t x_ld, int64_t y_ld, float scale,
+                     void* stream)
+{
+    if (rows < 0 || vocab < 0 || x_ld < vocab || y_ld < vocab) return MQ_ERR_SHAPE;
+    if (rows > (1 << 24) || vocab > (1 << 28)) return MQ_ERR_UNSUPPORTED;
+    if (!(scale > 0.0f) || !(scale * 1.5f < INFINITY)) return MQ_ERR_INVALID_ARG;
+    if (rows == 0 || vocab == 0) return MQ_OK;
+    if (!x || !y || (x == y && x_ld != y_ld)) return MQ_ERR_INVALID_ARG;
+    if (!aligned(x, 4) || !aligned(y, 4)) return MQ_ERR_ALIGN;
+    const mq::DeviceInfo* dev = nullptr;
+    mq_status st = current_dev(&dev);
+    if (st != MQ_OK) return st;
+    cudaError_t e = mq::launch_softmax(x, y, rows, vocab, x_ld, y_ld, scale, dev->num_sms, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+mq_status mq_verify_tree(const mq_verify_args* a, void* stream)
+{
+    if (!a || a->reserved != 0 || (a->flags & ~MQ_VERIFY_GREEDY)) return MQ_ERR_INVALID_ARG;
+    if (a->n_tokens < 0 || a->n_seqs < 0 || a->vocab < 1 || a->path_ld < 1 || a->target_ld < a->vocab) return MQ_ERR_SHAPE;
+    if (a->draft && a->draft_ld < a->vocab) return MQ_ERR_SHAPE;
+    if (a->vocab > (1 << 28) || a->n_seqs > MQ_MAX_SEQS) return MQ_ERR_UNSUPPORTED;
+    if (a->n_seqs == 0) return MQ_OK;
+    if (!a->tok_start || !a->path || !a->n_path || !a->next) return MQ_ERR_INVALID_ARG;
+    if (a->n_tokens > 0 && (!a->target || !a->token || !a->parent || (!a->u && !(a->flags & MQ_VERIFY_GREEDY))))
+        return MQ_ERR_INVALID_ARG;
+    if (!aligned(a->target, 4) || !aligned(a->draft, 4) || !aligned(a->tok_start, 4) || !aligned(a->token, 4) ||
+        !aligned(a->parent, 4) || !aligned(a->u, 4) || !aligned(a->path, 4) || !aligned(a->n_path, 4) || !aligned(a->next, 4))
+        return MQ_ERR_ALIGN;
+    const mq::DeviceInfo* dev = nullptr;
+    mq_status st = current_dev(&dev);
+    if (st != MQ_OK) return st;
+    mq_verify_args b = *a;
+    if (b.flags & MQ_VERIFY_GREEDY) b.draft = nullptr;
+    cudaError_t e = mq::launch_verify(b, dev->num_sms, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+int64_t mq_kv_pool_scratch(const mq_kv_cache* cache)
+{
+    return mq_check_kv_cache(cache) == MQ_OK ? 2 * cache->n_pages + 4 + cache->n_seqs : 0;
+}
+
+// *none: there is nothing to do
+static mq_status check_pool(const mq_kv_cache* cache, const mq_kv_pool* pool, int32_t n, bool* none)
+{
+    *none = false;
+    mq_status st = mq_check_kv_cache(cache);
+    if (st != MQ_OK) return st;
+    if (!pool) return MQ_ERR_INVALID_ARG;
+    if (n < 0) return MQ_ERR_SHAPE;
+    if (n > MQ_MAX_SEQS || int64_t(cache->n_seqs) * cache->table_ld > INT32_MAX || cache->n_pages > (1 << 29))
+        return MQ_ERR_UNSUPPORTED;
+    if (n == 0 || cache->n_seqs == 0) {
+        *none = true;
+        return MQ_OK;
+    }
+    if (!pool->refs || !pool->free_list || !pool->n_free || !pool->seq_pages || !pool->scratch) return MQ_ERR_INVALID_ARG;
+    if (!aligned(pool->refs, 4) || !aligned(pool->free_list, 4) || !aligned(pool->n_free, 4) ||
+        !aligned(pool->seq_pages, 4) || !aligned(pool->scratch, 4))
+        return MQ_ERR_ALIGN;
+    return MQ_OK;
+}
+
+mq_status mq_kv_grow(const mq_kv_cache* cache, const mq_kv_pool* pool, const int32_t* length, void* stream)
+{
+    bool none;
+    mq_status st = check_pool(cache, pool, 1, &none);
+    if (st != MQ_OK || none) return st;
+    if (!length) return MQ_ERR_INVALID_ARG;
+    if (!aligned(length, 4)) return MQ_ERR_ALIGN;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    cudaError_t e = mq::launch_kv_grow(*cache, *pool, length, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+mq_status mq_kv_fork(const mq_kv_cache* cache, const mq_kv_pool* pool, const int32_t* src, const int32_t* dst,
+                     const int32_t* length, int32_t n, void* stream)
+{
+    bool none;
+    mq_status st = check_pool(cache, pool, n, &none);
+    if (st != MQ_OK || none) return st;
+    if (!src || !dst || !length) return MQ_ERR_INVALID_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(length, 4)) return MQ_ERR_ALIGN;
+    if (n > cache->n_seqs) return MQ_ERR_SHAPE;  // a new sequence is named once
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    cudaError_t e = mq::launch_kv_fork(*cache, *pool, src, dst, length, n, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+mq_status mq_kv_free(const mq_kv_cache* cache, const mq_kv_pool* pool, const int32_t* seq, const int32_t* keep, int32_t n,
+                     void* stream)
+{
+    bool none;
+    mq_status st = check_pool(cache, pool, n, &none);
+    if (st != MQ_OK || none) return st;
+    if (!seq) return MQ_ERR_INVALID_ARG;
+    if (!aligned(seq, 4) || !aligned(keep, 4)) return MQ_ERR_ALIGN;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    cudaError_t e = mq::launch_kv_free(*cache, *pool, seq, keep, n, dev->status, as_stream(stream));
+    return e == cudaSuccess ? MQ_OK : cuda_fail(e);
+}
+
+mq_status mq_kv_compact(const mq_kv_cache* cache, const mq_kv_pool* pool, void* stream)
+{
+    bool none;
+    mq_status st = check_pool(cache, pool, 1, &none);
+    if (st != MQ_OK || none) return st;
+    const mq::DeviceInfo* dev = nullptr;
+    if ((st = current_dev(&dev)) != MQ_OK) return st;
+    cudaError_t e = mq::launch_kv_compact(*cache, *pool, dev->num_sms, as_stream(stream));
     return e == cudaSuccess ? MQ_OK : cuda_fail(e);
 }
 

@@ -49,17 +49,40 @@ __device__ __forceinline__ float attn_factor(float x)
     return fmaxf(ex2(x), 0x1p-126f);
 }
 
+// Which keys a kernel attends over: all of a sequence's; in a call with shared prefixes (attn_shared.cu) a sequence's
+// own ones, those behind the pages that its group shares; or those pages, for all tokens of a group's sequences, which
+// the kernel takes for one long sequence without a tree.  The last two leave their rows' maxima, sums and unnormalised
+// outputs for the join, but for a sequence without shared pages, which the second finishes.
+enum { kAttnAll = 0, kAttnOwn = 1, kAttnPrefix = 2 };
+
+// Rows (token * heads + head) in the workspace.  ml: the maximum less the kernel's shift, so that ml.y 2^ml.x is the
+// sum whichever kernel it is from; a negative ml.y: there is no result (a page outside the cache).
+struct AttnRows {
+    float2* ml;
+    float* o;  // [rows][D]
+};
+
+struct AttnShared {
+    const int32_t* grp_start;
+    const int32_t* grp_pages;
+    int n_groups, max_pages;
+    unsigned* abort;  // [0]: a wait ran out; [1]: a sequence contradicts the call's bounds or its group
+    AttnRows own, prefix;
+    int4* blocks;   // per row block and key/value head of the groups: first CTA, CTAs, slot of the first
+};
+
 struct AttnParams {
     mq_attn_args a;
     KvView c;
     int group;           // query heads per key/value head
-    uint32_t group_inv;  // 2^32 / group rounded up: x / group = umulhi(x, group_inv) for x < 2^16
+    uint32_t group_inv;  // 2^32 / group rounded up: x / group = umulhi(x, group_inv) for x < 2^32 / group
     float scale_log2;    // scale * log2(e): exp(x) = 2^(x log2 e)
     int4* shared;        // per CTA: the group that it starts and the next one goes on with (attn_shared)
     unsigned* counters;  // one per CTA: arrivals at the group that it starts and the next one goes on with
     float* parts;        // two slots of a segment's results per CTA
     uint64_t limit_ns;
     int withhold;  // test-only: the last page of a CTA's first segment is never delivered
+    AttnShared sh;  // not kAttnAll
 };
 
 // query row r of a sequence is head r % group of the group, of token r / group
@@ -68,22 +91,85 @@ __device__ __forceinline__ int attn_row_token(const AttnParams& p, int r)
     return p.group == 1 ? r : int(__umulhi(uint32_t(r), p.group_inv));
 }
 
-// sequence s as the device data has it; false (and nothing to do) where it is
-// empty, *bad where it contradicts the call's bounds or the cache
+// Group g of the sequences with a shared prefix; false where there is nothing to do for it, *bad where it contradicts
+// the call's bounds.
+struct AttnGroup {
+    int seq0, t0, T, pages;
+};
+__device__ __forceinline__ bool attn_group(const AttnParams& p, int g, AttnGroup* q, bool* bad)
+{
+    q->seq0 = __ldg(p.sh.grp_start + g);
+    const int end = __ldg(p.sh.grp_start + g + 1);
+    q->pages = __ldg(p.sh.grp_pages + g);
+    *bad = q->seq0 < 0 || end < q->seq0 || end > p.c.n_seqs || q->pages < 0 || q->pages > p.sh.max_pages ||
+           q->pages > p.c.table_ld;
+    q->t0 = q->T = 0;
+    if (*bad) return false;
+    q->t0 = __ldg(p.a.tok_start + q->seq0);
+    const int64_t T = int64_t(__ldg(p.a.tok_start + end)) - q->t0;
+    *bad = q->t0 < 0 || T < 0 || q->t0 + T > p.a.n_tokens;
+    q->T = int(T);
+    return T > 0 && q->pages > 0 && !*bad;
+}
+
+// the group of sequence s, or -1
+__device__ __forceinline__ int attn_group_of(const AttnParams& p, int s)
+{
+    int lo = 0, hi = p.sh.n_groups;  // the last group that starts at s or before it
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.sh.grp_start + mid) <= s)
+            lo = mid + 1;
+        else
+            hi = mid;
+    }
+    return lo > 0 && s < __ldg(p.sh.grp_start + lo) ? lo - 1 : -1;
+}
+
+// sequence s as the device data has it (kAttnPrefix: group s as one); false
+// (and nothing to do) where it is empty, *bad where it contradicts the call's
+// bounds or the cache
 struct AttnSeq {
     int t0, T, ctx, pages;
+    int row, skip;  // its row of the table; kAttnOwn: pages of the table before its own
 };
+template <int M>
 __device__ __forceinline__ bool attn_seq(const AttnParams& p, int s, AttnSeq* q, bool* bad)
 {
+    if constexpr (M == kAttnPrefix) {
+        AttnGroup g;
+        const bool there = attn_group(p, s, &g, bad);
+        q->t0 = g.t0, q->T = g.T, q->pages = g.pages, q->ctx = g.pages * kKvPage, q->row = g.seq0, q->skip = 0;
+        return there;
+    }
     q->t0 = __ldg(p.a.tok_start + s);
     const int64_t T = int64_t(__ldg(p.a.tok_start + s + 1)) - q->t0;
     q->ctx = __ldg(p.a.ctx_len + s);
-    const int64_t len = q->ctx + T;
+    int64_t len = q->ctx + T;
     *bad = q->t0 < 0 || T < 0 || T > p.a.max_tokens || q->t0 + T > p.a.n_tokens ||
            (T > 0 && (q->ctx < 0 || len > p.a.max_len || len > int64_t(p.c.table_ld) * kKvPage));
-    q->T = int(T);
+    q->T = int(T), q->row = s, q->skip = 0;
+    if constexpr (M == kAttnOwn) {
+        const int k = T > 0 && !*bad ? attn_group_of(p, s) : -1;
+        if (k >= 0) {  // its tokens lie in the group's, which the join goes by, its context reaches past the prefix
+            AttnGroup g;
+            bool bad_group;
+            const bool there = attn_group(p, k, &g, &bad_group);
+            *bad = bad_group || (there && (q->t0 < g.t0 || q->t0 + T > int64_t(g.t0) + g.T || q->ctx < g.pages * kKvPage));
+            if (there && !*bad) {
+                q->skip = g.pages;
+                q->ctx -= g.pages * kKvPage;
+                len -= g.pages * kKvPage;
+            }
+        }
+    }
     q->pages = int((len + kKvPage - 1) / kKvPage);
     return T > 0 && !*bad;
+}
+template <int M>
+__device__ __forceinline__ int attn_seqs(const AttnParams& p)
+{
+    return M == kAttnPrefix ? p.sh.n_groups : p.c.n_seqs;
 }
 
 // groups of sequence s with row blocks of RT rows; each has q.pages + (the group cost) units
@@ -109,15 +195,16 @@ struct AttnRange {
 };
 
 // The cut, and where this CTA's stretch starts; called by one whole warp.
+template <int M>
 __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status)
 {
     const int lane = threadIdx.x & 31, n = gridDim.x, c = blockIdx.x;
     int pages = 0, groups = 0;
     bool any_bad = false;
-    for (int s = lane; s < p.c.n_seqs; s += 32) {
+    for (int s = lane; s < attn_seqs<M>(p); s += 32) {
         AttnSeq q;
         bool bad;
-        if (attn_seq(p, s, &q, &bad)) {
+        if (attn_seq<M>(p, s, &q, &bad)) {
             const int k = attn_groups(p, q, RT);
             pages += k * q.pages;
             groups += k;
@@ -125,6 +212,10 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, uns
         any_bad |= bad;
     }
     if (any_bad && c == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+    if (M == kAttnOwn && c == 0) {  // the join looks closer then
+        any_bad = __any_sync(0xffffffffu, any_bad);
+        if (lane == 0) p.sh.abort[1] = any_bad;
+    }
     pages = __reduce_add_sync(0xffffffffu, pages);
     groups = __reduce_add_sync(0xffffffffu, groups);
     AttnRange r;
@@ -137,10 +228,10 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, uns
     r.last = c < r.ctas ? r.begin(c + 1) : r.total;
     r.seq = 0, r.seq_first = 0;
     // the sequence that holds unit r.first, 32 at a time
-    for (int s0 = 0; s0 < p.c.n_seqs && r.first < r.last; s0 += 32) {
+    for (int s0 = 0; s0 < attn_seqs<M>(p) && r.first < r.last; s0 += 32) {
         AttnSeq q;
         bool bad;
-        const int mine = s0 + lane < p.c.n_seqs && attn_seq(p, s0 + lane, &q, &bad)
+        const int mine = s0 + lane < attn_seqs<M>(p) && attn_seq<M>(p, s0 + lane, &q, &bad)
                              ? attn_groups(p, q, RT) * (q.pages + r.cost) : 0;
         int incl = mine;
 #pragma unroll
@@ -166,19 +257,21 @@ struct AttnSegment {
     int cta0, n_ctas; // the CTAs that share the group
     int slot0;        // workspace slot of the first of them (the others use 0)
     int slot;         // this CTA's slot
+    int skip;         // kAttnOwn: pages of the table before page 0; kAttnPrefix: number of the group
 };
 
 // The next segment of a CTA's stretch, which starts at unit *at of sequence
 // w->seq or a later one; *at moves past it.  False: there is none.
+template <int M>
 __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange* w, int* at, AttnSegment* g)
 {
     for (int u = *at; u < w->last;) {
         AttnSeq q;
         bool bad;
-        const int units = attn_seq(p, w->seq, &q, &bad) ? attn_groups(p, q, RT) * (q.pages + w->cost) : 0;
+        const int units = attn_seq<M>(p, w->seq, &q, &bad) ? attn_groups(p, q, RT) * (q.pages + w->cost) : 0;
         if (u >= w->seq_first + units) {
             w->seq_first += units;
-            if (++w->seq >= p.c.n_seqs) return false;  // not reached unless the lengths change under the call
+            if (++w->seq >= attn_seqs<M>(p)) return false;  // not reached unless the lengths change under the call
             continue;
         }
         const int blocks = (q.T * p.group + RT - 1) / RT, span = q.pages + w->cost;
@@ -188,7 +281,8 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange
             u = g0 + span;
             continue;
         }
-        g->seq = w->seq;
+        g->seq = q.row;
+        g->skip = M == kAttnPrefix ? w->seq : q.skip;
         g->t0 = q.t0, g->T = q.T, g->ctx = q.ctx;
         g->head = blocks == 1 ? k : k / blocks;
         g->row0 = (k - g->head * blocks) * RT;
@@ -205,6 +299,42 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange
     return false;
 }
 
+// a segment's page numbers; its keys' end
+template <int M>
+__device__ __forceinline__ const int32_t* attn_table(const AttnParams& p, const AttnSegment& g)
+{
+    return p.c.table + int64_t(g.seq) * p.c.table_ld + g.page0 + (M == kAttnOwn ? g.skip : 0);
+}
+template <int M>
+__device__ __forceinline__ int attn_len(const AttnSegment& g)
+{
+    return M == kAttnPrefix ? g.ctx : g.ctx + g.T;
+}
+// whether the segment's rows are left for the join of a prefix and what is behind it
+template <int M>
+__device__ __forceinline__ bool attn_raw(const AttnSegment& g)
+{
+    return M == kAttnPrefix || (M == kAttnOwn && g.skip > 0);
+}
+template <int M>
+__device__ __forceinline__ const AttnRows& attn_rows_of(const AttnParams& p)
+{
+    return M == kAttnPrefix ? p.sh.prefix : p.sh.own;
+}
+// a query row's place among the rows of a call
+__device__ __forceinline__ int64_t attn_place(const AttnParams& p, const AttnSegment& g, int row)
+{
+    const int node = attn_row_token(p, row);
+    return int64_t(g.t0 + node) * p.a.n_heads + (g.head - node) * p.group + row;
+}
+// where the join finds the row block at row0 of group k, whose tokens start at t0: the blocks of a group have numbers
+// of their own, whatever the groups' sizes are
+constexpr int kPrefixRows = 256;  // query rows of a block (attn_tc.cu)
+__device__ __forceinline__ int64_t attn_block(const AttnParams& p, int k, int t0, int row0, int head)
+{
+    return (int64_t(t0) * p.group / kPrefixRows + k + row0 / kPrefixRows) * p.c.n_kv_heads + head;
+}
+
 // A segment's results in the workspace: m[RT], l[RT], then RT rows of D
 // outputs.  A negative l says that there are none, and the group stays
 // unwritten: the segment met a page outside the cache, or its CTA gave up
@@ -217,7 +347,7 @@ constexpr int kAttnSharedBytes = 32;
 __device__ __forceinline__ void attn_shared(const AttnSegment& g, int4 (&s)[2])
 {
     s[0] = make_int4(g.t0, g.T, g.head, g.row0);
-    s[1] = make_int4(g.n_ctas, g.slot0, 0, 0);
+    s[1] = make_int4(g.n_ctas, g.slot0, g.skip, 0);
 }
 
 // a warp writes rows, four values d .. d + 3 per lane (the eight lanes of a block of 32 lie together)
@@ -256,6 +386,19 @@ __device__ __forceinline__ void attn_emit4(const AttnParams& p, const AttnSegmen
     ob[2 + d % 32 / 2] = uint16_t(code >> 16);
 }
 
+// a row's maximum (less the kernel's shift) and sum, and four of its unnormalised outputs, left for the join
+template <int M>
+__device__ __forceinline__ void attn_leave_ml(const AttnParams& p, const AttnSegment& g, int row, float m, float l)
+{
+    attn_rows_of<M>(p).ml[attn_place(p, g, row)] = make_float2(m, l);
+}
+template <int M>
+__device__ __forceinline__ void attn_leave4(const AttnParams& p, const AttnSegment& g, int row, bool there, int D, int d,
+                                            float4 v)
+{
+    if (there) *reinterpret_cast<float4*>(attn_rows_of<M>(p).o + attn_place(p, g, row) * D + d) = v;
+}
+
 // a segment's arrival at its group's counter, which is that of the group's first CTA (a CTA is the first of one
 // shared group at most: the one that reaches past its stretch); true in the CTA that came last
 // (one thread calls it, after the CTA's results are written and synchronised)
@@ -281,9 +424,9 @@ __device__ __forceinline__ bool barrier_any(int id, int n, bool v)
     return r != 0;
 }
 
-// the join behind the kernel that has just been launched
+// a kernel that may start before the one that has just been launched ends
 template <class K>
-cudaError_t attn_launch_join(K kernel, dim3 grid, int threads, size_t smem, const AttnParams& p, unsigned* status,
+cudaError_t attn_launch_pdl(K kernel, dim3 grid, int threads, size_t smem, const AttnParams& p, unsigned* status,
                              cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
@@ -303,5 +446,18 @@ cudaError_t attn_launch_join(K kernel, dim3 grid, int threads, size_t smem, cons
 int attn_tc_rows();
 cudaError_t launch_attn_tc(const mq_kv_cache& cache, const AttnParams& p, int grid, unsigned* status, cudaStream_t s);
 cudaError_t set_attn_tc_attributes();
+// calls with shared prefixes: the sequences' own keys by the kernels for few and for many rows, the prefixes, the join
+cudaError_t launch_attn_own_rows(const mq_kv_cache& cache, const AttnParams& p, int RT, int grid, unsigned* status,
+                                 cudaStream_t s);
+cudaError_t launch_attn_own_tc(const mq_kv_cache& cache, const AttnParams& p, int grid, unsigned* status, cudaStream_t s);
+cudaError_t launch_attn_prefix(const mq_kv_cache& cache, const AttnParams& p, int grid, unsigned* status, cudaStream_t s);
+cudaError_t set_attn_own_rows_attributes();
+cudaError_t set_attn_own_tc_attributes();
+cudaError_t set_attn_prefix_attributes();
+
+// what every attention call puts into its parameters, and where the parts of a workspace lie (attn.cu)
+AttnParams attn_params(const mq_kv_cache& cache, const mq_attn_args& a, void* ws, int num_sms);
+size_t attn_parts_offset(int num_sms);
+int attn_rows_for(int rows);  // query rows of a block of the kernel that takes `rows` per key/value head
 
 }  // namespace mq

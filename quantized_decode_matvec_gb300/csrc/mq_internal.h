@@ -174,6 +174,21 @@ cudaError_t launch_kv_accept(const mq_kv_cache& cache, const int32_t* ctx_len, c
 size_t attn_workspace_bytes(const mq_kv_cache& cache, int n_heads, int max_tokens, int num_sms);
 cudaError_t launch_attn(const mq_kv_cache& cache, const mq_attn_args& a, void* ws, int num_sms, unsigned* status,
                         cudaStream_t s);
+// shared prefixes (attn_shared.cu), probabilities and verification (softmax.cu, verify.cu), pages (pool.cu)
+size_t attn_shared_workspace_bytes(const mq_kv_cache& cache, int n_heads, int64_t n_tokens, int max_tokens,
+                                   int64_t n_groups, int num_sms);
+cudaError_t launch_attn_shared(const mq_kv_cache& cache, const mq_attn_args& a, const mq_attn_groups& g, void* ws,
+                               int num_sms, unsigned* status, cudaStream_t s);
+cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_t x_ld, int64_t y_ld, float scale,
+                           int num_sms, cudaStream_t s);
+cudaError_t launch_verify(const mq_verify_args& a, int num_sms, unsigned* status, cudaStream_t s);
+cudaError_t launch_kv_grow(const mq_kv_cache& cache, const mq_kv_pool& pool, const int32_t* length, unsigned* status,
+                           cudaStream_t s);
+cudaError_t launch_kv_fork(const mq_kv_cache& cache, const mq_kv_pool& pool, const int32_t* src, const int32_t* dst,
+                           const int32_t* length, int n, unsigned* status, cudaStream_t s);
+cudaError_t launch_kv_free(const mq_kv_cache& cache, const mq_kv_pool& pool, const int32_t* seq, const int32_t* keep,
+                           int n, unsigned* status, cudaStream_t s);
+cudaError_t launch_kv_compact(const mq_kv_cache& cache, const mq_kv_pool& pool, int num_sms, cudaStream_t s);
 // looks up the device address of the no-alloc FFN's fixed scratch on device
 // `dev` (current) and caches it
 cudaError_t noalloc_setup(int dev);

@@ -1,0 +1,212 @@
+// softmax.cu -- y = softmax(scale * x) of fp32 rows: the target's probabilities
+// from the logits of every node of a step.
+//
+//   y_i = 2^((x_i - m) k) / sum_j 2^((x_j - m) k),   m = max x,  k = scale * log2(e)
+//
+// Bound by its bytes, so a row passes through the chip once: a cluster of up to
+// eight CTAs holds it in registers.  Each CTA forms its own maximum and, with
+// that, its exponentials and their sum; the (maximum, sum) pairs go round the
+// cluster through distributed shared memory (one barrier), and what is left is a
+// factor per CTA.  Rows longer than eight CTAs hold are read twice.
+// (x - m) k is formed from k in two parts, so the exponent's error is that of
+// x - m alone.  Maxima, exponentials and sums are fp32.
+#include <cooperative_groups.h>
+
+#include <utility>
+
+#include "mq_internal.h"
+
+namespace mq {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
+
+struct SoftmaxArgs {
+    const float* x;
+    float* y;
+    int64_t x_ld, y_ld;
+    int vocab;
+    float k_hi, k_lo;
+};
+
+// 2^(d k); -inf is kept from meeting the two parts' signs, and NaN stays
+__device__ __forceinline__ float exp_of(float d, const SoftmaxArgs& p)
+{
+    d = d < -1e30f ? -1e30f : d;
+    return exp2f(fmaf(d, p.k_hi, d * p.k_lo));
+}
+
+// A larger maximum scales a sum by this; of a part that saw nothing (maximum -inf beside a finite one), 0.
+__device__ __forceinline__ float factor(float m, float top, const SoftmaxArgs& p)
+{
+    return m == top ? 1.0f : exp_of(m - top, p);
+}
+
+// maximum or sum over the CTA
+template <bool Max>
+__device__ __forceinline__ float cta_reduce(float v, float* s)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, o);
+        v = Max ? fmaxf(v, w) : v + w;
+    }
+    if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = s[0];
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) v = Max ? fmaxf(v, s[i]) : v + s[i];
+    return v;
+}
+
+// NV > 0: the CTA's part of the row is up to 4 * NV values per thread, in registers; 0: any length, read twice
+template <int NV>
+__global__ void __launch_bounds__(kThreads) softmax_kernel(const SoftmaxArgs p)
+{
+    __shared__ float max_s[kWarps], sum_s[kWarps];
+    __shared__ float2 part_s[kMaxCluster];  // every CTA's maximum and sum
+    cg::cluster_group cl = cg::this_cluster();
+    auto started = cl.barrier_arrive();  // the others' shared memory is written once they run
+    const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
+    const int64_t row = blockIdx.x / C;
+    const float* const x = p.x + row * p.x_ld;
+    float* const y = p.y + row * p.y_ld;
+    // units of four values that start at 16-byte boundaries of x: unit u holds the values 4u - off .. 4u - off + 3
+    const int off = int(reinterpret_cast<uintptr_t>(x) >> 2) & 3;
+    const int units = int((int64_t(p.vocab) + off + 3) / 4), per = (units + C - 1) / C;
+    const int first = rank * per, last = min(units, first + per);
+    const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(y)) & 15) == 0;
+    auto load = [&](int u, float (&v)[4]) {
+        const int i = 4 * u - off;
+        if (i >= 0 && i <= p.vocab - 4) {
+            const float4 w = __ldcs(reinterpret_cast<const float4*>(x + i));
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = i + e >= 0 && i + e < p.vocab ? x[i + e] : -INFINITY;
+        }
+    };
+    auto store = [&](int u, const float (&v)[4]) {
+        const int i = 4 * u - off;
+        if (same && i >= 0 && i <= p.vocab - 4) {
+            *reinterpret_cast<float4*>(y + i) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e >= 0 && i + e < p.vocab) y[i + e] = v[e];
+        }
+    };
+    float v[NV > 0 ? NV : 1][4];
+    float m = -INFINITY, l = 0.0f;
+    if constexpr (NV > 0) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int u = first + j * kThreads + int(threadIdx.x);
+            if (u < last) {
+                load(u, v[j]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[j][e] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, v[j][e]);
+        m = cta_reduce<true>(m, max_s);
+        // of a part of -inf alone (and of the padding) nothing comes; a row of -inf alone gives NaN below
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[j][e] = exp_of(v[j][e] - base, p);
+                l += v[j][e];
+            }
+    } else {
+        for (int u = first + threadIdx.x; u < last; u += kThreads) {
+            load(u, v[0]);
+            const float top = fmaxf(fmaxf(v[0][0], v[0][1]), fmaxf(v[0][2], v[0][3]));
+            if (top > m) {
+                l *= m == -INFINITY ? 0.0f : exp_of(m - top, p);
+                m = top;
+            }
+            const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l += exp_of(v[0][e] - base, p);
+        }
+        const float top = cta_reduce<true>(m, max_s);
+        l = m == -INFINITY ? l : l * factor(m, top, p);  // (a NaN among -inf stays)
+        m = top;
+    }
+    l = cta_reduce<false>(l, sum_s);
+    cl.barrier_wait(std::move(started));
+    if (int(threadIdx.x) < C) *cl.map_shared_rank(&part_s[rank], threadIdx.x) = make_float2(m, l);
+    cl.sync();
+    float top = -INFINITY, sum = 0.0f;
+    for (int c = 0; c < C; ++c) top = fmaxf(top, part_s[c].x);
+    for (int c = 0; c < C; ++c) sum += part_s[c].y == 0.0f ? 0.0f : part_s[c].y * factor(part_s[c].x, top, p);
+    if constexpr (NV > 0) {
+        // a row of -inf alone: 0 / 0
+        const float f = sum == 0.0f ? 0.0f : m == -INFINITY ? 0.0f : factor(m, top, p), inv = 1.0f / sum;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int u = first + j * kThreads + int(threadIdx.x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[j][e] = v[j][e] * f * inv;
+            if (u < last) store(u, v[j]);
+        }
+    } else {
+        const float inv = 1.0f / sum, base = top == -INFINITY ? 0.0f : top;
+        for (int u = first + threadIdx.x; u < last; u += kThreads) {
+            load(u, v[0]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[0][e] = exp_of(v[0][e] - base, p) * inv;
+            store(u, v[0]);
+        }
+    }
+}
+
+template <int NV>
+cudaError_t launch(const SoftmaxArgs& p, int64_t rows, int C, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(rows * C));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, softmax_kernel<NV>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_t x_ld, int64_t y_ld, float scale,
+                           int num_sms, cudaStream_t s)
+{
+    SoftmaxArgs p = {x, y, x_ld, y_ld, vocab, 0.0f, 0.0f};
+    const double k = double(scale) * 1.4426950408889634074;
+    p.k_hi = float(k);
+    p.k_lo = float(k - double(p.k_hi));
+    // the fewest CTAs that hold a row at 32 values per thread; more while SMs are idle and each has values left
+    const int64_t units = (int64_t(vocab) + 3 + 3) / 4;
+    int C = 1;
+    while (C < kMaxCluster && (units > int64_t(C) * kThreads * 8 || (int64_t(rows) * C * 2 <= num_sms && units > C * kThreads)))
+        C *= 2;
+    const int64_t per = ((units + C - 1) / C + kThreads - 1) / kThreads;  // units of a thread
+    if (per <= 1) return launch<1>(p, rows, C, s);
+    if (per <= 2) return launch<2>(p, rows, C, s);
+    if (per <= 4) return launch<4>(p, rows, C, s);
+    if (per <= 8) return launch<8>(p, rows, C, s);
+    if (per <= 16) return launch<16>(p, rows, C, s);
+    return launch<0>(p, rows, C, s);
+}
+
+}  // namespace mq

@@ -1,0 +1,407 @@
+// verify.cu -- verification of drafted trees against the target's
+// probabilities, from given random numbers (mq_verify_tree).
+//
+// At a node with target row p and draft row q, children x_1, x_2, .. (drawn from
+// q) are tried in order against what the refused ones have left of p:
+//   S_k = (p - a_k q)+,  W_k = sum S_k,   a_0 = 0, W_0 = 1,   a_(k+1) = a_k + W_k
+// (the residual (R_k - q)+ of the normalised R_k = S_k / W_k, scaled by W_k).
+// Child x is accepted where u q(x) W_k < S_k(x); the walk goes on at the first
+// that is.  Where none is, the last S is what the next token is drawn from: the
+// first index at which the running sum of S passes u W.
+//
+// Which token comes out hangs on sums over a vocabulary, so probabilities are
+// summed as integers, in units of 2^-60: exactly, and in any order.  A test of a
+// child is one comparison in 64-bit floating point.
+//
+// A cluster of CTAs per sequence: each takes a contiguous part of the
+// vocabulary, and keeps the sums of its tiles, so that the draw looks into one
+// tile only.  Every CTA walks the tree by itself from the same numbers; they meet
+// where a row's sum is needed, which is once for every refused child, and once
+// more at a node without children.  Bound by those rows' bytes for a batch, and
+// by the chain of loads and barriers for one sequence.
+#include <cooperative_groups.h>
+
+#include "mq_internal.h"
+
+namespace mq {
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxNodes = MQ_TREE_MAX_TOKENS;
+constexpr int kMaxCluster = 8;
+constexpr int kUnit = 512;       // values of a warp's step: 16 per lane
+constexpr int kMaxTiles = 1024;  // of a CTA
+constexpr int kOne = 60;         // 1.0 is 2^60
+constexpr double kInvOne = 1.0 / double(1ull << kOne);
+
+struct VerifyArgs {
+    mq_verify_args a;
+    int chunk, tile;  // values of a CTA (a multiple of tile) and of a tile (a multiple of kUnit)
+    int wide;         // rows may be read 16 bytes at a time
+};
+
+// A probability in units of 2^-60, rounded down; what is not a number above zero is zero, what is above one is one.
+__device__ __forceinline__ uint64_t fixed(float p)
+{
+    if (!(p > 0.0f)) return 0;
+    const uint32_t b = __float_as_uint(fminf(p, 1.0f));
+    const int e = int(b >> 23);  // p = m 2^(e - 150); subnormals are below the unit anyway
+    const uint64_t m = uint64_t((b & 0x7fffffu) | 0x800000u) << (kOne - 23);  // m 2^37, the value at e = 127
+    return 127 - e < 64 ? m >> (127 - e) : 0;
+}
+
+// a * q for a in units of 2^-57 (a < 64) and q in those of 2^-60
+__device__ __forceinline__ uint64_t times(uint64_t a, uint64_t q)
+{
+    return __umul64hi(a, q) << 7 | (a * q) >> 57;
+}
+constexpr uint64_t kAOne = 1ull << 57;
+
+__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ uint64_t warp_max(uint64_t v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = larger(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+struct Shared {
+    int tok[kMaxNodes], par[kMaxNodes];
+    float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];  // p, q: of the node's token at its parent
+    int path[kMaxNodes], gone[kMaxNodes];            // gone: refused tokens of the node at hand (point masses)
+    uint64_t tile[kMaxTiles];
+    uint64_t warp[kWarps];
+    uint64_t total[2];  // read by the whole cluster; of every other pass
+    int found;
+};
+
+// S at one index, in fixed point
+struct Residual {
+    const float* p;
+    const float* q;  // or null
+    uint64_t a;
+    int n_gone;
+    const int* gone;
+    __device__ __forceinline__ uint64_t of(float pv, float qv) const
+    {
+        const uint64_t P = fixed(pv);
+        if (a == 0) return P;
+        const uint64_t Q = a == kAOne ? fixed(qv) : times(a, fixed(qv));
+        return P > Q ? P - Q : 0;
+    }
+    __device__ __forceinline__ uint64_t at(int i) const
+    {
+        for (int k = 0; k < n_gone; ++k)
+            if (gone[k] == i) return 0;
+        return of(__ldg(p + i), a ? __ldg(q + i) : 0.0f);
+    }
+};
+
+// the order of fp32 numbers as unsigned integers (NaN and -inf: 0)
+__device__ __forceinline__ uint32_t ordered(float v)
+{
+    if (!(v > -INFINITY)) return 0;
+    const uint32_t b = __float_as_uint(v);
+    return b == 0x80000000u ? 0x80000000u : b & 0x80000000u ? ~b : b | 0x80000000u;  // -0 is 0
+}
+
+// One pass over the CTA's part of a row: f(index, p, q) of every value, lanes of a warp on neighbouring ones, the
+// tiles of the part going round the warps; done(tile) behind each.
+template <bool Both, class F, class Done>
+__device__ __forceinline__ void walk_row(const VerifyArgs& p, const float* prow, const float* qrow, int first, int last, F f,
+                                         Done done)
+{
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int t = warp; first + t * int64_t(p.tile) < last; t += kWarps) {
+        const int begin = first + t * p.tile, end = last - begin < p.tile ? last : begin + p.tile;
+        for (int i = begin; i < end; i += kUnit) {
+            if (p.wide && end - i >= kUnit) {
+                float4 x[4], y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[j] = __ldg(reinterpret_cast<const float4*>(prow + i + j * 128) + lane);
+                    if (Both) y[j] = __ldg(reinterpret_cast<const float4*>(qrow + i + j * 128) + lane);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = i + j * 128 + lane * 4;
+                    f(k, x[j].x, Both ? y[j].x : 0.0f);
+                    f(k + 1, x[j].y, Both ? y[j].y : 0.0f);
+                    f(k + 2, x[j].z, Both ? y[j].z : 0.0f);
+                    f(k + 3, x[j].w, Both ? y[j].w : 0.0f);
+                }
+            } else {
+                float x[16], y[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int k = i + j * 32 + lane;
+                    x[j] = k < end ? __ldg(prow + k) : 0.0f;
+                    y[j] = Both && k < end ? __ldg(qrow + k) : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (i + j * 32 + lane < end) f(i + j * 32 + lane, x[j], y[j]);
+            }
+        }
+        done(t);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, unsigned* status)
+{
+    __shared__ Shared sm;
+    cg::cluster_group cl = cg::this_cluster();
+    const int C = int(cl.num_blocks()), rank = int(cl.block_rank()), tid = threadIdx.x;
+    const int s = blockIdx.x / C, V = p.a.vocab;
+    const bool greedy = (p.a.flags & MQ_VERIFY_GREEDY) != 0;
+    const int t0 = __ldg(p.a.tok_start + s);
+    const int64_t T64 = int64_t(__ldg(p.a.tok_start + s + 1)) - t0;
+    if (t0 < 0 || T64 < 0 || T64 > kMaxNodes || t0 + T64 > p.a.n_tokens) {  // the same in the whole cluster
+        if (rank == 0 && tid == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+        return;
+    }
+    const int T = int(T64);
+    if (T == 0) {
+        if (rank == 0 && tid == 0) p.a.n_path[s] = 0, p.a.next[s] = -1;
+        return;
+    }
+    if (tid < T) {
+        const int tok = __ldg(p.a.token + t0 + tid), par = __ldg(p.a.parent + t0 + tid);
+        const bool ok = tid > 0 && par >= 0 && par < tid && tok >= 0 && tok < V;
+        if (tid > 0 && !ok && rank == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+        sm.tok[tid] = tok;
+        sm.par[tid] = ok ? par : -1;  // never a child
+        if (!greedy) {
+            sm.u[tid] = __ldg(p.a.u + t0 + tid);
+            sm.p[tid] = ok ? __ldg(p.a.target + (t0 + par) * p.a.target_ld + tok) : 0.0f;
+            sm.q[tid] = ok && p.a.draft ? __ldg(p.a.draft + (t0 + par) * p.a.draft_ld + tok) : 1.0f;
+        }
+    }
+    const int first = int(min(int64_t(rank) * p.chunk, int64_t(V))), last = int(min(int64_t(first) + p.chunk, int64_t(V)));
+    int passes = 0;
+    uint64_t before = 0, mine = 0;  // sums of the parts before the CTA's, and its own, in the last pass
+
+    // every CTA's value to all: the cluster's sum (and what lies before this CTA's part), or maximum
+    auto meet = [&](uint64_t v, bool maximum) {
+        if (tid == 0) sm.total[passes & 1] = v;
+        cl.sync();
+        uint64_t all = 0;
+        before = 0;
+        for (int c = 0; c < C; ++c) {
+            const uint64_t w = *cl.map_shared_rank(&sm.total[passes & 1], c);
+            if (c < rank) before += w;
+            all = maximum ? larger(all, w) : all + w;
+        }
+        mine = v;
+        ++passes;  // the other place next: who still reads this one is waited for there
+        return all;
+    };
+    auto cta_total = [&](uint64_t v, bool maximum) {  // of the warps' values
+        if (tid % 32 == 0) sm.warp[tid / 32] = v;
+        __syncthreads();
+        uint64_t all = 0;
+        for (int i = 0; i < kWarps; ++i)
+            all = maximum ? larger(all, sm.warp[i]) : all + sm.warp[i];
+        return all;
+    };
+    auto mass = [&](const Residual& r) {
+        uint64_t sum = 0, all = 0;
+        auto add = [&](int, float x, float y) { sum += r.of(x, y); };
+        auto done = [&](int t) {
+            sum = warp_sum(sum);
+            if (r.n_gone) {  // refused tokens weigh nothing
+                uint64_t less = 0;
+                const int begin = first + t * p.tile;
+                for (int k = tid % 32; k < r.n_gone; k += 32) {
+                    bool again = false;
+                    for (int j = 0; j < k; ++j) again |= r.gone[j] == r.gone[k];
+                    if (!again && r.gone[k] >= begin && r.gone[k] < last && r.gone[k] - begin < p.tile)
+                        less += r.of(__ldg(r.p + r.gone[k]), 0.0f);
+                }
+                sum -= warp_sum(less);
+            }
+            if (tid % 32 == 0) sm.tile[t] = sum;
+            all += sum;
+            sum = 0;
+        };
+        __syncthreads();  // the tiles and the warps' words of the pass before are read
+        if (r.a)
+            walk_row<true>(p, r.p, r.q, first, last, add, done);
+        else
+            walk_row<false>(p, r.p, r.p, first, last, add, done);
+        return meet(cta_total(all, false), false);
+    };
+    __syncthreads();
+
+    int cur = 0, len = 1, next = -1;
+    if (tid == 0) sm.path[0] = 0;
+    bool owner = rank == 0;  // who writes next
+    for (;;) {
+        const float* const prow = p.a.target + (t0 + int64_t(cur)) * p.a.target_ld;
+        int taken = -1;
+        const bool stop = len >= p.a.path_ld;
+        if (greedy) {
+            uint64_t best = 0;
+            __syncthreads();
+            walk_row<false>(
+                p, prow, prow, first, last,
+                [&](int i, float x, float) {
+                    const uint32_t o = ordered(x);
+                    if (o > uint32_t(best >> 32) || (o && o == uint32_t(best >> 32) && uint32_t(~i) > uint32_t(best)))
+                        best = uint64_t(o) << 32 | uint32_t(~i);
+                },
+                [](int) {});
+            best = meet(cta_total(warp_max(best), true), true);
+            next = best ? int(~uint32_t(best)) : -1;
+            for (int c = cur + 1; c < T && taken < 0 && !stop; ++c)
+                if (sm.par[c] == cur && sm.tok[c] == next) taken = c;
+            if (taken < 0) break;
+        } else {
+            Residual r = {prow, p.a.draft ? p.a.draft + (t0 + int64_t(cur)) * p.a.draft_ld : nullptr, 0, 0, sm.gone};
+            double a = 0.0, W = 1.0;
+            uint64_t mass_fixed = 0;
+            bool known = false;  // mass_fixed and the tiles are of r as it stands
+            for (int c = cur + 1; c < T && !stop; ++c) {
+                if (sm.par[c] != cur) continue;
+                const int x = sm.tok[c];
+                double S = double(sm.p[c]) - a * double(sm.q[c]);
+                if (!r.q)
+                    for (int k = 0; k < r.n_gone; ++k)
+                        if (sm.gone[k] == x) S = 0.0;
+                if (S > 0.0 && double(sm.u[c]) * double(sm.q[c]) * W < S) {
+                    taken = c;
+                    break;
+                }
+                if (r.q) {
+                    if (known && mass_fixed == 0) continue;  // nothing is left to accept, or to take away
+                    r.a = known ? r.a + (mass_fixed >> 3) : kAOne;
+                    a += W;
+                    mass_fixed = mass(r);
+                    W = double(mass_fixed) * kInvOne;
+                    known = true;
+                } else {
+                    W -= S > 0.0 ? S : 0.0;
+                    __syncthreads();
+                    if (tid == 0) sm.gone[r.n_gone] = x;
+                    __syncthreads();
+                    ++r.n_gone;
+                }
+            }
+            if (taken < 0) {
+                if (!known) mass_fixed = mass(r);
+                if (mass_fixed == 0 && (r.a || r.n_gone)) {  // the target's row itself where the residual is empty
+                    r.a = 0, r.n_gone = 0;
+                    mass_fixed = mass(r);
+                }
+                if (mass_fixed == 0) break;
+                // the first index whose running sum passes u W
+                const uint64_t u = fixed(sm.u[0]), U = u < (1ull << kOne) ? u : (1ull << kOne) - 1;
+                const uint64_t mark = __umul64hi(U << 4, mass_fixed);
+                owner = mark >= before && mark - before < mine;
+                if (owner) {
+                    uint64_t at = before;
+                    if (tid < 32) {
+                        // the tile, 32 at a time, then 32 runs of 16 of each of its units
+                        const int tiles = (last - first + p.tile - 1) / p.tile;
+                        int t = -1;
+                        for (int b = 0; b < tiles && t < 0; b += 32) {
+                            uint64_t incl = b + tid < tiles ? sm.tile[b + tid] : 0;
+                            const uint64_t own = incl;
+#pragma unroll
+                            for (int o = 1; o < 32; o <<= 1) {
+                                const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                                if (tid >= o) incl += v;
+                            }
+                            const unsigned past = __ballot_sync(0xffffffffu, at + incl > mark);
+                            const int l = past ? __ffs(past) - 1 : 31;
+                            at += __shfl_sync(0xffffffffu, past ? incl - own : incl, l);
+                            if (past) t = b + l;
+                        }
+                        const int begin = first + t * p.tile, end = last - begin < p.tile ? last : begin + p.tile;
+                        for (int i = begin; i < end; i += kUnit) {
+                            uint64_t own = 0;
+                            for (int j = 0; j < 16; ++j)
+                                if (i + tid * 16 + j < end) own += r.at(i + tid * 16 + j);
+                            uint64_t incl = own;
+#pragma unroll
+                            for (int o = 1; o < 32; o <<= 1) {
+                                const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                                if (tid >= o) incl += v;
+                            }
+                            const unsigned past = __ballot_sync(0xffffffffu, at + incl > mark);
+                            if (!past) {
+                                at += __shfl_sync(0xffffffffu, incl, 31);
+                                continue;
+                            }
+                            if (tid == __ffs(past) - 1) {
+                                uint64_t c = at + incl - own;
+                                for (int j = 0; j < 16; ++j) {
+                                    if (i + tid * 16 + j >= end) break;
+                                    c += r.at(i + tid * 16 + j);
+                                    if (c > mark) {
+                                        sm.found = i + tid * 16 + j;
+                                        break;
+                                    }
+                                }
+                            }
+                            break;
+                        }
+                    }
+                    __syncthreads();
+                    next = sm.found;
+                }
+                break;
+            }
+        }
+        cur = taken;
+        if (tid == 0) sm.path[len] = cur;
+        ++len;
+    }
+    __syncthreads();
+    if (rank == 0) {
+        if (tid < len) p.a.path[int64_t(s) * p.a.path_ld + tid] = sm.path[tid];
+        if (tid == 0) p.a.n_path[s] = len;
+    }
+    if (owner && tid == 0) p.a.next[s] = next;
+    cl.sync();  // what the others still read of this CTA's shared memory
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const mq_verify_args& a, int num_sms, unsigned* status, cudaStream_t s)
+{
+    VerifyArgs p;
+    p.a = a;
+    p.wide = (reinterpret_cast<uintptr_t>(a.target) & 15) == 0 && a.target_ld % 4 == 0 &&
+             (!a.draft || ((reinterpret_cast<uintptr_t>(a.draft) & 15) == 0 && a.draft_ld % 4 == 0));
+    int C = kMaxCluster;
+    while (C > 1 && a.vocab <= (C / 2) * kUnit * 4) C /= 2;  // at least four steps of a warp each
+    (void)num_sms;
+    const int64_t part = (int64_t(a.vocab) + C - 1) / C;
+    const int64_t units = (part + kUnit - 1) / kUnit;
+    p.tile = int((units + kMaxTiles - 1) / kMaxTiles) * kUnit;
+    p.chunk = int((part + p.tile - 1) / p.tile) * p.tile;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(a.n_seqs) * C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, verify_kernel, p, status);
+}
+
+}  // namespace mq

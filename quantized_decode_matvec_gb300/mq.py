@@ -42,6 +42,7 @@ MQ_DEV_DESC_ALIGN = 2
 MQ_DEV_TIMEOUT = 4
 MQ_DEV_ALIAS = 8
 MQ_DEV_KV_RANGE = 16
+MQ_DEV_KV_FULL = 32
 MQ_VARIANT_AUTO = 0
 MQ_VARIANT_FORCE_REGISTER = 1
 MQ_FAULT_NONE = 0
@@ -64,6 +65,8 @@ MQ_MMQ_MAX_NCOLS = 64
 MQ_KV_PAGE_TOKENS = 64
 MQ_TREE_MAX_TOKENS = 64
 MQ_ROPE_INTERLEAVED = 1
+MQ_MAX_SEQS = 4096
+MQ_VERIFY_GREEDY = 1
 MQ_PLAN_MATVEC = 0
 MQ_PLAN_DOWN = 1
 MQ_PLAN_GATE_UP = 2
@@ -109,6 +112,21 @@ class AttnArgs(ctypes.Structure):
                 ("max_tokens", c_i32), ("out_type", c_i32), ("scale", ctypes.c_float)]
 
 
+class AttnGroups(ctypes.Structure):
+    _fields_ = [("grp_start", c_vp), ("grp_pages", c_vp), ("n_groups", c_i32), ("max_pages", c_i32)]
+
+
+class VerifyArgs(ctypes.Structure):
+    _fields_ = [("target", c_vp), ("draft", c_vp), ("tok_start", c_vp), ("token", c_vp), ("parent", c_vp), ("u", c_vp),
+                ("path", c_vp), ("n_path", c_vp), ("next", c_vp), ("target_ld", c_i64), ("draft_ld", c_i64),
+                ("n_tokens", c_i32), ("n_seqs", c_i32), ("vocab", c_i32), ("path_ld", c_i32), ("flags", c_u32),
+                ("reserved", c_i32)]
+
+
+class KvPoolStruct(ctypes.Structure):
+    _fields_ = [("refs", c_vp), ("free_list", c_vp), ("n_free", c_vp), ("seq_pages", c_vp), ("scratch", c_vp)]
+
+
 def _sig(name, res, *args):
     f = getattr(_lib, name)
     f.restype = res
@@ -151,6 +169,17 @@ _sig("mq_kv_read", c_i32, ctypes.POINTER(KvCacheStruct), c_vp, c_vp, c_i32, c_vp
 _sig("mq_kv_accept", c_i32, ctypes.POINTER(KvCacheStruct), c_vp, c_vp, c_vp, c_i32, c_vp)
 _sig("mq_attn_workspace_bytes", c_i32, ctypes.POINTER(KvCacheStruct), c_i32, c_i32, ctypes.POINTER(ctypes.c_size_t))
 _sig("mq_attn_tree", c_i32, ctypes.POINTER(KvCacheStruct), ctypes.POINTER(AttnArgs), c_vp, ctypes.c_size_t, c_vp)
+_sig("mq_attn_shared_workspace_bytes", c_i32, ctypes.POINTER(KvCacheStruct), c_i32, c_i32, c_i32, c_i32,
+     ctypes.POINTER(ctypes.c_size_t))
+_sig("mq_attn_shared", c_i32, ctypes.POINTER(KvCacheStruct), ctypes.POINTER(AttnArgs), ctypes.POINTER(AttnGroups), c_vp,
+     ctypes.c_size_t, c_vp)
+_sig("mq_softmax", c_i32, c_vp, c_vp, c_i32, c_i32, c_i64, c_i64, ctypes.c_float, c_vp)
+_sig("mq_verify_tree", c_i32, ctypes.POINTER(VerifyArgs), c_vp)
+_sig("mq_kv_pool_scratch", c_i64, ctypes.POINTER(KvCacheStruct))
+_sig("mq_kv_grow", c_i32, ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvPoolStruct), c_vp, c_vp)
+_sig("mq_kv_fork", c_i32, ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvPoolStruct), c_vp, c_vp, c_vp, c_i32, c_vp)
+_sig("mq_kv_free", c_i32, ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvPoolStruct), c_vp, c_vp, c_i32, c_vp)
+_sig("mq_kv_compact", c_i32, ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvPoolStruct), c_vp)
 _sig("mq_debug_block_sums_q4K_q8_0", c_i32, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp)
 _sig("mq_debug_set_variant", c_i32, c_i32)
 _sig("mq_debug_set_fault", c_i32, c_i32)
@@ -166,6 +195,8 @@ EXPORTS = ["mq_status_string", "mq_abi_version", "mq_last_cuda_error", "mq_init"
            "mq_mmq_workspace_bytes", "mq_mmq_q4K_q8_0",
            "mq_kv_page_bytes", "mq_check_kv_cache", "mq_kv_append", "mq_kv_read", "mq_kv_accept",
            "mq_attn_workspace_bytes", "mq_attn_tree",
+           "mq_attn_shared_workspace_bytes", "mq_attn_shared", "mq_softmax", "mq_verify_tree", "mq_kv_pool_scratch",
+           "mq_kv_grow", "mq_kv_fork", "mq_kv_free", "mq_kv_compact",
            "mq_debug_block_sums_q4K_q8_0", "mq_debug_set_variant", "mq_debug_set_fault", "mq_debug_plan_mv",
            "mq_debug_plan_step"]
 
@@ -338,6 +369,46 @@ def mq_attn_workspace_bytes(cache: KvCacheStruct, n_heads: int, max_tokens: int)
 
 def mq_attn_tree(cache: KvCacheStruct, args: AttnArgs, workspace: int, ws_bytes: int, stream: int = 0) -> int:
     return _lib.mq_attn_tree(cache, args, workspace, ws_bytes, stream)
+
+
+def mq_attn_shared_workspace_bytes(cache: KvCacheStruct, n_heads: int, n_tokens: int, max_tokens: int, n_groups: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.mq_attn_shared_workspace_bytes(cache, n_heads, n_tokens, max_tokens, n_groups, ctypes.byref(n)),
+           "mq_attn_shared_workspace_bytes")
+    return n.value
+
+
+def mq_attn_shared(cache: KvCacheStruct, args: AttnArgs, groups: AttnGroups, workspace: int, ws_bytes: int,
+                   stream: int = 0) -> int:
+    return _lib.mq_attn_shared(cache, args, groups, workspace, ws_bytes, stream)
+
+
+def mq_softmax(x: int, y: int, rows: int, vocab: int, x_ld: int, y_ld: int, scale: float, stream: int = 0) -> int:
+    return _lib.mq_softmax(x, y, rows, vocab, x_ld, y_ld, scale, stream)
+
+
+def mq_verify_tree(args: VerifyArgs, stream: int = 0) -> int:
+    return _lib.mq_verify_tree(args, stream)
+
+
+def mq_kv_pool_scratch(cache: KvCacheStruct) -> int:
+    return _lib.mq_kv_pool_scratch(cache)
+
+
+def mq_kv_grow(cache: KvCacheStruct, pool: KvPoolStruct, length: int, stream: int = 0) -> int:
+    return _lib.mq_kv_grow(cache, pool, length, stream)
+
+
+def mq_kv_fork(cache: KvCacheStruct, pool: KvPoolStruct, src: int, dst: int, length: int, n: int, stream: int = 0) -> int:
+    return _lib.mq_kv_fork(cache, pool, src, dst, length, n, stream)
+
+
+def mq_kv_free(cache: KvCacheStruct, pool: KvPoolStruct, seq: int, keep: int, n: int, stream: int = 0) -> int:
+    return _lib.mq_kv_free(cache, pool, seq, keep, n, stream)
+
+
+def mq_kv_compact(cache: KvCacheStruct, pool: KvPoolStruct, stream: int = 0) -> int:
+    return _lib.mq_kv_compact(cache, pool, stream)
 
 
 def mq_debug_block_sums_q4K_q8_0(d_desc: int, rows: int, K: int, ncols: int, sumi: int, sumq: int,
@@ -640,18 +711,18 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _stream_on(stream, device) -> int:
+def _stream_on(stream, device, what: str = "the cache is") -> int:
     """The stream handle of a call on ``device`` (None: torch's current stream there).  The library launches on the
     current CUDA device, so a call whose memory is anywhere else is refused."""
     torch = _torch()
     if device.type != "cuda" or torch.cuda.current_device() != device.index:
-        raise ValueError(f"the cache is on {device}: the current CUDA device is wanted")
+        raise ValueError(f"{what} on {device}: the current CUDA device is wanted")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
     if isinstance(stream, int):
         return stream
     if stream.device != device:
-        raise ValueError(f"a stream of {stream.device}, the cache is on {device}")
+        raise ValueError(f"a stream of {stream.device}, {what} on {device}")
     return stream.cuda_stream
 
 
@@ -757,16 +828,8 @@ def attn_workspace(cache: KVCache, n_heads: int, max_tokens: int = MQ_TREE_MAX_T
         return out.zero_()
 
 
-def attn_tree(cache: KVCache, q, tok_start, ctx_len, mask=None, scale: Optional[float] = None,
-              max_len: Optional[int] = None, max_tokens: int = MQ_TREE_MAX_TOKENS, out_type: str = "f16", out=None,
-              workspace=None, stream=None):
-    """Attention of every tree's nodes (q: f16 [n, n_heads * head_dim], rows may be strided) over the cache.
-
-    ``mask``: int64 [n], bit j = node j of the token's tree is seen (None: a chain).  ``max_len`` bounds context plus
-    tree of any sequence (default: what the table can hold).  ``max_tokens`` bounds the tokens of any sequence, picks the
-    kernel and sizes the workspace: a decode step says 1, with the default it takes the kernel for large trees.  Returns
-    f16 [n, n_heads * head_dim], or with ``out_type="q8_0"`` uint8 [n, n_heads * head_dim / 32 * 34], the ``xq`` of a
-    projection.  A program that calls this every step keeps the workspace (attn_workspace)."""
+def _attn_args(cache: KVCache, q, tok_start, ctx_len, mask, scale, max_len, max_tokens, out_type, out, stream):
+    """The arguments that attn_tree and attn_shared have in common, and the output tensor."""
     torch = _torch()
     dev, D, S, i32 = cache.device, cache.head_dim, cache.n_seqs, torch.int32
     if q.dim() != 2 or q.shape[1] % D:
@@ -791,13 +854,181 @@ def attn_tree(cache: KVCache, q, tok_start, ctx_len, mask=None, scale: Optional[
     a = AttnArgs(qp, op, _want(tok_start, "tok_start", i32, (S + 1,), dev), _want(ctx_len, "ctx_len", i32, (S,), dev),
                  None if mask is None else _want(mask, "mask", torch.int64, (n,), dev), q_ld, out_ld, n, width // D,
                  max_len, max_tokens, kind, D ** -0.5 if scale is None else scale)
+    return a, out
+
+
+def attn_tree(cache: KVCache, q, tok_start, ctx_len, mask=None, scale: Optional[float] = None,
+              max_len: Optional[int] = None, max_tokens: int = MQ_TREE_MAX_TOKENS, out_type: str = "f16", out=None,
+              workspace=None, stream=None):
+    """Attention of every tree's nodes (q: f16 [n, n_heads * head_dim], rows may be strided) over the cache.
+
+    ``mask``: int64 [n], bit j = node j of the token's tree is seen (None: a chain).  ``max_len`` bounds context plus
+    tree of any sequence (default: what the table can hold).  ``max_tokens`` bounds the tokens of any sequence, picks the
+    kernel and sizes the workspace: a decode step says 1, with the default it takes the kernel for large trees.  Returns
+    f16 [n, n_heads * head_dim], or with ``out_type="q8_0"`` uint8 [n, n_heads * head_dim / 32 * 34], the ``xq`` of a
+    projection.  A program that calls this every step keeps the workspace (attn_workspace)."""
+    a, out = _attn_args(cache, q, tok_start, ctx_len, mask, scale, max_len, max_tokens, out_type, out, stream)
     if workspace is None:
-        workspace = attn_workspace(cache, width // D, max_tokens, stream)
-    st = _lib.mq_attn_tree(cache.struct, a, _want(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
-                           _stream_on(stream, dev))
+        workspace = attn_workspace(cache, a.n_heads, max_tokens, stream)
+    st = _lib.mq_attn_tree(cache.struct, a, _want(workspace, "workspace", _torch().uint8, None, cache.device),
+                           workspace.numel(), _stream_on(stream, cache.device))
     if st:
         raise MQError(st, "mq_attn_tree")
     return out
+
+
+def attn_shared_workspace(cache: KVCache, n_heads: int, n_tokens: int, n_groups: int, max_tokens: int = MQ_TREE_MAX_TOKENS,
+                          stream=None):
+    """A zeroed workspace for attn_shared calls with up to n_tokens tokens in all, n_groups groups and max_tokens tokens
+    per sequence (one per stream that runs them).  It serves any call whose workspace is no larger."""
+    torch = _torch()
+    handle = _stream_on(stream, cache.device)  # before the size, which goes by the current device
+    out = _new(mq_attn_shared_workspace_bytes(cache.struct, n_heads, n_tokens, max_tokens, n_groups), torch.uint8,
+               cache.device, stream)
+    with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(handle, device=cache.device)):
+        return out.zero_()
+
+
+def attn_shared(cache: KVCache, q, tok_start, ctx_len, grp_start, grp_pages, mask=None, scale: Optional[float] = None,
+                max_len: Optional[int] = None, max_tokens: int = MQ_TREE_MAX_TOKENS, max_pages: Optional[int] = None,
+                out_type: str = "f16", out=None, workspace=None, stream=None):
+    """attn_tree of a batch whose sequences share the pages of a prefix, each prefix attended once for all.
+
+    ``grp_start``: int32 [n_groups + 1], group g are the sequences grp_start[g]..grp_start[g + 1] - 1; ``grp_pages``:
+    int32 [n_groups], the pages at the start of their table rows that are the same for all of them (every context
+    reaches past them).  ``max_pages`` bounds grp_pages (default: what the table can hold).  The rest is attn_tree's;
+    the workspace is attn_shared_workspace's."""
+    i32, dev = _torch().int32, cache.device
+    a, out = _attn_args(cache, q, tok_start, ctx_len, mask, scale, max_len, max_tokens, out_type, out, stream)
+    n = grp_pages.numel()
+    g = AttnGroups(_want(grp_start, "grp_start", i32, (n + 1,), dev), _want(grp_pages, "grp_pages", i32, (n,), dev), n,
+                   cache.table.shape[1] if max_pages is None else max_pages)
+    if workspace is None:
+        workspace = attn_shared_workspace(cache, a.n_heads, a.n_tokens, n, max_tokens, stream)
+    st = _lib.mq_attn_shared(cache.struct, a, g, _want(workspace, "workspace", _torch().uint8, None, dev),
+                             workspace.numel(), _stream_on(stream, dev))
+    if st:
+        raise MQError(st, "mq_attn_shared")
+    return out
+
+
+def softmax(x, scale: float = 1.0, out=None, stream=None):
+    """exp(scale * x) / sum of it, along the rows of x (fp32 [n, vocab], rows may be strided); ``out`` may be x."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError(f"x: a 2-D tensor is wanted, got {tuple(x.shape)}")
+    n, vocab = x.shape
+    xp, x_ld = _rows(x, "x", torch.float32, x.device, vocab)
+    handle = _stream_on(stream, x.device, "x is")
+    if out is None:
+        out = _new((n, vocab), torch.float32, x.device, stream)
+    yp, y_ld = _rows(out, "out", torch.float32, x.device, vocab, n)
+    st = _lib.mq_softmax(xp, yp, n, vocab, x_ld, y_ld, scale, handle)
+    if st:
+        raise MQError(st, "mq_softmax")
+    return out
+
+
+def verify_tree(target, tok_start, token, parent, u=None, draft=None, greedy: bool = False, path_ld: Optional[int] = None,
+                path=None, n_path=None, next_token=None, stream=None):
+    """Verify drafted trees: (path int32 [n_seqs, path_ld], n_path int32 [n_seqs], next int32 [n_seqs]).
+
+    ``target``: fp32 [n, vocab], the target's probabilities behind every node (mq.softmax of the logits); ``draft``: fp32
+    [n, vocab], those that a node's children were drawn from (None: the drafts are looked up, not drawn).  ``token`` and
+    ``parent``: int32 [n], the drafted tokens and their parents' numbers in the tree (node 0, the root, is the token
+    that the step before ended with).  ``u``: fp32 [n] in [0, 1), a root's is what ``next`` is drawn with.  ``greedy``:
+    the largest target value instead of a draw (target may be logits; u and draft are not read).  ``path_ld`` bounds
+    the nodes of a path, the root included.  path and n_path are what kv_accept takes; of a new ``path`` the entries
+    behind n_path are zero, of one that is given they stay as they were."""
+    torch = _torch()
+    dev, i32, f32 = target.device, torch.int32, torch.float32
+    if target.dim() != 2:
+        raise ValueError(f"target: a 2-D tensor is wanted, got {tuple(target.shape)}")
+    n, vocab = target.shape
+    S = tok_start.numel() - 1
+    if S < 0:
+        raise ValueError("tok_start: n_seqs + 1 values are wanted")
+    handle = _stream_on(stream, dev, "target is")
+    tp, t_ld = _rows(target, "target", f32, dev, vocab)
+    dp, d_ld = (None, 0) if draft is None or greedy else _rows(draft, "draft", f32, dev, vocab, n)
+    if u is None and not greedy:
+        raise ValueError("u: random numbers are wanted (or greedy)")
+    if path is None:
+        path_ld = MQ_TREE_MAX_TOKENS if path_ld is None else path_ld
+        with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(handle, device=dev)):
+            path = torch.zeros((S, path_ld), dtype=i32, device=dev)
+    elif path.dim() != 2 or path_ld not in (None, path.shape[1]):
+        raise ValueError(f"path: [{S}, path_ld] is wanted, got {tuple(path.shape)}")
+    n_path = _new((S,), i32, dev, stream) if n_path is None else n_path
+    next_token = _new((S,), i32, dev, stream) if next_token is None else next_token
+    a = VerifyArgs(tp, dp, _want(tok_start, "tok_start", i32, (S + 1,), dev), _want(token, "token", i32, (n,), dev),
+                   _want(parent, "parent", i32, (n,), dev), None if u is None else _want(u, "u", f32, (n,), dev),
+                   _want(path, "path", i32, (S, path.shape[1]), dev), _want(n_path, "n_path", i32, (S,), dev),
+                   _want(next_token, "next_token", i32, (S,), dev), t_ld, d_ld, n, S, vocab, path.shape[1],
+                   MQ_VERIFY_GREEDY if greedy else 0, 0)
+    st = _lib.mq_verify_tree(a, handle)
+    if st:
+        raise MQError(st, "mq_verify_tree")
+    return path, n_path, next_token
+
+
+class KVPool:
+    """A cache's pages as a pool (mq_kv_pool), for kv_grow, kv_fork, kv_free and kv_compact, which keep its tensors and
+    the cache's table.  ``seq_pages``: int32 [n_seqs], pages of every sequence; ``refs``: int32 [n_pages], table entries
+    that name a page; ``free_list``: int32 [n_pages], of which the first ``n_free`` (int32 [1]) are the free pages, the
+    last of them the next to be taken."""
+
+    def __init__(self, cache: KVCache, seq_pages, refs, free_list, n_free):
+        torch = _torch()
+        i32, dev, P = torch.int32, cache.device, cache.struct.n_pages
+        self.seq_pages, self.refs, self.free_list, self.n_free = seq_pages, refs, free_list, n_free
+        self.scratch = torch.empty(mq_kv_pool_scratch(cache.struct), dtype=i32, device=dev)
+        self.struct = KvPoolStruct(_want(refs, "refs", i32, (P,), dev), _want(free_list, "free_list", i32, (P,), dev),
+                                   _want(n_free, "n_free", i32, (1,), dev),
+                                   _want(seq_pages, "seq_pages", i32, (cache.n_seqs,), dev), self.scratch.data_ptr())
+
+    @classmethod
+    def alloc(cls, cache: KVCache) -> "KVPool":
+        """A pool with every page of the cache free, the lowest taken first; the table is emptied."""
+        torch = _torch()
+        i32, dev, P = torch.int32, cache.device, cache.struct.n_pages
+        cache.table.fill_(-1)
+        return cls(cache, torch.zeros(cache.n_seqs, dtype=i32, device=dev), torch.zeros(P, dtype=i32, device=dev),
+                   torch.arange(P - 1, -1, -1, dtype=i32, device=dev), torch.full((1,), P, dtype=i32, device=dev))
+
+
+def kv_grow(cache: KVCache, pool: KVPool, length, stream=None) -> None:
+    """Give every sequence the pages that length[s] tokens need (int32 [n_seqs]); none loses one."""
+    st = _lib.mq_kv_grow(cache.struct, pool.struct, _want(length, "length", _torch().int32, (cache.n_seqs,), cache.device),
+                         _stream_on(stream, cache.device))
+    if st:
+        raise MQError(st, "mq_kv_grow")
+
+
+def kv_fork(cache: KVCache, pool: KVPool, src, dst, length, stream=None) -> None:
+    """Sequence dst[i] (without pages) continues the first length[i] tokens of src[i]: full pages are shared, the
+    tokens of a begun one are copied."""
+    i32, dev, n = _torch().int32, cache.device, src.numel()
+    st = _lib.mq_kv_fork(cache.struct, pool.struct, _want(src, "src", i32, (n,), dev), _want(dst, "dst", i32, (n,), dev),
+                         _want(length, "length", i32, (n,), dev), n, _stream_on(stream, dev))
+    if st:
+        raise MQError(st, "mq_kv_fork")
+
+
+def kv_free(cache: KVCache, pool: KVPool, seq, keep=None, stream=None) -> None:
+    """Sequences seq[i] give up their pages but the first keep[i] (None: all)."""
+    i32, dev, n = _torch().int32, cache.device, seq.numel()
+    st = _lib.mq_kv_free(cache.struct, pool.struct, _want(seq, "seq", i32, (n,), dev),
+                         None if keep is None else _want(keep, "keep", i32, (n,), dev), n, _stream_on(stream, dev))
+    if st:
+        raise MQError(st, "mq_kv_free")
+
+
+def kv_compact(cache: KVCache, pool: KVPool, stream=None) -> None:
+    """Move the pages in use to the front of the pool; the table, the counts and the free pages follow."""
+    st = _lib.mq_kv_compact(cache.struct, pool.struct, _stream_on(stream, cache.device))
+    if st:
+        raise MQError(st, "mq_kv_compact")
 
 
 class StepBuffers:

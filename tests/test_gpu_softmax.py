@@ -1,0 +1,99 @@
+"""softmax of rows against 64 bits.
+
+Bound, relative to the reference: an exponent is (x - m) k with x - m rounded once and the product once (2^-24 each of
+|x - max| scale, as a relative error of the exponential), twice where a CTA's own maximum stands between; exp2f and
+three products 2^-21; the sum of up to 64 values per thread, then of 5 + 16 + 8 levels, 2^-17.  2^-126 absolute, where
+the factors are below the normal range.
+"""
+import numpy as np
+import pytest
+
+from tests.test_gpu_kv import dev, ok_status
+
+pytestmark = pytest.mark.gpu
+
+
+def check(got, x, scale):
+    z = x.astype(np.float64) * np.float64(np.float32(scale))
+    d = z - z.max(-1, keepdims=True)
+    e = np.exp(d)
+    ref = e / e.sum(-1, keepdims=True)
+    with np.errstate(invalid="ignore"):
+        tol = np.where(e > 0, ref * (2**-17 + 2**-21 + 2**-22 * np.abs(d)), 0) + 2.0**-126
+    err = np.abs(got - ref)
+    assert (err <= tol).all(), (float((err / tol).max()), np.argwhere(err > tol)[:3])
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 1), (3, 2), (2, 31), (5, 32), (1, 2047), (1, 2048), (4, 2049), (200, 1000),
+                                        (7, 50001), (2, 131072), (1, 131071), (3, 200003), (1, 262144), (2, 300001),
+                                        (1, 1000003)])
+def test_sizes(cuda_ready, rows, vocab):
+    rng = np.random.default_rng(vocab)
+    x = (rng.standard_normal((rows, vocab)) * 4).astype(np.float32)
+    x[rng.random(x.shape) < 0.001] += 30
+    for scale in (1.0, 0.3, 2.5):
+        got = cuda_ready.softmax(dev(x), scale=scale)
+        ok_status(cuda_ready)
+        check(got.cpu().numpy().astype(np.float64), x, scale)
+
+
+@pytest.mark.parametrize("vocab", [1001, 70003, 300001])
+def test_strides_offsets_and_in_place(cuda_ready, vocab):
+    import torch
+    mq = cuda_ready
+    rng = np.random.default_rng(3)
+    full = (rng.standard_normal((4, vocab + 9)) * 3).astype(np.float32)
+    for x0 in range(4):
+        for y0 in (0, 1):
+            src, out = dev(full), torch.full((4, vocab + 7), -1.0, device="cuda")
+            mq.softmax(src[:, x0:x0 + vocab], out=out[:, y0:y0 + vocab])
+            ok_status(mq)
+            check(out[:, y0:y0 + vocab].cpu().numpy().astype(np.float64), full[:, x0:x0 + vocab], 1.0)
+            assert (out[:, :y0] == -1).all() and (out[:, y0 + vocab:] == -1).all()
+            same = src[:, x0:x0 + vocab]
+            mq.softmax(same, out=same)
+            ok_status(mq)
+            check(same.cpu().numpy().astype(np.float64), full[:, x0:x0 + vocab], 1.0)
+            assert np.array_equal(src.cpu().numpy()[:, x0 + vocab:], full[:, x0 + vocab:])
+
+
+@pytest.mark.parametrize("vocab", [5, 9000, 131072, 300001])
+def test_infinities_and_nan(cuda_ready, vocab):
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((8, vocab)).astype(np.float32)
+    x[0, :-1] = -np.inf                       # one value left
+    x[1, rng.random(vocab) < 0.9] = -np.inf   # a mask
+    x[1, 0] = 0.5
+    x[2] = -np.inf
+    x[3, 2] = np.inf
+    x[4, 3] = np.nan
+    x[5, :vocab // 2 + 1] = -np.inf           # whole parts of the row
+    x[6] = -3e38                              # the type's lowest values
+    x[6, 1] = -1e38
+    x[7, 4] = np.nan
+    x[7, 5:] = -np.inf
+    got = cuda_ready.softmax(dev(x), scale=1.0).cpu().numpy().astype(np.float64)
+    ok_status(cuda_ready)
+    fine = [0, 1, 5, 6] if vocab > 5 else [0, 1, 6]
+    check(got[fine], x[fine], 1.0)
+    assert got[0, -1] == 1.0 and got[6, 1] == 1.0
+    assert np.isnan(got[[2, 3, 4, 7]]).all()
+
+
+def test_captured_and_replayed(cuda_ready):
+    import torch
+    mq = cuda_ready
+    x, y = torch.randn((3, 40000), device="cuda"), torch.empty((3, 40000), device="cuda")
+    side = torch.cuda.Stream()
+    mq.softmax(x, out=y, stream=side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        mq.softmax(x, out=y, stream=side)
+    for _ in range(3):
+        x.normal_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, mq.softmax(x))
+    ok_status(mq)
