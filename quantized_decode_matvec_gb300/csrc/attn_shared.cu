@@ -71,13 +71,19 @@ cudaError_t launch_attn_shared(const mq_kv_cache& cache, const mq_attn_args& a, 
     const int64_t most = int64_t(cache.n_seqs) * ((int64_t(a.max_len) + kKvPage - 1) / kKvPage) * cache.n_kv_heads *
                          ((rows + RT - 1) / RT);
     const int grid = int(most < 1 ? 1 : most < num_sms ? most : num_sms);
+    const int64_t blocks = int64_t(a.n_tokens) * p.group / kPrefixRows + g.n_groups;
+    const int64_t units = blocks * cache.n_kv_heads * g.max_pages;
+    const int prefix_grid = int(units < num_sms ? units : num_sms);
+    p.sh.sms = num_sms, p.sh.prefix_grid = prefix_grid, p.sh.own_rows = RT;
     cudaError_t e = RT > 16 ? launch_attn_own_tc(cache, p, grid, status, s)
                             : launch_attn_own_rows(cache, p, RT, grid, status, s);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = int64_t(a.n_tokens) * p.group / kPrefixRows + g.n_groups;
-    const int64_t units = blocks * cache.n_kv_heads * g.max_pages;
-    p.parts = reinterpret_cast<float*>(w + at.parts);
-    return launch_attn_prefix(cache, p, int(units < num_sms ? units : num_sms), status, s);
+    AttnParams pre = p;
+    pre.parts = reinterpret_cast<float*>(w + at.parts);
+    if ((e = launch_attn_prefix(cache, pre, prefix_grid, status, s)) != cudaSuccess) return e;
+    e = RT > 16 ? launch_attn_own_tc_join(cache, p, grid, status, s)
+                : launch_attn_own_rows_join(cache, p, RT, grid, status, s);
+    return e != cudaSuccess ? e : launch_attn_shared_join(cache, pre, status, s);
 }
 
 cudaError_t set_attn_shared_attributes()

@@ -54,6 +54,7 @@ __device__ __forceinline__ float attn_factor(float x)
 // the kernel takes for one long sequence without a tree.  The last two leave their rows' maxima, sums and unnormalised
 // outputs for the join, but for a sequence without shared pages, which the second finishes.
 enum { kAttnAll = 0, kAttnOwn = 1, kAttnPrefix = 2 };
+constexpr int kPrefixRows = 256;  // query rows of a block (mq_attn_tc.cuh)
 
 // Rows (token * heads + head) in the workspace.  ml: the maximum less the kernel's shift, so that ml.y 2^ml.x is the
 // sum whichever kernel it is from; a negative ml.y: there is no result (a page outside the cache).
@@ -66,6 +67,7 @@ struct AttnShared {
     const int32_t* grp_start;
     const int32_t* grp_pages;
     int n_groups, max_pages;
+    int sms, prefix_grid, own_rows;  // SMs that the two kernels share out; the second's CTAs; the first's rows of a block
     unsigned* abort;  // [0]: a wait ran out; [1]: a sequence contradicts the call's bounds or its group
     AttnRows own, prefix;
     int4* blocks;   // per row block and key/value head of the groups: first CTA, CTAs, slot of the first
@@ -112,9 +114,16 @@ __device__ __forceinline__ bool attn_group(const AttnParams& p, int g, AttnGroup
     return T > 0 && q->pages > 0 && !*bad;
 }
 
-// the group of sequence s, or -1
+// The group of sequence s, or -1: the last that has it.
+constexpr int kLaneGroups = 32;  // up to here a warp keeps a group per lane (attn_range)
 __device__ __forceinline__ int attn_group_of(const AttnParams& p, int s)
 {
+    if (p.sh.n_groups <= kLaneGroups) {
+        int g = -1;
+        for (int k = 0; k < p.sh.n_groups; ++k)
+            if (s >= __ldg(p.sh.grp_start + k) && s < __ldg(p.sh.grp_start + k + 1)) g = k;
+        return g;
+    }
     int lo = 0, hi = p.sh.n_groups;  // the last group that starts at s or before it
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -126,6 +135,26 @@ __device__ __forceinline__ int attn_group_of(const AttnParams& p, int s)
     return lo > 0 && s < __ldg(p.sh.grp_start + lo) ? lo - 1 : -1;
 }
 
+// Groups in a warp's registers, one per lane: looked up without loads that wait for one another.
+struct AttnLaneGroup {
+    int seq0, end, t0, T, pages;
+    int state;  // 0: nothing to do, 1: there, 2: contradicts the bounds
+};
+__device__ __forceinline__ AttnLaneGroup attn_lane_group(const AttnParams& p)
+{
+    AttnLaneGroup l = {};
+    const int k = threadIdx.x & 31;
+    if (p.sh.n_groups <= kLaneGroups && k < p.sh.n_groups) {
+        AttnGroup q;
+        bool bad;
+        const bool there = attn_group(p, k, &q, &bad);
+        l.seq0 = q.seq0, l.end = __ldg(p.sh.grp_start + k + 1);
+        l.t0 = q.t0, l.T = q.T, l.pages = q.pages;
+        l.state = bad ? 2 : there ? 1 : 0;
+    }
+    return l;
+}
+
 // sequence s as the device data has it (kAttnPrefix: group s as one); false
 // (and nothing to do) where it is empty, *bad where it contradicts the call's
 // bounds or the cache
@@ -133,6 +162,16 @@ struct AttnSeq {
     int t0, T, ctx, pages;
     int row, skip;  // its row of the table; kAttnOwn: pages of the table before its own
 };
+// its tokens lie in the group's, which the join goes by, and its context reaches past the prefix
+__device__ __forceinline__ void attn_own(AttnSeq* q, bool* bad, int state, int t0, int T, int pages)
+{
+    *bad = state == 2 || (state == 1 && (q->t0 < t0 || q->t0 + int64_t(q->T) > int64_t(t0) + T || q->ctx < pages * kKvPage));
+    if (state == 1 && !*bad) {
+        q->skip = pages;
+        q->ctx -= pages * kKvPage;
+    }
+}
+// by a thread
 template <int M>
 __device__ __forceinline__ bool attn_seq(const AttnParams& p, int s, AttnSeq* q, bool* bad)
 {
@@ -145,26 +184,43 @@ __device__ __forceinline__ bool attn_seq(const AttnParams& p, int s, AttnSeq* q,
     q->t0 = __ldg(p.a.tok_start + s);
     const int64_t T = int64_t(__ldg(p.a.tok_start + s + 1)) - q->t0;
     q->ctx = __ldg(p.a.ctx_len + s);
-    int64_t len = q->ctx + T;
+    const int64_t len = q->ctx + T;
     *bad = q->t0 < 0 || T < 0 || T > p.a.max_tokens || q->t0 + T > p.a.n_tokens ||
            (T > 0 && (q->ctx < 0 || len > p.a.max_len || len > int64_t(p.c.table_ld) * kKvPage));
     q->T = int(T), q->row = s, q->skip = 0;
     if constexpr (M == kAttnOwn) {
         const int k = T > 0 && !*bad ? attn_group_of(p, s) : -1;
-        if (k >= 0) {  // its tokens lie in the group's, which the join goes by, its context reaches past the prefix
+        if (k >= 0) {
             AttnGroup g;
             bool bad_group;
             const bool there = attn_group(p, k, &g, &bad_group);
-            *bad = bad_group || (there && (q->t0 < g.t0 || q->t0 + T > int64_t(g.t0) + g.T || q->ctx < g.pages * kKvPage));
-            if (there && !*bad) {
-                q->skip = g.pages;
-                q->ctx -= g.pages * kKvPage;
-                len -= g.pages * kKvPage;
-            }
+            attn_own(q, bad, bad_group ? 2 : there, g.t0, g.T, g.pages);
         }
     }
-    q->pages = int((len + kKvPage - 1) / kKvPage);
+    q->pages = int((q->ctx + T + kKvPage - 1) / kKvPage);
     return T > 0 && !*bad;
+}
+// by a whole warp, which comes together: every lane its sequence (there: it has one)
+template <int M>
+__device__ __forceinline__ bool attn_seq(const AttnParams& p, const AttnLaneGroup& lg, int s, bool there, AttnSeq* q,
+                                         bool* bad)
+{
+    *bad = false;
+    if (M != kAttnOwn || p.sh.n_groups > kLaneGroups) return there && attn_seq<M>(p, s, q, bad);
+    if (there) there = attn_seq<kAttnAll>(p, s, q, bad);
+    int k = 0;
+    bool in = false;
+    for (int i = 0; i < p.sh.n_groups; ++i) {
+        const int from = __shfl_sync(0xffffffffu, lg.seq0, i), to = __shfl_sync(0xffffffffu, lg.end, i);
+        if (s >= from && s < to) k = i, in = true;
+    }
+    const int state = __shfl_sync(0xffffffffu, lg.state, k), t0 = __shfl_sync(0xffffffffu, lg.t0, k);
+    const int T = __shfl_sync(0xffffffffu, lg.T, k), pages = __shfl_sync(0xffffffffu, lg.pages, k);
+    if (there && in) {
+        attn_own(q, bad, state, t0, T, pages);
+        q->pages = (q->ctx + q->T + kKvPage - 1) / kKvPage;
+    }
+    return there && !*bad;
 }
 template <int M>
 __device__ __forceinline__ int attn_seqs(const AttnParams& p)
@@ -186,6 +242,7 @@ struct AttnRange {
     int first, last;  // this CTA's units
     int seq;          // sequence that the walk is at, and its first unit
     int seq_first;
+    AttnLaneGroup lg; // kAttnOwn
     __device__ __forceinline__ int begin(int c) const { return c * quot + min(c, rem); }
     __device__ __forceinline__ int owner(int u) const
     {
@@ -194,31 +251,106 @@ struct AttnRange {
     }
 };
 
-// The cut, and where this CTA's stretch starts; called by one whole warp.
-template <int M>
-__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, unsigned* status)
+// The SMs of a call with shared prefixes go to both kernels, x of N to the prefixes', such that they end together:
+//   d + A / x = B / (N - x)
+// in units of a page of the kernel for few rows, 0.45 us; a group is kAttnGroupCost more.  A page of 256 rows on the
+// tensor cores takes two units; of the sequences' own keys there, of few rows mostly, half a one, and a group twice as
+// much (1024 groups of 28 rows and 6 pages, f16: 67 us on 152 SMs).  d: what the prefixes' kernel starts later, and takes
+// longer to start and to leave its parts.
+__device__ __forceinline__ float attn_prefix_sms(const AttnParams& p, int pages, int groups, int pre_pages, int pre_groups)
 {
-    const int lane = threadIdx.x & 31, n = gridDim.x, c = blockIdx.x;
-    int pages = 0, groups = 0;
-    bool any_bad = false;
-    for (int s = lane; s < attn_seqs<M>(p); s += 32) {
-        AttnSeq q;
-        bool bad;
-        if (attn_seq<M>(p, s, &q, &bad)) {
-            const int k = attn_groups(p, q, RT);
-            pages += k * q.pages;
-            groups += k;
+    const bool tc = p.sh.own_rows > 16;
+    const float d = 16.0f, N = float(p.sh.sms), A = 2.0f * (pre_pages + float(kAttnGroupCost) * pre_groups);
+    const float B = (tc ? 0.5f : 1.0f) * pages + (tc ? 2.0f : 1.0f) * kAttnGroupCost * groups;
+    const float b = d * N - A - B;
+    return (b + sqrtf(b * b + 4.0f * d * A * N)) / (2.0f * d);
+}
+
+// What the sequences and the groups come to, formed by all warps of a CTA, 32 sequences each at a time, before
+// attn_range (kAttnAll: by the one warp that calls it).
+struct AttnTotals {
+    int own[(MQ_MAX_SEQS + 31) / 32][2];  // pages and groups of 32 sequences
+    int pages, groups, pre_pages, pre_groups, bad;
+};
+template <int M>
+__device__ __forceinline__ void attn_totals(const AttnParams& p, AttnTotals* t)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (threadIdx.x == 0) t->pages = t->groups = t->pre_pages = t->pre_groups = t->bad = 0;
+    __syncthreads();
+    const AttnLaneGroup lg = attn_lane_group(p);
+    AttnSeq q;
+    bool bad, any_bad = false;
+    for (int i = warp; 32 * i < p.c.n_seqs; i += warps) {
+        int pages = 0, groups = 0;
+        if (attn_seq<kAttnOwn>(p, lg, 32 * i + lane, 32 * i + lane < p.c.n_seqs, &q, &bad)) {
+            groups = attn_groups(p, q, p.sh.own_rows);
+            pages = groups * q.pages;
         }
         any_bad |= bad;
+        pages = __reduce_add_sync(0xffffffffu, pages);
+        groups = __reduce_add_sync(0xffffffffu, groups);
+        if (lane == 0) {
+            t->own[i][0] = pages, t->own[i][1] = groups;
+            atomicAdd(&t->pages, pages);
+            atomicAdd(&t->groups, groups);
+        }
     }
-    if (any_bad && c == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-    if (M == kAttnOwn && c == 0) {  // the join looks closer then
-        any_bad = __any_sync(0xffffffffu, any_bad);
-        if (lane == 0) p.sh.abort[1] = any_bad;
+    for (int i = warps - 1 - warp; 32 * i < p.sh.n_groups; i += warps) {  // from the last warp on
+        int pages = 0, groups = 0;
+        if (32 * i + lane < p.sh.n_groups) {
+            if (attn_seq<kAttnPrefix>(p, 32 * i + lane, &q, &bad)) {
+                groups = attn_groups(p, q, kPrefixRows);
+                pages = groups * q.pages;
+            }
+            any_bad |= bad;
+        }
+        pages = __reduce_add_sync(0xffffffffu, pages);
+        groups = __reduce_add_sync(0xffffffffu, groups);
+        if (lane == 0) {
+            atomicAdd(&t->pre_pages, pages);
+            atomicAdd(&t->pre_groups, groups);
+        }
     }
-    pages = __reduce_add_sync(0xffffffffu, pages);
-    groups = __reduce_add_sync(0xffffffffu, groups);
+    if (any_bad) t->bad = 1;
+    __syncthreads();
+}
+
+// The cut, and where this CTA's stretch starts; called by one whole warp.
+template <int M>
+__device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, const AttnTotals* t, unsigned* status)
+{
+    const int lane = threadIdx.x & 31, c = blockIdx.x;
+    int n = gridDim.x, pages = 0, groups = 0;
     AttnRange r;
+    r.lg = AttnLaneGroup{};
+    if constexpr (M == kAttnAll) {
+        bool any_bad = false;
+        for (int s = lane; s < p.c.n_seqs; s += 32) {
+            AttnSeq q;
+            bool bad;
+            if (attn_seq<M>(p, s, &q, &bad)) {
+                const int k = attn_groups(p, q, RT);
+                pages += k * q.pages;
+                groups += k;
+            }
+            any_bad |= bad;
+        }
+        if (any_bad && c == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+        pages = __reduce_add_sync(0xffffffffu, pages);
+        groups = __reduce_add_sync(0xffffffffu, groups);
+    } else {
+        r.lg = attn_lane_group(p);
+        int take = p.sh.sms - int(attn_prefix_sms(p, t->pages, t->groups, t->pre_pages, t->pre_groups) + 0.5f);
+        take = t->pre_pages > 0 ? min(max(take, p.sh.sms - p.sh.prefix_grid), p.sh.sms - 1) : p.sh.sms;
+        n = min(n, max(M == kAttnOwn ? take : p.sh.sms - take, 1));
+        pages = M == kAttnPrefix ? t->pre_pages : t->pages;
+        groups = M == kAttnPrefix ? t->pre_groups : t->groups;
+        if (M == kAttnOwn && c == 0 && lane == 0) {
+            p.sh.abort[1] = t->bad;  // the join looks closer then
+            if (t->bad) atomicOr(status, MQ_DEV_KV_RANGE);
+        }
+    }
     r.cost = pages > n ? kAttnGroupCost : 0;
     r.total = pages + groups * r.cost;
     r.ctas = min(r.total, n);
@@ -229,9 +361,16 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, uns
     r.seq = 0, r.seq_first = 0;
     // the sequence that holds unit r.first, 32 at a time
     for (int s0 = 0; s0 < attn_seqs<M>(p) && r.first < r.last; s0 += 32) {
+        if (M == kAttnOwn) {  // not among these
+            const int units = t->own[s0 / 32][0] + t->own[s0 / 32][1] * r.cost;
+            if (r.first >= r.seq_first + units) {
+                r.seq_first += units;
+                continue;
+            }
+        }
         AttnSeq q;
         bool bad;
-        const int mine = s0 + lane < attn_seqs<M>(p) && attn_seq<M>(p, s0 + lane, &q, &bad)
+        const int mine = attn_seq<M>(p, r.lg, s0 + lane, s0 + lane < attn_seqs<M>(p), &q, &bad)
                              ? attn_groups(p, q, RT) * (q.pages + r.cost) : 0;
         int incl = mine;
 #pragma unroll
@@ -261,14 +400,14 @@ struct AttnSegment {
 };
 
 // The next segment of a CTA's stretch, which starts at unit *at of sequence
-// w->seq or a later one; *at moves past it.  False: there is none.
+// w->seq or a later one; *at moves past it.  False: there is none.  Called by one whole warp.
 template <int M>
 __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange* w, int* at, AttnSegment* g)
 {
     for (int u = *at; u < w->last;) {
         AttnSeq q;
         bool bad;
-        const int units = attn_seq<M>(p, w->seq, &q, &bad) ? attn_groups(p, q, RT) * (q.pages + w->cost) : 0;
+        const int units = attn_seq<M>(p, w->lg, w->seq, true, &q, &bad) ? attn_groups(p, q, RT) * (q.pages + w->cost) : 0;
         if (u >= w->seq_first + units) {
             w->seq_first += units;
             if (++w->seq >= attn_seqs<M>(p)) return false;  // not reached unless the lengths change under the call
@@ -329,7 +468,6 @@ __device__ __forceinline__ int64_t attn_place(const AttnParams& p, const AttnSeg
 }
 // where the join finds the row block at row0 of group k, whose tokens start at t0: the blocks of a group have numbers
 // of their own, whatever the groups' sizes are
-constexpr int kPrefixRows = 256;  // query rows of a block (attn_tc.cu)
 __device__ __forceinline__ int64_t attn_block(const AttnParams& p, int k, int t0, int row0, int head)
 {
     return (int64_t(t0) * p.group / kPrefixRows + k + row0 / kPrefixRows) * p.c.n_kv_heads + head;
@@ -450,6 +588,12 @@ cudaError_t set_attn_tc_attributes();
 cudaError_t launch_attn_own_rows(const mq_kv_cache& cache, const AttnParams& p, int RT, int grid, unsigned* status,
                                  cudaStream_t s);
 cudaError_t launch_attn_own_tc(const mq_kv_cache& cache, const AttnParams& p, int grid, unsigned* status, cudaStream_t s);
+// the own keys' joins, where they are kernels: behind the prefixes' kernel, which shares the SMs with the first
+cudaError_t launch_attn_own_rows_join(const mq_kv_cache& cache, const AttnParams& p, int RT, int grid, unsigned* status,
+                                      cudaStream_t s);
+cudaError_t launch_attn_own_tc_join(const mq_kv_cache& cache, const AttnParams& p, int grid, unsigned* status,
+                                    cudaStream_t s);
+cudaError_t launch_attn_shared_join(const mq_kv_cache& cache, const AttnParams& p, unsigned* status, cudaStream_t s);
 cudaError_t launch_attn_prefix(const mq_kv_cache& cache, const AttnParams& p, int grid, unsigned* status, cudaStream_t s);
 cudaError_t set_attn_own_rows_attributes();
 cudaError_t set_attn_own_tc_attributes();

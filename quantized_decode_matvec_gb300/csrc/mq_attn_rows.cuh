@@ -523,7 +523,13 @@ __global__ void __launch_bounds__(RowsCfg<D, Q8, NT>::kThreads, 1)
     // the join, or the prefixes' kernel, may take its place; it waits for this grid's end
     if (!C::kJoins || M != kAttnAll) griddep_launch_dependents();
     AttnRange w;
-    if (warp == kWarps) w = attn_range<M>(p, RT, status);
+    if constexpr (M != kAttnAll) {
+        __shared__ AttnTotals totals_s;
+        attn_totals<M>(p, &totals_s);
+        if (warp == kWarps) w = attn_range<M>(p, RT, &totals_s, status);
+    } else {
+        if (warp == kWarps) w = attn_range<M>(p, RT, nullptr, status);
+    }
     __syncthreads();
 
     auto give_up = [&]() {
@@ -1000,18 +1006,21 @@ __global__ void __launch_bounds__(RowsJoin<D, NT>::kThreads) attn_rows_join_kern
     attn_emit4(p, g, g.row0 + row, there, D, d, o);
 }
 
+template <int D, int NT, int M>
+cudaError_t launch_rows_join(const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
+{
+    if (RowsCfg<D, true, NT>::kJoins || grid == 1) return cudaSuccess;  // one CTA shares no group
+    return attn_launch_pdl(attn_rows_join_kernel<D, NT, M>, dim3(grid), RowsJoin<D, NT>::kThreads,
+                           size_t(grid) * 2 * RowsJoin<D, NT>::kRows * sizeof(float), p, status, s);
+}
+
 template <int D, bool Q8, int NT, int M>
 cudaError_t launch_rows(const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
 {
     using C = RowsCfg<D, Q8, NT>;
     attn_rows_kernel<D, Q8, NT, M><<<grid, C::kThreads, C::kSmem, s>>>(p, status);
-    cudaError_t e = cudaGetLastError();
-    if constexpr (!C::kJoins) {
-        if (e == cudaSuccess && grid > 1)  // one CTA shares no group
-            e = attn_launch_pdl(attn_rows_join_kernel<D, NT, M>, dim3(grid), RowsJoin<D, NT>::kThreads,
-                                 size_t(grid) * 2 * C::kRows * sizeof(float), p, status, s);
-    }
-    return e;
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess || M != kAttnAll ? e : launch_rows_join<D, NT, M>(p, grid, status, s);
 }
 
 template <int NT, int M>

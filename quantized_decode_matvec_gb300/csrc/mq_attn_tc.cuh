@@ -370,7 +370,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
     fence_barrier_init();
     griddep_launch_dependents();  // the join may take its place; it waits for this grid's end
     AttnRange w;
-    if (warp == kWarpSeg) w = attn_range<M>(p, kTcRows, status);
+    if constexpr (M != kAttnAll) {
+        __shared__ AttnTotals totals_s;
+        attn_totals<M>(p, &totals_s);
+        if (warp == kWarpSeg) w = attn_range<M>(p, kTcRows, &totals_s, status);
+    } else {
+        if (warp == kWarpSeg) w = attn_range<M>(p, kTcRows, nullptr, status);
+    }
     if (warp == kWarpMma) tmem_alloc(&tmem_base, 512);
     tc_fence_before();
     __syncthreads();
@@ -827,8 +833,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    // the sequences' own keys' kernels, which may run beside this one, end before it does: the join waits for this one
-    if (M == kAttnPrefix) griddep_wait();
+    // the sequences' own keys' kernels, which run beside this one, end before it does: the join waits for this one
+    if (M == kAttnPrefix && blockIdx.x == 0) griddep_wait();
 }
 
 // ---- the groups that several CTAs share: their parts joined in CTA order -------------------------
@@ -839,55 +845,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const AttnParams
 // SMs read them.
 constexpr int kJoinAhead = 4;
 
-// kAttnPrefix: a CTA per (row block of the groups, key/value head, 32 rows), whether or not several CTAs share the
-// block; what a sequence's own keys gave is one part more, and so is a block that one CTA has finished.
 template <int D, int M>
 __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(const AttnParams p, unsigned* status)
 {
     extern __shared__ float part_s[];  // [parts][32] maxima, then sums
     __shared__ float top_s[D / 8][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta0 = blockIdx.x, slab = blockIdx.y * 32;
+    if (M == kAttnOwn) griddep_launch_dependents();
+    griddep_wait();
+    const int4 s0 = __ldcg(p.shared + 2 * cta0), s1 = __ldcg(p.shared + 2 * cta0 + 1);
+    const int n = s1.x;
     AttnSegment g;
-    int n, slab, cta0, slot0;
-    bool whole = false;  // kAttnPrefix: the block was finished by one CTA
-    if constexpr (M == kAttnPrefix) {
-        __shared__ int grp_s;
-        if (threadIdx.x == 0) grp_s = -1;
-        __syncthreads();
-        AttnGroup q;
-        bool bad;
-        for (int k = threadIdx.x; k < p.sh.n_groups; k += 4 * D)
-            if (attn_group(p, k, &q, &bad)) {
-                const int64_t at = int64_t(blockIdx.x) - (int64_t(q.t0) * p.group / kTcRows + k);
-                if (at >= 0 && at * kTcRows < int64_t(q.T) * p.group) grp_s = k;
-            }
-        __syncthreads();
-        if (grp_s < 0) return;
-        (void)attn_group(p, grp_s, &q, &bad);
-        slab = blockIdx.z * 32;
-        g.t0 = q.t0, g.T = q.T, g.head = blockIdx.y;
-        g.row0 = int(int64_t(blockIdx.x) - (int64_t(q.t0) * p.group / kTcRows + grp_s)) * kTcRows;
-        if (slab >= g.T * p.group - g.row0) return;
-        griddep_wait();
-        if (__ldcg(p.sh.abort)) return;  // nothing of the call's outputs is known to be whole
-        const int4 b = __ldcg(p.sh.blocks + attn_block(p, grp_s, g.t0, g.row0, g.head));
-        cta0 = b.x, n = b.y, slot0 = b.z;
-        whole = n < 2;
-        if (whole) n = 0;
-    } else {
-        if (M == kAttnOwn) griddep_launch_dependents();
-        cta0 = blockIdx.x, slab = blockIdx.y * 32;
-        griddep_wait();
-        const int4 s0 = __ldcg(p.shared + 2 * cta0), s1 = __ldcg(p.shared + 2 * cta0 + 1);
-        n = s1.x, slot0 = s1.y;
-        g.t0 = s0.x, g.T = s0.y, g.head = s0.z, g.row0 = s0.w, g.skip = s1.z;
-        if (n < 2) return;
-    }
+    g.t0 = s0.x, g.T = s0.y, g.head = s0.z, g.row0 = s0.w, g.skip = s1.z;
+    if (n < 2) return;
     const int rows = min(kTcRows, g.T * p.group - g.row0);
     if (slab >= rows) return;
-    bool mine = slab + lane < rows;
+    const bool mine = slab + lane < rows;
     const int row = min(slab + lane, rows - 1);
-    const float* const first = p.parts + (int64_t(cta0) * 2 + slot0) * attn_slot_floats(kTcRows, D);
+    const float* const first = p.parts + (int64_t(cta0) * 2 + s1.y) * attn_slot_floats(kTcRows, D);
     const float* const others = p.parts + int64_t(cta0) * 2 * attn_slot_floats(kTcRows, D);
     auto slot_of = [&](int c) { return c == 0 ? first : others + int64_t(c) * 2 * attn_slot_floats(kTcRows, D); };
     float4 x[kJoinAhead][2];
@@ -900,46 +875,17 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(con
             x[i][1] = __ldcg(src + kTcRows);
         }
     };
-    if (M != kAttnPrefix || n > 0) load(0);
-    // kAttnPrefix: the results that lie by row
-    const int64_t place = attn_place(p, g, g.row0 + row);
-    float2 ml[2];
-    float4 y[2][2];
-    if constexpr (M == kAttnPrefix) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const AttnRows& from = i == 0 ? p.sh.own : p.sh.prefix;
-            ml[i] = make_float2(kLowest, 0.0f);
-            y[i][0] = y[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i == 1 && !whole) continue;
-            ml[i] = __ldcg(from.ml + place);
-            const float4* const src = reinterpret_cast<const float4*>(from.o + place * D + 8 * warp);
-            y[i][0] = __ldcg(src), y[i][1] = __ldcg(src + 1);
-        }
-        if (__ldcg(p.sh.abort + 1)) {  // rows of a sequence that was skipped hold what was there
-            const int tok = g.t0 + attn_row_token(p, g.row0 + row);
-            bool found = false;
-            for (int s = 0; s < p.c.n_seqs && !found; ++s) {
-                AttnSeq q;
-                bool bad;
-                found = attn_seq<kAttnOwn>(p, s, &q, &bad) && q.skip > 0 && tok >= q.t0 && tok - q.t0 < q.T;
-            }
-            mine = mine && found;
-            if (!found) ml[0] = make_float2(kLowest, 0.0f);
-        }
-    }
-    constexpr float kLess = M == kAttnPrefix ? kTcShift : 0.0f;  // as the maxima by row are
+    load(0);
     float* const m_s = part_s;
     float* const l_s = part_s + n * 32;
     for (int c = warp; c < n; c += D / 8) {
-        m_s[c * 32 + lane] = __ldcg(slot_of(c) + row) - kLess;
+        m_s[c * 32 + lane] = __ldcg(slot_of(c) + row);
         l_s[c * 32 + lane] = __ldcg(slot_of(c) + kTcRows + row);
     }
     __syncthreads();
     float mm = kLowest, l = 0.0f, o[8];
     bool gone = false, bad = false;
     for (int c = 0; c < n; ++c) mm = fmaxf(mm, m_s[c * 32 + lane]);
-    if constexpr (M == kAttnPrefix) mm = fmaxf(mm, fmaxf(ml[0].x, ml[1].x));
     for (int c = 0; c < n; ++c) {
         const float lc = l_s[c * 32 + lane];
         gone |= lc < 0.0f;
@@ -948,24 +894,7 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(con
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-    if constexpr (M == kAttnPrefix) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i == 1 && !whole) continue;
-            gone |= ml[i].y < 0.0f;
-            bad |= ml[i].y == kAttnBadPage;
-            const float f = attn_factor(ml[i].x - mm);
-            l = fmaf(ml[i].y, f, l);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                o[4 * h] = fmaf(y[i][h].x, f, o[4 * h]);
-                o[4 * h + 1] = fmaf(y[i][h].y, f, o[4 * h + 1]);
-                o[4 * h + 2] = fmaf(y[i][h].z, f, o[4 * h + 2]);
-                o[4 * h + 3] = fmaf(y[i][h].w, f, o[4 * h + 3]);
-            }
-        }
-    }
-    for (int c0 = 0; M != kAttnPrefix || c0 < n;) {
+    for (int c0 = 0;;) {
 #pragma unroll
         for (int i = 0; i < kJoinAhead; ++i) {
             if (c0 + i >= n) break;
@@ -982,13 +911,13 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(con
         if (c0 >= n) break;
         load(c0);
     }
-    if (attn_raw<M>(g) && M == kAttnOwn) {
+    if (attn_raw<M>(g)) {
         if (!mine) return;
         if (warp == 0) {
             attn_leave_ml<M>(p, g, g.row0 + row, mm - kTcShift, gone ? kAttnBadPage : l);
             if (bad) atomicOr(status, MQ_DEV_KV_RANGE);
         }
-        float4* const dst = reinterpret_cast<float4*>(p.sh.own.o + place * D + 8 * warp);
+        float4* const dst = reinterpret_cast<float4*>(p.sh.own.o + attn_place(p, g, g.row0 + row) * D + 8 * warp);
         dst[0] = make_float4(o[0], o[1], o[2], o[3]);
         dst[1] = make_float4(o[4], o[5], o[6], o[7]);
         return;
@@ -1033,25 +962,23 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) attn_tc_join_kernel(con
     }
 }
 
+template <int D, int M>
+cudaError_t launch_tc_join(const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
+{
+    if (grid == 1) return cudaSuccess;  // one CTA shares no group
+    const int rows = p.group * p.a.max_tokens;
+    return attn_launch_pdl(attn_tc_join_kernel<D, M>, dim3(grid, ((rows < kTcRows ? rows : kTcRows) + 31) / 32), 4 * D,
+                           size_t(grid) * 2 * 32 * sizeof(float), p, status, s);  // 39 KB for 152 SMs
+}
+
 template <int D, bool Q8, int M>
 cudaError_t launch_tc(const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
 {
-    const size_t join_smem = size_t(grid) * 2 * 32 * sizeof(float);  // 39 KB for 152 SMs
-    if constexpr (M == kAttnPrefix) {  // beside the kernels before it, which is why it ends behind them
-        cudaError_t e = attn_launch_pdl(attn_tc_kernel<D, Q8, M>, dim3(grid), kTcThreads, TcCfg<D, Q8>::kSmem, p, status, s);
-        if (e != cudaSuccess) return e;
-        const int64_t rows = int64_t(p.a.n_tokens) * p.group;
-        return attn_launch_pdl(attn_tc_join_kernel<D, M>,
-                               dim3(unsigned(rows / kTcRows + p.sh.n_groups), unsigned(p.c.n_kv_heads),
-                                    unsigned(((rows < kTcRows ? rows : kTcRows) + 31) / 32)),
-                               4 * D, join_smem, p, status, s);
-    }
+    if constexpr (M == kAttnPrefix)  // beside the kernel before it
+        return attn_launch_pdl(attn_tc_kernel<D, Q8, M>, dim3(grid), kTcThreads, TcCfg<D, Q8>::kSmem, p, status, s);
     attn_tc_kernel<D, Q8, M><<<grid, kTcThreads, TcCfg<D, Q8>::kSmem, s>>>(p, status);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || grid == 1) return e;  // one CTA shares no group
-    const int rows = p.group * p.a.max_tokens;
-    return attn_launch_pdl(attn_tc_join_kernel<D, M>, dim3(grid, ((rows < kTcRows ? rows : kTcRows) + 31) / 32), 4 * D,
-                           join_smem, p, status, s);
+    return e != cudaSuccess || M != kAttnAll ? e : launch_tc_join<D, M>(p, grid, status, s);
 }
 
 template <int M>

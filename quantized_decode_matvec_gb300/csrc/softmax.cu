@@ -22,7 +22,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 16;
 
 struct SoftmaxArgs {
     const float* x;
@@ -63,8 +63,9 @@ __device__ __forceinline__ float cta_reduce(float v, float* s)
 }
 
 // NV > 0: the CTA's part of the row is up to 4 * NV values per thread, in registers; 0: any length, read twice
+// Several CTAs per SM, so that some load while others reduce or store.
 template <int NV>
-__global__ void __launch_bounds__(kThreads) softmax_kernel(const SoftmaxArgs p)
+__global__ void __launch_bounds__(kThreads, NV == 8 || NV == 4 ? 2 : 4) softmax_kernel(const SoftmaxArgs p)
 {
     __shared__ float max_s[kWarps], sum_s[kWarps];
     __shared__ float2 part_s[kMaxCluster];  // every CTA's maximum and sum
@@ -188,6 +189,16 @@ cudaError_t launch(const SoftmaxArgs& p, int64_t rows, int C, cudaStream_t s)
 
 }  // namespace
 
+cudaError_t set_softmax_attributes()
+{
+    cudaError_t e = cudaSuccess;
+#define MQ_SET(NV) \
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(softmax_kernel<NV>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    MQ_SET(0) MQ_SET(1) MQ_SET(2) MQ_SET(4) MQ_SET(8)
+#undef MQ_SET
+    return e;
+}
+
 cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_t x_ld, int64_t y_ld, float scale,
                            int num_sms, cudaStream_t s)
 {
@@ -196,7 +207,8 @@ cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_
     p.k_hi = float(k);
     p.k_lo = float(k - double(p.k_hi));
     // the fewest CTAs that hold a row at 32 values per thread; more while SMs are idle and each has values left
-    const int64_t units = (int64_t(vocab) + 3 + 3) / 4;
+    const bool whole = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && x_ld % 4 == 0;  // every row starts a unit
+    const int64_t units = (int64_t(vocab) + (whole ? 3 : 6)) / 4;
     int C = 1;
     while (C < kMaxCluster && (units > int64_t(C) * kThreads * 8 || (int64_t(rows) * C * 2 <= num_sms && units > C * kThreads)))
         C *= 2;
@@ -205,7 +217,6 @@ cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_
     if (per <= 2) return launch<2>(p, rows, C, s);
     if (per <= 4) return launch<4>(p, rows, C, s);
     if (per <= 8) return launch<8>(p, rows, C, s);
-    if (per <= 16) return launch<16>(p, rows, C, s);
     return launch<0>(p, rows, C, s);
 }
 

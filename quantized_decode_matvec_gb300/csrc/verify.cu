@@ -10,8 +10,12 @@
 // first index at which the running sum of S passes u W.
 //
 // Which token comes out hangs on sums over a vocabulary, so probabilities are
-// summed as integers, in units of 2^-60: exactly, and in any order.  A test of a
-// child is one comparison in 64-bit floating point.
+// rounded to multiples of 2^-46 and summed as integers, so that no sum depends on
+// its order; over 2^17 values the roundings come to some 2^-39, and the chance that
+// they change a draw is about 3e-7 (a sum in fp32 would change one in 70).  Two
+// 23-bit halves per value, in 32-bit arithmetic: with 64-bit numbers in units of
+// 2^-60 the pass was bound by some 45 instructions per value.  A test of a child is
+// one comparison in 64-bit floating point.
 //
 // A cluster of CTAs per sequence: each takes a contiguous part of the
 // vocabulary, and keeps the sums of its tiles, so that the draw looks into one
@@ -29,31 +33,38 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxNodes = MQ_TREE_MAX_TOKENS;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kUnit = 512;       // values of a warp's step: 16 per lane
 constexpr int kMaxTiles = 1024;  // of a CTA
-constexpr int kOne = 60;         // 1.0 is 2^60
+constexpr int kHalf = 23, kOne = 2 * kHalf;  // 1.0 is 2^46
 constexpr double kInvOne = 1.0 / double(1ull << kOne);
 
 struct VerifyArgs {
     mq_verify_args a;
-    int chunk, tile;  // values of a CTA (a multiple of tile) and of a tile (a multiple of kUnit)
-    int wide;         // rows may be read 16 bytes at a time
+    int chunk, tile;  // places of a CTA (a multiple of tile) and of a tile (a multiple of kUnit)
 };
 
-// A probability in units of 2^-60, rounded down; what is not a number above zero is zero, what is above one is one.
+// A probability in units of 2^-46, rounded to nearest: hi 2^23 + lo.  What is not a number above zero is zero, what is
+// above one is one.  Adding 1 leaves the first 23 bits in the mantissa, what they leave is exact, and so are its next 23.
+struct Fixed {
+    int hi, lo;
+};
+__device__ __forceinline__ Fixed halves(float p)
+{
+    p = __saturatef(p);
+    const float f = __fadd_rz(p, 1.0f), rest = p - (f - 1.0f), g = fmaf(rest, 8388608.0f, 1.0f);
+    return Fixed{__float_as_int(f) - 0x3f800000, __float_as_int(g) - 0x3f800000};
+}
+__device__ __forceinline__ uint64_t whole(int hi, int lo) { return (uint64_t(uint32_t(hi)) << kHalf) + uint32_t(lo); }
 __device__ __forceinline__ uint64_t fixed(float p)
 {
-    if (!(p > 0.0f)) return 0;
-    const uint32_t b = __float_as_uint(fminf(p, 1.0f));
-    const int e = int(b >> 23);  // p = m 2^(e - 150); subnormals are below the unit anyway
-    const uint64_t m = uint64_t((b & 0x7fffffu) | 0x800000u) << (kOne - 23);  // m 2^37, the value at e = 127
-    return 127 - e < 64 ? m >> (127 - e) : 0;
+    const Fixed x = halves(p);
+    return whole(x.hi, x.lo);
 }
 
-// a * q for a in units of 2^-57 (a < 64) and q in those of 2^-60
+// a * q for a in units of 2^-57 (a < 64) and q in those of 2^-46
 __device__ __forceinline__ uint64_t times(uint64_t a, uint64_t q)
 {
     return __umul64hi(a, q) << 7 | (a * q) >> 57;
@@ -78,6 +89,7 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v)
 struct Shared {
     int tok[kMaxNodes], par[kMaxNodes];
     float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];  // p, q: of the node's token at its parent
+    unsigned long long kids[kMaxNodes];              // of every node, a bit each
     int path[kMaxNodes], gone[kMaxNodes];            // gone: refused tokens of the node at hand (point masses)
     uint64_t tile[kMaxTiles];
     uint64_t warp[kWarps];
@@ -116,48 +128,47 @@ __device__ __forceinline__ uint32_t ordered(float v)
 }
 
 // One pass over the CTA's part of a row: f(index, p, q) of every value, lanes of a warp on neighbouring ones, the
-// tiles of the part going round the warps; done(tile) behind each.
-template <bool Both, class F, class Done>
-__device__ __forceinline__ void walk_row(const VerifyArgs& p, const float* prow, const float* qrow, int first, int last, F f,
-                                         Done done)
+// tiles of the part going round the warps; step() behind every 16 of a lane, done(tile) behind a tile.  Places are counted from the 16-byte boundary before
+// the row, `off` values before its first, so that they are read 16 bytes at a time wherever rows start.
+template <bool Both, class F, class Step, class Done>
+__device__ __forceinline__ void walk_row(const VerifyArgs& p, const float* prow, const float* qrow, int off, int first,
+                                         int last, F f, Step step, Done done)
 {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const bool wide = !Both || (int(reinterpret_cast<uintptr_t>(qrow) >> 2) & 3) == off;
     for (int t = warp; first + t * int64_t(p.tile) < last; t += kWarps) {
         const int begin = first + t * p.tile, end = last - begin < p.tile ? last : begin + p.tile;
         for (int i = begin; i < end; i += kUnit) {
-            if (p.wide && end - i >= kUnit) {
+            if (wide && i >= off && end - i >= kUnit) {
                 float4 x[4], y[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[j] = __ldg(reinterpret_cast<const float4*>(prow + i + j * 128) + lane);
-                    if (Both) y[j] = __ldg(reinterpret_cast<const float4*>(qrow + i + j * 128) + lane);
+                    x[j] = __ldg(reinterpret_cast<const float4*>(prow + (i - off) + j * 128) + lane);
+                    if (Both) y[j] = __ldg(reinterpret_cast<const float4*>(qrow + (i - off) + j * 128) + lane);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int k = i + j * 128 + lane * 4;
+                    const int k = i - off + j * 128 + lane * 4;
                     f(k, x[j].x, Both ? y[j].x : 0.0f);
                     f(k + 1, x[j].y, Both ? y[j].y : 0.0f);
                     f(k + 2, x[j].z, Both ? y[j].z : 0.0f);
                     f(k + 3, x[j].w, Both ? y[j].w : 0.0f);
                 }
             } else {
-                float x[16], y[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int k = i + j * 32 + lane;
-                    x[j] = k < end ? __ldg(prow + k) : 0.0f;
-                    y[j] = Both && k < end ? __ldg(qrow + k) : 0.0f;
+#pragma unroll 4
+                for (int j = 0; j < kUnit / 32; ++j) {
+                    const int k = i - off + j * 32 + lane;
+                    if (k >= 0 && k < end - off) f(k, __ldg(prow + k), Both ? __ldg(qrow + k) : 0.0f);
                 }
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (i + j * 32 + lane < end) f(i + j * 32 + lane, x[j], y[j]);
             }
+            step();
         }
         done(t);
     }
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, unsigned* status)
+// Four CTAs per SM, so that a batch of 64 sequences is on the chip at once.
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p, unsigned* status)
 {
     __shared__ Shared sm;
     cg::cluster_group cl = cg::this_cluster();
@@ -181,13 +192,17 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, un
         if (tid > 0 && !ok && rank == 0) atomicOr(status, MQ_DEV_KV_RANGE);
         sm.tok[tid] = tok;
         sm.par[tid] = ok ? par : -1;  // never a child
+        sm.kids[tid] = 0;
         if (!greedy) {
             sm.u[tid] = __ldg(p.a.u + t0 + tid);
             sm.p[tid] = ok ? __ldg(p.a.target + (t0 + par) * p.a.target_ld + tok) : 0.0f;
             sm.q[tid] = ok && p.a.draft ? __ldg(p.a.draft + (t0 + par) * p.a.draft_ld + tok) : 1.0f;
         }
     }
-    const int first = int(min(int64_t(rank) * p.chunk, int64_t(V))), last = int(min(int64_t(first) + p.chunk, int64_t(V)));
+    // the CTA's places in a row that starts `off` values behind a 16-byte boundary
+    const int first = int(min(int64_t(rank) * p.chunk, int64_t(V) + 3));
+    auto offset = [](const float* row) { return int(reinterpret_cast<uintptr_t>(row) >> 2) & 3; };
+    auto end_of = [&](int off) { return int(min(int64_t(first) + p.chunk, int64_t(V) + off)); };
     int passes = 0;
     uint64_t before = 0, mine = 0;  // sums of the parts before the CTA's, and its own, in the last pass
 
@@ -216,7 +231,21 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, un
     };
     auto mass = [&](const Residual& r) {
         uint64_t sum = 0, all = 0;
-        auto add = [&](int, float x, float y) { sum += r.of(x, y); };
+        int hi = 0, lo = 0;  // of a step
+        const int off = offset(r.p), last = end_of(off);
+        auto step = [&]() {
+            sum += (int64_t(hi) << kHalf) + lo;
+            hi = lo = 0;
+        };
+        auto add_p = [&](int, float x, float) {
+            const Fixed P = halves(x);
+            hi += P.hi, lo += P.lo;
+        };
+        auto add_diff = [&](int, float x, float y) {
+            const Fixed P = halves(x), Q = halves(y);
+            if (x > y) hi += P.hi - Q.hi, lo += P.lo - Q.lo;
+        };
+        auto add_any = [&](int, float x, float y) { sum += r.of(x, y); };
         auto done = [&](int t) {
             sum = warp_sum(sum);
             if (r.n_gone) {  // refused tokens weigh nothing
@@ -225,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, un
                 for (int k = tid % 32; k < r.n_gone; k += 32) {
                     bool again = false;
                     for (int j = 0; j < k; ++j) again |= r.gone[j] == r.gone[k];
-                    if (!again && r.gone[k] >= begin && r.gone[k] < last && r.gone[k] - begin < p.tile)
+                    if (!again && r.gone[k] + off >= begin && r.gone[k] + off < last && r.gone[k] + off - begin < p.tile)
                         less += r.of(__ldg(r.p + r.gone[k]), 0.0f);
                 }
                 sum -= warp_sum(less);
@@ -235,45 +264,48 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, un
             sum = 0;
         };
         __syncthreads();  // the tiles and the warps' words of the pass before are read
-        if (r.a)
-            walk_row<true>(p, r.p, r.q, first, last, add, done);
+        if (r.a == 0)
+            walk_row<false>(p, r.p, r.p, off, first, last, add_p, step, done);
+        else if (r.a == kAOne)
+            walk_row<true>(p, r.p, r.q, off, first, last, add_diff, step, done);
         else
-            walk_row<false>(p, r.p, r.p, first, last, add, done);
+            walk_row<true>(p, r.p, r.q, off, first, last, add_any, step, done);
         return meet(cta_total(all, false), false);
     };
     __syncthreads();
+    if (tid > 0 && tid < T && sm.par[tid] >= 0) atomicOr(&sm.kids[sm.par[tid]], 1ull << tid);
+    if (tid == 0) sm.path[0] = 0;
+    __syncthreads();
 
     int cur = 0, len = 1, next = -1;
-    if (tid == 0) sm.path[0] = 0;
     bool owner = rank == 0;  // who writes next
     for (;;) {
         const float* const prow = p.a.target + (t0 + int64_t(cur)) * p.a.target_ld;
         int taken = -1;
-        const bool stop = len >= p.a.path_ld;
+        unsigned long long kids = len < p.a.path_ld ? sm.kids[cur] : 0;  // in the order of their numbers
         if (greedy) {
             uint64_t best = 0;
             __syncthreads();
             walk_row<false>(
-                p, prow, prow, first, last,
+                p, prow, prow, offset(prow), first, end_of(offset(prow)),
                 [&](int i, float x, float) {
                     const uint32_t o = ordered(x);
                     if (o > uint32_t(best >> 32) || (o && o == uint32_t(best >> 32) && uint32_t(~i) > uint32_t(best)))
                         best = uint64_t(o) << 32 | uint32_t(~i);
                 },
-                [](int) {});
+                []() {}, [](int) {});
             best = meet(cta_total(warp_max(best), true), true);
             next = best ? int(~uint32_t(best)) : -1;
-            for (int c = cur + 1; c < T && taken < 0 && !stop; ++c)
-                if (sm.par[c] == cur && sm.tok[c] == next) taken = c;
+            for (; kids && taken < 0; kids &= kids - 1)
+                if (sm.tok[__ffsll(kids) - 1] == next) taken = __ffsll(kids) - 1;
             if (taken < 0) break;
         } else {
             Residual r = {prow, p.a.draft ? p.a.draft + (t0 + int64_t(cur)) * p.a.draft_ld : nullptr, 0, 0, sm.gone};
             double a = 0.0, W = 1.0;
             uint64_t mass_fixed = 0;
             bool known = false;  // mass_fixed and the tiles are of r as it stands
-            for (int c = cur + 1; c < T && !stop; ++c) {
-                if (sm.par[c] != cur) continue;
-                const int x = sm.tok[c];
+            for (; kids; kids &= kids - 1) {
+                const int c = __ffsll(kids) - 1, x = sm.tok[c];
                 double S = double(sm.p[c]) - a * double(sm.q[c]);
                 if (!r.q)
                     for (int k = 0; k < r.n_gone; ++k)
@@ -284,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, un
                 }
                 if (r.q) {
                     if (known && mass_fixed == 0) continue;  // nothing is left to accept, or to take away
-                    r.a = known ? r.a + (mass_fixed >> 3) : kAOne;
+                    r.a = known ? r.a + (mass_fixed << (57 - kOne)) : kAOne;
                     a += W;
                     mass_fixed = mass(r);
                     W = double(mass_fixed) * kInvOne;
@@ -306,10 +338,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, un
                 if (mass_fixed == 0) break;
                 // the first index whose running sum passes u W
                 const uint64_t u = fixed(sm.u[0]), U = u < (1ull << kOne) ? u : (1ull << kOne) - 1;
-                const uint64_t mark = __umul64hi(U << 4, mass_fixed);
+                const uint64_t mark = __umul64hi(U << (64 - kOne), mass_fixed);
                 owner = mark >= before && mark - before < mine;
                 if (owner) {
                     uint64_t at = before;
+                    const int off = offset(r.p), last = end_of(off);
                     if (tid < 32) {
                         // the tile, 32 at a time, then 32 runs of 16 of each of its units
                         const int tiles = (last - first + p.tile - 1) / p.tile;
@@ -331,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, un
                         for (int i = begin; i < end; i += kUnit) {
                             uint64_t own = 0;
                             for (int j = 0; j < 16; ++j)
-                                if (i + tid * 16 + j < end) own += r.at(i + tid * 16 + j);
+                                if (i + tid * 16 + j >= off && i + tid * 16 + j < end) own += r.at(i + tid * 16 + j - off);
                             uint64_t incl = own;
 #pragma unroll
                             for (int o = 1; o < 32; o <<= 1) {
@@ -346,10 +379,11 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, un
                             if (tid == __ffs(past) - 1) {
                                 uint64_t c = at + incl - own;
                                 for (int j = 0; j < 16; ++j) {
+                                    if (i + tid * 16 + j < off) continue;
                                     if (i + tid * 16 + j >= end) break;
-                                    c += r.at(i + tid * 16 + j);
+                                    c += r.at(i + tid * 16 + j - off);
                                     if (c > mark) {
-                                        sm.found = i + tid * 16 + j;
+                                        sm.found = i + tid * 16 + j - off;
                                         break;
                                     }
                                 }
@@ -378,16 +412,20 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs p, un
 
 }  // namespace
 
+cudaError_t set_verify_attributes()
+{
+    return cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
 cudaError_t launch_verify(const mq_verify_args& a, int num_sms, unsigned* status, cudaStream_t s)
 {
     VerifyArgs p;
     p.a = a;
-    p.wide = (reinterpret_cast<uintptr_t>(a.target) & 15) == 0 && a.target_ld % 4 == 0 &&
-             (!a.draft || ((reinterpret_cast<uintptr_t>(a.draft) & 15) == 0 && a.draft_ld % 4 == 0));
-    int C = kMaxCluster;
-    while (C > 1 && a.vocab <= (C / 2) * kUnit * 4) C /= 2;  // at least four steps of a warp each
-    (void)num_sms;
-    const int64_t part = (int64_t(a.vocab) + C - 1) / C;
+    // a step of every warp for each CTA at least; sixteen of them only for few sequences, since a larger cluster waits
+    // for a whole neighbourhood of SMs
+    int C = int64_t(a.n_seqs) * kMaxCluster <= num_sms ? kMaxCluster : kMaxCluster / 2;
+    while (C > 1 && a.vocab <= (C / 2) * kUnit * kWarps) C /= 2;
+    const int64_t part = (int64_t(a.vocab) + 3 + C - 1) / C;
     const int64_t units = (part + kUnit - 1) / kUnit;
     p.tile = int((units + kMaxTiles - 1) / kMaxTiles) * kUnit;
     p.chunk = int((part + p.tile - 1) / p.tile) * p.tile;
