@@ -556,7 +556,7 @@ mq_status mq_softmax(const float* x, float* y, int32_t rows, int32_t vocab, int6
  * that holds it is accepted; target may be logits then, and draft and u are not
  * read.
  * path[s][0..n_path[s]-1] are the accepted nodes, root first, and n_path[s] their
- * number, as mq_kv_accept takes them; entries behind are not written.  A path
+ * number, as mq_kv_accept takes them; entries behind are zero.  A path
  * ends at path_ld nodes (>= 1), at the last as if it had no children.  A sequence
  * without nodes has n_path 0 and next -1.
  * Probabilities are >= 0 (what is not counts as 0, above 1 as 1) and u in [0, 1).

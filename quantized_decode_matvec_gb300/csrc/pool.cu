@@ -209,11 +209,12 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PoolArgs p, u
     if (tid == 0 && !full && total) *p.pool.n_free = n_free - total;
 }
 
-__device__ __forceinline__ void copy16(uint8_t* dst, const uint8_t* src, int bytes)
+// by `step` threads, number `at` of which calls; their first kAhead loads are on their way together
+template <int kAhead>
+__device__ __forceinline__ void copy16(uint8_t* dst, const uint8_t* src, int bytes, int at, int step)
 {
-    constexpr int kAhead = 4;
-    const int n = bytes / 16, step = blockDim.x;
-    for (int i = threadIdx.x; i < n; i += kAhead * step) {
+    const int n = bytes / 16;
+    for (int i = at; i < n; i += kAhead * step) {
         uint4 v[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
@@ -259,10 +260,11 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, unsign
     }
     const uint8_t* const in = p.c.pages + (int64_t(x) * p.c.n_kv_heads + h) * B::kBytes;
     uint8_t* const out = p.c.pages + (int64_t(page) * p.c.n_kv_heads + h) * B::kBytes;
-    constexpr int kPlanes = Q8 ? 1 : D / 64;
-#pragma unroll 1
-    for (int k = 0; k < 2 * kPlanes; ++k)
-        copy16(out + k * kKvPage * B::kRow, in + k * kKvPage * B::kRow, rest * B::kRow);
+    // K's and V's planes by a share of the threads each, every byte of a thread in one round
+    constexpr int kPlanes = 2 * (Q8 ? 1 : D / 64), kShare = 256 / kPlanes;
+    const int k = threadIdx.x / kShare;
+    copy16<kKvPage * B::kRow / 16 / kShare>(out + k * kKvPage * B::kRow, in + k * kKvPage * B::kRow, rest * B::kRow,
+                                            threadIdx.x % kShare, kShare);
     if (Q8) {
         constexpr int kWords = D / 64;  // 32-bit words of a row's scales
         for (int i = threadIdx.x; i < 2 * rest * kWords; i += 256) {
@@ -275,29 +277,30 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, unsign
 // ---- a cluster's view of a call -------------------------------------------------------------
 struct ClusterSum {
     int warp[kWarps];
-    int total[4];  // by use; read by the whole cluster
+    int2 total[4];  // sum and flag, by use; read by the whole cluster
 };
 
-// Sum of v over the CTA, all CTAs' sums met: *before those of the CTAs before this one; returns the cluster's.
-// Global writes before it are seen by the cluster behind it.
-__device__ __forceinline__ int cluster_sum(cg::cluster_group& cl, ClusterSum& s, int use, int v, int* before)
+// Sum of v over the CTA, all CTAs' sums met: *before those of the CTAs before this one; returns the cluster's.  *any:
+// whether one thread's flag was set.  Global writes before it are seen by the cluster behind it (the barrier releases
+// and acquires).
+__device__ __forceinline__ int cluster_sum(cg::cluster_group& cl, ClusterSum& s, int use, int v, int* before, bool flag = false,
+                                           int* any = nullptr)
 {
     v = __reduce_add_sync(0xffffffffu, v);
+    flag = __syncthreads_or(flag);
     if (threadIdx.x % 32 == 0) s.warp[threadIdx.x / 32] = v;
     __syncthreads();
     if (threadIdx.x < 32) {
         const int all = __reduce_add_sync(0xffffffffu, s.warp[threadIdx.x]);
-        if (threadIdx.x == 0) s.total[use] = all;
+        if (threadIdx.x == 0) s.total[use] = make_int2(all, flag);
     }
-    __threadfence();
     cl.sync();
-    int all = 0;
-    *before = 0;
-    for (int c = 0; c < int(cl.num_blocks()); ++c) {
-        const int w = *cl.map_shared_rank(&s.total[use], c);
-        if (c < int(cl.block_rank())) *before += w;
-        all += w;
-    }
+    // a lane per CTA: one after the other these loads take 0.3 us each
+    const int c = threadIdx.x % 32;
+    const int2 w = c < int(cl.num_blocks()) ? *cl.map_shared_rank(&s.total[use], c) : make_int2(0, 0);
+    const int all = __reduce_add_sync(0xffffffffu, w.x), flags = __any_sync(0xffffffffu, w.y != 0);
+    *before = __reduce_add_sync(0xffffffffu, c < int(cl.block_rank()) ? w.x : 0);
+    if (any) *any = flags;
     return all;
 }
 
@@ -323,7 +326,7 @@ __device__ __forceinline__ int cta_rank(bool flag, int* warp_s, int* count)
 // ---- free -----------------------------------------------------------------------------------
 // Positions are the references that the call gives up, in its order.  A page whose count comes to zero is pushed at
 // its last position.  scratch[page]: the page's last position in the call.
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) free_kernel(const PoolArgs p, unsigned* status)
+__global__ void __launch_bounds__(kThreads) free_kernel(const PoolArgs p, unsigned* status)
 {
     __shared__ int off_s[kSeqs + 1], warp_s[kWarps];
     __shared__ int first_s[kSeqs];  // by sequence: the first entry that names it
@@ -367,7 +370,8 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) fre
         if (tid == 0 && rank == 0) atomicOr(status, MQ_DEV_KV_RANGE);
     }
     if (total == 0 || bad_free) return;  // the same in the whole cluster
-    const int per = (total + kCluster - 1) / kCluster, begin = min(rank * per, total), end = min(begin + per, total);
+    const int ctas = int(cl.num_blocks());
+    const int per = (total + ctas - 1) / ctas, begin = min(rank * per, total), end = min(begin + per, total);
     // the table's entry at a position; its page, or -1
     auto place = [&](int pos, int64_t* where) {
         const int e = entry_of(off_s, p.n, pos), s = __ldg(p.a + e), k = p.b ? __ldg(p.b + e) : 0;
@@ -375,40 +379,60 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) fre
         const int page = __ldcg(p.table + *where);
         return page >= 0 && page < p.c.n_pages ? page : -1;
     };
+    // a page with one reference goes where that is; only of one that others name too has the last to be found
     int64_t w;
+    int page, before, alone = 0, shared = 0;
+    int page0 = -1;  // of the thread's first position, which is its only one mostly: kept, with the rest of it
+    int64_t w0 = 0;
+    bool flag0 = false;
     for (int pos = begin + tid; pos < end; pos += kThreads) {
-        const int page = place(pos, &w);
-        if (page >= 0)
-            __stcg(p.pool.scratch + page, -1);
-        else
+        page = place(pos, &w);
+        if (pos == begin + tid) page0 = page, w0 = w;
+        if (page < 0) {
             atomicOr(status, MQ_DEV_KV_RANGE);
+            continue;
+        }
+        const int refs = __ldcg(p.pool.refs + page);
+        if (pos == begin + tid) flag0 = refs == 1;
+        alone += refs == 1;
+        shared |= refs > 1;
+        __stcg(p.pool.scratch + page, -1);
     }
-    __threadfence();
-    cl.sync();
-    for (int pos = begin + tid; pos < end; pos += kThreads) {
-        const int page = place(pos, &w);
-        if (page < 0) continue;
-        atomicMax(p.pool.scratch + page, pos);
-        atomicSub(p.pool.refs + page, 1);
-    }
-    __threadfence();
-    cl.sync();
+    int pushed = cluster_sum(cl, sum_s, 0, alone, &before, shared, &shared);
     auto freed = [&](int pos, int* page, int64_t* where) {
         *page = place(pos, where);
-        return *page >= 0 && __ldcg(p.pool.refs + *page) == 0 && __ldcg(p.pool.scratch + *page) == pos;
+        if (*page < 0) return false;
+        const int refs = __ldcg(p.pool.refs + *page);
+        return shared ? refs == 0 && __ldcg(p.pool.scratch + *page) == pos : refs == 1;
     };
-    int count = 0, page, before;
-    for (int pos = begin + tid; pos < end; pos += kThreads) count += freed(pos, &page, &w);
-    const int pushed = cluster_sum(cl, sum_s, 0, count, &before);
+    if (shared) {  // the same in the whole cluster
+        for (int pos = begin + tid; pos < end; pos += kThreads) {
+            if ((page = place(pos, &w)) >= 0) {
+                atomicMax(p.pool.scratch + page, pos);
+                atomicSub(p.pool.refs + page, 1);
+            }
+        }
+        cl.sync();
+        int count = 0;
+        for (int pos = begin + tid; pos < end; pos += kThreads) count += freed(pos, &page, &w);
+        pushed = cluster_sum(cl, sum_s, 1, count, &before);
+    }
     if (n_free + pushed > p.c.n_pages) {  // the stack names pages that are in use
         if (tid == 0 && rank == 0) atomicOr(status, MQ_DEV_KV_RANGE);
     }
     for (int base = begin; base < end; base += kThreads) {
         const int pos = base + tid;
-        const bool flag = pos < end && freed(pos, &page, &w);
+        bool flag;
+        if (base == begin && !shared) {
+            flag = pos < end && flag0;
+            page = page0, w = w0;
+        } else {
+            flag = pos < end && freed(pos, &page, &w);
+        }
         int here;
         const int to = n_free + before + cta_rank(flag, warp_s, &here);
         if (flag && to < p.c.n_pages) p.pool.free_list[to] = page;
+        if (flag && !shared) p.pool.refs[page] = 0;
         if (pos < end) p.table[w] = -1;
         before += here;
     }
@@ -423,55 +447,45 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) fre
 
 // ---- compact --------------------------------------------------------------------------------
 // With U pages in use, the k-th page in use from U on goes to the k-th free one before U.  scratch: n_pages words,
-// the place that a page from U on goes to; then the moves' sources and targets in turn; the word behind both: how many.
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) compact_plan_kernel(const PoolArgs p)
+// the place that a page from U on goes to; then the free pages before U in ascending order, and the pages in use from
+// U on in descending order (their ranks among all pages in use are known before their number is); then both's number
+// and U.
+__global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PoolArgs p)
 {
     __shared__ int warp_s[kWarps];
     __shared__ ClusterSum sum_s;
     griddep_launch_dependents();
     cg::cluster_group cl = cg::this_cluster();
-    const int tid = threadIdx.x, rank = int(cl.block_rank()), n = int(p.c.n_pages);
-    const int per = (n + kCluster - 1) / kCluster, begin = min(int64_t(rank) * per, int64_t(n)), end = min(int64_t(begin) + per, int64_t(n));
+    const int tid = threadIdx.x, rank = int(cl.block_rank()), ctas = int(cl.num_blocks()), n = int(p.c.n_pages);
+    const int per = (n + ctas - 1) / ctas;
+    const int begin = int(min(int64_t(rank) * per, int64_t(n))), end = int(min(int64_t(begin) + per, int64_t(n)));
     int32_t* const map = p.pool.scratch;
-    int32_t* const hole = map + n;  // the k-th free page before U
-    int32_t* const far = hole + (n + 1) / 2;  // the k-th page in use from U on
-    int count = 0, unused;
+    int32_t* const hole = map + n;
+    int32_t* const far = hole + (n + 1) / 2;
+    int count = 0, before;
     for (int i = begin + tid; i < end; i += kThreads) count += p.pool.refs[i] > 0;
-    const int used = cluster_sum(cl, sum_s, 0, count, &unused);
-    int holes = 0, fars = 0;
-    for (int i = begin + tid; i < end; i += kThreads) {
-        const bool in_use = p.pool.refs[i] > 0;
-        holes += i < used && !in_use;
-        fars += i >= used && in_use;
-    }
-    int hole_before, far_before;
-    const int n_holes = cluster_sum(cl, sum_s, 1, holes, &hole_before);
-    (void)cluster_sum(cl, sum_s, 2, fars, &far_before);
+    const int used = cluster_sum(cl, sum_s, 0, count, &before);
+    int holes = 0, unused;
     for (int base = begin; base < end; base += kThreads) {
         const int i = base + tid;
         const bool in_use = i < end && p.pool.refs[i] > 0;
         int here;
-        bool flag = i < end && i < used && !in_use;
-        int at = hole_before + cta_rank(flag, warp_s, &here);
-        if (flag) __stcg(hole + at, i);
-        hole_before += here;
-        flag = i >= used && in_use;
-        at = far_before + cta_rank(flag, warp_s, &here);
-        if (flag) __stcg(far + at, i);
-        far_before += here;
+        const int at = before + cta_rank(in_use, warp_s, &here);  // pages in use before page i
+        if (i < end && i < used && !in_use) __stcg(hole + i - at, i), ++holes;
+        if (i >= used && in_use) __stcg(far + used - 1 - at, i);
         if (i >= used && i < end) p.pool.free_list[n - 1 - i] = i;
+        before += here;
     }
-    __threadfence();
-    cl.sync();
-    for (int k = rank * kThreads + tid; k < n_holes; k += kCluster * kThreads) {
-        const int from = __ldcg(far + k), to = __ldcg(hole + k);
+    const int moves = cluster_sum(cl, sum_s, 1, holes, &unused);
+    for (int k = rank * kThreads + tid; k < moves; k += ctas * kThreads) {
+        const int from = __ldcg(far + moves - 1 - k), to = __ldcg(hole + k);
         map[from] = to;
         p.pool.refs[to] = p.pool.refs[from];
         p.pool.refs[from] = 0;
     }
     if (rank == 0 && tid == 0) {
         *p.pool.n_free = n - used;
-        map[2 * n + 2] = n_holes;
+        map[2 * n + 2] = moves;
         map[2 * n + 3] = used;
     }
     cl.sync();
@@ -489,8 +503,9 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const PoolAr
     const int parts = (p.page_bytes + kMoveBytes - 1) / kMoveBytes;
     for (int64_t w = blockIdx.x; w < int64_t(moves) * parts; w += gridDim.x) {
         const int k = int(w / parts), at = int(w % parts) * kMoveBytes;
-        copy16(p.c.pages + int64_t(__ldcg(hole + k)) * p.page_bytes + at,
-               p.c.pages + int64_t(__ldcg(far + k)) * p.page_bytes + at, min(kMoveBytes, p.page_bytes - at));
+        copy16<4>(p.c.pages + int64_t(__ldcg(hole + k)) * p.page_bytes + at,
+                  p.c.pages + int64_t(__ldcg(far + moves - 1 - k)) * p.page_bytes + at, min(kMoveBytes, p.page_bytes - at),
+                  threadIdx.x, kMoveThreads);
     }
     for (int64_t i = int64_t(blockIdx.x) * kMoveThreads + threadIdx.x; i < int64_t(p.c.n_seqs) * p.c.table_ld;
          i += int64_t(gridDim.x) * kMoveThreads) {
@@ -499,6 +514,24 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const PoolAr
         const int page = p.table[i];
         if (page >= used && page < n) p.table[i] = __ldcg(p.pool.scratch + page);
     }
+}
+
+// One CTA where its threads have a few items each, else a cluster: a barrier of one costs a third of a cluster's.
+template <class K, class... A>
+cudaError_t launch_cluster(K kernel, int64_t items, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    const int ctas = items <= 8 * kThreads ? 1 : kCluster;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <class K>
@@ -561,15 +594,13 @@ cudaError_t launch_kv_free(const mq_kv_cache& c, const mq_kv_pool& pool, const i
 {
     PoolArgs p = pool_args(c, pool);
     p.a = seq, p.b = keep, p.n = n;
-    free_kernel<<<kCluster, kThreads, 0, s>>>(p, status);
-    return cudaGetLastError();
+    return launch_cluster(free_kernel, int64_t(n) * c.table_ld, s, p, status);
 }
 
 cudaError_t launch_kv_compact(const mq_kv_cache& c, const mq_kv_pool& pool, int num_sms, cudaStream_t s)
 {
     PoolArgs p = pool_args(c, pool);
-    compact_plan_kernel<<<kCluster, kThreads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_cluster(compact_plan_kernel, c.n_pages, s, p);
     if (e != cudaSuccess) return e;
     return launch_behind(compact_move_kernel, dim3(unsigned(num_sms) * 8), kMoveThreads, s, p, nullptr);
 }

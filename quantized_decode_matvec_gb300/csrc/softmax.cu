@@ -15,6 +15,7 @@
 #include <utility>
 
 #include "mq_internal.h"
+#include "mq_tma.cuh"
 
 namespace mq {
 
@@ -30,6 +31,7 @@ struct SoftmaxArgs {
     int64_t x_ld, y_ld;
     int vocab;
     float k_hi, k_lo;
+    int rows, ahead;  // rows that are on the chip at once: a later one's part is called for when a CTA starts
 };
 
 // 2^(d k); -inf is kept from meeting the two parts' signs, and NaN stays
@@ -100,6 +102,12 @@ __global__ void __launch_bounds__(kThreads, NV == 8 || NV == 4 ? 2 : 4) softmax_
                 if (i + e >= 0 && i + e < p.vocab) y[i + e] = v[e];
         }
     };
+    if (threadIdx.x == 0 && row + p.ahead < p.rows && NV >= 4) {
+        const float* const next = x + p.ahead * p.x_ld;
+        const int o = int(reinterpret_cast<uintptr_t>(next) >> 2) & 3, from = 4 * first > o ? 4 * first : 4;
+        const int to = min(4 * last, p.vocab + o) & ~3;
+        if (from < to) prefetch_l2(next + (from - o), uint32_t(to - from) * 4);
+    }
     float v[NV > 0 ? NV : 1][4];
     float m = -INFINITY, l = 0.0f;
     if constexpr (NV > 0) {
@@ -202,7 +210,7 @@ cudaError_t set_softmax_attributes()
 cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_t x_ld, int64_t y_ld, float scale,
                            int num_sms, cudaStream_t s)
 {
-    SoftmaxArgs p = {x, y, x_ld, y_ld, vocab, 0.0f, 0.0f};
+    SoftmaxArgs p = {x, y, x_ld, y_ld, vocab, 0.0f, 0.0f, rows, 0};
     const double k = double(scale) * 1.4426950408889634074;
     p.k_hi = float(k);
     p.k_lo = float(k - double(p.k_hi));
@@ -212,6 +220,7 @@ cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_
     int C = 1;
     while (C < kMaxCluster && (units > int64_t(C) * kThreads * 8 || (int64_t(rows) * C * 2 <= num_sms && units > C * kThreads)))
         C *= 2;
+    p.ahead = 2 * num_sms / C;
     const int64_t per = ((units + C - 1) / C + kThreads - 1) / kThreads;  // units of a thread
     if (per <= 1) return launch<1>(p, rows, C, s);
     if (per <= 2) return launch<2>(p, rows, C, s);

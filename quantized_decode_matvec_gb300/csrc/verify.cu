@@ -26,6 +26,7 @@
 #include <cooperative_groups.h>
 
 #include "mq_internal.h"
+#include "mq_tma.cuh"
 
 namespace mq {
 
@@ -64,12 +65,17 @@ __device__ __forceinline__ uint64_t fixed(float p)
     return whole(x.hi, x.lo);
 }
 
-// a * q for a in units of 2^-57 (a < 64) and q in those of 2^-46
-__device__ __forceinline__ uint64_t times(uint64_t a, uint64_t q)
+// p - a q where that is above zero, else 0, for a of two parts: the product in two parts, whose second is rounded to the
+// unit by itself.  A difference of rounded numbers that comes out below zero is zero.
+__device__ __forceinline__ Fixed less(float p, float q, float a_hi, float a_lo)
 {
-    return __umul64hi(a, q) << 7 | (a * q) >> 57;
+    p = __saturatef(p), q = __saturatef(q);
+    const float y = a_hi * q, rest = fmaf(a_lo, q, fmaf(a_hi, q, -y));
+    if (!((p - y) - rest > 0.0f)) return Fixed{0, 0};
+    const Fixed P = halves(p), Y = halves(y);
+    const int hi = P.hi - Y.hi, lo = P.lo - Y.lo - (__float_as_int(fmaf(rest, 0x1p46f, 12582912.0f)) - 0x4b400000);
+    return hi <= 1 && hi * (1 << kHalf) + lo < 0 ? Fixed{0, 0} : Fixed{hi, lo};
 }
-constexpr uint64_t kAOne = 1ull << 57;
 
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
@@ -86,6 +92,8 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v)
     return v;
 }
 
+enum { kEnd, kAccept, kRefuse };
+
 struct Shared {
     int tok[kMaxNodes], par[kMaxNodes];
     float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];  // p, q: of the node's token at its parent
@@ -95,27 +103,29 @@ struct Shared {
     uint64_t warp[kWarps];
     uint64_t total[2];  // read by the whole cluster; of every other pass
     int found;
+    int act, child;     // what the walk does next
+    float a_hi, a_lo;
+    int n_gone;
 };
 
 // S at one index, in fixed point
 struct Residual {
     const float* p;
     const float* q;  // or null
-    uint64_t a;
+    float a_hi, a_lo;  // 0: the row as it is
     int n_gone;
     const int* gone;
-    __device__ __forceinline__ uint64_t of(float pv, float qv) const
+    __device__ __forceinline__ int64_t of(float pv, float qv) const
     {
-        const uint64_t P = fixed(pv);
-        if (a == 0) return P;
-        const uint64_t Q = a == kAOne ? fixed(qv) : times(a, fixed(qv));
-        return P > Q ? P - Q : 0;
+        if (a_hi == 0.0f) return int64_t(fixed(pv));
+        const Fixed x = less(pv, qv, a_hi, a_lo);
+        return int64_t(x.hi) * (1 << kHalf) + x.lo;
     }
-    __device__ __forceinline__ uint64_t at(int i) const
+    __device__ __forceinline__ int64_t at(int i) const
     {
         for (int k = 0; k < n_gone; ++k)
             if (gone[k] == i) return 0;
-        return of(__ldg(p + i), a ? __ldg(q + i) : 0.0f);
+        return of(__ldg(p + i), a_hi != 0.0f ? __ldg(q + i) : 0.0f);
     }
 };
 
@@ -184,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
     const int T = int(T64);
     if (T == 0) {
         if (rank == 0 && tid == 0) p.a.n_path[s] = 0, p.a.next[s] = -1;
+        for (int i = tid; rank == 0 && i < p.a.path_ld; i += kThreads) p.a.path[int64_t(s) * p.a.path_ld + i] = 0;
         return;
     }
     if (tid < T) {
@@ -210,13 +221,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
     auto meet = [&](uint64_t v, bool maximum) {
         if (tid == 0) sm.total[passes & 1] = v;
         cl.sync();
-        uint64_t all = 0;
-        before = 0;
-        for (int c = 0; c < C; ++c) {
-            const uint64_t w = *cl.map_shared_rank(&sm.total[passes & 1], c);
-            if (c < rank) before += w;
-            all = maximum ? larger(all, w) : all + w;
-        }
+        // a lane per CTA: one after the other these loads take 0.3 us each
+        const int c = tid % 32;
+        const uint64_t w = c < C ? *cl.map_shared_rank(&sm.total[passes & 1], c) : 0;
+        const uint64_t all = maximum ? warp_max(w) : warp_sum(w);
+        before = warp_sum(c < rank ? w : 0);
         mine = v;
         ++passes;  // the other place next: who still reads this one is waited for there
         return all;
@@ -234,42 +243,51 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
         int hi = 0, lo = 0;  // of a step
         const int off = offset(r.p), last = end_of(off);
         auto step = [&]() {
-            sum += (int64_t(hi) << kHalf) + lo;
+            sum += uint64_t(int64_t(hi) * (1 << kHalf) + lo);
             hi = lo = 0;
         };
         auto add_p = [&](int, float x, float) {
             const Fixed P = halves(x);
             hi += P.hi, lo += P.lo;
         };
-        auto add_diff = [&](int, float x, float y) {
+        auto add_diff = [&](int, float x, float y) {  // a = 1, which gives the same numbers
             const Fixed P = halves(x), Q = halves(y);
-            if (x > y) hi += P.hi - Q.hi, lo += P.lo - Q.lo;
+            if (__saturatef(x) > __saturatef(y)) hi += P.hi - Q.hi, lo += P.lo - Q.lo;
         };
-        auto add_any = [&](int, float x, float y) { sum += r.of(x, y); };
+        auto add = [&](int, float x, float y) {
+            const Fixed S = less(x, y, r.a_hi, r.a_lo);
+            hi += S.hi, lo += S.lo;
+        };
         auto done = [&](int t) {
             sum = warp_sum(sum);
             if (r.n_gone) {  // refused tokens weigh nothing
-                uint64_t less = 0;
+                uint64_t away = 0;
                 const int begin = first + t * p.tile;
                 for (int k = tid % 32; k < r.n_gone; k += 32) {
                     bool again = false;
                     for (int j = 0; j < k; ++j) again |= r.gone[j] == r.gone[k];
                     if (!again && r.gone[k] + off >= begin && r.gone[k] + off < last && r.gone[k] + off - begin < p.tile)
-                        less += r.of(__ldg(r.p + r.gone[k]), 0.0f);
+                        away += uint64_t(r.of(__ldg(r.p + r.gone[k]), 0.0f));
                 }
-                sum -= warp_sum(less);
+                sum -= warp_sum(away);
             }
             if (tid % 32 == 0) sm.tile[t] = sum;
             all += sum;
             sum = 0;
         };
+        // the whole part on its way to L2 at once: the warps' own loads are a few rounds, each of which would wait for HBM
+        if (tid < 2 && first < last && (tid == 0 || r.a_hi != 0.0f)) {
+            const float* const row = tid == 0 ? r.p : r.q;
+            const int o = offset(row), from = first > o ? first : 4, to = min(first + p.chunk, V + o) & ~3;
+            if (from < to) prefetch_l2(row + (from - o), uint32_t(to - from) * 4);
+        }
         __syncthreads();  // the tiles and the warps' words of the pass before are read
-        if (r.a == 0)
+        if (r.a_hi == 0.0f)
             walk_row<false>(p, r.p, r.p, off, first, last, add_p, step, done);
-        else if (r.a == kAOne)
+        else if (r.a_hi == 1.0f && r.a_lo == 0.0f)
             walk_row<true>(p, r.p, r.q, off, first, last, add_diff, step, done);
         else
-            walk_row<true>(p, r.p, r.q, off, first, last, add_any, step, done);
+            walk_row<true>(p, r.p, r.q, off, first, last, add, step, done);
         return meet(cta_total(all, false), false);
     };
     __syncthreads();
@@ -300,46 +318,59 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
                 if (sm.tok[__ffsll(kids) - 1] == next) taken = __ffsll(kids) - 1;
             if (taken < 0) break;
         } else {
-            Residual r = {prow, p.a.draft ? p.a.draft + (t0 + int64_t(cur)) * p.a.draft_ld : nullptr, 0, 0, sm.gone};
-            double a = 0.0, W = 1.0;
+            Residual r = {prow, p.a.draft ? p.a.draft + (t0 + int64_t(cur)) * p.a.draft_ld : nullptr, 0.0f, 0.0f, 0, sm.gone};
+            double a = 0.0, W = 1.0;  // thread 0's: fp64 of a whole CTA takes 16 cycles per warp and instruction
             uint64_t mass_fixed = 0;
             bool known = false;  // mass_fixed and the tiles are of r as it stands
-            for (; kids; kids &= kids - 1) {
-                const int c = __ffsll(kids) - 1, x = sm.tok[c];
-                double S = double(sm.p[c]) - a * double(sm.q[c]);
-                if (!r.q)
-                    for (int k = 0; k < r.n_gone; ++k)
-                        if (sm.gone[k] == x) S = 0.0;
-                if (S > 0.0 && double(sm.u[c]) * double(sm.q[c]) * W < S) {
-                    taken = c;
-                    break;
+            for (;;) {
+                __syncthreads();
+                if (tid == 0) {
+                    sm.act = kEnd;
+                    for (; kids; kids &= kids - 1) {
+                        const int c = __ffsll(kids) - 1, x = sm.tok[c];
+                        double S = double(sm.p[c]) - a * double(sm.q[c]);
+                        if (!r.q)
+                            for (int k = 0; k < r.n_gone; ++k)
+                                if (sm.gone[k] == x) S = 0.0;
+                        if (S > 0.0 && double(sm.u[c]) * double(sm.q[c]) * W < S) {
+                            sm.act = kAccept, sm.child = c;
+                            break;
+                        }
+                        if (r.q) {
+                            if (known && mass_fixed == 0) continue;  // nothing is left to accept, or to take away
+                            a += W;
+                            sm.a_hi = float(a);
+                            sm.a_lo = float(a - double(sm.a_hi));
+                            sm.act = kRefuse;
+                            kids &= kids - 1;
+                            break;
+                        }
+                        W -= S > 0.0 ? S : 0.0;
+                        sm.gone[r.n_gone++] = x;
+                    }
+                    sm.n_gone = r.n_gone;
                 }
-                if (r.q) {
-                    if (known && mass_fixed == 0) continue;  // nothing is left to accept, or to take away
-                    r.a = known ? r.a + (mass_fixed << (57 - kOne)) : kAOne;
-                    a += W;
-                    mass_fixed = mass(r);
-                    W = double(mass_fixed) * kInvOne;
-                    known = true;
-                } else {
-                    W -= S > 0.0 ? S : 0.0;
-                    __syncthreads();
-                    if (tid == 0) sm.gone[r.n_gone] = x;
-                    __syncthreads();
-                    ++r.n_gone;
-                }
+                __syncthreads();
+                const int act = sm.act;
+                r.n_gone = sm.n_gone;
+                if (act == kAccept) taken = sm.child;
+                if (act != kRefuse) break;
+                r.a_hi = sm.a_hi, r.a_lo = sm.a_lo;
+                mass_fixed = mass(r);
+                if (tid == 0) W = double(mass_fixed) * kInvOne;
+                known = true;
             }
             if (taken < 0) {
                 if (!known) mass_fixed = mass(r);
-                if (mass_fixed == 0 && (r.a || r.n_gone)) {  // the target's row itself where the residual is empty
-                    r.a = 0, r.n_gone = 0;
+                if (mass_fixed == 0 && (r.a_hi != 0.0f || r.n_gone)) {  // the target's row itself where the residual is empty
+                    r.a_hi = 0.0f, r.n_gone = 0;
                     mass_fixed = mass(r);
                 }
                 if (mass_fixed == 0) break;
                 // the first index whose running sum passes u W
                 const uint64_t u = fixed(sm.u[0]), U = u < (1ull << kOne) ? u : (1ull << kOne) - 1;
                 const uint64_t mark = __umul64hi(U << (64 - kOne), mass_fixed);
-                owner = mark >= before && mark - before < mine;
+                owner = int64_t(mark) >= int64_t(before) && int64_t(mark - before) < int64_t(mine);
                 if (owner) {
                     uint64_t at = before;
                     const int off = offset(r.p), last = end_of(off);
@@ -355,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
                                 const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
                                 if (tid >= o) incl += v;
                             }
-                            const unsigned past = __ballot_sync(0xffffffffu, at + incl > mark);
+                            const unsigned past = __ballot_sync(0xffffffffu, int64_t(at + incl) > int64_t(mark));
                             const int l = past ? __ffs(past) - 1 : 31;
                             at += __shfl_sync(0xffffffffu, past ? incl - own : incl, l);
                             if (past) t = b + l;
@@ -363,15 +394,16 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
                         const int begin = first + t * p.tile, end = last - begin < p.tile ? last : begin + p.tile;
                         for (int i = begin; i < end; i += kUnit) {
                             uint64_t own = 0;
+#pragma unroll
                             for (int j = 0; j < 16; ++j)
-                                if (i + tid * 16 + j >= off && i + tid * 16 + j < end) own += r.at(i + tid * 16 + j - off);
+                                if (i + tid * 16 + j >= off && i + tid * 16 + j < end) own += uint64_t(r.at(i + tid * 16 + j - off));
                             uint64_t incl = own;
 #pragma unroll
                             for (int o = 1; o < 32; o <<= 1) {
                                 const uint64_t v = __shfl_up_sync(0xffffffffu, incl, o);
                                 if (tid >= o) incl += v;
                             }
-                            const unsigned past = __ballot_sync(0xffffffffu, at + incl > mark);
+                            const unsigned past = __ballot_sync(0xffffffffu, int64_t(at + incl) > int64_t(mark));
                             if (!past) {
                                 at += __shfl_sync(0xffffffffu, incl, 31);
                                 continue;
@@ -381,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
                                 for (int j = 0; j < 16; ++j) {
                                     if (i + tid * 16 + j < off) continue;
                                     if (i + tid * 16 + j >= end) break;
-                                    c += r.at(i + tid * 16 + j - off);
-                                    if (c > mark) {
+                                    c += uint64_t(r.at(i + tid * 16 + j - off));
+                                    if (int64_t(c) > int64_t(mark)) {
                                         sm.found = i + tid * 16 + j - off;
                                         break;
                                     }
@@ -403,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
     }
     __syncthreads();
     if (rank == 0) {
-        if (tid < len) p.a.path[int64_t(s) * p.a.path_ld + tid] = sm.path[tid];
+        for (int i = tid; i < p.a.path_ld; i += kThreads) p.a.path[int64_t(s) * p.a.path_ld + i] = i < len ? sm.path[i] : 0;
         if (tid == 0) p.a.n_path[s] = len;
     }
     if (owner && tid == 0) p.a.next[s] = next;

@@ -938,8 +938,7 @@ def verify_tree(target, tok_start, token, parent, u=None, draft=None, greedy: bo
     ``parent``: int32 [n], the drafted tokens and their parents' numbers in the tree (node 0, the root, is the token
     that the step before ended with).  ``u``: fp32 [n] in [0, 1), a root's is what ``next`` is drawn with.  ``greedy``:
     the largest target value instead of a draw (target may be logits; u and draft are not read).  ``path_ld`` bounds
-    the nodes of a path, the root included.  path and n_path are what kv_accept takes; of a new ``path`` the entries
-    behind n_path are zero, of one that is given they stay as they were."""
+    the nodes of a path, the root included.  path (zeros behind the nodes) and n_path are what kv_accept takes."""
     torch = _torch()
     dev, i32, f32 = target.device, torch.int32, torch.float32
     if target.dim() != 2:
@@ -959,10 +958,10 @@ def verify_tree(target, tok_start, token, parent, u=None, draft=None, greedy: bo
     else:  # with what else is missing, in one buffer
         ld = MQ_TREE_MAX_TOKENS if path_ld is None else path_ld
         if stream is None:
-            new = torch.zeros(S * (ld + 2), dtype=i32, device=dev)
+            new = torch.empty(S * (ld + 2), dtype=i32, device=dev)
         else:
             with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-                new = torch.zeros(S * (ld + 2), dtype=i32, device=dev)
+                new = torch.empty(S * (ld + 2), dtype=i32, device=dev)
         path, left = new[:S * ld].view(S, ld), new[S * ld:]
         n_path = left[:S] if n_path is None else n_path
         next_token = left[S:] if next_token is None else next_token
