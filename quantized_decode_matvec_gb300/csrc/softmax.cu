@@ -67,7 +67,7 @@ __device__ __forceinline__ float cta_reduce(float v, float* s)
 // NV > 0: the CTA's part of the row is up to 4 * NV values per thread, in registers; 0: any length, read twice
 // Several CTAs per SM, so that some load while others reduce or store.
 template <int NV>
-__global__ void __launch_bounds__(kThreads, NV == 8 || NV == 4 ? 2 : 4) softmax_kernel(const SoftmaxArgs p)
+__global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(const SoftmaxArgs p)
 {
     __shared__ float max_s[kWarps], sum_s[kWarps];
     __shared__ float2 part_s[kMaxCluster];  // every CTA's maximum and sum
@@ -202,7 +202,7 @@ cudaError_t set_softmax_attributes()
     cudaError_t e = cudaSuccess;
 #define MQ_SET(NV) \
     if (e == cudaSuccess) e = cudaFuncSetAttribute(softmax_kernel<NV>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    MQ_SET(0) MQ_SET(1) MQ_SET(2) MQ_SET(4) MQ_SET(8)
+    MQ_SET(0) MQ_SET(1) MQ_SET(2) MQ_SET(4) MQ_SET(8) MQ_SET(9)
 #undef MQ_SET
     return e;
 }
@@ -218,7 +218,7 @@ cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_
     const bool whole = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && x_ld % 4 == 0;  // every row starts a unit
     const int64_t units = (int64_t(vocab) + (whole ? 3 : 6)) / 4;
     int C = 1;
-    while (C < kMaxCluster && (units > int64_t(C) * kThreads * 8 || (int64_t(rows) * C * 2 <= num_sms && units > C * kThreads)))
+    while (C < kMaxCluster && (units > int64_t(C) * kThreads * (C < 8 ? 8 : 9) || (int64_t(rows) * C * 2 <= num_sms && units > C * kThreads)))
         C *= 2;
     p.ahead = 2 * num_sms / C;
     const int64_t per = ((units + C - 1) / C + kThreads - 1) / kThreads;  // units of a thread
@@ -226,6 +226,7 @@ cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_
     if (per <= 2) return launch<2>(p, rows, C, s);
     if (per <= 4) return launch<4>(p, rows, C, s);
     if (per <= 8) return launch<8>(p, rows, C, s);
+    if (per <= 9) return launch<9>(p, rows, C, s);
     return launch<0>(p, rows, C, s);
 }
 
