@@ -497,9 +497,9 @@ mq_status mq_attn_tree(const mq_kv_cache* h_cache, const mq_attn_args* h_args, v
 
 /* Attention as mq_attn_tree, of a batch whose sequences have the pages of a
  * prefix in common.  Group g are the sequences grp_start[g]..grp_start[g+1]-1:
- * the first grp_pages[g] pages of the table are the same for all of them (those
- * of the group's first sequence are read), and each has at least 64 *
- * grp_pages[g] tokens of context.  grp_start must not decrease; sequences in no
+ * the first grp_pages[g] pages of the table are the same for all of them that
+ * have tokens (those of the first of these are read), and each of these has at
+ * least 64 * grp_pages[g] tokens of context.  grp_start must not decrease; sequences in no
  * group, and those of a group with 0 pages, have no prefix in common.  The
  * result is mq_attn_tree's up to rounding, and so are the rules for what a node
  * sees, for masks, infinities and NaN.  A sequence that contradicts its group,
@@ -511,7 +511,7 @@ mq_status mq_attn_tree(const mq_kv_cache* h_cache, const mq_attn_args* h_args, v
  * below 2^31 (MQ_ERR_UNSUPPORTED).  Three or four launches; without groups or
  * pages, mq_attn_tree's.
  * workspace: as mq_attn_tree's, of mq_attn_shared_workspace_bytes; it serves
- * any call whose own size is no larger. */
+ * any call of either whose own size is no larger. */
 typedef struct mq_attn_groups {
     const int32_t* grp_start; /* device [n_groups + 1] */
     const int32_t* grp_pages; /* device [n_groups] */
@@ -614,7 +614,8 @@ mq_status mq_verify_tree(const mq_verify_args* h_args, void* stream);
  *  - mq_kv_compact: with U pages in use, the k-th of those from page U on (in
  *    ascending order) moves to the k-th free page before U, bytes and count, and
  *    the table follows; free_list becomes n_pages - 1 down to U.
- * One launch (grow, free), two (fork, compact). */
+ * Calls on one pool must not overlap on the GPU.  One launch (grow, free), two
+ * (fork, compact). */
 typedef struct mq_kv_pool {
     int32_t* refs;      /* [n_pages] */
     int32_t* free_list; /* [n_pages] */

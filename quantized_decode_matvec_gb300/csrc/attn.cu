@@ -4,12 +4,14 @@
 
 namespace mq {
 
-// Workspace: what the join kernels read of the CTAs, the counters, parts.  Where each begins goes by the device alone,
-// so a call finds the counters at zero whatever cache, sequences and rows the call before had.
-size_t attn_parts_offset(int num_sms)
+// Workspace: what the join kernels read of the CTAs, the counters, the words of the calls with shared prefixes, parts.
+// Where each begins goes by the device alone, so a call finds the counters at zero whatever cache, sequences and rows
+// the call before had, and whichever of the two calls it was.
+size_t attn_words_offset(int num_sms)
 {
     return (size_t(num_sms) * (kAttnSharedBytes + sizeof(unsigned)) + 127) / 128 * 128;
 }
+size_t attn_parts_offset(int num_sms) { return attn_words_offset(num_sms) + 128; }
 
 // The most query rows of a key/value head that the warp kernels take.  16 rows, 8 key/value heads of 128, here and by
 // attn_tc.cu: one sequence of 300 tokens, f16 11.6 and 11.7 us, q8_0 11.9 and 11.9; of 16000 25.3 and 25.8, 23.2 and

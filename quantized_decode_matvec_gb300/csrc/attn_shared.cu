@@ -19,23 +19,20 @@ namespace mq {
 
 namespace {
 
-constexpr size_t kHead = 128;  // the abort word and its neighbour
-
 size_t up(size_t n) { return (n + 127) / 128 * 128; }
 
 struct SharedLayout {
-    size_t own, parts, blocks, own_ml, own_o, pre_ml, pre_o, bytes;
+    size_t parts, blocks, own_ml, own_o, pre_ml, pre_o, bytes;
 };
 
-// Words that a call finds as the call before left them (the abort word, the counters of the own keys' kernels) lie
-// where the device alone says; everything else is written before it is read in every call.
+// Words that a call finds as the call before left them (the abort word, the counters of the own keys' kernels) lie in
+// the part that mq_attn_tree's workspace has too; everything else is written before it is read in every call.
 SharedLayout shared_layout(const mq_kv_cache& c, int n_heads, int64_t n_tokens, int max_tokens, int64_t n_groups, int num_sms)
 {
     SharedLayout w;
     const int D = c.head_dim, group = n_heads / c.n_kv_heads;
     const size_t rows = size_t(n_tokens) * n_heads;
-    w.own = kHead;
-    w.parts = up(w.own + attn_workspace_bytes(c, n_heads, max_tokens, num_sms));
+    w.parts = up(attn_workspace_bytes(c, n_heads, max_tokens, num_sms));  // which the own keys' kernels use
     w.blocks = up(w.parts + size_t(num_sms) * 2 * attn_slot_floats(kPrefixRows, D) * sizeof(float));
     w.own_ml = up(w.blocks + (size_t(n_tokens) * group / kPrefixRows + n_groups + 1) * c.n_kv_heads * sizeof(int4));
     w.own_o = up(w.own_ml + rows * sizeof(float2));
@@ -58,11 +55,11 @@ cudaError_t launch_attn_shared(const mq_kv_cache& cache, const mq_attn_args& a, 
 {
     uint8_t* const w = static_cast<uint8_t*>(ws);
     const SharedLayout at = shared_layout(cache, a.n_heads, a.n_tokens, a.max_tokens, g.n_groups, num_sms);
-    if (g.n_groups == 0 || g.max_pages == 0) return launch_attn(cache, a, w + at.own, num_sms, status, s);
-    AttnParams p = attn_params(cache, a, w + at.own, num_sms);
+    if (g.n_groups == 0 || g.max_pages == 0) return launch_attn(cache, a, w, num_sms, status, s);
+    AttnParams p = attn_params(cache, a, w, num_sms);
     p.sh.grp_start = g.grp_start, p.sh.grp_pages = g.grp_pages;
     p.sh.n_groups = g.n_groups, p.sh.max_pages = g.max_pages;
-    p.sh.abort = reinterpret_cast<unsigned*>(w);
+    p.sh.abort = reinterpret_cast<unsigned*>(w + attn_words_offset(num_sms));
     p.sh.blocks = reinterpret_cast<int4*>(w + at.blocks);
     p.sh.own = AttnRows{reinterpret_cast<float2*>(w + at.own_ml), reinterpret_cast<float*>(w + at.own_o)};
     p.sh.prefix = AttnRows{reinterpret_cast<float2*>(w + at.pre_ml), reinterpret_cast<float*>(w + at.pre_o)};

@@ -97,6 +97,7 @@ __device__ __forceinline__ int attn_row_token(const AttnParams& p, int r)
 // the call's bounds.
 struct AttnGroup {
     int seq0, t0, T, pages;
+    int row;  // of the table: that of the first sequence with tokens
 };
 __device__ __forceinline__ bool attn_group(const AttnParams& p, int g, AttnGroup* q, bool* bad)
 {
@@ -105,13 +106,15 @@ __device__ __forceinline__ bool attn_group(const AttnParams& p, int g, AttnGroup
     q->pages = __ldg(p.sh.grp_pages + g);
     *bad = q->seq0 < 0 || end < q->seq0 || end > p.c.n_seqs || q->pages < 0 || q->pages > p.sh.max_pages ||
            q->pages > p.c.table_ld;
-    q->t0 = q->T = 0;
+    q->t0 = q->T = 0, q->row = q->seq0;
     if (*bad) return false;
     q->t0 = __ldg(p.a.tok_start + q->seq0);
     const int64_t T = int64_t(__ldg(p.a.tok_start + end)) - q->t0;
     *bad = q->t0 < 0 || T < 0 || q->t0 + T > p.a.n_tokens;
     q->T = int(T);
-    return T > 0 && q->pages > 0 && !*bad;
+    if (!(T > 0 && q->pages > 0 && !*bad)) return false;
+    while (q->row + 1 < end && __ldg(p.a.tok_start + q->row + 1) == q->t0) ++q->row;
+    return true;
 }
 
 // The group of sequence s, or -1: the last that has it.
@@ -178,7 +181,7 @@ __device__ __forceinline__ bool attn_seq(const AttnParams& p, int s, AttnSeq* q,
     if constexpr (M == kAttnPrefix) {
         AttnGroup g;
         const bool there = attn_group(p, s, &g, bad);
-        q->t0 = g.t0, q->T = g.T, q->pages = g.pages, q->ctx = g.pages * kKvPage, q->row = g.seq0, q->skip = 0;
+        q->t0 = g.t0, q->T = g.T, q->pages = g.pages, q->ctx = g.pages * kKvPage, q->row = g.row, q->skip = 0;
         return there;
     }
     q->t0 = __ldg(p.a.tok_start + s);
@@ -601,6 +604,7 @@ cudaError_t set_attn_prefix_attributes();
 
 // what every attention call puts into its parameters, and where the parts of a workspace lie (attn.cu)
 AttnParams attn_params(const mq_kv_cache& cache, const mq_attn_args& a, void* ws, int num_sms);
+size_t attn_words_offset(int num_sms);
 size_t attn_parts_offset(int num_sms);
 int attn_rows_for(int rows);  // query rows of a block of the kernel that takes `rows` per key/value head
 

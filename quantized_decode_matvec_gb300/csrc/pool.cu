@@ -516,12 +516,12 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const PoolAr
     }
 }
 
-// One CTA where its threads have a few items each, else a cluster: a barrier of one costs a third of a cluster's.
+// One CTA where its threads have an item each, else a cluster.  4923 pages: 10 us by a cluster, 15 by one CTA.
 template <class K, class... A>
 cudaError_t launch_cluster(K kernel, int64_t items, cudaStream_t s, A... args)
 {
     cudaLaunchConfig_t cfg = {};
-    const int ctas = items <= 8 * kThreads ? 1 : kCluster;
+    const int ctas = items <= kThreads ? 1 : kCluster;
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;

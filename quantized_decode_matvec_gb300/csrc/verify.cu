@@ -233,10 +233,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
     auto cta_total = [&](uint64_t v, bool maximum) {  // of the warps' values
         if (tid % 32 == 0) sm.warp[tid / 32] = v;
         __syncthreads();
-        uint64_t all = 0;
-        for (int i = 0; i < kWarps; ++i)
-            all = maximum ? larger(all, sm.warp[i]) : all + sm.warp[i];
-        return all;
+        const uint64_t w = tid % 32 < kWarps ? sm.warp[tid % 32] : 0;
+        return maximum ? warp_max(w) : warp_sum(w);
     };
     auto mass = [&](const Residual& r) {
         uint64_t sum = 0, all = 0;

@@ -880,7 +880,8 @@ def attn_tree(cache: KVCache, q, tok_start, ctx_len, mask=None, scale: Optional[
 def attn_shared_workspace(cache: KVCache, n_heads: int, n_tokens: int, n_groups: int, max_tokens: int = MQ_TREE_MAX_TOKENS,
                           stream=None):
     """A zeroed workspace for attn_shared calls with up to n_tokens tokens in all, n_groups groups and max_tokens tokens
-    per sequence (one per stream that runs them).  It serves any call whose workspace is no larger."""
+    per sequence (one per stream that runs them).  It serves any call of attn_shared or attn_tree whose workspace is no
+    larger."""
     torch = _torch()
     handle = _stream_on(stream, cache.device)  # before the size, which goes by the current device
     out = _new(mq_attn_shared_workspace_bytes(cache.struct, n_heads, n_tokens, max_tokens, n_groups), torch.uint8,
@@ -895,8 +896,8 @@ def attn_shared(cache: KVCache, q, tok_start, ctx_len, grp_start, grp_pages, mas
     """attn_tree of a batch whose sequences share the pages of a prefix, each prefix attended once for all.
 
     ``grp_start``: int32 [n_groups + 1], group g are the sequences grp_start[g]..grp_start[g + 1] - 1; ``grp_pages``:
-    int32 [n_groups], the pages at the start of their table rows that are the same for all of them (every context
-    reaches past them).  ``max_pages`` bounds grp_pages (default: what the table can hold).  The rest is attn_tree's;
+    int32 [n_groups], the pages at the start of their table rows that are the same for all of them that have tokens (every
+    such context reaches past them).  ``max_pages`` bounds grp_pages (default: what the table can hold).  The rest is attn_tree's;
     the workspace is attn_shared_workspace's."""
     i32, dev = _torch().int32, cache.device
     a, out = _attn_args(cache, q, tok_start, ctx_len, mask, scale, max_len, max_tokens, out_type, out, stream)
@@ -982,7 +983,7 @@ class KVPool:
     """A cache's pages as a pool (mq_kv_pool), for kv_grow, kv_fork, kv_free and kv_compact, which keep its tensors and
     the cache's table.  ``seq_pages``: int32 [n_seqs], pages of every sequence; ``refs``: int32 [n_pages], table entries
     that name a page; ``free_list``: int32 [n_pages], of which the first ``n_free`` (int32 [1]) are the free pages, the
-    last of them the next to be taken."""
+    last of them the next to be taken.  Calls on one pool must not overlap on the GPU."""
 
     def __init__(self, cache: KVCache, seq_pages, refs, free_list, n_free):
         torch = _torch()

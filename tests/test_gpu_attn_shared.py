@@ -236,6 +236,32 @@ def test_agrees_call_by_call_in_one_workspace(cuda_ready):
         batches[0].call(mq, workspace=ws[:1024])
 
 
+def test_one_workspace_for_this_and_the_tree_attention(cuda_ready):
+    import torch
+    mq = cuda_ready
+    b = [Batch(np.random.default_rng(i), [(20, [(50, t)] * 9)], 28, 4, 128, "q8_0") for i, t in enumerate((1, 2, 9))]
+    caches = [x.cache(mq) for x in b]
+    size = max(mq.attn_shared_workspace(c, 28, sum(x.new), 1, max(x.new)).numel() for x, c in zip(b, caches))
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 1, 0, 2):
+        for tree in (True, False, True):
+            b[i].check(b[i].call(mq, caches[i], workspace=ws, tree=tree))
+    ok_status(mq)
+
+
+def test_sequences_without_tokens_need_no_pages(cuda_ready):
+    # answers that are given up stay in their group: their rows of the table are empty, the first's too
+    mq = cuda_ready
+    b = Batch(np.random.default_rng(3), [(4, [(9, 0), (3, 0), (40, 2), (5, 0), (70, 1)]), (2, [(5, 0), (6, 0)]), (3, [(1, 1)])],
+              28, 4, 128, "q8_0")
+    for s in (0, 1, 3, 5, 6):
+        b.table[s] = -1
+        b.ctx[s] = 0
+    out = b.call(mq)
+    ok_status(mq)
+    b.check(out, only=[2, 4, 7])
+
+
 def test_graph_replay_follows_device_lengths(cuda_ready):
     # a captured call: lengths, groups and prefixes change between replays; two graphs share a workspace
     import torch
