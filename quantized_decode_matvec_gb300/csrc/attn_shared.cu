@@ -11,8 +11,13 @@
 //           key/value head where mq_attn_tree reads it once per sequence;
 //   join    the prefix's parts and the own result of every row, and its output.
 // The prefixes' kernel runs beside the own keys' on the SMs that those leave
-// (programmatic dependence): neither reads what the other writes, and each
-// costs about 10 us of latencies however little it has to do.
+// (programmatic dependence; attn_prefix_sms shares them out): neither reads what
+// the other writes, and each costs about 10 us of latencies however little it has
+// to do.  Where the own keys' parts are joined by a kernel, that comes behind the
+// prefixes' kernel: in front of it its waiting CTAs held the SMs' shared memory.
+// Measured (28 heads on 4 of 128, q8_0, with a q8_0 output's expansion in torch):
+// 64 sequences behind 8192 tokens 43 us (66 one kernel after the other, with a
+// slower join), 4 behind 1000 18.5 (22.7).
 #include "mq_attn.cuh"
 
 namespace mq {

@@ -1,7 +1,7 @@
 // mq_attn_tc.cuh -- attention of many query rows per key/value head (trees of more
 // than a few tokens) over the paged cache, on the tensor cores.
 //
-// The same sums as attn.cu; with dozens to hundreds of query rows per
+// The same sums as mq_attn_rows.cuh; with dozens to hundreds of query rows per
 // key/value head every cached byte is used that often, and the products and
 // the exponentials bound it instead of the cache's bytes.  Per CTA (one per
 // SM, an equal share of all pages, mq_attn.cuh), in steps of two pages:

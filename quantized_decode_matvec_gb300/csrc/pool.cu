@@ -8,7 +8,10 @@
 // work, or one cluster's where all references of the call, or all pages of the
 // pool, have to be looked at; bytes are then copied by a kernel behind it, on all
 // SMs.  Bound by the copied bytes in large calls, by the chain of launches,
-// barriers and dependent loads (page table, count, stack) in small ones.
+// barriers and dependent loads (page table, count, stack) in small ones: a fork of
+// 128 sequences of 500 to 9000 tokens (f16, 36 MB copied) 9.7 us, of 3 5.7; free of
+// 16 sequences 7; a compaction of 4923 pages that moves 142 MB 35, of which the
+// moves are 22 (6.5 TB/s).
 // Nothing on the device is trusted: an entry that contradicts the pool is left
 // out, and sets MQ_DEV_KV_RANGE.
 #include <cooperative_groups.h>

@@ -21,8 +21,10 @@
 // vocabulary, and keeps the sums of its tiles, so that the draw looks into one
 // tile only.  Every CTA walks the tree by itself from the same numbers; they meet
 // where a row's sum is needed, which is once for every refused child, and once
-// more at a node without children.  Bound by those rows' bytes for a batch, and
-// by the chain of loads and barriers for one sequence.
+// more at a node without children.  Bound by the chain of loads, passes and
+// barriers: 131072 values, children refused at the root 0, 1, 2 and 3: one sequence
+// 8.4, 12.4, 18 and 25 us, 64 of them 13.7, 22, 38 and 53 (a pass reads 67 MB then);
+// 64 trees of 16 nodes 47 us.
 #include <cooperative_groups.h>
 
 #include "mq_internal.h"
