@@ -953,19 +953,10 @@ def verify_tree(target, tok_start, token, parent, u=None, draft=None, greedy: bo
     dp, d_ld = (None, 0) if draft is None or greedy else _rows(draft, "draft", f32, dev, vocab, n)
     if u is None and not greedy:
         raise ValueError("u: random numbers are wanted (or greedy)")
-    if path is not None:
-        if path.dim() != 2 or path_ld not in (None, path.shape[1]):
-            raise ValueError(f"path: [{S}, path_ld] is wanted, got {tuple(path.shape)}")
-    else:  # with what else is missing, in one buffer
-        ld = MQ_TREE_MAX_TOKENS if path_ld is None else path_ld
-        if stream is None:
-            new = torch.empty(S * (ld + 2), dtype=i32, device=dev)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-                new = torch.empty(S * (ld + 2), dtype=i32, device=dev)
-        path, left = new[:S * ld].view(S, ld), new[S * ld:]
-        n_path = left[:S] if n_path is None else n_path
-        next_token = left[S:] if next_token is None else next_token
+    if path is None:
+        path = _new((S, MQ_TREE_MAX_TOKENS if path_ld is None else path_ld), i32, dev, stream)
+    elif path.dim() != 2 or path_ld not in (None, path.shape[1]):
+        raise ValueError(f"path: [{S}, path_ld] is wanted, got {tuple(path.shape)}")
     n_path = _new((S,), i32, dev, stream) if n_path is None else n_path
     next_token = _new((S,), i32, dev, stream) if next_token is None else next_token
     a = VerifyArgs(tp, dp, _want(tok_start, "tok_start", i32, (S + 1,), dev), _want(token, "token", i32, (n,), dev),
