@@ -1018,7 +1018,8 @@ mq_status mq_attn_shared(const mq_kv_cache* cache, const mq_attn_args* a, const 
     if (g->max_pages < 0) return MQ_ERR_SHAPE;
     if ((st = check_shared_shape(cache, a->n_heads, a->n_tokens, g->n_groups)) != MQ_OK) return st;
     const double group = a->n_heads / cache->n_kv_heads;
-    if ((a->n_tokens * group / 256 + g->n_groups) * (g->max_pages + 12.0) * cache->n_kv_heads >= 2147483648.0)
+    // (a page counts for three units at most)
+    if ((a->n_tokens * group / 256 + g->n_groups) * (g->max_pages + 12.0) * 3 * cache->n_kv_heads >= 2147483648.0)
         return MQ_ERR_UNSUPPORTED;
     if (none) return MQ_OK;
     if (g->n_groups > 0 && (!g->grp_start || !g->grp_pages)) return MQ_ERR_INVALID_ARG;

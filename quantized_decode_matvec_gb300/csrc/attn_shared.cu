@@ -16,8 +16,9 @@
 // to do.  Where the own keys' parts are joined by a kernel, that comes behind the
 // prefixes' kernel: in front of it its waiting CTAs held the SMs' shared memory.
 // Measured (28 heads on 4 of 128, q8_0, with a q8_0 output's expansion in torch):
-// 64 sequences behind 8192 tokens 43 us (66 one kernel after the other, with a
-// slower join), 4 behind 1000 18.5 (22.7).
+// 64 sequences behind 8192 tokens 44 us (66 one kernel after the other, with a
+// slower join), 4 behind 1000 19 (22.7); f16, 32 heads on 8: 126 behind three of up
+// to 20011 tokens, trees of up to 7, 238 (252).
 #include "mq_attn.cuh"
 
 namespace mq {
@@ -76,6 +77,10 @@ cudaError_t launch_attn_shared(const mq_kv_cache& cache, const mq_attn_args& a, 
     const int64_t blocks = int64_t(a.n_tokens) * p.group / kPrefixRows + g.n_groups;
     const int64_t units = blocks * cache.n_kv_heads * g.max_pages;
     const int prefix_grid = int(units < num_sms ? units : num_sms);
+    // f16: a page of a block of up to 128 rows takes two thirds of the time of one of 256 (one CTA's stretches of equal
+    // pages 137 and 201 us); q8_0: the same, since the conversion of its codes is
+    p.sh.full = cache.type == MQ_TYPE_F16 ? 3 : 1;
+    p.sh.part = cache.type == MQ_TYPE_F16 ? 2 : 1;
     p.sh.sms = num_sms, p.sh.prefix_grid = prefix_grid, p.sh.own_rows = RT;
     cudaError_t e = RT > 16 ? launch_attn_own_tc(cache, p, grid, status, s)
                             : launch_attn_own_rows(cache, p, RT, grid, status, s);

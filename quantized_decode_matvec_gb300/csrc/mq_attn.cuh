@@ -68,6 +68,7 @@ struct AttnShared {
     const int32_t* grp_pages;
     int n_groups, max_pages;
     int sms, prefix_grid, own_rows;  // SMs that the two kernels share out; the second's CTAs; the first's rows of a block
+    int full, part;  // units of a prefix's page in a block of 256 rows, and of up to 128
     unsigned* abort;  // [0]: a wait ran out; [1]: a sequence contradicts the call's bounds or its group
     AttnRows own, prefix;
     int4* blocks;   // per row block and key/value head of the groups: first CTA, CTAs, slot of the first
@@ -237,6 +238,26 @@ __device__ __forceinline__ int attn_groups(const AttnParams& p, const AttnSeq& q
     return p.c.n_kv_heads * ((q.T * p.group + RT - 1) / RT);
 }
 
+// kAttnPrefix: a block of up to 128 rows is one tile of the tensor cores, of more two, so a page of a sequence's last
+// block may count for less
+__device__ __forceinline__ int attn_unit(const AttnParams& p, const AttnSeq& q, int block)
+{
+    return q.T * p.group - block * kPrefixRows > kPrefixRows / 2 ? p.sh.full : p.sh.part;
+}
+// units of a key/value head's blocks of sequence s, and of all heads'
+template <int M>
+__device__ __forceinline__ int attn_head_units(const AttnParams& p, const AttnSeq& q, int RT, int cost)
+{
+    const int blocks = (q.T * p.group + RT - 1) / RT;
+    if (M != kAttnPrefix) return blocks * (q.pages + cost);
+    return ((blocks - 1) * p.sh.full + attn_unit(p, q, blocks - 1)) * q.pages + blocks * cost;
+}
+template <int M>
+__device__ __forceinline__ int attn_units(const AttnParams& p, const AttnSeq& q, int RT, int cost)
+{
+    return p.c.n_kv_heads * attn_head_units<M>(p, q, RT, cost);
+}
+
 // The cut of the line, and where this CTA's stretch starts.
 struct AttnRange {
     int total, ctas;  // all units; the CTAs that take part (each has a unit at least)
@@ -257,14 +278,15 @@ struct AttnRange {
 // The SMs of a call with shared prefixes go to both kernels, x of N to the prefixes', such that they end together:
 //   d + A / x = B / (N - x)
 // in units of a page of the kernel for few rows, 0.45 us; a group is kAttnGroupCost more.  A page of 256 rows on the
-// tensor cores takes two units; of the sequences' own keys there, of few rows mostly, half a one, and a group twice as
-// much (1024 groups of 28 rows and 6 pages, f16: 67 us on 152 SMs).  d: what the prefixes' kernel starts later, and takes
+// tensor cores takes two units; of the sequences' own keys there, of few rows mostly, about half a one, and a group
+// twice as much (1024 groups of 28 rows and 6 pages, f16: 67 us on 152 SMs).  d: what the prefixes' kernel starts later, and takes
 // longer to start and to leave its parts.
 __device__ __forceinline__ float attn_prefix_sms(const AttnParams& p, int pages, int groups, int pre_pages, int pre_groups)
 {
     const bool tc = p.sh.own_rows > 16;
-    const float d = 16.0f, N = float(p.sh.sms), A = 2.0f * (pre_pages + float(kAttnGroupCost) * pre_groups);
-    const float B = (tc ? 0.5f : 1.0f) * pages + (tc ? 2.0f : 1.0f) * kAttnGroupCost * groups;
+    const float d = 16.0f, N = float(p.sh.sms);
+    const float A = 2.0f * (pre_pages / float(p.sh.full) + float(kAttnGroupCost) * pre_groups);
+    const float B = (tc ? 0.55f : 1.0f) * pages + (tc ? 2.2f : 1.0f) * kAttnGroupCost * groups;
     const float b = d * N - A - B;
     return (b + sqrtf(b * b + 4.0f * d * A * N)) / (2.0f * d);
 }
@@ -273,7 +295,7 @@ __device__ __forceinline__ float attn_prefix_sms(const AttnParams& p, int pages,
 // attn_range (kAttnAll: by the one warp that calls it).
 struct AttnTotals {
     int own[(MQ_MAX_SEQS + 31) / 32][2];  // pages and groups of 32 sequences
-    int pages, groups, pre_pages, pre_groups, bad;
+    int pages, groups, pre_pages, pre_groups, bad;  // (pre_pages: their units)
 };
 template <int M>
 __device__ __forceinline__ void attn_totals(const AttnParams& p, AttnTotals* t)
@@ -304,7 +326,7 @@ __device__ __forceinline__ void attn_totals(const AttnParams& p, AttnTotals* t)
         if (32 * i + lane < p.sh.n_groups) {
             if (attn_seq<kAttnPrefix>(p, 32 * i + lane, &q, &bad)) {
                 groups = attn_groups(p, q, kPrefixRows);
-                pages = groups * q.pages;
+                pages = attn_units<kAttnPrefix>(p, q, kPrefixRows, 0);
             }
             any_bad |= bad;
         }
@@ -354,9 +376,11 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, con
             if (t->bad) atomicOr(status, MQ_DEV_KV_RANGE);
         }
     }
-    r.cost = pages > n ? kAttnGroupCost : 0;
+    const int unit = M == kAttnPrefix ? p.sh.full : 1;
+    r.cost = pages > n * unit ? kAttnGroupCost * unit : 0;
     r.total = pages + groups * r.cost;
-    r.ctas = min(r.total, n);
+    // a CTA between others that share a group has a page at least
+    r.ctas = M == kAttnPrefix ? min(max(r.total / unit, min(r.total, 1)), n) : min(r.total, n);
     r.quot = r.ctas ? r.total / r.ctas : 0;
     r.rem = r.total - r.quot * r.ctas;
     r.first = c < r.ctas ? r.begin(c) : r.total;
@@ -374,7 +398,7 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, con
         AttnSeq q;
         bool bad;
         const int mine = attn_seq<M>(p, r.lg, s0 + lane, s0 + lane < attn_seqs<M>(p), &q, &bad)
-                             ? attn_groups(p, q, RT) * (q.pages + r.cost) : 0;
+                             ? attn_units<M>(p, q, RT, r.cost) : 0;
         int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -410,32 +434,50 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, int RT, AttnRange
     for (int u = *at; u < w->last;) {
         AttnSeq q;
         bool bad;
-        const int units = attn_seq<M>(p, w->lg, w->seq, true, &q, &bad) ? attn_groups(p, q, RT) * (q.pages + w->cost) : 0;
+        const int units = attn_seq<M>(p, w->lg, w->seq, true, &q, &bad) ? attn_units<M>(p, q, RT, w->cost) : 0;
         if (u >= w->seq_first + units) {
             w->seq_first += units;
             if (++w->seq >= attn_seqs<M>(p)) return false;  // not reached unless the lengths change under the call
             continue;
         }
-        const int blocks = (q.T * p.group + RT - 1) / RT, span = q.pages + w->cost;
-        const int k = u - w->seq_first < span ? 0 : (u - w->seq_first) / span;  // group within the sequence
-        const int g0 = w->seq_first + k * span, g1 = g0 + q.pages;
-        if (u >= g1) {
-            u = g0 + span;
+        const int blocks = (q.T * p.group + RT - 1) / RT;
+        int g0, end, unit = 1, head, block;  // the group's first unit, its end, units of a page
+        if constexpr (M == kAttnPrefix) {
+            const int of_head = units / p.c.n_kv_heads, span = p.sh.full * q.pages + w->cost, in = u - w->seq_first;
+            head = in / of_head;
+            block = min((in - head * of_head) / span, blocks - 1);
+            unit = attn_unit(p, q, block);
+            g0 = w->seq_first + head * of_head + block * span;
+            end = g0 + unit * q.pages + w->cost;
+        } else {
+            const int span = q.pages + w->cost;
+            const int k = u - w->seq_first < span ? 0 : (u - w->seq_first) / span;  // group within the sequence
+            g0 = w->seq_first + k * span;
+            end = g0 + span;
+            head = blocks == 1 ? k : k / blocks;
+            block = k - head * blocks;
+        }
+        const int g1 = g0 + unit * q.pages;
+        // a page is the CTA's that has its first unit
+        int from = u - g0, to = min(g1, w->last) - g0;
+        if constexpr (M == kAttnPrefix) from = (from + unit - 1) / unit, to = (to + unit - 1) / unit;
+        if (u >= g1 || from >= to) {
+            u = w->last >= g1 ? end : w->last;
             continue;
         }
         g->seq = q.row;
         g->skip = M == kAttnPrefix ? w->seq : q.skip;
         g->t0 = q.t0, g->T = q.T, g->ctx = q.ctx;
-        g->head = blocks == 1 ? k : k / blocks;
-        g->row0 = (k - g->head * blocks) * RT;
-        g->page0 = u - g0;
-        g->n = min(g1, w->last) - u;
-        const bool whole = g0 >= w->first && g1 <= w->last;
+        g->head = head;
+        g->row0 = block * RT;
+        g->page0 = from;
+        g->n = to - from;
+        const bool whole = from == 0 && to == q.pages;
         g->cta0 = whole ? int(blockIdx.x) : w->owner(g0);
-        g->n_ctas = whole ? 1 : w->owner(g1 - 1) - g->cta0 + 1;
+        g->n_ctas = whole ? 1 : w->owner(g1 - unit) - g->cta0 + 1;
         g->slot0 = g0 > w->begin(g->cta0) ? 1 : 0;
         g->slot = u > w->first ? 1 : 0;
-        *at = u + g->n;
+        *at = min(g0 + unit * to, w->last);
         return true;
     }
     return false;

@@ -974,11 +974,16 @@ cudaError_t launch_tc_join(const AttnParams& p, int grid, unsigned* status, cuda
 template <int D, bool Q8, int M>
 cudaError_t launch_tc(const AttnParams& p, int grid, unsigned* status, cudaStream_t s)
 {
-    if constexpr (M == kAttnPrefix)  // beside the kernel before it
+    if constexpr (M == kAttnPrefix) {  // beside the kernel before it
         return attn_launch_pdl(attn_tc_kernel<D, Q8, M>, dim3(grid), kTcThreads, TcCfg<D, Q8>::kSmem, p, status, s);
-    attn_tc_kernel<D, Q8, M><<<grid, kTcThreads, TcCfg<D, Q8>::kSmem, s>>>(p, status);
-    const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess || M != kAttnAll ? e : launch_tc_join<D, M>(p, grid, status, s);
+    } else {
+        attn_tc_kernel<D, Q8, M><<<grid, kTcThreads, TcCfg<D, Q8>::kSmem, s>>>(p, status);
+        const cudaError_t e = cudaGetLastError();
+        if constexpr (M == kAttnAll)
+            return e != cudaSuccess ? e : launch_tc_join<D, M>(p, grid, status, s);
+        else
+            return e;
+    }
 }
 
 template <int M>
