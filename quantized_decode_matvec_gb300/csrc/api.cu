@@ -22,7 +22,6 @@ cudaError_t set_gemm_attributes(int max_smem);
 cudaError_t set_mmq_attributes(int max_smem);
 cudaError_t set_attn_attributes(int max_smem);
 cudaError_t set_attn_shared_attributes();
-cudaError_t set_softmax_attributes();
 cudaError_t set_verify_attributes();
 void plan_ring(MvPlan& q, int64_t units, int kind, int nc, const DeviceInfo& dev, int64_t unit_bytes,
                bool allow_cols);
@@ -451,7 +450,6 @@ cudaError_t set_kernel_attributes(int max_smem)
     if (e == cudaSuccess) e = set_mmq_attributes(max_smem);
     if (e == cudaSuccess) e = set_attn_attributes(max_smem);
     if (e == cudaSuccess) e = set_attn_shared_attributes();
-    if (e == cudaSuccess) e = set_softmax_attributes();
     if (e == cudaSuccess) e = set_verify_attributes();
     return e;
 }

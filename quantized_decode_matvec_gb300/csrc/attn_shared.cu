@@ -16,9 +16,9 @@
 // to do.  Where the own keys' parts are joined by a kernel, that comes behind the
 // prefixes' kernel: in front of it its waiting CTAs held the SMs' shared memory.
 // Measured (28 heads on 4 of 128, q8_0, with a q8_0 output's expansion in torch):
-// 64 sequences behind 8192 tokens 44 us (66 one kernel after the other, with a
-// slower join), 4 behind 1000 19 (22.7); f16, 32 heads on 8: 126 behind three of up
-// to 20011 tokens, trees of up to 7, 238 (252).
+// 64 sequences behind 8192 tokens 44 us (39 alone, where mq_attn_tree takes 98; 66
+// one kernel after the other, with a slower join), 4 behind 1000 19 (22.7); f16, 32
+// heads on 8: 126 behind three of up to 20011 tokens, trees of up to 7, 238 (252).
 #include "mq_attn.cuh"
 
 namespace mq {

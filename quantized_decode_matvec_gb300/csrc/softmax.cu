@@ -4,16 +4,17 @@
 //   y_i = 2^((x_i - m) k) / sum_j 2^((x_j - m) k),   m = max x,  k = scale * log2(e)
 //
 // Bound by its bytes, so a row passes through the chip once: a cluster of up to
-// eight (long rows: 16) CTAs holds it in registers.  Each CTA forms its own maximum and, with
+// eight CTAs holds it in registers.  Each CTA forms its own maximum and, with
 // that, its exponentials and their sum; the (maximum, sum) pairs go round the
 // cluster through distributed shared memory (one barrier), and what is left is a
-// factor per CTA.  Rows longer than 16 CTAs hold are read twice.
+// factor per CTA.  Rows longer than eight CTAs hold are read twice
+// (again from L2: no more rows are on the chip at once than it holds).
 // A CTA calls for the part of a later row when it starts, so HBM is read while
 // others reduce and store.  Measured: 512 x 131072 110 us, 4.9 TB/s (124 without
 // the prefetch; 244 with one CTA per SM); 512 x 50001 53 us, 7 x 50001 4.6 us.
-// Clusters of 16 hold rows of up to 262144 (256 of them 147 us, 3.7 TB/s) and are
-// slower to place: 512 x 131071 took 240 us by 16 CTAs and takes 125 by eight with
-// a ninth unit per thread.
+// Clusters of 16, which would hold rows of up to 262144, are slower to place: 256 x
+// 200003 140 us, read twice by clusters of eight 123; 512 x 131071 240, and by eight
+// with a ninth unit per thread 125.
 // (x - m) k is formed from k in two parts, so the exponent's error is that of
 // x - m alone.  Maxima, exponentials and sums are fp32.
 #include <cooperative_groups.h>
@@ -29,7 +30,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 16;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
 
 struct SoftmaxArgs {
     const float* x;
@@ -203,16 +204,6 @@ cudaError_t launch(const SoftmaxArgs& p, int64_t rows, int C, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t set_softmax_attributes()
-{
-    cudaError_t e = cudaSuccess;
-#define MQ_SET(NV) \
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(softmax_kernel<NV>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    MQ_SET(0) MQ_SET(1) MQ_SET(2) MQ_SET(4) MQ_SET(8) MQ_SET(9)
-#undef MQ_SET
-    return e;
-}
-
 cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_t x_ld, int64_t y_ld, float scale,
                            int num_sms, cudaStream_t s)
 {
@@ -224,10 +215,10 @@ cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_
     const bool whole = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && x_ld % 4 == 0;  // every row starts a unit
     const int64_t units = (int64_t(vocab) + (whole ? 3 : 6)) / 4;
     int C = 1;
-    while (C < kMaxCluster && (units > int64_t(C) * kThreads * (C < 8 ? 8 : 9) || (int64_t(rows) * C * 2 <= num_sms && units > C * kThreads)))
+    while (C < kMaxCluster && (units > int64_t(C) * kThreads * 8 || (int64_t(rows) * C * 2 <= num_sms && units > C * kThreads)))
         C *= 2;
-    p.ahead = 2 * num_sms / C;
     const int64_t per = ((units + C - 1) / C + kThreads - 1) / kThreads;  // units of a thread
+    p.ahead = 2 * num_sms / C;
     if (per <= 1) return launch<1>(p, rows, C, s);
     if (per <= 2) return launch<2>(p, rows, C, s);
     if (per <= 4) return launch<4>(p, rows, C, s);
