@@ -302,3 +302,27 @@ def test_alloc_and_captured_calls(cuda_ready):
         m.release(e, [0, 0])
         m.compact()
         p.same(m)
+
+
+def test_on_a_given_stream(cuda_ready):
+    # by its handle, behind what it is doing
+    import torch
+    mq = cuda_ready
+    m = Model(40, 5, 8, "f16", 2, 64, np.random.default_rng(4))
+    p = Pool(mq, m)
+    side = torch.cuda.Stream()
+    lens, src, dst, n, gone = i32([200, 70, 0, 0, 0]), i32([0, 1]), i32([4, 2]), i32([130, 70]), i32([1])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(int(2e8))
+    h = side.cuda_stream
+    mq.kv_grow(p.cache, p.pool, lens, stream=h)
+    mq.kv_fork(p.cache, p.pool, src, dst, n, stream=h)
+    mq.kv_free(p.cache, p.pool, gone, stream=h)
+    mq.kv_compact(p.cache, p.pool, stream=h)
+    assert not side.query()
+    m.grow([200, 70, 0, 0, 0])
+    m.fork([0, 1], [4, 2], [130, 70])
+    m.release([1], [0])
+    m.compact()
+    p.same(m)

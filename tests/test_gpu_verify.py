@@ -281,3 +281,34 @@ def test_large_vocabulary_in_many_tiles(cuda_ready):
             assert int(last) == i, (i, kw)
         x[0, i] = 1e-12
     ok_status(mq)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_on_a_given_stream_and_captured(cuda_ready, handle):
+    # behind what the stream is doing; a captured call follows the numbers
+    import torch
+    mq = cuda_ready
+    rng = np.random.default_rng(29)
+    target, draft, start, token, parent, u = batch(rng, [9, 4, 16], 3000, 0.5)
+    d = dict(target=dev(target), draft=dev(draft), start=dev(start), token=dev(token), parent=dev(parent), u=dev(u))
+    call = lambda **k: mq.verify_tree(d["target"], d["start"], d["token"], d["parent"], u=d["u"], draft=d["draft"], path_ld=8, **k)
+    want = call()
+    side = torch.cuda.Stream()
+    on = side.cuda_stream if handle else side
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(int(2e8))
+    got = call(stream=on)
+    assert not side.query()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        call(stream=on, path=got[0], n_path=got[1], next_token=got[2])
+    for _ in range(3):
+        d["u"].uniform_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, call()))
+    ok_status(mq)
