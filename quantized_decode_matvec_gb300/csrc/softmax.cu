@@ -10,16 +10,16 @@
 // factor per CTA.  Rows longer than eight CTAs hold are read twice
 // (again from L2: no more rows are on the chip at once than it holds).
 // A CTA calls for the part of a later row when it starts, so HBM is read while
-// others reduce and store.  Measured: 512 x 131072 110 us, 4.9 TB/s (124 without
-// the prefetch; 244 with one CTA per SM); 512 x 50001 53 us, 7 x 50001 4.6 us.
+// others reduce and store.  Measured: 512 x 131072 98 us, 5.5 TB/s; 512 x 131071
+// 109, 512 x 50001 46, 7 x 50001 4.2.  An earlier form took 124 us for the first
+// without the prefetch and 110 with it, and 244 with one CTA per SM.
 // Clusters of 16, which would hold rows of up to 262144, are slower to place: 256 x
-// 200003 140 us, read twice by clusters of eight 123; 512 x 131071 240, and by eight
-// with a ninth unit per thread 125.
-// (x - m) k is formed from k in two parts, so the exponent's error is that of
-// x - m alone.  Maxima, exponentials and sums are fp32.
+// 200003 140 us, read twice by clusters of eight 117; 512 x 131071 240.
+// Maxima, exponentials and sums are fp32; x - m, its product with k and k itself
+// are rounded once each, relative to |x - m|, and the exponential is the hardware's
+// (2^-22).  (With exp2f and k in two parts a value took 31 instructions, and their
+// issue bound the kernel.)
 #include <cooperative_groups.h>
-
-#include <utility>
 
 #include "mq_internal.h"
 #include "mq_tma.cuh"
@@ -37,15 +37,16 @@ struct SoftmaxArgs {
     float* y;
     int64_t x_ld, y_ld;
     int vocab;
-    float k_hi, k_lo;
+    float k;
     int rows, ahead;  // rows that are on the chip at once: a later one's part is called for when a CTA starts
 };
 
-// 2^(d k); -inf is kept from meeting the two parts' signs, and NaN stays
+// 2^(d k): -inf gives 0, NaN stays
 __device__ __forceinline__ float exp_of(float d, const SoftmaxArgs& p)
 {
-    d = d < -1e30f ? -1e30f : d;
-    return exp2f(fmaf(d, p.k_hi, d * p.k_lo));
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * p.k));
+    return y;
 }
 
 // A larger maximum scales a sum by this; of a part that saw nothing (maximum -inf beside a finite one), 0.
@@ -79,7 +80,8 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
     __shared__ float max_s[kWarps], sum_s[kWarps];
     __shared__ float2 part_s[kMaxCluster];  // every CTA's maximum and sum
     cg::cluster_group cl = cg::this_cluster();
-    auto started = cl.barrier_arrive();  // the others' shared memory is written once they run
+    // the others' shared memory is written once they run; nothing else has to be seen, so no fence
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int C = int(cl.num_blocks()), rank = int(cl.block_rank());
     const int64_t row = blockIdx.x / C;
     const float* const x = p.x + row * p.x_ld;
@@ -117,12 +119,20 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
     }
     float v[NV > 0 ? NV : 1][4];
     float m = -INFINITY, l = 0.0f;
+    // no unit of the part reaches past the row's ends: no test per unit but that there is one
+    const bool inner = same && 4 * first >= off && 4 * last - off <= p.vocab;
     if constexpr (NV > 0) {
+        const float4* const at = reinterpret_cast<const float4*>(x - off) + first + threadIdx.x;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int u = first + j * kThreads + int(threadIdx.x);
             if (u < last) {
-                load(u, v[j]);
+                if (inner) {
+                    const float4 w = __ldcs(at + j * kThreads);
+                    v[j][0] = w.x, v[j][1] = w.y, v[j][2] = w.z, v[j][3] = w.w;
+                } else {
+                    load(u, v[j]);
+                }
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[j][e] = -INFINITY;
@@ -159,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
         m = top;
     }
     l = cta_reduce<false>(l, sum_s);
-    cl.barrier_wait(std::move(started));
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (int(threadIdx.x) < C) *cl.map_shared_rank(&part_s[rank], threadIdx.x) = make_float2(m, l);
     cl.sync();
     float top = -INFINITY, sum = 0.0f;
@@ -167,13 +177,18 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
     for (int c = 0; c < C; ++c) sum += part_s[c].y == 0.0f ? 0.0f : part_s[c].y * factor(part_s[c].x, top, p);
     if constexpr (NV > 0) {
         // a row of -inf alone: 0 / 0
-        const float f = sum == 0.0f ? 0.0f : m == -INFINITY ? 0.0f : factor(m, top, p), inv = 1.0f / sum;
+        float4* const to = reinterpret_cast<float4*>(y - off) + first + threadIdx.x;
+        const float f = (sum == 0.0f || m == -INFINITY ? 0.0f : factor(m, top, p)) * (1.0f / sum);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int u = first + j * kThreads + int(threadIdx.x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[j][e] = v[j][e] * f * inv;
-            if (u < last) store(u, v[j]);
+            for (int e = 0; e < 4; ++e) v[j][e] *= f;
+            if (inner) {
+                if (u < last) *(to + j * kThreads) = make_float4(v[j][0], v[j][1], v[j][2], v[j][3]);
+            } else if (u < last) {
+                store(u, v[j]);
+            }
         }
     } else {
         const float inv = 1.0f / sum, base = top == -INFINITY ? 0.0f : top;
@@ -207,10 +222,7 @@ cudaError_t launch(const SoftmaxArgs& p, int64_t rows, int C, cudaStream_t s)
 cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_t x_ld, int64_t y_ld, float scale,
                            int num_sms, cudaStream_t s)
 {
-    SoftmaxArgs p = {x, y, x_ld, y_ld, vocab, 0.0f, 0.0f, rows, 0};
-    const double k = double(scale) * 1.4426950408889634074;
-    p.k_hi = float(k);
-    p.k_lo = float(k - double(p.k_hi));
+    SoftmaxArgs p = {x, y, x_ld, y_ld, vocab, float(double(scale) * 1.4426950408889634074), rows, 0};
     // the fewest CTAs that hold a row at 32 values per thread; more while SMs are idle and each has values left
     const bool whole = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && x_ld % 4 == 0;  // every row starts a unit
     const int64_t units = (int64_t(vocab) + (whole ? 3 : 6)) / 4;

@@ -1,8 +1,8 @@
 """softmax of rows against 64 bits.
 
-Bound, relative to the reference: an exponent is (x - m) k with x - m rounded once and the product once (2^-24 each of
-|x - max| scale, as a relative error of the exponential), twice where a CTA's own maximum stands between; exp2f and
-three products 2^-21; the sum of up to 64 values per thread, then of 5 + 16 + 8 levels, 2^-17.  2^-126 absolute, where
+Bound, relative to the reference: an exponent is (x - m) k with x - m and the product rounded once (2^-24 each of
+|x - max| scale, as a relative error of the exponential) and k to 2^-25, in two steps that add up to x - max where a CTA's
+own maximum stands between: 2.5 * 2^-24; two exponentials and three products 2^-21; the sum of up to 64 values per thread, then of 5 + 16 + 8 levels, 2^-17.  2^-126 absolute, where
 the factors are below the normal range.
 """
 import numpy as np
