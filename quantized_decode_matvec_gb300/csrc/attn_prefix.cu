@@ -10,7 +10,9 @@ namespace {
 // prefixes' kernel's CTAs left (or, of a block that one CTA finished, its rows), and what the sequences' own keys gave,
 // which lies by row too.  With a running maximum, so that a part's values need not wait for the maxima of the others.
 
-// the row block that a CTA of either kernel is for, before anything is read that another kernel writes; false: none
+// the row block that a CTA of either kernel is for, before anything is read that another kernel writes; false: none.
+// Whoever comes after this kernel takes its end for the call's, so every CTA of it waits for the kernels before, those
+// without rows too: where no group has any (no pages, no tokens) there are no others.
 __device__ __forceinline__ bool join_block(const AttnParams& p, int* grp_s, AttnSegment* g, int* group)
 {
     if (threadIdx.x == 0) *grp_s = -1;
@@ -100,7 +102,10 @@ __global__ void __launch_bounds__(32 * kFewWarps) attn_shared_join_few_kernel(co
     __shared__ int grp_s;
     AttnSegment g;
     int k;
-    if (!join_block(p, &grp_s, &g, &k)) return;
+    if (!join_block(p, &grp_s, &g, &k)) {
+        griddep_wait();
+        return;
+    }
     const int z = int(blockIdx.z) * kFewWarps + int(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int slab = z / (D / 32) * 32, rows = min(kPrefixRows, g.T * p.group - g.row0);
     const int row = min(slab + lane, rows - 1);
@@ -140,9 +145,12 @@ __global__ void __launch_bounds__(32 * kManyWarps) attn_shared_join_kernel(const
     const int slab = int(blockIdx.z) / (D / 32) * 32, d0 = int(blockIdx.z) % (D / 32) * 32;
     AttnSegment g;
     int k;
-    if (!join_block(p, &grp_s, &g, &k)) return;
-    const int rows = min(kPrefixRows, g.T * p.group - g.row0);
-    if (slab >= rows) return;
+    const bool any = join_block(p, &grp_s, &g, &k);
+    const int rows = any ? min(kPrefixRows, g.T * p.group - g.row0) : 0;
+    if (slab >= rows) {
+        griddep_wait();
+        return;
+    }
     const int row = min(slab + lane, rows - 1);
     JoinParts<D> parts = {p, {}, attn_place(p, g, g.row0 + row), row, d0};
     griddep_wait();

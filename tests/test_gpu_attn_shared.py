@@ -395,3 +395,45 @@ def test_on_a_given_stream_beside_another_call(cuda_ready):
     torch.cuda.synchronize()
     ok_status(mq)
     assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("ctype", ["q8_0", "f16"])
+@pytest.mark.parametrize("T", [1, 2, 40])
+@pytest.mark.parametrize("where", ["no pages", "no tokens"])
+def test_call_in_which_no_group_has_work_ends_when_its_outputs_are_written(cuda_ready, ctype, T, where):
+    # groups without pages, or without tokens beside sequences in no group: the join has no rows, and the own keys'
+    # kernel writes all there is.  In a graph the copy behind the call, and the next call in the same workspace, start
+    # when the call ends.  (7, 14 and 280 query rows of a key/value head: each of the kernels)
+    import torch
+    mq = cuda_ready
+    own = [(5000, T), (70, T), (2000, T)]
+    groups = [(0, own), (0, [(9, T)])] if where == "no pages" else [(0, own), (3, [(9, 0), (70, 0)])]
+    b = Batch(np.random.default_rng(T), groups, 28, 4, 128, ctype, lead=where != "no pages")
+    cache, n = b.cache(mq), sum(b.new)
+    args = (cache, dev(b.q), dev(b.start), dev(np.array(b.ctx, np.int32)), dev(b.grp_start), dev(b.grp_pages))
+    kw = dict(mask=dev(as_i64([x for s in b.bits for x in s])), max_len=6000, max_tokens=T, max_pages=4,
+              workspace=mq.attn_shared_workspace(cache, 28, n, len(b.grp_pages), T))
+    out = torch.empty((n, 28 * 128), dtype=torch.float16, device="cuda")
+    got = [torch.empty_like(out) for _ in range(4)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        mq.attn_shared(*args, out=out, **kw)
+    side.synchronize()
+    ok_status(mq)
+    b.check(out)
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        for x in got:
+            out.fill_(3.0)
+            mq.attn_shared(*args, out=out, **kw)
+            x.copy_(out)
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want) for x in got)
+    ok_status(mq)
