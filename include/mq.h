@@ -499,7 +499,8 @@ mq_status mq_attn_tree(const mq_kv_cache* h_cache, const mq_attn_args* h_args, v
  * prefix in common.  Group g are the sequences grp_start[g]..grp_start[g+1]-1:
  * the first grp_pages[g] pages of the table are the same for all of them that
  * have tokens (those of the first of these are read), and each of these has at
- * least 64 * grp_pages[g] tokens of context.  grp_start must not decrease; sequences in no
+ * least 64 * grp_pages[g] tokens of context.  grp_start must not decrease (where it
+ * does nothing is written: MQ_DEV_KV_RANGE); sequences in no
  * group, and those of a group with 0 pages, have no prefix in common.  The
  * result is mq_attn_tree's up to rounding, and so are the rules for what a node
  * sees, for masks, infinities and NaN.  A sequence that contradicts its group,

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) attn_shared_join_few_kernel(co
     griddep_wait();
     parts.b = __ldcg(p.sh.blocks + attn_block(p, k, g.t0, g.row0, g.head));
     const uint2 flags = __ldcg(reinterpret_cast<const uint2*>(p.sh.abort));
-    if (flags.x || slab >= rows) return;  // a wait ran out: nothing of the call's outputs is known to be whole
+    // a wait ran out: nothing of the call's outputs is known to be whole; or nothing was done
+    if (flags.x || (flags.y & kAttnBadOrder) || slab >= rows) return;
     JoinSum sum;
     for (int c = 0; c < parts.count(); ++c) {
         float m, l;
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(32 * kManyWarps) attn_shared_join_kernel(const
     griddep_wait();
     parts.b = __ldcg(p.sh.blocks + attn_block(p, k, g.t0, g.row0, g.head));
     const uint2 flags = __ldcg(reinterpret_cast<const uint2*>(p.sh.abort));
-    if (flags.x) return;
+    if (flags.x || (flags.y & kAttnBadOrder)) return;
     const int n = parts.count();
     JoinSum own;
     for (int c = warp; c < n; c += W) {

@@ -63,13 +63,17 @@ struct AttnRows {
     float* o;  // [rows][D]
 };
 
+// what the device's data contradicts: a sequence the call's bounds or its group (it is skipped), or the groups the order
+// of grp_start, so that a sequence might lie in two of them (the whole call is skipped)
+constexpr int kAttnBadSeq = 1, kAttnBadOrder = 2;
+
 struct AttnShared {
     const int32_t* grp_start;
     const int32_t* grp_pages;
     int n_groups, max_pages;
     int sms, prefix_grid, own_rows;  // SMs that the two kernels share out; the second's CTAs; the first's rows of a block
     int full, part;  // units of a prefix's page in a block of 256 rows, and of up to 128
-    unsigned* abort;  // [0]: a wait ran out; [1]: a sequence contradicts the call's bounds or its group
+    unsigned* abort;  // [0]: a wait ran out; [1]: kAttnBadSeq, kAttnBadOrder
     AttnRows own, prefix;
     int4* blocks;   // per row block and key/value head of the groups: first CTA, CTAs, slot of the first
 };
@@ -296,7 +300,7 @@ __device__ __forceinline__ float attn_prefix_sms(const AttnParams& p, int pages,
 // attn_range (kAttnAll: by the one warp that calls it).
 struct AttnTotals {
     int own[(MQ_MAX_SEQS + 31) / 32][2];  // pages and groups of 32 sequences
-    int pages, groups, pre_pages, pre_groups, bad;  // (pre_pages: their units)
+    int pages, groups, pre_pages, pre_groups, bad;  // (pre_pages: their units; bad: kAttnBadSeq, kAttnBadOrder)
 };
 template <int M>
 __device__ __forceinline__ void attn_totals(const AttnParams& p, AttnTotals* t)
@@ -306,7 +310,9 @@ __device__ __forceinline__ void attn_totals(const AttnParams& p, AttnTotals* t)
     __syncthreads();
     const AttnLaneGroup lg = attn_lane_group(p);
     AttnSeq q;
-    bool bad, any_bad = false;
+    bool bad, any_bad = false, order = false;
+    for (int k = threadIdx.x; k < p.sh.n_groups; k += blockDim.x)
+        order |= __ldg(p.sh.grp_start + k + 1) < __ldg(p.sh.grp_start + k);
     for (int i = warp; 32 * i < p.c.n_seqs; i += warps) {
         int pages = 0, groups = 0;
         if (attn_seq<kAttnOwn>(p, lg, 32 * i + lane, 32 * i + lane < p.c.n_seqs, &q, &bad)) {
@@ -338,7 +344,7 @@ __device__ __forceinline__ void attn_totals(const AttnParams& p, AttnTotals* t)
             atomicAdd(&t->pre_groups, groups);
         }
     }
-    if (any_bad) t->bad = 1;
+    if (any_bad || order) atomicOr(&t->bad, (any_bad ? kAttnBadSeq : 0) | (order ? kAttnBadOrder : 0));
     __syncthreads();
 }
 
@@ -372,6 +378,7 @@ __device__ __forceinline__ AttnRange attn_range(const AttnParams& p, int RT, con
         n = min(n, max(M == kAttnOwn ? take : p.sh.sms - take, 1));
         pages = M == kAttnPrefix ? t->pre_pages : t->pages;
         groups = M == kAttnPrefix ? t->pre_groups : t->groups;
+        if (t->bad & kAttnBadOrder) pages = groups = 0;
         if (M == kAttnOwn && c == 0 && lane == 0) {
             p.sh.abort[1] = t->bad;  // the join looks closer then
             if (t->bad) atomicOr(status, MQ_DEV_KV_RANGE);

@@ -456,3 +456,25 @@ def test_prefix_of_more_pages_than_a_context_can_have(cuda_ready, T):
         assert mq.mq_read_device_status(0) == mq.MQ_DEV_KV_RANGE
         b.check(out, only=[2])
         assert (out[:2 * T] == 3).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 40])
+@pytest.mark.parametrize("groups", [3, 50])
+def test_groups_out_of_order_are_reported_and_write_nothing(cuda_ready, T, groups):
+    # two groups over the same sequences, the one between them empty backwards: whose prefix it is cannot be told
+    import torch
+    mq = cuda_ready
+    b = Batch(np.random.default_rng(T), [(2, [(30, T), (5, T)]), (1, [(70, T)])], 8, 2, 64, "f16")
+    good = b.grp_start, b.grp_pages
+    cache = b.cache(mq)
+    ws = mq.attn_shared_workspace(cache, 8, 3 * T, groups, T)
+    b.grp_start = np.array([0] * (groups - 2) + [3, 0, 3], np.int32)
+    b.grp_pages = np.array([0] * (groups - 3) + [2, 0, 1], np.int32)
+    out = torch.full((3 * T, 8 * 64), 3.0, dtype=torch.float16, device="cuda")
+    b.call(mq, cache, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    assert mq.mq_read_device_status(0) == mq.MQ_DEV_KV_RANGE and (out == 3).all()
+    b.grp_start, b.grp_pages = good
+    b.call(mq, cache, out=out, workspace=ws)
+    ok_status(mq)
+    b.check(out)
