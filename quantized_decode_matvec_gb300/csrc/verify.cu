@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
         sm.kids[tid] = 0;
         if (!greedy) {
             sm.u[tid] = __ldg(p.a.u + t0 + tid);
-            sm.p[tid] = ok ? __ldg(p.a.target + (t0 + par) * p.a.target_ld + tok) : 0.0f;
-            sm.q[tid] = ok && p.a.draft ? __ldg(p.a.draft + (t0 + par) * p.a.draft_ld + tok) : 1.0f;
+            // of the numbers that the sums are of, too: NaN and what is below 0 are 0, above 1 is 1
+            sm.p[tid] = ok ? __saturatef(__ldg(p.a.target + (t0 + par) * p.a.target_ld + tok)) : 0.0f;
+            sm.q[tid] = ok && p.a.draft ? __saturatef(__ldg(p.a.draft + (t0 + par) * p.a.draft_ld + tok)) : 1.0f;
         }
     }
     // the CTA's places in a row that starts `off` values behind a 16-byte boundary

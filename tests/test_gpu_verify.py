@@ -312,3 +312,33 @@ def test_on_a_given_stream_and_captured(cuda_ready, handle):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, call()))
     ok_status(mq)
+
+
+@pytest.mark.parametrize("mode", ["draft", "lookup"])
+def test_odd_numbers_at_drafted_tokens(cuda_ready, mode):
+    # NaN, infinities, negative and large values where a child is tested: the same numbers there as in the sums
+    mq = cuda_ready
+    rng = np.random.default_rng(31)
+    odd = np.array([np.nan, np.inf, -np.inf, -0.5, -2.0**-20, 3.0, 1.5, -0.0], np.float32)
+    clean = lambda x: None if x is None else np.clip(np.where(np.isnan(x), 0, x), 0, 1).astype(np.float32)
+    ends = set()
+    for V in (5, 40, 700):
+        sizes = [16] * 24
+        target, draft, start, token, parent, u = batch(rng, sizes, V, 2.0, mode == "lookup")
+        for s, t in enumerate(sizes):
+            for i in range(1, t):
+                row = start[s] + parent[start[s] + i]
+                if rng.random() < 0.4:
+                    target[row, token[start[s] + i]] = rng.choice(odd)
+                if draft is not None and rng.random() < 0.4:
+                    draft[row, token[start[s] + i]] = rng.choice(odd)
+        path, n_path, last = (x.cpu().numpy() for x in mq.verify_tree(
+            dev(target), dev(start), dev(token), dev(parent), u=dev(u), draft=None if draft is None else dev(draft), path_ld=16))
+        ok_status(mq)
+        P, Q = clean(target), clean(draft)
+        for s in range(len(sizes)):
+            a, b = start[s], start[s + 1]
+            want, tok = walk(P[a:b], None if Q is None else Q[a:b], token[a:b], parent[a:b], u[a:b], 16)
+            assert path[s, :n_path[s]].tolist() == want and last[s] == tok, (V, s, path[s], want, last[s], tok)
+            ends.add(len(want))
+    assert len(ends) > 2
