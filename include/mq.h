@@ -562,7 +562,8 @@ mq_status mq_softmax(const float* x, float* y, int32_t rows, int32_t vocab, int6
  * without nodes has n_path 0 and next -1.
  * Probabilities are >= 0 (what is not counts as 0, above 1 as 1) and u in [0, 1).
  * Sums are of integers, probabilities being rounded to multiples of 2^-46; a
- * test of a child is made in fp64.
+ * test of a child is made in fp64.  Where a sum comes to 2^17 or more the walk
+ * ends, and next is -1: MQ_DEV_KV_RANGE.
  * A node whose parent or token is outside its range is never accepted, a
  * sequence whose nodes are is not written: MQ_DEV_KV_RANGE.
  * vocab <= 2^28.  One launch. */

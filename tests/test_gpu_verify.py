@@ -342,3 +342,38 @@ def test_odd_numbers_at_drafted_tokens(cuda_ready, mode):
             assert path[s, :n_path[s]].tolist() == want and last[s] == tok, (V, s, path[s], want, last[s], tok)
             ends.add(len(want))
     assert len(ends) > 2
+
+
+def test_rows_that_sum_to_too_much(cuda_ready):
+    # 2^17 - 1 is drawn from, exactly; from 2^17 on a row holds no probabilities: the walk ends there, and says so
+    import torch
+    mq = cuda_ready
+    V = 2**18 + 4099
+    start, zero2 = dev(np.array([0, 2], np.int32)), dev(np.zeros(2, np.int32))
+    target = torch.zeros((2, V), device="cuda")
+    token = dev(np.array([0, V - 1], np.int32))
+    draft = torch.zeros((2, V), device="cuda")
+    for ones in (2**17 - 1, 2**17, 2**18, V - 1):
+        for value in (1.0, 7.0):  # above 1 is 1
+            target[:] = 0
+            target[0, 1:1 + ones] = value
+            target[0, V - 1] = 0  # the child's: refused
+            held = min(ones, V - 2)
+            for u0 in (0.0, 0.5, 1 - 2.0**-24):
+                for d in (None, draft):
+                    path, n_path, last = mq.verify_tree(target, start, token, zero2, u=dev(np.array([u0, 0.5], np.float32)),
+                                                        draft=d, path_ld=4)
+                    torch.cuda.synchronize()
+                    st = mq.mq_read_device_status(0)
+                    assert path.tolist() == [[0, 0, 0, 0]] and n_path.tolist() == [1]
+                    if held < 2**17:
+                        assert st == 0 and int(last) == 1 + int(u0 * held), (ones, u0)
+                    else:
+                        assert st == mq.MQ_DEV_KV_RANGE and int(last) == -1, (ones, u0)
+    # the largest vocabulary, all ones
+    if torch.cuda.mem_get_info()[0] > 3 * 2**30:
+        target = torch.ones((1, 2**28), device="cuda")
+        _, _, last = mq.verify_tree(target, start[:1].repeat(2) + dev(np.array([0, 1], np.int32)), zero2[:1], zero2[:1],
+                                    u=dev(np.array([0.5], np.float32)))
+        torch.cuda.synchronize()
+        assert mq.mq_read_device_status(0) == mq.MQ_DEV_KV_RANGE and int(last) == -1
