@@ -597,6 +597,8 @@ mq_status mq_verify_tree(const mq_verify_args* h_args, void* stream);
  * order, *n_free = n_pages) and the calls keep; they write the cache's table too.
  * A call does what its list says as if entry by entry, in the list's order.  An
  * entry outside the cache or the pool's state is left out and sets
+ * MQ_DEV_KV_RANGE.  Where the stack names a page to be taken that is outside the
+ * pool or has a count (in use, or on the stack twice), nothing is changed:
  * MQ_DEV_KV_RANGE.  Lists have up to MQ_MAX_SEQS entries, and n_seqs * table_ld
  * is below 2^31 (MQ_ERR_UNSUPPORTED).
  *  - mq_kv_grow: sequence s gets pages behind its own until it has ceil(length[s]

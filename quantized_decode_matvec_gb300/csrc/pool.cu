@@ -97,6 +97,14 @@ __device__ __forceinline__ int free_pages(const PoolArgs& p, bool* bad)
     return *bad ? 0 : n;
 }
 
+// Takes a free page: false where the stack names none (a page outside the pool, or one with a count: in use, or named
+// twice).  The count becomes 1; give_back undoes that.
+__device__ __forceinline__ bool take_page(const PoolArgs& p, int page)
+{
+    return page >= 0 && page < p.c.n_pages && atomicCAS(p.pool.refs + page, 0, 1) == 0;
+}
+__device__ __forceinline__ void give_back(const PoolArgs& p, int page) { p.pool.refs[page] = 0; }
+
 // ---- grow -----------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads) grow_kernel(const PoolArgs p, unsigned* status)
 {
@@ -132,13 +140,17 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PoolArgs p, unsign
         if (tid == 0) atomicOr(status, MQ_DEV_KV_FULL);
         return;
     }
+    // all pages are taken before any is written down: where the stack names one that is not free, none is
+    int got = 0;  // the thread's, up to the first that is not
+    while (tid + got * kThreads < total && take_page(p, p.pool.free_list[n_free - 1 - tid - got * kThreads])) ++got;
+    if (__syncthreads_or(tid + got * kThreads < total)) {
+        if (tid == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+        for (int k = 0; k < got; ++k) give_back(p, p.pool.free_list[n_free - 1 - tid - k * kThreads]);
+        return;
+    }
     for (int pos = tid; pos < total; pos += kThreads) {
-        const int s = entry_of(off_s, n, pos), page = p.pool.free_list[n_free - 1 - pos];
-        p.table[int64_t(s) * p.c.table_ld + have_s[s] + pos - off_s[s]] = page;
-        if (page >= 0 && page < p.c.n_pages)
-            p.pool.refs[page] = 1;
-        else
-            atomicOr(status, MQ_DEV_KV_RANGE);
+        const int s = entry_of(off_s, n, pos);
+        p.table[int64_t(s) * p.c.table_ld + have_s[s] + pos - off_s[s]] = p.pool.free_list[n_free - 1 - pos];
     }
     for (int s = tid; s < n; s += kThreads)
         if (off_s[s + 1] > off_s[s]) p.pool.seq_pages[s] = have_s[s] + off_s[s + 1] - off_s[s];
@@ -193,23 +205,27 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PoolArgs p, u
     }
     const bool full = total > n_free;
     if (full && tid == 0) atomicOr(status, MQ_DEV_KV_FULL);
+    int page[kPer];
+    bool wrong = false, took[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        page[k] = ok[k] && !full ? kNone : kSkip;
+        took[k] = false;
+        if (page[k] == kNone && v[k]) {
+            page[k] = p.pool.free_list[n_free - 1 - at[k]];
+            took[k] = take_page(p, page[k]);
+            wrong |= !took[k];
+        }
+    }
+    wrong = __syncthreads_or(wrong);  // the stack names a page that is not free: nothing is forked
+    if (wrong && tid == 0) atomicOr(status, MQ_DEV_KV_RANGE);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
         const int i = tid * kPer + k;
-        if (i >= p.n) continue;
-        int page = ok[k] && !full ? kNone : kSkip;
-        if (page == kNone && v[k]) {
-            page = p.pool.free_list[n_free - 1 - at[k]];
-            if (page >= 0 && page < p.c.n_pages) {
-                p.pool.refs[page] = 1;
-            } else {
-                page = kSkip;
-                atomicOr(status, MQ_DEV_KV_RANGE);
-            }
-        }
-        p.pool.scratch[i] = page;
+        if (wrong && took[k]) give_back(p, page[k]);
+        if (i < p.n) p.pool.scratch[i] = wrong ? kSkip : page[k];
     }
-    if (tid == 0 && !full && total) *p.pool.n_free = n_free - total;
+    if (tid == 0 && !full && !wrong && total) *p.pool.n_free = n_free - total;
 }
 
 // by `step` threads, number `at` of which calls; their first kAhead loads are on their way together

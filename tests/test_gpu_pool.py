@@ -326,3 +326,42 @@ def test_on_a_given_stream(cuda_ready):
     m.release([1], [0])
     m.compact()
     p.same(m)
+
+
+def state(p):
+    """Everything of a pool, to compare."""
+    return [x.clone() for x in (p.cache.table, p.cache.pages, p.pool.refs, p.pool.seq_pages, p.pool.n_free, p.pool.free_list)]
+
+
+@pytest.mark.parametrize("what", ["in use", "twice", "behind", "negative"])
+@pytest.mark.parametrize("at", [0, 3, 1500])
+def test_stack_that_names_a_page_that_is_not_free_changes_nothing(cuda_ready, what, at):
+    # `at` pages below the top: grow takes it with 2000 others, fork with 40; the pages taken before are free again
+    import torch
+    mq = cuda_ready
+    m = Model(2300, 50, 60, "q8_0", 1, 64, np.random.default_rng(at))
+    lens = np.zeros(50, np.int64)
+    lens[:4] = [70, 30, 64, 500]
+    assert m.grow(lens)
+    p = Pool(mq, m)
+    more = np.concatenate([lens[:4], np.full(46, 40 * 64 + 1)])
+    forks = i32(np.arange(40) % 4), i32(np.arange(4, 44)), i32([20] * 40)
+    calls = [lambda: mq.kv_grow(p.cache, p.pool, i32(more))] + \
+        [lambda: mq.kv_fork(p.cache, p.pool, *forks)] * (at < 40)
+    n = int(p.pool.n_free)
+    good = p.pool.free_list.clone()
+    p.pool.free_list[n - 1 - at] = {"in use": int(m.table[3, 2]), "twice": int(good[n - 3 - at]), "behind": 2300,
+                                    "negative": -1}[what]
+    for call in calls:
+        before = state(p)
+        call()
+        ok_status(mq, mq.MQ_DEV_KV_RANGE)
+        assert all(torch.equal(a, b) for a, b in zip(state(p), before))
+    p.pool.free_list.copy_(good)
+    if at < 40:
+        calls[1]()
+        assert m.fork(np.arange(40) % 4, np.arange(4, 44), [20] * 40)
+    else:
+        calls[0]()
+        assert m.grow(more)
+    p.same(m)
