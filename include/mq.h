@@ -614,7 +614,9 @@ mq_status mq_verify_tree(const mq_verify_args* h_args, void* stream);
  *  - mq_kv_free: sequence seq[i] gives up its pages but the first keep[i] (all of
  *    them where keep is NULL); their table entries become -1, and a page that no
  *    entry names any more goes onto the stack, where its last reference in the
- *    call was given up.  A sequence named again is left out.
+ *    call was given up.  A sequence named again is left out.  A page whose count
+ *    was not above zero stays off the stack, and one that the call's sequences
+ *    name more often than it has counts goes there once: MQ_DEV_KV_RANGE.
  *  - mq_kv_compact: with U pages in use, the k-th of those from page U on (in
  *    ascending order) moves to the k-th free page before U, bytes and count, and
  *    the table follows; free_list becomes n_pages - 1 down to U.

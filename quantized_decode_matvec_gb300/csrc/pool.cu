@@ -344,7 +344,9 @@ __device__ __forceinline__ int cta_rank(bool flag, int* warp_s, int* count)
 
 // ---- free -----------------------------------------------------------------------------------
 // Positions are the references that the call gives up, in its order.  A page whose count comes to zero is pushed at
-// its last position.  scratch[page]: the page's last position in the call.
+// its last position.  A page without a count, or that the call names more often than its count says, contradicts the
+// pool: the first stays as it is, the second is pushed once.  scratch[page]: the page's last position in the call;
+// scratch[n_pages + page]: how often the call names it (both only where a page may be named twice).
 __global__ void __launch_bounds__(kThreads) free_kernel(const PoolArgs p, unsigned* status)
 {
     __shared__ int off_s[kSeqs + 1], warp_s[kWarps];
@@ -398,12 +400,14 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const PoolArgs p, unsign
         const int page = __ldcg(p.table + *where);
         return page >= 0 && page < p.c.n_pages ? page : -1;
     };
-    // a page with one reference goes where that is; only of one that others name too has the last to be found
+    // a page with one reference goes where that is; only of one that others name too has the last to be found, which is
+    // any whose count was not one
+    int32_t* const last = p.pool.scratch;
+    int32_t* const named = p.pool.scratch + p.c.n_pages;
     int64_t w;
     int page, before, alone = 0, shared = 0;
     int page0 = -1;  // of the thread's first position, which is its only one mostly: kept, with the rest of it
     int64_t w0 = 0;
-    bool flag0 = false;
     for (int pos = begin + tid; pos < end; pos += kThreads) {
         page = place(pos, &w);
         if (pos == begin + tid) page0 = page, w0 = w;
@@ -411,29 +415,37 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const PoolArgs p, unsign
             atomicOr(status, MQ_DEV_KV_RANGE);
             continue;
         }
-        const int refs = __ldcg(p.pool.refs + page);
-        if (pos == begin + tid) flag0 = refs == 1;
+        const int refs = atomicSub(p.pool.refs + page, 1);
         alone += refs == 1;
-        shared |= refs > 1;
-        __stcg(p.pool.scratch + page, -1);
+        shared |= refs != 1;
+        __stcg(last + page, -1);
+        __stcg(named + page, 0);
     }
     int pushed = cluster_sum(cl, sum_s, 0, alone, &before, shared, &shared);
-    auto freed = [&](int pos, int* page, int64_t* where) {
+    // whether a position is where its page is pushed; *count: the page's count before the call, less what the call names
+    auto freed = [&](int pos, int* page, int64_t* where, int* count) {
         *page = place(pos, where);
+        *count = 0;
         if (*page < 0) return false;
-        const int refs = __ldcg(p.pool.refs + *page);
-        return shared ? refs == 0 && __ldcg(p.pool.scratch + *page) == pos : refs == 1;
+        if (!shared) return true;
+        if (__ldcg(last + *page) != pos) return false;
+        *count = __ldcg(p.pool.refs + *page);
+        return *count <= 0 && *count + __ldcg(named + *page) > 0;
     };
+    int rest;
     if (shared) {  // the same in the whole cluster
         for (int pos = begin + tid; pos < end; pos += kThreads) {
             if ((page = place(pos, &w)) >= 0) {
-                atomicMax(p.pool.scratch + page, pos);
-                atomicSub(p.pool.refs + page, 1);
+                atomicMax(last + page, pos);
+                atomicAdd(named + page, 1);
             }
         }
         cl.sync();
         int count = 0;
-        for (int pos = begin + tid; pos < end; pos += kThreads) count += freed(pos, &page, &w);
+        for (int pos = begin + tid; pos < end; pos += kThreads) {
+            count += freed(pos, &page, &w, &rest);
+            if (rest < 0) atomicOr(status, MQ_DEV_KV_RANGE);
+        }
         pushed = cluster_sum(cl, sum_s, 1, count, &before);
     }
     if (n_free + pushed > p.c.n_pages) {  // the stack names pages that are in use
@@ -441,17 +453,19 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const PoolArgs p, unsign
     }
     for (int base = begin; base < end; base += kThreads) {
         const int pos = base + tid;
-        bool flag;
+        bool flag = false;
+        rest = 0;
         if (base == begin && !shared) {
-            flag = pos < end && flag0;
+            flag = pos < end && page0 >= 0;
             page = page0, w = w0;
-        } else {
-            flag = pos < end && freed(pos, &page, &w);
+        } else if (pos < end) {
+            flag = freed(pos, &page, &w, &rest);
         }
         int here;
         const int to = n_free + before + cta_rank(flag, warp_s, &here);
         if (flag && to < p.c.n_pages) p.pool.free_list[to] = page;
-        if (flag && !shared) p.pool.refs[page] = 0;
+        // below zero: named too often, or without a count before, which it has again
+        if (rest < 0) p.pool.refs[page] = flag ? 0 : rest + __ldcg(named + page);
         if (pos < end) p.table[w] = -1;
         before += here;
     }

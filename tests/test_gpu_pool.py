@@ -365,3 +365,39 @@ def test_stack_that_names_a_page_that_is_not_free_changes_nothing(cuda_ready, wh
         calls[0]()
         assert m.grow(more)
     p.same(m)
+
+
+@pytest.mark.parametrize("ld", [20, 400])  # one CTA; a cluster
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("counts", [[1], [0], [-3], [1, 0, 2, -1, 1]])
+def test_pages_named_more_often_than_counted_are_freed_once(cuda_ready, ld, shared, counts):
+    # entries of the table over each other's pages, and pages without a count, among sequences in order
+    mq = cuda_ready
+    rng = np.random.default_rng(ld + len(counts))
+    m = Model(9 * ld, 8, ld, "f16", 1, 64, rng)
+    assert m.grow([64 * 19, 64 * (ld - 1), 64 * 7, 64 * 3, 64 * ld, 0, 0, 64])
+    if shared:
+        assert m.fork([1, 4], [5, 6], [64 * 5, 64 * 9 + 1])
+    for j, c in enumerate(counts):
+        page = m.table[1, 8 + j]  # of nobody else
+        m.refs[page] = c
+        if c > 0:  # named c times more than it is counted
+            for k in range(c):
+                m.refs[m.table[4, ld - 8 + 3 * j + k - 7]] = 0  # (whose page is given up by nobody)
+                m.table[4, ld - 8 + 3 * j + k - 7] = page
+    p = Pool(mq, m)
+    gone, keep = [4, 2, 1, 5], [2, 0, 1, 0]
+    where = [(s, i) for s, k in zip(gone, keep) for i in range(k, m.seq_pages[s])]
+    names = [int(m.table[s, i]) for s, i in where]
+    for at, ((s, i), page) in enumerate(zip(where, names)):
+        m.table[s, i] = -1
+        n = names.count(page)
+        if page in names[at + 1:] or m.refs[page] <= 0:
+            continue
+        m.refs[page] = max(m.refs[page] - n, 0)
+        if m.refs[page] == 0:
+            m.free.append(page)
+    for s, k in zip(gone, keep):
+        m.seq_pages[s] = min(m.seq_pages[s], k)
+    mq.kv_free(p.cache, p.pool, i32(gone), i32(keep))
+    p.same(m, mq.MQ_DEV_KV_RANGE)
