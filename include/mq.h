@@ -610,7 +610,9 @@ mq_status mq_verify_tree(const mq_verify_args* h_args, void* stream);
  *    the last is not full it takes a free one, into which the page's written
  *    tokens are copied (length[i] % 64 of them; the rest stays as it was).  A dst
  *    is named once, and is no src of the same call.  Too few free pages: nothing
- *    is changed, MQ_DEV_KV_FULL.
+ *    is changed, MQ_DEV_KV_FULL.  A full page of src that is outside the pool or
+ *    has no count is not shared, its place in dst's table becomes -1; from a begun
+ *    one outside the pool nothing is copied: MQ_DEV_KV_RANGE.
  *  - mq_kv_free: sequence seq[i] gives up its pages but the first keep[i] (all of
  *    them where keep is NULL); their table entries become -1, and a page that no
  *    entry names any more goes onto the stack, where its last reference in the

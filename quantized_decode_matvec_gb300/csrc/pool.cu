@@ -259,9 +259,12 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, unsign
     int32_t* const to = p.table + int64_t(dst) * p.c.table_ld;
     if (h == 0) {
         for (int i = threadIdx.x; i < full; i += 256) {
-            const int x = from[i];
+            // a page that nobody has is on the stack, or lost: it is not shared (no other entry makes it one with a
+            // count, since none takes such a one)
+            int x = from[i];
+            if (x < 0 || x >= p.c.n_pages || __ldcg(p.pool.refs + x) <= 0) x = -1;
             to[i] = x;
-            if (x >= 0 && x < p.c.n_pages)
+            if (x >= 0)
                 atomicAdd(p.pool.refs + x, 1);
             else
                 atomicOr(status, MQ_DEV_KV_RANGE);
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, unsign
     }
     if (rest == 0) return;
     const int x = from[full];
-    if (x < 0 || x >= p.c.n_pages) {
+    if (x < 0 || x >= p.c.n_pages) {  // nothing to copy: the new page stays as it was
         if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
         return;
     }

@@ -401,3 +401,27 @@ def test_pages_named_more_often_than_counted_are_freed_once(cuda_ready, ld, shar
         m.seq_pages[s] = min(m.seq_pages[s], k)
     mq.kv_free(p.cache, p.pool, i32(gone), i32(keep))
     p.same(m, mq.MQ_DEV_KV_RANGE)
+
+
+def test_fork_does_not_share_pages_that_are_not_in_use(cuda_ready):
+    # outside the pool, or without a count: -1 in the new tables, counts and the other entries as they should be
+    mq = cuda_ready
+    m = Model(60, 8, 12, "q8_0", 2, 64, np.random.default_rng(8))
+    assert m.grow([640, 700, 0, 0, 0, 0, 0, 0])
+    free = int(m.free[0])  # the stack's lowest: taken by nobody here
+    m.table[0, [1, 4, 6, 9]] = [60, -9, free, 2**31 - 1]
+    p = Pool(mq, m)
+    mq.kv_fork(p.cache, p.pool, i32([0, 1, 0, 0]), i32([3, 4, 6, 5]), i32([640, 65, 9 * 64 + 5, 64]))
+    for s, d, n in ((0, 3, 640), (1, 4, 65), (0, 6, 9 * 64 + 5), (0, 5, 64)):
+        for i in range(n // 64):
+            page = m.table[s, i]
+            fine = 0 <= page < 60 and page != free
+            m.table[d, i] = page if fine else -1
+            if fine:
+                m.refs[page] += 1
+        if n % 64:
+            m.table[d, n // 64] = m.take()
+            if s == 1:  # (sequence 0's begun page is outside the pool)
+                m.pages[m.table[d, 1]][:, m.rows(1)] = m.pages[m.table[1, 1]][:, m.rows(1)]
+        m.seq_pages[d] = -(-n // 64)
+    p.same(m, mq.MQ_DEV_KV_RANGE)
