@@ -621,7 +621,9 @@ mq_status mq_verify_tree(const mq_verify_args* h_args, void* stream);
  *    name more often than it has counts goes there once: MQ_DEV_KV_RANGE.
  *  - mq_kv_compact: with U pages in use, the k-th of those from page U on (in
  *    ascending order) moves to the k-th free page before U, bytes and count, and
- *    the table follows; free_list becomes n_pages - 1 down to U.
+ *    the table follows; free_list becomes n_pages - 1 down to U.  In use is what
+ *    has a count above zero; an entry of a sequence that names another page, or
+ *    none of the pool, becomes -1, and a count below zero 0: MQ_DEV_KV_RANGE.
  * Calls on one pool must not overlap on the GPU.  One launch (grow, free), two
  * (fork, compact). */
 typedef struct mq_kv_pool {

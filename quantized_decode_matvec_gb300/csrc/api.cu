@@ -1143,7 +1143,7 @@ mq_status mq_kv_compact(const mq_kv_cache* cache, const mq_kv_pool* pool, void* 
     if (st != MQ_OK || none) return st;
     const mq::DeviceInfo* dev = nullptr;
     if ((st = current_dev(&dev)) != MQ_OK) return st;
-    cudaError_t e = mq::launch_kv_compact(*cache, *pool, dev->num_sms, as_stream(stream));
+    cudaError_t e = mq::launch_kv_compact(*cache, *pool, dev->num_sms, dev->status, as_stream(stream));
     return e == cudaSuccess ? MQ_OK : cuda_fail(e);
 }
 

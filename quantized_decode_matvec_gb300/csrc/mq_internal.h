@@ -188,7 +188,8 @@ cudaError_t launch_kv_fork(const mq_kv_cache& cache, const mq_kv_pool& pool, con
                            const int32_t* length, int n, unsigned* status, cudaStream_t s);
 cudaError_t launch_kv_free(const mq_kv_cache& cache, const mq_kv_pool& pool, const int32_t* seq, const int32_t* keep,
                            int n, unsigned* status, cudaStream_t s);
-cudaError_t launch_kv_compact(const mq_kv_cache& cache, const mq_kv_pool& pool, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_compact(const mq_kv_cache& cache, const mq_kv_pool& pool, int num_sms, unsigned* status,
+                              cudaStream_t s);
 // looks up the device address of the no-alloc FFN's fixed scratch on device
 // `dev` (current) and caches it
 cudaError_t noalloc_setup(int dev);

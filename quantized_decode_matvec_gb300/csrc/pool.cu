@@ -16,8 +16,6 @@
 // out, and sets MQ_DEV_KV_RANGE.
 #include <cooperative_groups.h>
 
-#include <type_traits>
-
 #include "mq_internal.h"
 #include "mq_kv.cuh"
 #include "mq_stream.cuh"
@@ -483,10 +481,9 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const PoolArgs p, unsign
 
 // ---- compact --------------------------------------------------------------------------------
 // With U pages in use, the k-th page in use from U on goes to the k-th free one before U.  scratch: n_pages words,
-// the place that a page from U on goes to; then the free pages before U in ascending order, and the pages in use from
-// U on in descending order (their ranks among all pages in use are known before their number is); then both's number
-// and U.
-__global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PoolArgs p)
+// the place that a page in use goes to, -1 of one that is not; then the free pages before U in ascending order, and the pages in use from
+// U on in descending order (their ranks among all pages in use are known before their number is); then both's number.
+__global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PoolArgs p, unsigned* status)
 {
     __shared__ int warp_s[kWarps];
     __shared__ ClusterSum sum_s;
@@ -504,9 +501,15 @@ __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PoolArgs p
     int holes = 0, unused;
     for (int base = begin; base < end; base += kThreads) {
         const int i = base + tid;
-        const bool in_use = i < end && p.pool.refs[i] > 0;
+        const int refs = i < end ? p.pool.refs[i] : 0;
+        const bool in_use = refs > 0;
         int here;
         const int at = before + cta_rank(in_use, warp_s, &here);  // pages in use before page i
+        if (refs < 0) {
+            p.pool.refs[i] = 0;
+            atomicOr(status, MQ_DEV_KV_RANGE);
+        }
+        if (i < end && !(i >= used && in_use)) __stcg(map + i, in_use ? i : -1);
         if (i < end && i < used && !in_use) __stcg(hole + i - at, i), ++holes;
         if (i >= used && in_use) __stcg(far + used - 1 - at, i);
         if (i >= used && i < end) p.pool.free_list[n - 1 - i] = i;
@@ -522,18 +525,16 @@ __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const PoolArgs p
     if (rank == 0 && tid == 0) {
         *p.pool.n_free = n - used;
         map[2 * n + 2] = moves;
-        map[2 * n + 3] = used;
     }
     cl.sync();
 }
 
 constexpr int kMoveThreads = 256, kMoveBytes = 16 * 1024;  // of a CTA's turn
 
-__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const PoolArgs p)
+__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const PoolArgs p, unsigned* status)
 {
     griddep_wait();
-    const int n = int(p.c.n_pages), moves = __ldcg(p.pool.scratch + 2 * n + 2), used = __ldcg(p.pool.scratch + 2 * n + 3);
-    if (moves == 0) return;
+    const int n = int(p.c.n_pages), moves = __ldcg(p.pool.scratch + 2 * n + 2);
     const int32_t* const hole = p.pool.scratch + n;
     const int32_t* const far = hole + (n + 1) / 2;
     const int parts = (p.page_bytes + kMoveBytes - 1) / kMoveBytes;
@@ -545,10 +546,13 @@ __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const PoolAr
     }
     for (int64_t i = int64_t(blockIdx.x) * kMoveThreads + threadIdx.x; i < int64_t(p.c.n_seqs) * p.c.table_ld;
          i += int64_t(gridDim.x) * kMoveThreads) {
-        const int s = int(i / p.c.table_ld);
-        if (i - int64_t(s) * p.c.table_ld >= p.pool.seq_pages[s]) continue;
-        const int page = p.table[i];
-        if (page >= used && page < n) p.table[i] = __ldcg(p.pool.scratch + page);
+        const int s = int(i / p.c.table_ld), have = p.pool.seq_pages[s], at = int(i - int64_t(s) * p.c.table_ld);
+        if (at == 0 && (have < 0 || have > p.c.table_ld)) atomicOr(status, MQ_DEV_KV_RANGE);
+        if (at >= have) continue;
+        // an entry that names a page that is not in use names none from now on: another one's may come to lie there
+        const int page = p.table[i], to = page >= 0 && page < n ? __ldcg(p.pool.scratch + page) : -1;
+        if (to < 0) atomicOr(status, MQ_DEV_KV_RANGE);
+        if (to != page) p.table[i] = to;
     }
 }
 
@@ -582,10 +586,7 @@ cudaError_t launch_behind(K kernel, dim3 grid, int threads, cudaStream_t s, cons
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if constexpr (std::is_same_v<K, void (*)(PoolArgs)>)
-        return cudaLaunchKernelEx(&cfg, kernel, p);
-    else
-        return cudaLaunchKernelEx(&cfg, kernel, p, status);
+    return cudaLaunchKernelEx(&cfg, kernel, p, status);
 }
 
 PoolArgs pool_args(const mq_kv_cache& c, const mq_kv_pool& pool)
@@ -633,12 +634,12 @@ cudaError_t launch_kv_free(const mq_kv_cache& c, const mq_kv_pool& pool, const i
     return launch_cluster(free_kernel, int64_t(n) * c.table_ld, s, p, status);
 }
 
-cudaError_t launch_kv_compact(const mq_kv_cache& c, const mq_kv_pool& pool, int num_sms, cudaStream_t s)
+cudaError_t launch_kv_compact(const mq_kv_cache& c, const mq_kv_pool& pool, int num_sms, unsigned* status, cudaStream_t s)
 {
     PoolArgs p = pool_args(c, pool);
-    const cudaError_t e = launch_cluster(compact_plan_kernel, c.n_pages, s, p);
+    const cudaError_t e = launch_cluster(compact_plan_kernel, c.n_pages, s, p, status);
     if (e != cudaSuccess) return e;
-    return launch_behind(compact_move_kernel, dim3(unsigned(num_sms) * 8), kMoveThreads, s, p, nullptr);
+    return launch_behind(compact_move_kernel, dim3(unsigned(num_sms) * 8), kMoveThreads, s, p, status);
 }
 
 }  // namespace mq

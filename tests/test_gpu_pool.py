@@ -425,3 +425,36 @@ def test_fork_does_not_share_pages_that_are_not_in_use(cuda_ready):
                 m.pages[m.table[d, 1]][:, m.rows(1)] = m.pages[m.table[1, 1]][:, m.rows(1)]
         m.seq_pages[d] = -(-n // 64)
     p.same(m, mq.MQ_DEV_KV_RANGE)
+
+
+@pytest.mark.parametrize("n_pages", [60, 3000])  # one CTA; a cluster
+@pytest.mark.parametrize("moves", [True, False])
+def test_compact_takes_pages_without_a_count_out_of_the_table(cuda_ready, n_pages, moves):
+    # before and behind the pages in use, where another page moves to and where none does; what earlier calls left in
+    # the scratch is nothing to go by
+    mq = cuda_ready
+    rng = np.random.default_rng(n_pages)
+    m = Model(n_pages, 6, 12, "q8_0", 1, 64, rng)
+    if not moves:
+        m.free = sorted(m.free, reverse=True)
+    assert m.grow([64 * 10, 64 * 7, 300, 64, 64 * 12, 64])
+    p = Pool(mq, m)
+    p.pool.scratch.copy_(dev(rng.integers(-5, n_pages, p.pool.scratch.numel()).astype(np.int32)))
+    used, held = int((m.refs > 0).sum()), m.table.copy()
+    low = [x for x in range(used) if m.refs[x] == 0][:2] if moves else []
+    lost = low + [int(x) for x in m.free[:2]] + [n_pages, -1, 2**31 - 1]
+    for j, x in enumerate(lost):  # the pages that were named there stay in use, nobody names them
+        m.table[4, 2 + j] = x
+    for x in m.free[2:4]:
+        m.refs[x] = -7
+    p.cache.table.copy_(dev(m.table))
+    p.pool.refs.copy_(dev(m.refs))
+    assert (m.table[4, 2:2 + len(lost)] != held[4, 2:2 + len(lost)]).all()
+    m.table[4, 2:2 + len(lost)] = -1
+    m.refs[m.refs < 0] = 0
+    m.compact()
+    mq.kv_compact(p.cache, p.pool)
+    p.same(m, mq.MQ_DEV_KV_RANGE)
+    p.pool.seq_pages[2] = 13
+    mq.kv_compact(p.cache, p.pool)
+    ok_status(mq, mq.MQ_DEV_KV_RANGE)
