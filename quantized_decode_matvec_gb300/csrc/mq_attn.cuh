@@ -109,9 +109,8 @@ __device__ __forceinline__ bool attn_group(const AttnParams& p, int g, AttnGroup
     q->seq0 = __ldg(p.sh.grp_start + g);
     const int end = __ldg(p.sh.grp_start + g + 1);
     q->pages = __ldg(p.sh.grp_pages + g);
-    // (a context counts its tokens in 31 bits: no sequence has more pages, and their tokens stay in range below)
     *bad = q->seq0 < 0 || end < q->seq0 || end > p.c.n_seqs || q->pages < 0 || q->pages > p.sh.max_pages ||
-           q->pages > p.c.table_ld || q->pages > INT32_MAX / kKvPage;
+           q->pages > p.c.table_ld;
     q->t0 = q->T = 0, q->row = q->seq0;
     if (*bad) return false;
     q->t0 = __ldg(p.a.tok_start + q->seq0);

@@ -440,25 +440,6 @@ def test_call_in_which_no_group_has_work_ends_when_its_outputs_are_written(cuda_
 
 
 @pytest.mark.parametrize("T", [1, 2, 40])
-def test_prefix_of_more_pages_than_a_context_can_have(cuda_ready, T):
-    # 2^25 pages are 2^31 tokens, and 2^26 none in 32 bits: the group is skipped
-    import torch
-    mq = cuda_ready
-    b = Batch(np.random.default_rng(T), [(2, [(30, T), (5, T)]), (1, [(70, T)])], 4, 1, 64, "f16")
-    wide = torch.full((3, 2**26), -1, dtype=torch.int32, device="cuda")
-    wide[:, :b.table.shape[1]] = dev(b.table)
-    cache = mq.KVCache(dev(b.pages), wide, "f16", 1, 64)
-    for pages in (2**25, 2**25 + 1, 2**26 - 1, 2**26):
-        b.grp_pages = np.array([pages, 1], np.int32)
-        out = torch.full((3 * T, 4 * 64), 3.0, dtype=torch.float16, device="cuda")
-        b.call(mq, cache, out=out, max_pages=2**26, max_len=1000)
-        torch.cuda.synchronize()
-        assert mq.mq_read_device_status(0) == mq.MQ_DEV_KV_RANGE
-        b.check(out, only=[2])
-        assert (out[:2 * T] == 3).all()
-
-
-@pytest.mark.parametrize("T", [1, 2, 40])
 @pytest.mark.parametrize("groups", [3, 50])
 def test_groups_out_of_order_are_reported_and_write_nothing(cuda_ready, T, groups):
     # two groups over the same sequences, the one between them empty backwards: whose prefix it is cannot be told
