@@ -37,22 +37,23 @@ struct SoftmaxArgs {
     float* y;
     int64_t x_ld, y_ld;
     int vocab;
-    float k;
+    float h, k;  // scale * log2(e) = h k
     int rows, ahead;  // rows that are on the chip at once: a later one's part is called for when a CTA starts
 };
 
-// 2^(d k): -inf gives 0, NaN stays
-__device__ __forceinline__ float exp_of(float d, const SoftmaxArgs& p)
+// 2^((x - m) h k), mh = m h: -inf gives 0, NaN stays.  h is 1/2 for scales below 1, where a difference that passes the
+// largest number may weigh something; x - m is rounded once all the same.
+__device__ __forceinline__ float exp_of(float x, float mh, const SoftmaxArgs& p)
 {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * p.k));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(x, p.h, -mh) * p.k));
     return y;
 }
 
 // A larger maximum scales a sum by this; of a part that saw nothing (maximum -inf beside a finite one), 0.
 __device__ __forceinline__ float factor(float m, float top, const SoftmaxArgs& p)
 {
-    return m == top ? 1.0f : exp_of(m - top, p);
+    return m == top ? 1.0f : exp_of(m, top * p.h, p);
 }
 
 // maximum or sum over the CTA
@@ -144,12 +145,12 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
             for (int e = 0; e < 4; ++e) m = fmaxf(m, v[j][e]);
         m = cta_reduce<true>(m, max_s);
         // of a part of -inf alone (and of the padding) nothing comes; a row of -inf alone gives NaN below
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = m == -INFINITY ? 0.0f : m * p.h;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                v[j][e] = exp_of(v[j][e] - base, p);
+                v[j][e] = exp_of(v[j][e], base, p);
                 l += v[j][e];
             }
     } else {
@@ -157,12 +158,12 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
             load(u, v[0]);
             const float top = fmaxf(fmaxf(v[0][0], v[0][1]), fmaxf(v[0][2], v[0][3]));
             if (top > m) {
-                l *= m == -INFINITY ? 0.0f : exp_of(m - top, p);
+                l *= m == -INFINITY ? 0.0f : exp_of(m, top * p.h, p);
                 m = top;
             }
-            const float base = m == -INFINITY ? 0.0f : m;
+            const float base = m == -INFINITY ? 0.0f : m * p.h;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) l += exp_of(v[0][e] - base, p);
+            for (int e = 0; e < 4; ++e) l += exp_of(v[0][e], base, p);
         }
         const float top = cta_reduce<true>(m, max_s);
         l = m == -INFINITY ? l : l * factor(m, top, p);  // (a NaN among -inf stays)
@@ -191,11 +192,11 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
             }
         }
     } else {
-        const float inv = 1.0f / sum, base = top == -INFINITY ? 0.0f : top;
+        const float inv = 1.0f / sum, base = top == -INFINITY ? 0.0f : top * p.h;
         for (int u = first + threadIdx.x; u < last; u += kThreads) {
             load(u, v[0]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[0][e] = exp_of(v[0][e] - base, p) * inv;
+            for (int e = 0; e < 4; ++e) v[0][e] = exp_of(v[0][e], base, p) * inv;
             store(u, v[0]);
         }
     }
@@ -222,7 +223,8 @@ cudaError_t launch(const SoftmaxArgs& p, int64_t rows, int C, cudaStream_t s)
 cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_t x_ld, int64_t y_ld, float scale,
                            int num_sms, cudaStream_t s)
 {
-    SoftmaxArgs p = {x, y, x_ld, y_ld, vocab, float(double(scale) * 1.4426950408889634074), rows, 0};
+    const float h = scale < 1.0f ? 0.5f : 1.0f;
+    SoftmaxArgs p = {x, y, x_ld, y_ld, vocab, h, float(double(scale) / h * 1.4426950408889634074), rows, 0};
     // the fewest CTAs that hold a row at 32 values per thread; more while SMs are idle and each has values left
     const bool whole = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && x_ld % 4 == 0;  // every row starts a unit
     const int64_t units = (int64_t(vocab) + (whole ? 3 : 6)) / 4;

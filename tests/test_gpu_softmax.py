@@ -97,3 +97,21 @@ def test_captured_and_replayed(cuda_ready):
         torch.cuda.synchronize()
         assert torch.equal(y, mq.softmax(x))
     ok_status(mq)
+
+
+@pytest.mark.parametrize("vocab", [3, 700, 3000, 9000, 50001, 131072, 300001])
+@pytest.mark.parametrize("scale", [1e-45, 1e-39, 1e-38, 3e-38, 1e-30, 0.99, 1.0, 2.0, 1e30])
+def test_finite_rows_whose_values_are_further_apart_than_the_largest_number(cuda_ready, vocab, scale):
+    # a difference beyond 3.4e38 still weighs something at a small scale: (3e38 + 3e38) 1e-38 = 6
+    rng = np.random.default_rng(vocab)
+    x = np.stack([rng.uniform(-1, 1, vocab) * 3.4e38, np.full(vocab, -3.4e38), np.full(vocab, 3.4e38),
+                  rng.standard_normal(vocab) * 1e38])
+    with np.errstate(over="ignore"):
+        x = x.astype(np.float32)  # the normal numbers reach an infinity in some rows: NaN
+    x[1, rng.integers(0, vocab)] = 3.4e38
+    x[2, rng.integers(0, vocab)] = -3.4e38
+    got = cuda_ready.softmax(dev(x), scale=scale).cpu().numpy().astype(np.float64)
+    ok_status(cuda_ready)
+    fine = ~np.isinf(x).any(-1)
+    assert fine[:3].all() and np.isnan(got[(x == np.inf).any(-1)]).all()
+    check(got[fine], x[fine], scale)
