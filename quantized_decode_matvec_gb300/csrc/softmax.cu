@@ -154,16 +154,24 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
                 l += v[j][e];
             }
     } else {
+        // A thread adds up to 65536 values: with what each addition rounds off kept beside the sum, or 8192 equal ones
+        // would be off by 2^-13.  The base of the exponentials follows the maximum once that is 2^8 above, so a rising row
+        // scales (and rounds) the sum a few times instead of at every unit.
+        float lost = 0.0f, base = 0.0f;
         for (int u = first + threadIdx.x; u < last; u += kThreads) {
             load(u, v[0]);
             const float top = fmaxf(fmaxf(v[0][0], v[0][1]), fmaxf(v[0][2], v[0][3]));
-            if (top > m) {
-                l *= m == -INFINITY ? 0.0f : exp_of(m, top * p.h, p);
+            if (fmaf(top, p.h, -(m * p.h)) * p.k > 8.0f) {
+                const float f = m == -INFINITY ? 0.0f : exp_of(m, top * p.h, p);
+                l *= f, lost *= f;
                 m = top;
+                base = m * p.h;
             }
-            const float base = m == -INFINITY ? 0.0f : m * p.h;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) l += exp_of(v[0][e], base, p);
+            const float add = (exp_of(v[0][0], base, p) + exp_of(v[0][1], base, p)) +
+                              (exp_of(v[0][2], base, p) + exp_of(v[0][3], base, p)) - lost;
+            const float sum = l + add;
+            lost = (sum - l) - add;
+            l = sum;
         }
         const float top = cta_reduce<true>(m, max_s);
         l = m == -INFINITY ? l : l * factor(m, top, p);  // (a NaN among -inf stays)

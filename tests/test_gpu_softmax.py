@@ -115,3 +115,29 @@ def test_finite_rows_whose_values_are_further_apart_than_the_largest_number(cuda
     fine = ~np.isinf(x).any(-1)
     assert fine[:3].all() and np.isnan(got[(x == np.inf).any(-1)]).all()
     check(got[fine], x[fine], scale)
+
+
+@pytest.mark.parametrize("vocab", [1000003, 2**22 + 1, 2**25])
+def test_sums_of_long_rows(cuda_ready, vocab):
+    # Values that round alike when a thread adds them one after the other (8192 of them at 2^25: 2^-13), rising and falling
+    # ones.  Of an output: its own exponential 2^-22 + 2^-23 (|d| + 6), the base being up to 2^8 (5.6) below the maximum;
+    # the sum's exponentials alike, weighted by themselves, with a mean |d| of at most ln(vocab) < 18: 2^-18.1; its
+    # additions 2^-19 (a unit's, and 29 levels over threads and CTAs), its scalings, of which some six still count, 2^-19;
+    # the factors behind it 2^-22: 2^-17 + 2^-21 + 2^-22 |d| as above.
+    import torch
+    mq = cuda_ready
+    steps = torch.arange(vocab, device="cuda", dtype=torch.float32)
+    for name, x in (("0.7", torch.full((vocab,), float(np.log(0.7)), device="cuda")),
+                    ("0.1", torch.full((vocab,), float(np.log(0.1)), device="cuda")),
+                    ("rising", steps * (30.0 / vocab)), ("falling", steps * (-30.0 / vocab)),
+                    ("rising fast", steps * 0.01), ("steps", (steps % 997) * 0.01)):
+        x[vocab // 2] = max(0.0, float(x.max()))
+        for scale in (1.0, 0.4):
+            got = mq.softmax(x[None], scale=scale)[0].double()
+            ok_status(mq)
+            z = x.double() * float(np.float32(scale))
+            d = z - z.max()
+            ref = torch.exp(d)
+            ref /= ref.sum()
+            tol = ref * (2**-17 + 2**-21 + 2**-22 * d.abs()) + 2.0**-126
+            assert bool(((got - ref).abs() <= tol).all()), (name, scale, float(((got - ref).abs() / tol).max()))
