@@ -37,23 +37,26 @@ struct SoftmaxArgs {
     float* y;
     int64_t x_ld, y_ld;
     int vocab;
-    float h, k;  // scale * log2(e) = h k
+    float k;  // scale * log2(e), or twice that (H)
     int rows, ahead;  // rows that are on the chip at once: a later one's part is called for when a CTA starts
 };
 
-// 2^((x - m) h k), mh = m h: -inf gives 0, NaN stays.  h is 1/2 for scales below 1, where a difference that passes the
-// largest number may weigh something; x - m is rounded once all the same.
+// 2^((x - m) k), mh = m, or with H of halves and mh = m / 2: -inf gives 0, NaN stays.  A difference that passes the
+// largest number, 3.4e38, weighs something at scales below some 3e-37 only: H is for those (x - m is rounded once all
+// the same).  For every scale it cost 512 x 131072 2 us of 98.
+template <bool H>
 __device__ __forceinline__ float exp_of(float x, float mh, const SoftmaxArgs& p)
 {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaf(x, p.h, -mh) * p.k));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((H ? fmaf(x, 0.5f, -mh) : x - mh) * p.k));
     return y;
 }
 
 // A larger maximum scales a sum by this; of a part that saw nothing (maximum -inf beside a finite one), 0.
+template <bool H>
 __device__ __forceinline__ float factor(float m, float top, const SoftmaxArgs& p)
 {
-    return m == top ? 1.0f : exp_of(m, top * p.h, p);
+    return m == top ? 1.0f : exp_of<H>(m, H ? top * 0.5f : top, p);
 }
 
 // maximum or sum over the CTA
@@ -75,9 +78,10 @@ __device__ __forceinline__ float cta_reduce(float v, float* s)
 
 // NV > 0: the CTA's part of the row is up to 4 * NV values per thread, in registers; 0: any length, read twice
 // Several CTAs per SM, so that some load while others reduce or store.
-template <int NV>
+template <int NV, bool H>
 __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(const SoftmaxArgs p)
 {
+    constexpr float h = H ? 0.5f : 1.0f;
     __shared__ float max_s[kWarps], sum_s[kWarps];
     __shared__ float2 part_s[kMaxCluster];  // every CTA's maximum and sum
     cg::cluster_group cl = cg::this_cluster();
@@ -145,12 +149,12 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
             for (int e = 0; e < 4; ++e) m = fmaxf(m, v[j][e]);
         m = cta_reduce<true>(m, max_s);
         // of a part of -inf alone (and of the padding) nothing comes; a row of -inf alone gives NaN below
-        const float base = m == -INFINITY ? 0.0f : m * p.h;
+        const float base = m == -INFINITY ? 0.0f : m * h;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                v[j][e] = exp_of(v[j][e], base, p);
+                v[j][e] = exp_of<H>(v[j][e], base, p);
                 l += v[j][e];
             }
     } else {
@@ -161,20 +165,20 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
         for (int u = first + threadIdx.x; u < last; u += kThreads) {
             load(u, v[0]);
             const float top = fmaxf(fmaxf(v[0][0], v[0][1]), fmaxf(v[0][2], v[0][3]));
-            if (fmaf(top, p.h, -(m * p.h)) * p.k > 8.0f) {
-                const float f = m == -INFINITY ? 0.0f : exp_of(m, top * p.h, p);
+            if (fmaf(top, h, -(m * h)) * p.k > 8.0f) {
+                const float f = m == -INFINITY ? 0.0f : exp_of<H>(m, top * h, p);
                 l *= f, lost *= f;
                 m = top;
-                base = m * p.h;
+                base = m * h;
             }
-            const float add = (exp_of(v[0][0], base, p) + exp_of(v[0][1], base, p)) +
-                              (exp_of(v[0][2], base, p) + exp_of(v[0][3], base, p)) - lost;
+            const float add = (exp_of<H>(v[0][0], base, p) + exp_of<H>(v[0][1], base, p)) +
+                              (exp_of<H>(v[0][2], base, p) + exp_of<H>(v[0][3], base, p)) - lost;
             const float sum = l + add;
             lost = (sum - l) - add;
             l = sum;
         }
         const float top = cta_reduce<true>(m, max_s);
-        l = m == -INFINITY ? l : l * factor(m, top, p);  // (a NaN among -inf stays)
+        l = m == -INFINITY ? l : l * factor<H>(m, top, p);  // (a NaN among -inf stays)
         m = top;
     }
     l = cta_reduce<false>(l, sum_s);
@@ -183,11 +187,11 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
     cl.sync();
     float top = -INFINITY, sum = 0.0f;
     for (int c = 0; c < C; ++c) top = fmaxf(top, part_s[c].x);
-    for (int c = 0; c < C; ++c) sum += part_s[c].y == 0.0f ? 0.0f : part_s[c].y * factor(part_s[c].x, top, p);
+    for (int c = 0; c < C; ++c) sum += part_s[c].y == 0.0f ? 0.0f : part_s[c].y * factor<H>(part_s[c].x, top, p);
     if constexpr (NV > 0) {
         // a row of -inf alone: 0 / 0
         float4* const to = reinterpret_cast<float4*>(y - off) + first + threadIdx.x;
-        const float f = (sum == 0.0f || m == -INFINITY ? 0.0f : factor(m, top, p)) * (1.0f / sum);
+        const float f = (sum == 0.0f || m == -INFINITY ? 0.0f : factor<H>(m, top, p)) * (1.0f / sum);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int u = first + j * kThreads + int(threadIdx.x);
@@ -200,17 +204,17 @@ __global__ void __launch_bounds__(kThreads, NV >= 4 ? 2 : 4) softmax_kernel(cons
             }
         }
     } else {
-        const float inv = 1.0f / sum, base = top == -INFINITY ? 0.0f : top * p.h;
+        const float inv = 1.0f / sum, base = top == -INFINITY ? 0.0f : top * h;
         for (int u = first + threadIdx.x; u < last; u += kThreads) {
             load(u, v[0]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[0][e] = exp_of(v[0][e], base, p) * inv;
+            for (int e = 0; e < 4; ++e) v[0][e] = exp_of<H>(v[0][e], base, p) * inv;
             store(u, v[0]);
         }
     }
 }
 
-template <int NV>
+template <int NV, bool H = false>
 cudaError_t launch(const SoftmaxArgs& p, int64_t rows, int C, cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
@@ -223,7 +227,7 @@ cudaError_t launch(const SoftmaxArgs& p, int64_t rows, int C, cudaStream_t s)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, softmax_kernel<NV>, p);
+    return cudaLaunchKernelEx(&cfg, softmax_kernel<NV, H>, p);
 }
 
 }  // namespace
@@ -231,8 +235,8 @@ cudaError_t launch(const SoftmaxArgs& p, int64_t rows, int C, cudaStream_t s)
 cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_t x_ld, int64_t y_ld, float scale,
                            int num_sms, cudaStream_t s)
 {
-    const float h = scale < 1.0f ? 0.5f : 1.0f;
-    SoftmaxArgs p = {x, y, x_ld, y_ld, vocab, h, float(double(scale) / h * 1.4426950408889634074), rows, 0};
+    const bool halves = scale < 1e-36f;
+    SoftmaxArgs p = {x, y, x_ld, y_ld, vocab, float(double(scale) * (halves ? 2 : 1) * 1.4426950408889634074), rows, 0};
     // the fewest CTAs that hold a row at 32 values per thread; more while SMs are idle and each has values left
     const bool whole = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && x_ld % 4 == 0;  // every row starts a unit
     const int64_t units = (int64_t(vocab) + (whole ? 3 : 6)) / 4;
@@ -241,6 +245,7 @@ cudaError_t launch_softmax(const float* x, float* y, int rows, int vocab, int64_
         C *= 2;
     const int64_t per = ((units + C - 1) / C + kThreads - 1) / kThreads;  // units of a thread
     p.ahead = 2 * num_sms / C;
+    if (halves) return launch<0, true>(p, rows, C, s);
     if (per <= 1) return launch<1>(p, rows, C, s);
     if (per <= 2) return launch<2>(p, rows, C, s);
     if (per <= 4) return launch<4>(p, rows, C, s);

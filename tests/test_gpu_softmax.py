@@ -141,3 +141,21 @@ def test_sums_of_long_rows(cuda_ready, vocab):
             ref /= ref.sum()
             tol = ref * (2**-17 + 2**-21 + 2**-22 * d.abs()) + 2.0**-126
             assert bool(((got - ref).abs() <= tol).all()), (name, scale, float(((got - ref).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("vocab", [5, 9000, 131072, 300001])
+@pytest.mark.parametrize("scale", [1e-37, 9.99e-37, 1.01e-36, 1e-35])
+def test_smallest_scales(cuda_ready, vocab, scale):
+    # on both sides of where differences are taken of halves: masks, NaN and infinities as at any scale
+    rng = np.random.default_rng(vocab)
+    x = (rng.uniform(-3.4, 3.4, (6, vocab)) * 1e38).astype(np.float32)
+    x[0, :-1] = -np.inf
+    x[1, rng.random(vocab) < 0.5] = -np.inf
+    x[1, 0] = 1.0
+    x[2] = -np.inf
+    x[3, 1] = np.inf
+    x[4, 2] = np.nan
+    got = cuda_ready.softmax(dev(x), scale=scale).cpu().numpy().astype(np.float64)
+    ok_status(cuda_ready)
+    check(got[[0, 1, 5]], x[[0, 1, 5]], scale)
+    assert np.isnan(got[[2, 3, 4]]).all() and got[0, -1] == 1.0
