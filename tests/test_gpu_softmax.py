@@ -159,3 +159,30 @@ def test_smallest_scales(cuda_ready, vocab, scale):
     ok_status(cuda_ready)
     check(got[[0, 1, 5]], x[[0, 1, 5]], scale)
     assert np.isnan(got[[2, 3, 4]]).all() and got[0, -1] == 1.0
+
+
+# (rows, values): a row in 2, 4 and 8 units of a thread by one CTA, in clusters of two, four and eight, and in 9 units;
+# more rows than are on the chip at once, so that parts of later ones are called for ahead
+@pytest.mark.parametrize("rows,vocab", [(400, 3000), (400, 6001), (400, 14002), (200, 20003), (100, 50001), (60, 100000),
+                                        (60, 131072), (50, 131071), (50, 147000), (40, 200003)])
+@pytest.mark.parametrize("at,pad", [(0, 0), (0, 3), (1, 0), (3, 5)])
+def test_many_rows_wherever_they_start(cuda_ready, rows, vocab, at, pad):
+    import torch
+    mq = cuda_ready
+    torch.manual_seed(rows + vocab)
+    full = torch.randn((rows, vocab + at + pad), device="cuda") * 3
+    full[:, :at] = full[:, at + vocab:] = float("nan")
+    x, out = full[:, at:at + vocab], torch.full((rows, vocab + 5), -1.0, device="cuda")
+    want = torch.softmax(x.double(), -1)
+    d = x.double() - x.double().amax(-1, keepdim=True)
+    tol = want * (2**-17 + 2**-21 + 2**-22 * d.abs()) + 2.0**-126
+    for y0 in (0, 1):
+        out.fill_(-1)
+        mq.softmax(x, out=out[:, y0:y0 + vocab])
+        ok_status(mq)
+        err = (out[:, y0:y0 + vocab].double() - want).abs()
+        assert bool((err <= tol).all()), float((err / tol).max())
+        assert (out[:, :y0] == -1).all() and (out[:, y0 + vocab:] == -1).all()
+    mq.softmax(x, out=x)
+    ok_status(mq)
+    assert torch.equal(x, out[:, 1:1 + vocab]) and bool(torch.isnan(full[:, :at]).all() and torch.isnan(full[:, at + vocab:]).all())

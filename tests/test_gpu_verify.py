@@ -377,3 +377,72 @@ def test_rows_that_sum_to_too_much(cuda_ready):
                                     u=dev(np.array([0.5], np.float32)))
         torch.cuda.synchronize()
         assert mq.mq_read_device_status(0) == mq.MQ_DEV_KV_RANGE and int(last) == -1
+
+
+def walk_64(target, draft, token, parent, u, path_ld):
+    """walk() of rows on the GPU in fp64: the sums are off by some 2^-50, which changes a draw about never."""
+    import torch
+    path, i = [0], 0
+    while True:
+        kids = [c for c in range(1, len(token)) if parent[c] == i] if len(path) < path_ld else []
+        p, q = target[i].double(), None if draft is None else draft[i].double()
+        S, W, a, go = p.clone(), 1.0, 0.0, None
+        for c in kids:
+            x = token[c]
+            if float(S[x]) > 0 and float(u[c]) * (1.0 if q is None else float(q[x])) * W < float(S[x]):
+                go = c
+                break
+            if q is None:
+                W -= float(S[x])
+                S[x] = 0
+            else:
+                a += W
+                S = (p - a * q).clamp(min=0)
+                W = float(S.sum())
+        if go is None:
+            S = S if float(S.sum()) > 0 else p
+            run = S.cumsum(0)
+            return path, int(torch.searchsorted(run, float(u[0]) * run[-1], right=True))
+        path.append(go)
+        i = go
+
+
+@pytest.mark.parametrize("seqs,V", [(9, 40000), (9, 131072), (9, 151936), (10, 131072), (20, 131071), (3, 262147),
+                                    (1, 9_000_011), (10, 4_500_003)])
+@pytest.mark.parametrize("mode", ["draft", "lookup"])
+def test_large_vocabularies(cuda_ready, seqs, V, mode):
+    # clusters of sixteen (up to 9 sequences) and of eight; tiles of several units (the last two)
+    import torch
+    mq = cuda_ready
+    torch.manual_seed(V)
+    rng = np.random.default_rng(V)
+    sizes = [6] * seqs if V < 10**6 else [3] * seqs
+    n = sum(sizes)
+    x = torch.randn((n, V), device="cuda") * 2.5
+    target = torch.softmax(x, -1)
+    draft = torch.softmax(x.add_(0.7 * torch.randn((n, V), device="cuda")), -1) if mode == "draft" else None
+    del x
+    start = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    parent = np.concatenate([tree(rng, t, 3) for t in sizes]).astype(np.int32)
+    up = [int(start[s]) + int(parent[start[s] + i]) for s, t in enumerate(sizes) for i in range(t)]
+    source = target if draft is None else draft
+    token = np.array([int(torch.searchsorted(source[r].double().cumsum(0), rng.random())) for r in up], np.int32).clip(0, V - 1)
+    refused = 0
+    for case in range(4):
+        u = rng.random(n, dtype=np.float32)
+        if case >= 2:
+            u[:] = 0.999
+            u[start[:-1]] = rng.random(seqs, dtype=np.float32)
+        if case == 3:  # tokens that the draft likes better than the target: every child is refused at first
+            for i, r in enumerate(up):
+                token[i] = int((target[r] if draft is None else target[r] - draft[r]).argmin())
+        path, n_path, last = (v.cpu().numpy() for v in mq.verify_tree(
+            target, dev(start), dev(token), dev(parent), u=dev(u), draft=draft, path_ld=6))
+        ok_status(mq)
+        for s in range(seqs):
+            a, b = start[s], start[s + 1]
+            want, tok = walk_64(target[a:b], None if draft is None else draft[a:b], token[a:b].tolist(), parent[a:b].tolist(),
+                                u[a:b], 6)
+            assert path[s, :n_path[s]].tolist() == want and last[s] == tok, (s, path[s], want, last[s], tok)
+            refused += len(want) == 1
+    assert refused
