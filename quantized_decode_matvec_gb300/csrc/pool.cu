@@ -88,9 +88,9 @@ __device__ __forceinline__ int entry_of(const int* off_s, int n, int pos)
     return lo;
 }
 
-__device__ __forceinline__ int free_pages(const PoolArgs& p, bool* bad)
+// n: *p.pool.n_free, which is loaded ahead of the sums
+__device__ __forceinline__ int free_pages(const PoolArgs& p, int n, bool* bad)
 {
-    const int n = *p.pool.n_free;
     *bad = n < 0 || n > p.c.n_pages;
     return *bad ? 0 : n;
 }
@@ -107,7 +107,7 @@ __device__ __forceinline__ void give_back(const PoolArgs& p, int page) { p.pool.
 __global__ void __launch_bounds__(kThreads) grow_kernel(const PoolArgs p, unsigned* status)
 {
     __shared__ int off_s[kSeqs + 1], have_s[kSeqs], warp_s[kWarps];
-    const int tid = threadIdx.x, n = p.c.n_seqs;
+    const int tid = threadIdx.x, n = p.c.n_seqs, stack = __ldcg(p.pool.n_free);
     int v[kPer], at[kPer];
     bool bad = false;
 #pragma unroll
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PoolArgs p, unsign
         if (tid * kPer + k < n) off_s[tid * kPer + k] = at[k];
     if (tid == 0) off_s[n] = total;
     bool bad_free;
-    const int n_free = free_pages(p, &bad_free);
+    const int n_free = free_pages(p, stack, &bad_free);
     if (__syncthreads_or(bad) || bad_free) {
         if (tid == 0) atomicOr(status, MQ_DEV_KV_RANGE);
     }
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PoolArgs p, u
     __shared__ int dst_s[kSeqs];          // the first entry that forks into a sequence
     __shared__ uint32_t src_s[kSeqs / 32];  // sequences that an entry forks from
     griddep_launch_dependents();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, stack = __ldcg(p.pool.n_free);
     for (int i = tid; i < kSeqs; i += kThreads) dst_s[i] = INT32_MAX;
     if (tid < kSeqs / 32) src_s[tid] = 0;
     __syncthreads();
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const PoolArgs p, u
     }
     const int total = scan(v, at, warp_s);
     bool bad_free;
-    const int n_free = free_pages(p, &bad_free);
+    const int n_free = free_pages(p, stack, &bad_free);
     if (__syncthreads_or(bad) || bad_free) {
         if (tid == 0) atomicOr(status, MQ_DEV_KV_RANGE);
     }
@@ -249,17 +249,21 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, unsign
     using B = KvBlock<D, Q8>;
     const int e = blockIdx.x, h = blockIdx.y;
     const int src = __ldg(p.a + e), dst = __ldg(p.b + e), len = __ldg(p.len + e);
-    griddep_wait();
-    const int page = __ldcg(p.pool.scratch + e);
-    if (page == kSkip) return;
     const int full = len / kKvPage, rest = len % kKvPage;
     const int32_t* const from = p.table + int64_t(src) * p.c.table_ld;
     int32_t* const to = p.table + int64_t(dst) * p.c.table_ld;
+    // the source's pages, which the plan leaves as they are, ahead of it: a thread's first, and the begun one
+    const bool known = src >= 0 && src < p.c.n_seqs && len >= 0;
+    const int first = known && h == 0 && threadIdx.x < min(full, p.c.table_ld) ? __ldcg(from + threadIdx.x) : -1;
+    const int begun = known && full < p.c.table_ld ? __ldcg(from + full) : -1;
+    griddep_wait();
+    const int page = __ldcg(p.pool.scratch + e);
+    if (page == kSkip) return;
     if (h == 0) {
         for (int i = threadIdx.x; i < full; i += 256) {
             // a page that nobody has is on the stack, or lost: it is not shared (no other entry makes it one with a
             // count, since none takes such a one)
-            int x = from[i];
+            int x = i < 256 ? first : from[i];
             if (x < 0 || x >= p.c.n_pages || __ldcg(p.pool.refs + x) <= 0) x = -1;
             to[i] = x;
             if (x >= 0)
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const PoolArgs p, unsign
         }
     }
     if (rest == 0) return;
-    const int x = from[full];
+    const int x = begun;
     if (x < 0 || x >= p.c.n_pages) {  // nothing to copy: the new page stays as it was
         if (threadIdx.x == 0) atomicOr(status, MQ_DEV_KV_RANGE);
         return;
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const PoolArgs p, unsign
     __shared__ int first_s[kSeqs];  // by sequence: the first entry that names it
     __shared__ ClusterSum sum_s;
     cg::cluster_group cl = cg::this_cluster();
-    const int tid = threadIdx.x, rank = int(cl.block_rank());
+    const int tid = threadIdx.x, rank = int(cl.block_rank()), stack = __ldcg(p.pool.n_free);
     for (int i = tid; i < kSeqs; i += kThreads) first_s[i] = INT32_MAX;
     __syncthreads();
     int seq[kPer], keep[kPer], have[kPer], v[kPer], at[kPer];
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) free_kernel(const PoolArgs p, unsign
         if (tid * kPer + k < p.n) off_s[tid * kPer + k] = at[k];
     if (tid == 0) off_s[p.n] = total;
     bool bad_free;
-    const int n_free = free_pages(p, &bad_free);
+    const int n_free = free_pages(p, stack, &bad_free);
     if (__syncthreads_or(bad) || bad_free) {
         if (tid == 0 && rank == 0) atomicOr(status, MQ_DEV_KV_RANGE);
     }
