@@ -43,12 +43,14 @@ constexpr int kUnit = 512;       // values of a warp's step: 16 per lane
 constexpr int kMaxTiles = 1024;  // of a CTA
 constexpr int kHalf = 23, kOne = 2 * kHalf;  // 1.0 is 2^46
 constexpr double kInvOne = 1.0 / double(1ull << kOne);
-// A row that sums to 2^17 or more holds no probabilities; the sums stop here, so that they compare as signed numbers.
-// (A warp's part of a tile is below 2^62: kMaxTiles tiles hold 2^28 / 8 values.)
+// A row that sums to 2^17 or more holds no probabilities.  Up to 2^18 values of at most 1 their sums stay in range as
+// unsigned numbers; of more they stop at this one.  (A warp's part of a tile is below 2^62: kMaxTiles tiles hold 2^28 / 8
+// values.)
 constexpr uint64_t kTooMuch = (1ull << 63) - 1;
 
 struct VerifyArgs {
     mq_verify_args a;
+    bool capped;      // sums may pass 64 bits
     int chunk, tile;  // places of a CTA (a multiple of tile) and of a tile (a multiple of kUnit)
 };
 
@@ -91,9 +93,8 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v)
     return v;
 }
 // of numbers up to kTooMuch, as such a one
-__device__ __forceinline__ uint64_t warp_sum_capped(uint64_t v)
+__device__ __noinline__ uint64_t warp_sum_capped(uint64_t v)
 {
-    if (!__any_sync(0xffffffffu, (v >> 58) != 0)) return warp_sum(v);
     for (int o = 16; o; o >>= 1) v = min(v + __shfl_xor_sync(0xffffffffu, v, o), kTooMuch);
     return v;
 }
@@ -237,8 +238,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
         // a lane per CTA: one after the other these loads take 0.3 us each
         const int c = tid % 32;
         const uint64_t w = c < C ? *cl.map_shared_rank(&sm.total[passes & 1], c) : 0;
-        const uint64_t all = maximum ? warp_max(w) : warp_sum_capped(w);
-        before = maximum ? 0 : warp_sum_capped(c < rank ? w : 0);
+        const uint64_t all = maximum ? warp_max(w) : p.capped ? warp_sum_capped(w) : warp_sum(w);
+        if (!maximum) before = p.capped ? warp_sum_capped(c < rank ? w : 0) : warp_sum(c < rank ? w : 0);
         mine = v;
         ++passes;  // the other place next: who still reads this one is waited for there
         return all;
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
         if (tid % 32 == 0) sm.warp[tid / 32] = v;
         __syncthreads();
         const uint64_t w = tid % 32 < kWarps ? sm.warp[tid % 32] : 0;
-        return maximum ? warp_max(w) : warp_sum_capped(w);
+        return maximum ? warp_max(w) : p.capped ? warp_sum_capped(w) : warp_sum(w);
     };
     auto mass = [&](const Residual& r) {
         uint64_t sum = 0, all = 0;
@@ -283,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
                 sum -= warp_sum(away);
             }
             if (tid % 32 == 0) sm.tile[t] = sum;
-            all = min(all + sum, kTooMuch);
+            all += sum;
+            if (p.capped) all = min(all, kTooMuch);
             sum = 0;
         };
         // the whole part on its way to L2 at once: the warps' own loads are a few rounds, each of which would wait for HBM
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
                 mass_fixed = mass(r);
                 if (tid == 0) W = double(mass_fixed) * kInvOne;
                 known = true;
-                if (mass_fixed == kTooMuch) break;
+                if (mass_fixed >= kTooMuch) break;
             }
             if (taken < 0) {
                 if (!known) mass_fixed = mass(r);
@@ -378,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyArgs p,
                     r.a_hi = 0.0f, r.n_gone = 0;
                     mass_fixed = mass(r);
                 }
-                if (mass_fixed == kTooMuch && rank == 0 && tid == 0) atomicOr(status, MQ_DEV_KV_RANGE);
-                if (mass_fixed == 0 || mass_fixed == kTooMuch) break;
+                if (mass_fixed >= kTooMuch && rank == 0 && tid == 0) atomicOr(status, MQ_DEV_KV_RANGE);
+                if (mass_fixed == 0 || mass_fixed >= kTooMuch) break;
                 // the first index whose running sum passes u W
                 const uint64_t u = fixed(sm.u[0]), U = u < (1ull << kOne) ? u : (1ull << kOne) - 1;
                 const uint64_t mark = __umul64hi(U << (64 - kOne), mass_fixed);
@@ -466,6 +468,7 @@ cudaError_t launch_verify(const mq_verify_args& a, int num_sms, unsigned* status
 {
     VerifyArgs p;
     p.a = a;
+    p.capped = a.vocab >= 1 << 18;
     // a step of every warp for each CTA at least; sixteen of them only for few sequences, since a larger cluster waits
     // for a whole neighbourhood of SMs
     int C = int64_t(a.n_seqs) * kMaxCluster <= num_sms ? kMaxCluster : kMaxCluster / 2;
