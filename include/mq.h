@@ -510,7 +510,8 @@ mq_status mq_attn_tree(const mq_kv_cache* h_cache, const mq_attn_args* h_args, v
  * below 2^32, mq_attn_tree's bound holds, and (n_tokens *
  * (n_heads/n_kv_heads) / 256 + n_groups) * (max_pages + 12) * 3 * n_kv_heads
  * stays below 2^31 (MQ_ERR_UNSUPPORTED).  Three or four launches; without groups or
- * pages, mq_attn_tree's.
+ * pages, mq_attn_tree's, which is the faster call where little is shared (about: less
+ * than 16 sequences behind 8192 tokens, or 64 behind 2048).
  * workspace: as mq_attn_tree's, of mq_attn_shared_workspace_bytes; it serves
  * any call of either whose own size is no larger. */
 typedef struct mq_attn_groups {
